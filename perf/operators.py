@@ -228,8 +228,8 @@ def _run_own(s):
     if op == "logprobs_train":
         e8q.e8q_token_logprobs(s["logits"], ws, s["status"], tokens=s["tokens"], scale=case["scale"],
                                logprob_out=s["logprob"], lse_out=s["lse"], entropy_out=s["entropy"])
-        e8q.e8q_token_logprobs_backward(s["logits"], s["lse"], s["grad_logits"], tokens=s["tokens"],
-                                        grad_logprob=s["grad_logprob"], scale=case["scale"],
+        e8q.e8q_token_logprobs_backward(s["logits"], s["lse"], s["grad_logits"], s["status"],
+                                        tokens=s["tokens"], grad_logprob=s["grad_logprob"], scale=case["scale"],
                                         entropy=s["entropy"] if case["entropy"] else None,
                                         grad_entropy=s["grad_entropy"])
         return {"logprob": s["logprob"], "entropy": s["entropy"], "grad_logits": s["grad_logits"]}
