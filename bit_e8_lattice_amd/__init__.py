@@ -21,12 +21,18 @@ __all__ = [
     "e8q_ste_backward_hadamard", "e8q_decode_core_escape", "e8q_decode_workspace_size",
     "e8q_gemv_core_escape", "e8q_gemv_workspace_size", "e8q_pack_escapes", "e8q_unpack_escapes",
     "e8q_pack_workspace_size", "PACKED_RECORD_BYTES", "e8q_ptq_init", "e8q_ptq_workspace_size",
+    "e8q_token_logprobs", "e8q_token_logprobs_workspace_size", "e8q_token_logprobs_backward",
+    "e8q_token_logprobs_grad", "e8q_embed", "e8q_embed_backward", "e8q_embed_backward_workspace_size",
+    "e8q_orthogonalize", "e8q_orthogonal_step", "e8q_orthogonalize_workspace_size", "NEWTON_SCHULZ",
     "e8q_core_size",
     "e8q_status_string", "e8q_version",
-    "ESCAPE_RECORD_BYTES", "STATUS_BITS", "F32", "BF16",
+    "ESCAPE_RECORD_BYTES", "STATUS_BITS", "F32", "BF16", "I32", "I64",
 ]
 
 F32, BF16 = 0, 1
+I32, I64 = 0, 1
+# sigma -> a sigma + b sigma^3 + c sigma^5: five steps bring singular values in [0.01, 1] into [0.68, 1.21]
+NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)
 ESCAPE_RECORD_BYTES = 20
 ENCODE_NOALLOC_SCRATCH_BYTES = 64 << 20      # E8Q_ENCODE_NOALLOC_SCRATCH_BYTES
 PACKED_RECORD_BYTES = 8
@@ -103,6 +109,28 @@ def lib():
     L.e8q_sgd_rotated_project_hadamard.restype = e
     L.e8q_ste_backward.argtypes = [vp, vp, vp, f32, e, i64, vp]
     L.e8q_ste_backward.restype = e
+    L.e8q_token_logprobs.argtypes = [vp, e, i64, i64, i64, f32, vp, e, i64, vp, vp, vp, i64, vp, vp, vp, sz, vp, vp]
+    L.e8q_token_logprobs.restype = e
+    L.e8q_token_logprobs_workspace_size.argtypes = [i64, i64, i64]
+    L.e8q_token_logprobs_workspace_size.restype = sz
+    L.e8q_token_logprobs_backward.argtypes = [vp, e, i64, i64, i64, f32, vp, e, i64, vp, vp, vp, vp, vp, i64, vp, vp]
+    L.e8q_token_logprobs_backward.restype = e
+    L.e8q_token_logprobs_grad.argtypes = [vp, e, i64, i64, i64, f32, vp, e, i64, vp, vp, vp, vp, vp, vp, i64,
+                                          vp, sz, vp, vp]
+    L.e8q_token_logprobs_grad.restype = e
+    L.e8q_embed.argtypes = [vp, e, i64, i64, vp, e, i64, f32, vp, e, vp, vp]
+    L.e8q_embed.restype = e
+    L.e8q_embed_backward.argtypes = [vp, e, i64, i64, vp, e, i64, f32, vp, e, vp, f32, vp, sz, vp, vp]
+    L.e8q_embed_backward.restype = e
+    L.e8q_embed_backward_workspace_size.argtypes = [i64, i64, i64]
+    L.e8q_embed_backward_workspace_size.restype = sz
+    L.e8q_orthogonalize.argtypes = [vp, e, i64, i64, i64, i32, f32, f32, f32, vp, vp, sz, vp, vp]
+    L.e8q_orthogonalize.restype = e
+    L.e8q_orthogonal_step.argtypes = [vp, vp, vp, e, vp, vp, f32, i32, f32, f32, f32, i64, i64, i64,
+                                      i32, f32, f32, f32, vp, sz, vp, vp]
+    L.e8q_orthogonal_step.restype = e
+    L.e8q_orthogonalize_workspace_size.argtypes = [i64, i64, i64]
+    L.e8q_orthogonalize_workspace_size.restype = sz
     L.e8q_core_size.argtypes = [i32]
     L.e8q_core_size.restype = i64
     L.e8q_status_string.argtypes = [e]
@@ -429,6 +457,195 @@ def e8q_ptq_init(w, base_scale, alphas, core_bound, scale_out, core_idx_out, two
                               _ptr(err_out), _ptr(core_idx_out), _ptr(two_z_out), _ptr(workspace),
                               workspace.numel(), _ptr(status), _stream(w, stream))
     _check("e8q_ptq_init", code)
+
+
+# ------------------------------------------------------------------ around the projection
+
+_IDX = (torch.int32, torch.int64)
+
+
+def _index_code(t):
+    return I64 if t is not None and t.dtype == torch.int64 else I32
+
+
+def _size(t):
+    return 0 if t is None else t.numel()
+
+
+def _rows(t, name, dtypes):
+    """Row stride of a [rows, vocab] device tensor whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a device tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} dtype {t.dtype} not in {dtypes}")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [rows, vocab] with contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _token_count(tokens, rows):
+    """Tokens per row of ``tokens`` [rows] or [rows, n]."""
+    _dev(tokens, "tokens", _IDX)
+    if tokens is None:
+        return 0
+    if tokens.dim() not in (1, 2) or tokens.shape[0] != rows:
+        raise ValueError("tokens must be [rows] or [rows, n]")
+    return tokens.shape[1] if tokens.dim() == 2 else 1
+
+
+def _sized(t, name, n, dtypes=(torch.float32,)):
+    _dev(t, name, dtypes)
+    if t is not None and t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements, has {t.numel()}")
+
+
+def e8q_token_logprobs_workspace_size(rows, vocab, top_k=0):
+    return int(lib().e8q_token_logprobs_workspace_size(int(rows), int(vocab), int(top_k)))
+
+
+def e8q_token_logprobs(logits, workspace, status, tokens=None, scale=1.0, logprob_out=None, lse_out=None,
+                       entropy_out=None, top_idx_out=None, top_logprob_out=None, stream=None):
+    """``e8q_token_logprobs``: log probabilities of ``tokens`` ([rows] or
+    [rows, n], negative: ignored) under ``softmax(scale * logits)``, the rows'
+    log-sum-exp and entropy, and the most likely alternatives (``top_idx_out``
+    int32 and/or ``top_logprob_out`` float32, [rows, k])."""
+    stride = _rows(logits, "logits", _WDT)
+    rows, vocab = logits.shape
+    n = _token_count(tokens, rows)
+    k = 0
+    for t, nm, dt in ((top_idx_out, "top_idx_out", torch.int32), (top_logprob_out, "top_logprob_out", torch.float32)):
+        if t is not None:
+            k = k or t.numel() // max(rows, 1)
+            _sized(t, nm, rows * k, (dt,))
+    _sized(logprob_out, "logprob_out", rows * n); _sized(lse_out, "lse_out", rows)
+    _sized(entropy_out, "entropy_out", rows)
+    _dev(workspace, "workspace", (torch.uint8,)); _dev(status, "status", (torch.int32,))
+    code = lib().e8q_token_logprobs(_ptr(logits), _dtype_code(logits), rows, vocab, stride, float(scale),
+                                    _ptr(tokens) if n else None, _index_code(tokens), n, _ptr(logprob_out),
+                                    _ptr(lse_out), _ptr(entropy_out), k, _ptr(top_idx_out), _ptr(top_logprob_out),
+                                    _ptr(workspace), _size(workspace), _ptr(status), _stream(logits, stream))
+    _check("e8q_token_logprobs", code)
+
+
+def e8q_token_logprobs_backward(logits, lse, grad_logits, status, tokens=None, grad_logprob=None, scale=1.0,
+                                entropy=None, grad_entropy=None, stream=None):
+    """``e8q_token_logprobs_backward``: the gradient of ``sum(grad_logprob *
+    logprob) + sum(grad_entropy * entropy)`` with respect to ``logits``
+    (``grad_logits`` may be ``logits``)."""
+    stride, gstride = _rows(logits, "logits", _WDT), _rows(grad_logits, "grad_logits", (logits.dtype,))
+    rows, vocab = logits.shape
+    if grad_logits.shape != logits.shape:
+        raise ValueError("grad_logits must have the shape of logits")
+    n = _token_count(tokens, rows)
+    _sized(lse, "lse", rows); _sized(grad_logprob, "grad_logprob", rows * n); _sized(entropy, "entropy", rows)
+    _sized(grad_entropy, "grad_entropy", rows); _dev(status, "status", (torch.int32,))
+    if grad_entropy is None:
+        entropy = None
+    code = lib().e8q_token_logprobs_backward(_ptr(logits), _dtype_code(logits), rows, vocab, stride, float(scale),
+                                             _ptr(tokens) if n else None, _index_code(tokens), n, _ptr(lse),
+                                             _ptr(grad_logprob), _ptr(entropy), _ptr(grad_entropy),
+                                             _ptr(grad_logits), gstride, _ptr(status), _stream(logits, stream))
+    _check("e8q_token_logprobs_backward", code)
+
+
+def e8q_token_logprobs_grad(logits, tokens, grad_logprob, grad_logits, workspace, status, grad_entropy=None,
+                            scale=1.0, logprob_out=None, lse_out=None, entropy_out=None, stream=None):
+    """``e8q_token_logprobs_grad``: log probabilities (and entropy) and, for
+    upstream gradients known beforehand, the gradient of the logits in one
+    call (``grad_logits`` may be ``logits``)."""
+    stride, gstride = _rows(logits, "logits", _WDT), _rows(grad_logits, "grad_logits", (logits.dtype,))
+    rows, vocab = logits.shape
+    if grad_logits.shape != logits.shape:
+        raise ValueError("grad_logits must have the shape of logits")
+    n = _token_count(tokens, rows)
+    _sized(grad_logprob, "grad_logprob", rows * n); _sized(grad_entropy, "grad_entropy", rows)
+    _sized(logprob_out, "logprob_out", rows * n); _sized(lse_out, "lse_out", rows)
+    _sized(entropy_out, "entropy_out", rows)
+    _dev(workspace, "workspace", (torch.uint8,)); _dev(status, "status", (torch.int32,))
+    code = lib().e8q_token_logprobs_grad(_ptr(logits), _dtype_code(logits), rows, vocab, stride, float(scale),
+                                         _ptr(tokens) if n else None, _index_code(tokens), n, _ptr(grad_logprob),
+                                         _ptr(grad_entropy), _ptr(logprob_out), _ptr(lse_out), _ptr(entropy_out),
+                                         _ptr(grad_logits), gstride, _ptr(workspace), _size(workspace), _ptr(status),
+                                         _stream(logits, stream))
+    _check("e8q_token_logprobs_grad", code)
+
+
+def e8q_embed(table, tokens, out, status, scale=1.0, stream=None):
+    """``e8q_embed``: ``out[t] = scale * table[tokens[t]]`` (negative ids: zeros)."""
+    _dev(table, "table", _WDT); _dev(tokens, "tokens", _IDX); _dev(out, "out", _WDT)
+    _dev(status, "status", (torch.int32,))
+    if table.dim() != 2:
+        raise ValueError("table must be [vocab, dim]")
+    vocab, dim = table.shape
+    _sized(out, "out", tokens.numel() * dim, _WDT)
+    code = lib().e8q_embed(_ptr(table), _dtype_code(table), vocab, dim, _ptr(tokens), _index_code(tokens),
+                           tokens.numel(), float(scale), _ptr(out), _dtype_code(out), _ptr(status),
+                           _stream(table, stream))
+    _check("e8q_embed", code)
+
+
+def e8q_embed_backward_workspace_size(n, vocab, dim):
+    return int(lib().e8q_embed_backward_workspace_size(int(n), int(vocab), int(dim)))
+
+
+def e8q_embed_backward(grad_out, tokens, vocab, workspace, status, scale=1.0, grad_table=None, w_latent=None, lr=1.0,
+                       stream=None):
+    """``e8q_embed_backward``: the table's gradient by sorted tokens
+    (``grad_table`` [vocab, dim], written whole) and/or SGD on the bf16
+    latents of the rows that occur (``w_latent`` [vocab, dim], in place)."""
+    _dev(grad_out, "grad_out", _WDT); _dev(tokens, "tokens", _IDX); _dev(workspace, "workspace", (torch.uint8,))
+    _dev(status, "status", (torch.int32,))
+    n = tokens.numel()
+    if n == 0 or grad_out.numel() % n:
+        raise ValueError("grad_out must be [n, dim] for n tokens")
+    dim = grad_out.numel() // n
+    _sized(grad_table, "grad_table", int(vocab) * dim, _WDT)
+    _sized(w_latent, "w_latent", int(vocab) * dim, (torch.bfloat16,))
+    code = lib().e8q_embed_backward(_ptr(grad_out), _dtype_code(grad_out), n, dim, _ptr(tokens), _index_code(tokens),
+                                    int(vocab), float(scale), _ptr(grad_table),
+                                    _dtype_code(grad_table) if grad_table is not None else F32, _ptr(w_latent),
+                                    float(lr), _ptr(workspace), workspace.numel(), _ptr(status),
+                                    _stream(grad_out, stream))
+    _check("e8q_embed_backward", code)
+
+
+def e8q_orthogonalize_workspace_size(batch, rows, cols):
+    return int(lib().e8q_orthogonalize_workspace_size(int(batch), int(rows), int(cols)))
+
+
+def e8q_orthogonalize(g, update_out, workspace, status, steps=5, coeffs=NEWTON_SCHULZ, stream=None):
+    """``e8q_orthogonalize``: every matrix of ``g`` towards its orthogonal factor
+    by ``steps`` Newton-Schulz products (``update_out`` bf16)."""
+    _dev(g, "g", _WDT); _dev(update_out, "update_out", (torch.bfloat16,))
+    _dev(workspace, "workspace", (torch.uint8,)); _dev(status, "status", (torch.int32,))
+    if update_out.shape != g.shape:
+        raise ValueError("update_out must have the shape of g")
+    b, r, c = _shape3(g)
+    ca, cb, cc = (float(v) for v in coeffs)
+    code = lib().e8q_orthogonalize(_ptr(g), _dtype_code(g), b, r, c, int(steps), ca, cb, cc, _ptr(update_out),
+                                   _ptr(workspace), workspace.numel(), _ptr(status), _stream(g, stream))
+    _check("e8q_orthogonalize", code)
+
+
+def e8q_orthogonal_step(w, grad, momentum, workspace, status, mu=0.95, nesterov=True, lr=0.02, decay=0.0, gamma=1.0,
+                        steps=5, coeffs=NEWTON_SCHULZ, w_out=None, momentum_out=None, stream=None):
+    """``e8q_orthogonal_step``: momentum, its orthogonalization and the step of
+    the bf16 latents ``w`` (in place unless ``w_out`` / ``momentum_out`` are
+    given)."""
+    w_out = w if w_out is None else w_out
+    momentum_out = momentum if momentum_out is None else momentum_out
+    _dev(w, "w", (torch.bfloat16,)); _dev(grad, "grad", _WDT); _dev(momentum, "momentum", (torch.float32,))
+    _dev(w_out, "w_out", (torch.bfloat16,)); _dev(momentum_out, "momentum_out", (torch.float32,))
+    _dev(workspace, "workspace", (torch.uint8,)); _dev(status, "status", (torch.int32,))
+    if any(t.shape != w.shape for t in (grad, momentum, w_out, momentum_out)):
+        raise ValueError("grad, momentum and outputs must have the shape of w")
+    b, r, c = _shape3(w)
+    ca, cb, cc = (float(v) for v in coeffs)
+    code = lib().e8q_orthogonal_step(_ptr(w), _ptr(w_out), _ptr(grad), _dtype_code(grad), _ptr(momentum),
+                                     _ptr(momentum_out), float(mu), int(bool(nesterov)), float(lr), float(decay),
+                                     float(gamma), b, r, c, int(steps), ca, cb, cc, _ptr(workspace),
+                                     workspace.numel(), _ptr(status), _stream(w, stream))
+    _check("e8q_orthogonal_step", code)
 
 
 def e8q_core_size(core_bound):

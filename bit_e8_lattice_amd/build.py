@@ -19,7 +19,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libe8q.so")
 
 SOURCES = ["e8q_common.hip", "e8q_tables.hip", "e8q_project.hip", "e8q_encode.hip", "e8q_ste.hip",
-           "e8q_decode.hip", "e8q_roots.hip", "e8q_ptq.hip"]
+           "e8q_decode.hip", "e8q_roots.hip", "e8q_ptq.hip", "e8q_logprobs.hip", "e8q_embed.hip",
+           "e8q_orthogonal.hip"]
 # host program run before the library is compiled: writes the device table
 # blob and its layout header (embedded by e8q_tables.hip)
 TABLEGEN_SOURCES = ["e8q_tablegen.cpp", "e8q_tables_build.cpp", "e8q_core_table.cpp"]

@@ -1,0 +1,703 @@
+// e8q_token_logprobs, its gradient, and both in one call.
+//
+// Forward.  One pass over a row keeps, per thread, the running maximum m of the
+// logits, s = sum exp2((x - m) k) and t = sum exp2((x - m) k) (x - m) k with
+// k = scale log2 e; a new maximum rescales both.  At the end
+//   lse = scale m + ln s,   entropy = ln s - ln 2 * t / s,
+//   logprob = scale (x_t - m) - ln s,
+// so every exponent is formed from a difference of logits, exact where it
+// matters (near the maximum), and not from scale x - lse.
+//
+// Alternatives.  Each wave keeps the 64 best keys of its part of the row,
+// sorted, one per lane.  A key orders by value, then by lower index:
+// (order-preserving bits of x) << 32 | ~index.  The k-th best key so far is
+// the threshold; a vector without an element above it costs one comparison.
+// Elements above it are appended to a list in LDS, and every 64 of them are
+// sorted and merged (bitonic, in registers).  The first threshold is the k-th
+// largest of the 64 lanes' maxima over their first vectors (at least k
+// elements reach it), so that a row in random order appends about k ln(V / k)
+// elements; one in ascending order appends every element and is still right.
+//
+// Few rows are split over blocks (partial m, s, t and keys in the workspace)
+// and joined by a second kernel.
+#include <float.h>
+
+#include "e8q_device.hpp"
+#include "e8q_host.hpp"
+#include "e8q_vec.hpp"
+
+namespace e8q {
+
+constexpr int kLpBlock = 256;
+constexpr int kLpWaves = kLpBlock / kWave;
+constexpr int kLpUnroll = 4;          // vectors in flight per thread
+constexpr int kTopMax = 64;           // one key per lane
+constexpr int kMaxTokens = 1024;
+constexpr int kMaxSplits = 256;
+constexpr int64_t kMaxRows = int64_t(1) << 24;   // a block per row, fewer than 2^32 threads
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+// Stands in for an exponent of -inf where it is multiplied (0 * -inf is NaN):
+// exp2 of it is 0, and times any sum it stays finite.
+constexpr float kFloor = -1e9f;
+
+struct LpArgs {
+    const void* x;
+    int64_t stride;
+    uint32_t rows, vocab;
+    float scale;
+    const void* tokens;
+    uint32_t ntok;
+    int i64;                    // token ids are int64
+    float* logprob;
+    float* lse;
+    float* ent;
+    int32_t* top_idx;
+    float* top_lp;
+    uint32_t k;
+    uint32_t splits;            // blocks per row
+    uint32_t per_split;         // vectors per block
+    float4* part;               // [rows, splits] m, s, t
+    uint64_t* part_keys;        // [rows, splits, 64]
+    const float* g_lp;
+    const float* g_ent;
+    const float* lse_in;
+    const float* ent_in;
+    void* dx;
+    int64_t dx_stride;
+    uint32_t* status;
+};
+
+__device__ __forceinline__ int64_t token_at(const LpArgs& a, uint64_t i) {
+    return a.i64 ? static_cast<const int64_t*>(a.tokens)[i] : int64_t(static_cast<const int32_t*>(a.tokens)[i]);
+}
+
+__device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
+
+// ------------------------------------------------------------ softmax statistics
+
+struct Stat {
+    float m, s, t;
+};
+
+__device__ __forceinline__ Stat stat_empty() { return {-FLT_MAX, 0.0f, 0.0f}; }
+
+__device__ __forceinline__ Stat stat_join(const Stat& a, const Stat& b, float k) {
+    const float m = fmaxf(a.m, b.m);
+    const float da = fmaxf((a.m - m) * k, kFloor), db = fmaxf((b.m - m) * k, kFloor);
+    // a NaN in (a.m - m) can only come from m = inf, where s is a NaN already
+    const float ea = exp2_fast(da), eb = exp2_fast(db);
+    return {m, a.s * ea + b.s * eb, ea * (a.t + a.s * da) + eb * (b.t + b.s * db)};
+}
+
+template <int N>
+__device__ __forceinline__ void stat_add(Stat& st, const float (&v)[N], float k) {
+    float cm = v[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) cm = fmaxf(cm, v[i]);
+    const float m = fmaxf(st.m, cm);
+    const float d = fmaxf((st.m - m) * k, kFloor);
+    const float r = exp2_fast(d);
+    st.t = r * (st.t + st.s * d);
+    st.s *= r;
+    st.m = m;
+    float s0 = 0.0f, s1 = 0.0f, t0 = 0.0f, t1 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const float d0 = (v[i] - m) * k, d1 = (v[i + 1] - m) * k;
+        const float e0 = exp2_fast(d0), e1 = exp2_fast(d1);
+        s0 += e0;
+        s1 += e1;
+        t0 = fmaf(e0, fmaxf(d0, kFloor), t0);
+        t1 = fmaf(e1, fmaxf(d1, kFloor), t1);
+    }
+    st.s += s0 + s1;
+    st.t += t0 + t1;
+}
+
+__device__ __forceinline__ Stat stat_wave(Stat st, float k) {
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) {
+        const Stat o = {__shfl_xor(st.m, off, 64), __shfl_xor(st.s, off, 64), __shfl_xor(st.t, off, 64)};
+        // in the order of the lanes, so that both partners get the same bits
+        const bool hi = (__lane_id() & uint32_t(off)) != 0u;
+        st = hi ? stat_join(o, st, k) : stat_join(st, o, k);
+    }
+    return st;
+}
+
+// ------------------------------------------------------------ sorted keys
+
+__device__ __forceinline__ uint64_t key_of(float v, uint32_t idx) {
+    const uint32_t b = __float_as_uint(v + 0.0f);                // -0 counts as +0
+    uint32_t h = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+    h = v != v ? 0xFFFFFFFFu : h;                                // NaN above everything
+    return (uint64_t(h) << 32) | uint32_t(~idx);
+}
+
+__device__ __forceinline__ uint64_t shfl_xor64(uint64_t v, int mask) {
+    const uint32_t lo = __shfl_xor(uint32_t(v), mask, 64), hi = __shfl_xor(uint32_t(v >> 32), mask, 64);
+    return (uint64_t(hi) << 32) | lo;
+}
+
+__device__ __forceinline__ uint64_t shfl64(uint64_t v, int lane) {
+    const uint32_t lo = __shfl(uint32_t(v), lane, 64), hi = __shfl(uint32_t(v >> 32), lane, 64);
+    return (uint64_t(hi) << 32) | lo;
+}
+
+__device__ __forceinline__ uint64_t keep(uint64_t a, uint64_t b, bool larger) { return (a > b) == larger ? a : b; }
+
+// Descending over the lanes.
+__device__ __forceinline__ uint64_t sort_desc(uint64_t v, uint32_t lane) {
+#pragma unroll
+    for (uint32_t k = 2; k <= 64; k <<= 1)
+#pragma unroll
+        for (uint32_t j = k >> 1; j > 0; j >>= 1)
+            v = keep(v, shfl_xor64(v, int(j)), ((lane & j) == 0u) == ((lane & k) == 0u));
+    return v;
+}
+
+// The 64 largest of two descending lists, descending.
+__device__ __forceinline__ uint64_t merge_desc(uint64_t a, uint64_t b, uint32_t lane) {
+    const uint64_t r = shfl64(b, int(63u - lane));
+    uint64_t v = a > r ? a : r;
+#pragma unroll
+    for (uint32_t j = 32; j > 0; j >>= 1) v = keep(v, shfl_xor64(v, int(j)), (lane & j) == 0u);
+    return v;
+}
+
+// A wave's alternatives: its 64 best keys so far, and candidates not merged yet.
+struct TopList {
+    uint64_t best;        // lane's place in the descending list
+    uint64_t thr;         // k-th best key (wave-uniform)
+    uint32_t count;       // candidates in LDS (wave-uniform, < 64 between vectors)
+    uint64_t* buf;        // [128] of this wave
+
+    __device__ __forceinline__ void flush(uint32_t n, uint32_t k, uint32_t lane) {
+        const uint64_t c = lane < n ? buf[lane] : 0ull;
+        best = merge_desc(best, sort_desc(c, lane), lane);
+        const uint64_t kth = shfl64(best, int(k - 1));
+        thr = kth > thr ? kth : thr;
+    }
+
+    // Appends the lanes' keys above the threshold.
+    __device__ __forceinline__ void offer(uint64_t key, uint32_t k, uint32_t lane) {
+        const bool in = key > thr;
+        const uint64_t who = __ballot(in);
+        if (!who) return;
+        if (in) buf[count + __popcll(who & ((1ull << lane) - 1ull))] = key;
+        count += uint32_t(__popcll(who));
+        if (count >= 64u) {
+            __builtin_amdgcn_wave_barrier();
+            flush(64u, k, lane);
+            const uint64_t rest = buf[64u + lane];
+            __builtin_amdgcn_wave_barrier();
+            buf[lane] = rest;
+            count -= 64u;
+            __builtin_amdgcn_wave_barrier();
+        }
+    }
+};
+
+// ------------------------------------------------------------ one row's part
+
+// A row as vectors of 16 bytes from its first element, whatever its alignment
+// (gfx950 loads and stores dwordx4 at any element), so that the order of the
+// sums does not depend on where a tensor lies.
+template <typename T>
+struct __attribute__((packed, aligned(sizeof(T)))) RowVec {
+    u32x4_t v;
+};
+
+template <typename T>
+__device__ __forceinline__ void load_logits(const T* row, uint32_t vocab, uint32_t j, float (&v)[kVec<T>]) {
+    constexpr int VE = kVec<T>;
+    const uint32_t e0 = j * VE;
+    if (e0 + VE <= vocab) {
+        unpack(reinterpret_cast<const RowVec<T>*>(row + e0)->v, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VE; ++i) v[i] = e0 + i < vocab ? widen(row[e0 + i]) : -INFINITY;
+    }
+}
+
+// Statistics (all waves end with the block's) and alternatives (wave 0 ends
+// with the block's) of the vectors [lo, hi) of a row.
+template <typename T, bool TOP>
+__device__ __forceinline__ Stat row_part(const T* row, uint32_t vocab, uint32_t lo, uint32_t hi,
+                                         float k2, uint32_t top_k, uint64_t& best) {
+    constexpr int VE = kVec<T>;
+    __shared__ Stat s_stat[kLpWaves];
+    __shared__ uint64_t s_keys[TOP ? kLpWaves * 128 : 1];
+    const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
+    Stat st = stat_empty();
+    TopList top{0ull, 0ull, 0u, s_keys + (TOP ? wave * 128 : 0)};
+    bool first = true;
+    for (uint32_t base = lo; base < hi; base += kLpBlock * kLpUnroll) {
+        float v[kLpUnroll * VE];
+#pragma unroll
+        for (int u = 0; u < kLpUnroll; ++u) {
+            const uint32_t j = base + u * kLpBlock + tid;
+            float w[VE];
+            if (j < hi) {
+                load_logits<T>(row, vocab, j, w);
+            } else {
+#pragma unroll
+                for (int i = 0; i < VE; ++i) w[i] = -INFINITY;
+            }
+#pragma unroll
+            for (int i = 0; i < VE; ++i) v[u * VE + i] = w[i];
+        }
+        stat_add(st, v, k2);
+        if constexpr (TOP) {
+            if (first) {
+                uint64_t mine = 0ull;
+#pragma unroll
+                for (int u = 0; u < kLpUnroll; ++u) {
+                    const uint32_t j = base + u * kLpBlock + tid;
+#pragma unroll
+                    for (int i = 0; i < VE; ++i) {
+                        const uint64_t key = key_of(v[u * VE + i], 0xFFFFFFFFu);     // value alone
+                        if (j < hi && j * VE + i < vocab) mine = key > mine ? key : mine;
+                    }
+                }
+                top.thr = shfl64(sort_desc(mine, lane), int(top_k - 1));
+                first = false;
+            }
+#pragma unroll
+            for (int u = 0; u < kLpUnroll; ++u) {
+                const uint32_t j = base + u * kLpBlock + tid;
+                uint64_t most = 0ull;
+                uint64_t key[VE];
+#pragma unroll
+                for (int i = 0; i < VE; ++i) {
+                    const uint32_t e = j * VE + i;
+                    key[i] = j < hi && e < vocab ? key_of(v[u * VE + i], e) : 0ull;
+                    most = key[i] > most ? key[i] : most;
+                }
+                if (__ballot(most > top.thr)) {
+#pragma unroll
+                    for (int i = 0; i < VE; ++i) top.offer(key[i], top_k, lane);
+                }
+            }
+        }
+    }
+    if constexpr (TOP) {
+        __builtin_amdgcn_wave_barrier();
+        if (top.count) top.flush(top.count, top_k, lane);
+    }
+    st = stat_wave(st, k2);
+    if (lane == 0) s_stat[wave] = st;
+    if constexpr (TOP) {
+        __builtin_amdgcn_wave_barrier();
+        top.buf[lane] = top.best;
+    }
+    __syncthreads();
+    st = s_stat[0];
+#pragma unroll
+    for (int w = 1; w < kLpWaves; ++w) st = stat_join(st, s_stat[w], k2);
+    if constexpr (TOP) {
+        best = top.best;
+        if (wave == 0)
+            for (int w = 1; w < kLpWaves; ++w) best = merge_desc(best, s_keys[w * 128 + lane], lane);
+    }
+    return st;
+}
+
+struct RowEnd {
+    float ln_s, lse, ent;
+};
+
+// Row of -inf only: s = 0.
+__device__ __forceinline__ RowEnd row_end(const Stat& st, float scale) {
+    if (st.s == 0.0f) return {0.0f, -INFINITY, 0.0f};
+    const float l2 = __log2f(st.s);
+    const float ln_s = l2 * kLn2;
+    return {ln_s, scale * st.m + ln_s, (l2 - st.t / st.s) * kLn2};
+}
+
+__device__ __forceinline__ float logprob_of(float x, const Stat& st, const RowEnd& e, float scale) {
+    return st.s == 0.0f ? -INFINITY : scale * (x - st.m) - e.ln_s;
+}
+
+// Outputs of one row, by one block; `best` is wave 0's list.
+template <typename T, bool TOP>
+__device__ __forceinline__ void write_row(const LpArgs& a, uint32_t row, const T* x, const Stat& st, uint64_t best) {
+    const uint32_t tid = threadIdx.x;
+    const RowEnd e = row_end(st, a.scale);
+    uint32_t flags = 0u;
+    if (tid == 0) {
+        if (a.lse) a.lse[row] = e.lse;
+        if (a.ent) a.ent[row] = e.ent;
+        if (st.s != st.s) flags |= E8Q_STATUS_NONFINITE;
+    }
+    for (uint32_t j = tid; j < a.ntok; j += blockDim.x) {
+        const int64_t t = token_at(a, uint64_t(row) * a.ntok + j);
+        if (t >= int64_t(a.vocab)) flags |= E8Q_STATUS_BAD_INDEX;
+        if (a.logprob)
+            a.logprob[uint64_t(row) * a.ntok + j] =
+                t >= 0 && t < int64_t(a.vocab) ? logprob_of(widen(x[t]), st, e, a.scale) : 0.0f;
+    }
+    if constexpr (TOP) {
+        if (tid < a.k) {
+            const uint32_t idx = ~uint32_t(best);
+            if (a.top_idx) a.top_idx[uint64_t(row) * a.k + tid] = int32_t(idx);
+            if (a.top_lp) a.top_lp[uint64_t(row) * a.k + tid] = logprob_of(widen(x[idx]), st, e, a.scale);
+        }
+    }
+    flush_status(flags, a.status);
+}
+
+template <typename T, bool TOP>
+__global__ __launch_bounds__(kLpBlock) void logprobs_kernel(LpArgs a) {
+    const uint32_t row = a.splits == 1 ? blockIdx.x : blockIdx.x / a.splits;
+    const uint32_t sp = blockIdx.x - row * a.splits;
+    const T* x = static_cast<const T*>(a.x) + int64_t(row) * a.stride;
+    const uint32_t nvec = (a.vocab + kVec<T> - 1) / kVec<T>;
+    const uint32_t lo = min(sp * a.per_split, nvec), hi = min(lo + a.per_split, nvec);
+    uint64_t best = 0ull;
+    const Stat st = row_part<T, TOP>(x, a.vocab, lo, hi, a.scale * kLog2e, a.k, best);
+    if (a.splits == 1) {
+        write_row<T, TOP>(a, row, x, st, best);
+        return;
+    }
+    if (threadIdx.x == 0) a.part[blockIdx.x] = make_float4(st.m, st.s, st.t, 0.0f);
+    if constexpr (TOP) {
+        if (threadIdx.x < kTopMax) a.part_keys[uint64_t(blockIdx.x) * kTopMax + threadIdx.x] = best;
+    }
+}
+
+// Joins the parts of one row.
+template <typename T, bool TOP>
+__global__ __launch_bounds__(kLpBlock) void logprobs_join_kernel(LpArgs a) {
+    __shared__ Stat s_stat[kLpWaves];
+    __shared__ uint64_t s_keys[TOP ? kLpWaves * kTopMax : 1];
+    const uint32_t row = blockIdx.x, tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
+    const T* x = static_cast<const T*>(a.x) + int64_t(row) * a.stride;
+    const float k2 = a.scale * kLog2e;
+    Stat st = stat_empty();
+    if (tid < a.splits) {
+        const float4 p = a.part[uint64_t(row) * a.splits + tid];
+        st = {p.x, p.y, p.z};
+    }
+    uint64_t best = 0ull;
+    if constexpr (TOP) {
+        const uint64_t* keys = a.part_keys + uint64_t(row) * a.splits * kTopMax + lane;
+        for (uint32_t i = wave; i < a.splits; i += kLpWaves) best = merge_desc(best, keys[i * kTopMax], lane);
+        s_keys[tid] = best;
+    }
+    st = stat_wave(st, k2);
+    if (lane == 0) s_stat[wave] = st;
+    __syncthreads();
+    st = s_stat[0];
+#pragma unroll
+    for (int w = 1; w < kLpWaves; ++w) st = stat_join(st, s_stat[w], k2);
+    if constexpr (TOP) {
+        if (wave == 0)
+            for (int w = 1; w < kLpWaves; ++w) best = merge_desc(best, s_keys[w * kTopMax + lane], lane);
+    }
+    write_row<T, TOP>(a, row, x, st, best);
+}
+
+// ------------------------------------------------------------ gradient
+
+// dx = p' (c0 + c1 d) with d = (x a - b) k, p' = exp2(d): the row's constants.
+struct GradRow {
+    float a, b, k, c0, c1;
+};
+
+__device__ __forceinline__ float grad_at(float x, const GradRow& g) {
+    const float d = (x * g.a - g.b) * g.k;
+    return exp2_fast(d) * fmaf(g.c1, fmaxf(d, kFloor), g.c0);
+}
+
+// The row's live tokens, their logits and upstream gradients in LDS.
+struct RowTokens {
+    int32_t id[kMaxTokens];
+    float g[kMaxTokens];
+    float x[kMaxTokens];
+};
+
+template <typename T>
+__device__ __forceinline__ float load_tokens(const LpArgs& a, uint32_t row, const T* x, RowTokens& s) {
+    uint32_t flags = 0u;
+    for (uint32_t j = threadIdx.x; j < a.ntok; j += blockDim.x) {
+        const int64_t t = token_at(a, uint64_t(row) * a.ntok + j);
+        const bool live = t >= 0 && t < int64_t(a.vocab);
+        if (t >= int64_t(a.vocab)) flags |= E8Q_STATUS_BAD_INDEX;
+        s.id[j] = live ? int32_t(t) : -1;
+        s.g[j] = live ? a.g_lp[uint64_t(row) * a.ntok + j] : 0.0f;
+        s.x[j] = live ? widen(x[t]) : 0.0f;
+    }
+    flush_status(flags, a.status);
+    __syncthreads();
+    float sum = 0.0f;
+    for (uint32_t j = 0; j < a.ntok; ++j) sum += s.g[j];
+    return sum;
+}
+
+// The vectors [lo, hi) of the gradient row, then its given tokens among them
+// (the logits of the tokens were read before the first store: dx may be x).
+template <typename T>
+__device__ __forceinline__ void grad_part(const LpArgs& a, const T* x, T* dx, uint32_t lo, uint32_t hi,
+                                          const GradRow& g, bool zero, const RowTokens& s) {
+    constexpr int VE = kVec<T>;
+    for (uint32_t j = lo + threadIdx.x; j < hi; j += blockDim.x) {
+        float v[VE], d[VE];
+        load_logits<T>(x, a.vocab, j, v);
+#pragma unroll
+        for (int i = 0; i < VE; ++i) d[i] = zero ? 0.0f : grad_at(v[i], g);
+        const uint32_t e0 = j * VE;
+        if (e0 + VE <= a.vocab) {
+            reinterpret_cast<RowVec<T>*>(dx + e0)->v = pack(d);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VE; ++i)
+                if (e0 + i < a.vocab) dx[e0 + i] = narrow<T>(d[i]);
+        }
+    }
+    if (!a.ntok) return;
+    __syncthreads();
+    const int64_t first = int64_t(lo) * VE, last = int64_t(hi) * VE;
+    for (uint32_t j = threadIdx.x; j < a.ntok; j += blockDim.x) {
+        const int32_t t = s.id[j];
+        if (t < 0 || t < first || t >= last || zero) continue;
+        float sum = 0.0f;                                  // equal tokens: the same sum for each
+        for (uint32_t i = 0; i < a.ntok; ++i) sum += s.id[i] == t ? s.g[i] : 0.0f;
+        dx[t] = narrow<T>(fmaf(a.scale, sum, grad_at(s.x[j], g)));
+    }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kLpBlock) void logprobs_backward_kernel(LpArgs a) {
+    __shared__ RowTokens s_tok;
+    const uint32_t row = a.splits == 1 ? blockIdx.x : blockIdx.x / a.splits;
+    const uint32_t sp = blockIdx.x - row * a.splits;
+    const T* x = static_cast<const T*>(a.x) + int64_t(row) * a.stride;
+    T* dx = static_cast<T*>(a.dx) + int64_t(row) * a.dx_stride;
+    const uint32_t nvec = (a.vocab + kVec<T> - 1) / kVec<T>;
+    const uint32_t lo = min(sp * a.per_split, nvec), hi = min(lo + a.per_split, nvec);
+    const float sum = load_tokens<T>(a, row, x, s_tok);
+    const float lse = a.lse_in[row];
+    const float gh = a.g_ent ? a.g_ent[row] : 0.0f, h = a.g_ent ? a.ent_in[row] : 0.0f;
+    const GradRow g = {a.scale, lse, kLog2e, -a.scale * (sum + gh * h), -a.scale * gh * kLn2};
+    grad_part<T>(a, x, dx, lo, hi, g, lse == -INFINITY, s_tok);
+}
+
+// Statistics and gradient of a whole row by one block (the second reading of
+// the row is served by the caches).
+template <typename T>
+__global__ __launch_bounds__(kLpBlock) void logprobs_grad_kernel(LpArgs a) {
+    __shared__ RowTokens s_tok;
+    const uint32_t row = blockIdx.x;
+    const T* x = static_cast<const T*>(a.x) + int64_t(row) * a.stride;
+    T* dx = static_cast<T*>(a.dx) + int64_t(row) * a.dx_stride;
+    const uint32_t nvec = (a.vocab + kVec<T> - 1) / kVec<T>;
+    const float sum = load_tokens<T>(a, row, x, s_tok);
+    uint64_t none = 0ull;
+    const Stat st = row_part<T, false>(x, a.vocab, 0u, nvec, a.scale * kLog2e, 0u, none);
+    write_row<T, false>(a, row, x, st, 0ull);
+    __syncthreads();                 // the tokens' logits are read before dx (maybe x) is written
+    const RowEnd e = row_end(st, a.scale);
+    const float inv = 1.0f / st.s, gh = a.g_ent ? a.g_ent[row] : 0.0f;
+    const float c = a.scale * inv;
+    const GradRow g = {1.0f, st.m, a.scale * kLog2e, -c * (sum + gh * (e.ent - e.ln_s)), -c * gh * kLn2};
+    grad_part<T>(a, x, dx, 0u, nvec, g, st.s == 0.0f, s_tok);
+}
+
+// ------------------------------------------------------------ host
+
+// Blocks per row: enough blocks for every CU to hold several, each with at
+// least `kLpBlock * kLpUnroll` vectors to read.
+static uint32_t lp_splits(int64_t rows, int64_t vocab, size_t esz, uint32_t& per_split) {
+    const uint64_t ve = 16 / esz, nvec = (uint64_t(vocab) + ve - 1) / ve;
+    const uint64_t want = (uint64_t(device_cu_count()) * 4 + uint64_t(rows) - 1) / uint64_t(rows);
+    const uint64_t most = (nvec + kLpBlock * kLpUnroll - 1) / (kLpBlock * kLpUnroll);
+    uint64_t n = want < most ? want : most;
+    if (n > kMaxSplits) n = kMaxSplits;
+    if (n < 1) n = 1;
+    per_split = uint32_t((nvec + n - 1) / n);
+    return uint32_t((nvec + per_split - 1) / per_split);
+}
+
+static e8q_status_t lp_check(const void* logits, e8q_dtype_t dtype, int64_t rows, int64_t vocab, int64_t stride,
+                             float scale, const void* tokens, e8q_index_t index_type, int64_t ntok,
+                             uint32_t* status) {
+    if (!logits || !status || rows <= 0 || vocab <= 0 || stride < vocab || ntok < 0) return E8Q_ERR_INVALID;
+    if (dtype != E8Q_F32 && dtype != E8Q_BF16) return E8Q_ERR_INVALID;
+    if (!(scale > 0.0f) || __builtin_isinf(scale)) return E8Q_ERR_INVALID;
+    if ((ntok > 0) != (tokens != nullptr)) return E8Q_ERR_INVALID;
+    if (index_type != E8Q_I32 && index_type != E8Q_I64) return E8Q_ERR_INVALID;
+    const size_t esz = dtype == E8Q_BF16 ? 2 : 4, isz = index_type == E8Q_I64 ? 8 : 4;
+    if (reinterpret_cast<uintptr_t>(logits) % esz || reinterpret_cast<uintptr_t>(tokens) % isz) return E8Q_ERR_INVALID;
+    if (vocab >= (int64_t(1) << 31) - 16 || rows >= kMaxRows || ntok > kMaxTokens ||
+        stride >= (int64_t(1) << 40))
+        return E8Q_ERR_UNSUPPORTED;
+    return E8Q_OK;
+}
+
+static LpArgs lp_args(const void* logits, int64_t rows, int64_t vocab, int64_t stride, float scale,
+                      const void* tokens, e8q_index_t index_type, int64_t ntok, uint32_t* status) {
+    LpArgs a{};
+    a.x = logits;
+    a.stride = stride;
+    a.rows = uint32_t(rows);
+    a.vocab = uint32_t(vocab);
+    a.scale = scale;
+    a.tokens = tokens;
+    a.ntok = uint32_t(ntok);
+    a.i64 = index_type == E8Q_I64;
+    a.status = status;
+    return a;
+}
+
+static size_t lp_part_bytes(uint64_t blocks) { return size_t((blocks * sizeof(float4) + 255) / 256 * 256); }
+
+static size_t lp_workspace(int64_t rows, int64_t vocab, size_t esz, int64_t top_k) {
+    uint32_t per = 0;
+    const uint64_t splits = lp_splits(rows, vocab, esz, per);
+    if (splits == 1) return 0;
+    // without alternatives: room for the rows' lse and entropy (e8q_token_logprobs_grad)
+    return lp_part_bytes(uint64_t(rows) * splits) +
+           (top_k ? size_t(uint64_t(rows) * splits * kTopMax * 8) : size_t(rows) * 8);
+}
+
+// Forward launches; the arguments are checked.
+template <typename T, bool TOP>
+static void lp_forward(LpArgs& a, void* ws, hipStream_t st) {
+    a.splits = lp_splits(a.rows, a.vocab, sizeof(T), a.per_split);
+    a.part = static_cast<float4*>(ws);
+    a.part_keys = reinterpret_cast<uint64_t*>(static_cast<char*>(ws) + lp_part_bytes(uint64_t(a.rows) * a.splits));
+    launch(logprobs_kernel<T, TOP>, dim3(a.rows * a.splits), dim3(kLpBlock), 0, st, a);
+    if (a.splits > 1) launch(logprobs_join_kernel<T, TOP>, dim3(a.rows), dim3(kLpBlock), 0, st, a);
+}
+
+template <typename T>
+static void lp_backward(LpArgs& a, hipStream_t st) {
+    a.splits = lp_splits(a.rows, a.vocab, sizeof(T), a.per_split);
+    launch(logprobs_backward_kernel<T>, dim3(a.rows * a.splits), dim3(kLpBlock), 0, st, a);
+}
+
+}  // namespace e8q
+
+extern "C" size_t e8q_token_logprobs_workspace_size(int64_t rows, int64_t vocab, int64_t top_k) {
+    using namespace e8q;
+    if (rows <= 0 || vocab <= 0 || top_k < 0 || top_k > kTopMax || rows >= kMaxRows ||
+        vocab >= (int64_t(1) << 31) - 16)
+        return 0;
+    const size_t b = lp_workspace(rows, vocab, 2, top_k), f = lp_workspace(rows, vocab, 4, top_k);
+    return b > f ? b : f;
+}
+
+extern "C" e8q_status_t e8q_token_logprobs(const void* logits, e8q_dtype_t dtype, int64_t rows, int64_t vocab,
+                                           int64_t row_stride, float scale, const void* tokens,
+                                           e8q_index_t index_type, int64_t n_tokens, float* logprob_out,
+                                           float* lse_out, float* entropy_out, int64_t top_k, int32_t* top_idx_out,
+                                           float* top_logprob_out, void* workspace, size_t workspace_bytes,
+                                           uint32_t* status_dev, void* stream) {
+    using namespace e8q;
+    e8q_status_t st = lp_check(logits, dtype, rows, vocab, row_stride, scale, tokens, index_type, n_tokens, status_dev);
+    if (st != E8Q_OK) return st;
+    if (top_k < 0 || top_k > vocab || (top_k > 0) != (top_idx_out || top_logprob_out)) return E8Q_ERR_INVALID;
+    if ((logprob_out && !n_tokens) || (!logprob_out && !lse_out && !entropy_out && !top_k)) return E8Q_ERR_INVALID;
+    if (top_k > kTopMax) return E8Q_ERR_UNSUPPORTED;
+    const size_t need = lp_workspace(rows, vocab, dtype == E8Q_BF16 ? 2 : 4, top_k);
+    if (need && (!workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 256))
+        return E8Q_ERR_INVALID;
+    LpArgs a = lp_args(logits, rows, vocab, row_stride, scale, tokens, index_type, n_tokens, status_dev);
+    a.logprob = logprob_out;
+    a.lse = lse_out;
+    a.ent = entropy_out;
+    a.k = uint32_t(top_k);
+    a.top_idx = top_idx_out;
+    a.top_lp = top_logprob_out;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    if (dtype == E8Q_BF16)
+        top_k ? lp_forward<uint16_t, true>(a, workspace, s) : lp_forward<uint16_t, false>(a, workspace, s);
+    else
+        top_k ? lp_forward<float, true>(a, workspace, s) : lp_forward<float, false>(a, workspace, s);
+    return launch_status();
+}
+
+namespace e8q {
+
+static e8q_status_t lp_check_grad(const void* logits, int64_t vocab, int64_t row_stride, int64_t n_tokens,
+                                  const float* grad_logprob, const void* grad_logits, int64_t grad_stride,
+                                  e8q_dtype_t dtype) {
+    if (!grad_logits || grad_stride < vocab || (n_tokens > 0 && !grad_logprob)) return E8Q_ERR_INVALID;
+    if (grad_logits == logits && grad_stride != row_stride) return E8Q_ERR_INVALID;
+    if (reinterpret_cast<uintptr_t>(grad_logits) % (dtype == E8Q_BF16 ? 2 : 4)) return E8Q_ERR_INVALID;
+    return grad_stride >= (int64_t(1) << 40) ? E8Q_ERR_UNSUPPORTED : E8Q_OK;
+}
+
+}  // namespace e8q
+
+extern "C" e8q_status_t e8q_token_logprobs_backward(const void* logits, e8q_dtype_t dtype, int64_t rows,
+                                                    int64_t vocab, int64_t row_stride, float scale,
+                                                    const void* tokens, e8q_index_t index_type, int64_t n_tokens,
+                                                    const float* lse, const float* grad_logprob,
+                                                    const float* entropy, const float* grad_entropy,
+                                                    void* grad_logits, int64_t grad_stride, uint32_t* status_dev,
+                                                    void* stream) {
+    using namespace e8q;
+    e8q_status_t st = lp_check(logits, dtype, rows, vocab, row_stride, scale, tokens, index_type, n_tokens, status_dev);
+    if (st != E8Q_OK) return st;
+    if (!lse || (entropy == nullptr) != (grad_entropy == nullptr)) return E8Q_ERR_INVALID;
+    st = lp_check_grad(logits, vocab, row_stride, n_tokens, grad_logprob, grad_logits, grad_stride, dtype);
+    if (st != E8Q_OK) return st;
+    LpArgs a = lp_args(logits, rows, vocab, row_stride, scale, tokens, index_type, n_tokens, status_dev);
+    a.lse_in = lse;
+    a.g_lp = grad_logprob;
+    a.ent_in = entropy;
+    a.g_ent = grad_entropy;
+    a.dx = grad_logits;
+    a.dx_stride = grad_stride;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    if (dtype == E8Q_BF16) lp_backward<uint16_t>(a, s);
+    else lp_backward<float>(a, s);
+    return launch_status();
+}
+
+extern "C" e8q_status_t e8q_token_logprobs_grad(const void* logits, e8q_dtype_t dtype, int64_t rows, int64_t vocab,
+                                                int64_t row_stride, float scale, const void* tokens,
+                                                e8q_index_t index_type, int64_t n_tokens, const float* grad_logprob,
+                                                const float* grad_entropy, float* logprob_out, float* lse_out,
+                                                float* entropy_out, void* grad_logits, int64_t grad_stride,
+                                                void* workspace, size_t workspace_bytes, uint32_t* status_dev,
+                                                void* stream) {
+    using namespace e8q;
+    e8q_status_t st = lp_check(logits, dtype, rows, vocab, row_stride, scale, tokens, index_type, n_tokens, status_dev);
+    if (st != E8Q_OK) return st;
+    if (logprob_out && !n_tokens) return E8Q_ERR_INVALID;
+    st = lp_check_grad(logits, vocab, row_stride, n_tokens, grad_logprob, grad_logits, grad_stride, dtype);
+    if (st != E8Q_OK) return st;
+    const size_t need = lp_workspace(rows, vocab, dtype == E8Q_BF16 ? 2 : 4, 0);
+    if (need && (!workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 256))
+        return E8Q_ERR_INVALID;
+    LpArgs a = lp_args(logits, rows, vocab, row_stride, scale, tokens, index_type, n_tokens, status_dev);
+    a.logprob = logprob_out;
+    a.lse = lse_out;
+    a.ent = entropy_out;
+    a.g_lp = grad_logprob;
+    a.g_ent = grad_entropy;
+    a.dx = grad_logits;
+    a.dx_stride = grad_stride;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    if (!need) {
+        a.splits = 1;
+        if (dtype == E8Q_BF16) launch(logprobs_grad_kernel<uint16_t>, dim3(a.rows), dim3(kLpBlock), 0, s, a);
+        else launch(logprobs_grad_kernel<float>, dim3(a.rows), dim3(kLpBlock), 0, s, a);
+        return launch_status();
+    }
+    // few rows: the two split passes, with the rows' statistics in the workspace where no output takes them
+    float* stats = reinterpret_cast<float*>(static_cast<char*>(workspace) + need - size_t(rows) * 8);
+    if (!a.lse) a.lse = stats;
+    if (grad_entropy && !a.ent) a.ent = stats + rows;
+    if (dtype == E8Q_BF16) lp_forward<uint16_t, false>(a, workspace, s);
+    else lp_forward<float, false>(a, workspace, s);
+    a.lse_in = a.lse;
+    a.ent_in = a.ent;
+    if (dtype == E8Q_BF16) lp_backward<uint16_t>(a, s);
+    else lp_backward<float>(a, s);
+    return launch_status();
+}

@@ -1,0 +1,728 @@
+// e8q_orthogonalize and e8q_orthogonal_step: Newton-Schulz products on the
+// matrix cores.
+//
+// With n the smaller and m the larger side, X is n x m.  One step is three
+// products: A = X X^T, then D = (a - alpha) I + b A + c A^2, then
+// X <- alpha X + D X, alpha = a + b tr(A)/n + c tr(A^2)/n the mean of the
+// diagonal of M = aI + bA + cA^2.
+//
+// Why alpha is taken out.  The operands of the matrix cores are float16.  With
+// X <- M X the rounding of X (2^-12) lands on every singular direction alike
+// and grows with the small singular values (up to a^steps = 485 times), so a
+// gradient of low rank would come out with errors of several percent.  With
+// alpha X kept to 22 bits (two float16 parts) the rounding only passes through
+// D, which is small where the singular values are near each other and which
+// maps the strong directions' error back onto the strong directions.  Measured
+// against float64: 6e-4 to 1.2e-3 of |O|_F, for flat, falling and low-rank
+// spectra alike.  Problems too small to fill the chip (64-wide tiles) wait for
+// memory and launches, not for the matrix cores: there every operand has its
+// low part too and a product is three (hi hi, hi lo, lo hi), which leaves the
+// rounding of the result (a small matrix has few entries for errors to average
+// over: 9e-3 of |O|_F for a rank-1 8 x 8 without the low parts).
+//
+// Ranges.  X is stored times 2^s, s = floor(log2(sqrt(n m))) <= 15, A times
+// 2^14, D times 2^12: the entries' bounds (singular values <= 1.5) stay below
+// 65504 and typical entries well above float16's smallest normal number.
+//
+// Layout.  Every product is C[p][q] = sum_k P[p][k] Q[q][k] with k contiguous
+// in both operands: A = (X, X), A^2 = (A, A) (symmetric), D X = (D, X^T).  So
+// X is kept as X [n, m] and X^T [m, n]; the last product writes both.  Sides
+// are padded with zeros to whole tiles, which every step maps to zeros.  The
+// two symmetric products compute the tiles on and below the diagonal and write
+// each twice.
+#include <cmath>
+
+#include "e8q_device.hpp"
+#include "e8q_host.hpp"
+#include "e8q_vec.hpp"
+
+namespace e8q {
+
+typedef _Float16 half_t;
+typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
+typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
+
+constexpr int kBK = 64;                 // elements of k per stage
+constexpr int kScaleA = 14, kScaleD = 12;
+constexpr int kNormBlocks = 64;         // partial sums of |G|^2 per matrix
+
+// ------------------------------------------------------------ input
+
+struct OrthoIn {
+    const void* g;
+    int g_f32;
+    const float* mom_in;       // null: U = G
+    float* mom_out;
+    float mu;
+    int nesterov;
+    uint64_t cells;            // per matrix
+    uint32_t rows, cols;
+    uint32_t np, mp;
+    int tall;
+    int s;                     // X is scaled by 2^s
+    half_t* x;                 // [batch, np, mp]
+    half_t* xt;                // [batch, mp, np]
+    half_t* xt_lo;
+    half_t* x_lo;              // or null
+    double* norm;              // [batch, kNormBlocks]
+    uint32_t* status;
+};
+
+// The update direction before orthogonalization.
+__device__ __forceinline__ float direction(const OrthoIn& a, float g, float m1) {
+    return a.mom_in ? (a.nesterov ? fmaf(a.mu, m1, g) : m1) : g;
+}
+
+__device__ __forceinline__ void load_g8(const OrthoIn& a, uint64_t i, float (&v)[8]) {
+    if (a.g_f32) {
+        const float* p = static_cast<const float*>(a.g) + i;
+        float w[4];
+        unpack(*reinterpret_cast<const u32x4_t*>(p), w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = w[j];
+        unpack(*reinterpret_cast<const u32x4_t*>(p + 4), w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[4 + j] = w[j];
+    } else {
+        unpack(*reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(a.g) + i), v);
+    }
+}
+
+__device__ __forceinline__ void load_f8(const float* p, float (&v)[8]) {
+    float w[4];
+    unpack(*reinterpret_cast<const u32x4_t*>(p), w);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = w[j];
+    unpack(*reinterpret_cast<const u32x4_t*>(p + 4), w);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[4 + j] = w[j];
+}
+
+// New momentum, and partial sums of |U|^2 (float64: any magnitude of G).
+__global__ __launch_bounds__(256) void ortho_norm_kernel(OrthoIn a) {
+    __shared__ double s_sum[4];
+    const uint64_t base = uint64_t(blockIdx.y) * a.cells;
+    double sum = 0.0;
+    for (uint64_t i = (uint64_t(blockIdx.x) * 256u + threadIdx.x) * 8u; i < a.cells; i += uint64_t(gridDim.x) * 2048u) {
+        float g[8], m1[8] = {};
+        load_g8(a, base + i, g);
+        if (a.mom_in) {
+            float m0[8];
+            load_f8(a.mom_in + base + i, m0);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) m1[j] = fmaf(a.mu, m0[j], g[j]);
+            float lo[4] = {m1[0], m1[1], m1[2], m1[3]}, hi[4] = {m1[4], m1[5], m1[6], m1[7]};
+            *reinterpret_cast<u32x4_t*>(a.mom_out + base + i) = pack(lo);
+            *reinterpret_cast<u32x4_t*>(a.mom_out + base + i + 4) = pack(hi);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const double u = double(direction(a, g[j], m1[j]));
+            sum = fma(u, u, sum);
+        }
+    }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
+    if ((threadIdx.x & 63u) == 0u) s_sum[threadIdx.x >> 6] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        a.norm[uint64_t(blockIdx.y) * kNormBlocks + blockIdx.x] = (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
+}
+
+// X = U / |U| as float16 parts in both layouts, by tiles of 64 x 64 of U's own
+// layout; cells outside U are zeros.
+__global__ __launch_bounds__(256) void ortho_split_kernel(OrthoIn a) {
+    __shared__ half_t s_hi[64][72];
+    __shared__ half_t s_lo[64][72];
+    __shared__ double s_scale;
+    const uint32_t tid = threadIdx.x, item = blockIdx.z;
+    if (tid < 64u) {
+        double sum = tid < uint32_t(kNormBlocks) ? a.norm[uint64_t(item) * kNormBlocks + tid] : 0.0;
+#pragma unroll
+        for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
+        if (tid == 0u) {
+            const bool bad = !(sum <= 1.7976931348623157e308);
+            s_scale = bad ? __longlong_as_double(0x7FF8000000000000ll) : sum > 0.0 ? ldexp(1.0 / sqrt(sum), a.s) : 0.0;
+            if (bad && blockIdx.x == 0u && blockIdx.y == 0u) atomicOr(a.status, uint32_t(E8Q_STATUS_NONFINITE));
+        }
+    }
+    __syncthreads();
+    const double scale = s_scale;
+    const uint32_t r0 = blockIdx.y * 64u, c0 = blockIdx.x * 64u;
+    const uint32_t prows = a.tall ? a.mp : a.np, pcols = a.tall ? a.np : a.mp;    // padded sides of U
+    const uint64_t item_g = uint64_t(item) * a.cells, item_x = uint64_t(item) * a.np * a.mp;
+    half_t* same_hi = (a.tall ? a.xt : a.x) + item_x;
+    half_t* turn_hi = (a.tall ? a.x : a.xt) + item_x;
+    const uint32_t c = (tid & 7u) * 8u;
+#pragma unroll
+    for (uint32_t it = 0; it < 2; ++it) {
+        const uint32_t r = (tid >> 3) + it * 32u;
+        half8_t hi = {}, lo = {};
+        if (r0 + r < a.rows && c0 + c < a.cols) {
+            const uint64_t i = item_g + uint64_t(r0 + r) * a.cols + c0 + c;
+            float g[8], m1[8] = {};
+            load_g8(a, i, g);
+            if (a.mom_in) load_f8(a.mom_out + i, m1);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float x = float(double(direction(a, g[j], m1[j])) * scale);
+                hi[j] = half_t(x);
+                lo[j] = half_t(x - float(hi[j]));
+            }
+        }
+        *reinterpret_cast<half8_t*>(&s_hi[r][c]) = hi;
+        *reinterpret_cast<half8_t*>(&s_lo[r][c]) = lo;
+        const uint64_t at = uint64_t(r0 + r) * pcols + c0 + c;
+        *reinterpret_cast<half8_t*>(same_hi + at) = hi;
+        half_t* same_lo = a.tall ? a.xt_lo : a.x_lo;
+        if (same_lo) *reinterpret_cast<half8_t*>(same_lo + item_x + at) = lo;
+    }
+    __syncthreads();
+#pragma unroll
+    for (uint32_t it = 0; it < 2; ++it) {
+        const uint32_t r = (tid >> 3) + it * 32u;        // row of the turned tile
+        half8_t hi, lo;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            hi[j] = s_hi[c + j][r];
+            lo[j] = s_lo[c + j][r];
+        }
+        const uint64_t at = uint64_t(c0 + r) * prows + r0 + c;
+        *reinterpret_cast<half8_t*>(turn_hi + at) = hi;
+        half_t* turn_lo = a.tall ? a.x_lo : a.xt_lo;
+        if (turn_lo) *reinterpret_cast<half8_t*>(turn_lo + item_x + at) = lo;
+    }
+}
+
+// ------------------------------------------------------------ products
+
+enum { kGram = 0, kPoly = 1, kApply = 2, kLast = 3 };
+
+struct OrthoMul {
+    const half_t* p;           // [batch, np, k]
+    const half_t* q;           // [batch, (np or mp), k]
+    const half_t* p_lo;        // low parts (SPLIT)
+    const half_t* q_lo;
+    uint64_t p_item, q_item;   // elements per matrix
+    uint32_t k;                // padded, a multiple of kBK
+    uint32_t tiles_p, tiles_q; // kGram, kPoly: tiles_p on a side, lower triangle
+    uint32_t per_item;         // tiles per matrix
+    uint32_t n, np, mp;
+    float ca, cb, cc;
+    int s;
+    half_t* out;               // kGram: A; kPoly: D; kApply: X [np, mp]
+    half_t* out_lo;            // its low part (SPLIT)
+    const half_t* a;           // kPoly: A
+    const half_t* a_lo;
+    float* sums;               // [batch, per-item tiles of the triangle, 2]: tr A, |A|^2 of a tile
+    uint32_t sum_tiles;
+    float* alpha;              // [batch]
+    const half_t* xt;          // kApply, kLast: X^T before the step, and its low part
+    const half_t* xt_lo;
+    half_t* xt_out;
+    half_t* xt_lo_out;         // may be xt_lo (without SPLIT, where it is no operand)
+    // kLast
+    uint32_t rows, cols;
+    int tall;
+    uint16_t* update;          // or null: the latents' step
+    const uint16_t* w;
+    uint16_t* w_out;
+    float keep, step;          // w_out = w * keep - step * O
+};
+
+typedef __attribute__((address_space(3))) void lds_void;
+typedef const __attribute__((address_space(1))) void global_void;
+
+// 64 lanes x 16 bytes straight to LDS at `to` (wave-uniform) + 16 * lane.
+__device__ __forceinline__ void load_lds16(const half_t* from, half_t* to) {
+    __builtin_amdgcn_global_load_lds((global_void*)from, (lds_void*)to, 16, 0, 0);
+}
+
+__device__ __forceinline__ void tri_tile(uint32_t t, uint32_t& ti, uint32_t& tj) {
+    uint32_t i = uint32_t((sqrtf(8.0f * float(t) + 1.0f) - 1.0f) * 0.5f);
+    while ((i + 1u) * (i + 2u) / 2u <= t) ++i;
+    while (i * (i + 1u) / 2u > t) --i;
+    ti = i;
+    tj = t - i * (i + 1u) / 2u;
+}
+
+// Workgroups are dealt to the 8 XCDs in turn; this gives each XCD a contiguous
+// range of tiles, whose operands then meet in its L2.
+__device__ __forceinline__ uint32_t xcd_order(uint32_t b, uint32_t total) {
+    const uint32_t each = total / 8u, rest = total % 8u, x = b % 8u, i = b / 8u;
+    return x * each + min(x, rest) + i;
+}
+
+template <int B, int WP, int WQ, bool SPLIT, int MODE>
+__global__ __launch_bounds__(WP* WQ * 64) void ortho_mul_kernel(OrthoMul a) {
+    constexpr int kWaves = WP * WQ, FP = B / WP / 16, FQ = B / WQ / 16;
+    constexpr int kLoads = B / 8 / kWaves;           // wave loads per operand and stage
+    constexpr int kParts = SPLIT ? 2 : 1;
+    __shared__ half_t s_p[2][kParts][B * kBK];
+    __shared__ half_t s_q[2][kParts][B * kBK];
+    const uint32_t tid = threadIdx.x, lane = tid & 63u;
+    const uint32_t wave = uint32_t(__builtin_amdgcn_readfirstlane(int(tid >> 6)));
+    const uint32_t tile = xcd_order(blockIdx.x, gridDim.x);
+    const uint32_t item = tile / a.per_item, t = tile - item * a.per_item;
+    uint32_t ti, tj;
+    if constexpr (MODE == kGram || MODE == kPoly) {
+        tri_tile(t, ti, tj);
+    } else {
+        tj = t / a.tiles_p;
+        ti = t - tj * a.tiles_p;
+    }
+    // stage loads: a wave load fills 8 rows of 128 bytes; the 16-byte chunk c of
+    // row r sits at position c ^ (r & 7), so that the fragments' reads (16 rows,
+    // one chunk) spread over all banks
+    const uint32_t lrow = lane >> 3, lchunk = (lane & 7u) ^ lrow;
+    const uint64_t op = uint64_t(item) * a.p_item + uint64_t(ti * B + wave * (kLoads * 8) + lrow) * a.k + lchunk * 8u;
+    const uint64_t oq = uint64_t(item) * a.q_item + uint64_t(tj * B + wave * (kLoads * 8) + lrow) * a.k + lchunk * 8u;
+    auto stage = [&](int buf, uint32_t k) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const uint64_t at = uint64_t(i * 8) * a.k + k;
+            const int to = (wave * kLoads + i) * 8 * kBK;
+            load_lds16(a.p + op + at, &s_p[buf][0][to]);
+            load_lds16(a.q + oq + at, &s_q[buf][0][to]);
+            if constexpr (SPLIT) {
+                load_lds16(a.p_lo + op + at, &s_p[buf][1][to]);
+                load_lds16(a.q_lo + oq + at, &s_q[buf][1][to]);
+            }
+        }
+    };
+    const uint32_t wp = wave / WQ, wq = wave - wp * WQ;
+    const uint32_t frow = lane & 15u, fk = lane >> 4;
+    f32x4_t acc[FP][FQ] = {};
+    stage(0, 0u);
+    int buf = 0;
+    for (uint32_t k = 0; k < a.k; k += kBK) {
+        __syncthreads();                    // stage k has landed; stage k - 1 is no longer read
+        if (k + kBK < a.k) stage(buf ^ 1, k + kBK);
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            half8_t fp[kParts][FP], fq[kParts][FQ];
+            const uint32_t chunk = ((kk * 4 + fk) ^ (frow & 7u)) * 8u;
+#pragma unroll
+            for (int h = 0; h < kParts; ++h) {
+#pragma unroll
+                for (int i = 0; i < FP; ++i)
+                    fp[h][i] = *reinterpret_cast<const half8_t*>(&s_p[buf][h][((wp * FP + i) * 16 + frow) * kBK + chunk]);
+#pragma unroll
+                for (int j = 0; j < FQ; ++j)
+                    fq[h][j] = *reinterpret_cast<const half8_t*>(&s_q[buf][h][((wq * FQ + j) * 16 + frow) * kBK + chunk]);
+            }
+#pragma unroll
+            for (int i = 0; i < FP; ++i)
+#pragma unroll
+                for (int j = 0; j < FQ; ++j) {
+                    if constexpr (SPLIT) {
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fp[1][i], fq[0][j], acc[i][j], 0, 0, 0);
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fp[0][i], fq[1][j], acc[i][j], 0, 0, 0);
+                    }
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fp[0][i], fq[0][j], acc[i][j], 0, 0, 0);
+                }
+        }
+        buf ^= 1;
+    }
+    __syncthreads();
+    constexpr int kStrip = FQ * 16 + 8;     // a wave's 16 x 16 FQ strip on its way to rows (kStrip halfs per row)
+    half_t* strip = &s_p[0][0][0] + wave * kParts * 16 * kStrip;
+    half_t* strip_lo = strip + 16 * kStrip;
+
+    // lane: rows p0 + 0..3 of P, row q of Q, for fragment (i, j)
+    const uint32_t pw = ti * B + wp * FP * 16, qw = tj * B + wq * FQ * 16;
+
+    float alpha = 0.0f;
+    if constexpr (MODE == kPoly) {
+        // every block of a matrix adds the tiles' sums up in the same order
+        __shared__ float s_sum[2][kWaves];
+        const float* sums = a.sums + uint64_t(item) * a.sum_tiles * 2u;
+        float tr = 0.0f, sq = 0.0f;
+        for (uint32_t i = tid; i < a.sum_tiles; i += kWaves * 64u) {
+            tr += sums[2u * i];
+            sq += sums[2u * i + 1u];
+        }
+#pragma unroll
+        for (int off = 32; off >= 1; off >>= 1) {
+            tr += __shfl_xor(tr, off, 64);
+            sq += __shfl_xor(sq, off, 64);
+        }
+        if (lane == 0u) {
+            s_sum[0][wave] = tr;
+            s_sum[1][wave] = sq;
+        }
+        __syncthreads();
+        tr = sq = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            tr += s_sum[0][w];
+            sq += s_sum[1][w];
+        }
+        alpha = a.ca + (a.cb * tr + a.cc * sq) / float(a.n);
+        if (t == 0u && tid == 0u) a.alpha[item] = alpha;
+    }
+    if constexpr (MODE == kApply || MODE == kLast) alpha = a.alpha[item];
+
+    const float to_a = ldexpf(1.0f, kScaleA - 2 * a.s);
+    float tr = 0.0f, sq = 0.0f;
+#pragma unroll
+    for (int i = 0; i < FP; ++i) {
+#pragma unroll
+        for (int j = 0; j < FQ; ++j) {
+            const uint32_t p0 = pw + i * 16u + fk * 4u, q = qw + j * 16u + frow;
+            f32x4_t v = acc[i][j];
+            half4_t h, l;
+            if constexpr (MODE == kGram) {
+                const uint64_t at = uint64_t(item) * a.np * a.np + uint64_t(q) * a.np + p0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float r = v[e] * to_a;
+                    h[e] = half_t(r);
+                    l[e] = half_t(r - float(h[e]));
+                    sq = fmaf(r, r, sq);
+                    if (p0 + e == q) tr += r;
+                }
+                *reinterpret_cast<half4_t*>(a.out + at) = h;
+                if constexpr (SPLIT) *reinterpret_cast<half4_t*>(a.out_lo + at) = l;
+            }
+            if constexpr (MODE == kPoly) {
+                const uint64_t at = uint64_t(item) * a.np * a.np + uint64_t(q) * a.np + p0;
+                const half4_t av = *reinterpret_cast<const half4_t*>(a.a + at);
+                half4_t al = {};
+                if constexpr (SPLIT) al = *reinterpret_cast<const half4_t*>(a.a_lo + at);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float d = fmaf(a.cc * 0x1p-28f, v[e], a.cb * 0x1p-14f * (float(av[e]) + float(al[e])));
+                    if (p0 + e == q) d += a.ca - alpha;
+                    d *= 0x1p12f;
+                    h[e] = half_t(d);
+                    l[e] = half_t(d - float(h[e]));
+                }
+                *reinterpret_cast<half4_t*>(a.out + at) = h;
+                if constexpr (SPLIT) *reinterpret_cast<half4_t*>(a.out_lo + at) = l;
+            }
+            if constexpr (MODE == kApply || MODE == kLast) {
+                const uint64_t at = uint64_t(item) * a.np * a.mp + uint64_t(q) * a.np + p0;
+                const half4_t hi = *reinterpret_cast<const half4_t*>(a.xt + at);
+                const half4_t lo = *reinterpret_cast<const half4_t*>(a.xt_lo + at);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    v[e] = fmaf(alpha, float(hi[e]) + float(lo[e]), v[e] * 0x1p-12f);
+                    h[e] = half_t(v[e]);
+                    l[e] = half_t(v[e] - float(h[e]));
+                }
+                if constexpr (MODE == kApply) {
+                    *reinterpret_cast<half4_t*>(a.xt_out + at) = h;
+                    *reinterpret_cast<half4_t*>(a.xt_lo_out + at) = l;
+                } else {
+                    const float back = ldexpf(1.0f, -a.s);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t r = a.tall ? q : p0 + e, c = a.tall ? p0 + e : q;
+                        if (r >= a.rows || c >= a.cols) continue;
+                        const uint64_t o = (uint64_t(item) * a.rows + r) * a.cols + c;
+                        const float x = v[e] * back;
+                        if (a.update) a.update[o] = narrow<uint16_t>(x);
+                        else a.w_out[o] = narrow<uint16_t>(fmaf(-a.step, x, widen(a.w[o]) * a.keep));
+                    }
+                }
+            }
+            if constexpr (MODE != kLast) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    strip[(fk * 4 + e) * kStrip + j * 16 + frow] = h[e];
+                    if constexpr (SPLIT) strip_lo[(fk * 4 + e) * kStrip + j * 16 + frow] = l[e];
+                }
+            }
+        }
+        if constexpr (MODE != kLast) {
+            // rows of the strip, 16 bytes a lane; the wave's own LDS, in order
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            constexpr int kPerRow = FQ * 2;                    // 16-byte pieces
+            const uint32_t width = MODE == kApply ? a.mp : a.np;
+            const uint64_t out = uint64_t(item) * a.np * width + uint64_t(pw + i * 16u) * width + qw;
+#pragma unroll
+            for (int c = 0; c < 16 * kPerRow; c += 64) {
+                const uint32_t r = (c + lane) / kPerRow, x = (c + lane) % kPerRow;
+                if (MODE == kApply || ti != tj) {
+                    const uint64_t at = out + uint64_t(r) * width + x * 8u;
+                    *reinterpret_cast<half8_t*>(a.out + at) =
+                        *reinterpret_cast<const half8_t*>(&strip[r * kStrip + x * 8]);
+                    if constexpr (SPLIT)
+                        *reinterpret_cast<half8_t*>(a.out_lo + at) =
+                            *reinterpret_cast<const half8_t*>(&strip_lo[r * kStrip + x * 8]);
+                }
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        }
+    }
+    if constexpr (MODE == kGram) {
+        __shared__ float s_sum[2][kWaves];
+        tr *= 0x1p-14f;
+        sq *= ti != tj ? 0x1p-27f : 0x1p-28f;              // an entry off the diagonal stands for two
+#pragma unroll
+        for (int off = 32; off >= 1; off >>= 1) {
+            tr += __shfl_xor(tr, off, 64);
+            sq += __shfl_xor(sq, off, 64);
+        }
+        if (lane == 0u) {
+            s_sum[0][wave] = tr;
+            s_sum[1][wave] = sq;
+        }
+        __syncthreads();
+        if (tid == 0u) {
+            tr = sq = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                tr += s_sum[0][w];
+                sq += s_sum[1][w];
+            }
+            float* out = a.sums + (uint64_t(item) * a.sum_tiles + t) * 2u;
+            out[0] = tr;
+            out[1] = sq;
+        }
+    }
+}
+
+// ------------------------------------------------------------ host
+
+struct OrthoPlan {
+    uint32_t n, m, np, mp, tile, side;     // side: tiles along n
+    int tall, s;
+    size_t x, xt0, xt1, lo, a, d, sums, alpha, norm, total;
+    size_t x_lo, lo1, a_lo, d_lo;           // 64-wide tiles only
+};
+
+static size_t ortho_align(size_t v) { return (v + 255) / 256 * 256; }
+
+static OrthoPlan ortho_plan(int64_t batch, int64_t rows, int64_t cols) {
+    OrthoPlan p{};
+    p.tall = rows > cols;
+    p.n = uint32_t(p.tall ? cols : rows);
+    p.m = uint32_t(p.tall ? rows : cols);
+    auto tiles = [&](uint32_t t) { return uint64_t(batch) * ((p.n + t - 1) / t) * ((p.m + t - 1) / t); };
+    const uint64_t cus = uint64_t(device_cu_count());
+    p.tile = tiles(256) * 4 >= cus * 3 ? 256u : tiles(128) >= cus ? 128u : 64u;
+    p.np = (p.n + p.tile - 1) / p.tile * p.tile;
+    p.mp = (p.m + p.tile - 1) / p.tile * p.tile;
+    p.side = p.np / p.tile;
+    p.s = int(std::floor(0.5 * std::log2(double(p.n) * double(p.m))));
+    if (p.s > 15) p.s = 15;
+    const size_t rect = size_t(batch) * p.np * p.mp * 2, sq = size_t(batch) * p.np * p.np * 2;
+    size_t at = 0;
+    auto take = [&](size_t bytes) { const size_t o = at; at += ortho_align(bytes); return o; };
+    p.x = take(rect);
+    p.xt0 = take(rect);
+    p.xt1 = take(rect);
+    p.lo = take(rect);
+    p.a = take(sq);
+    p.d = take(sq);
+    p.sums = take(size_t(batch) * p.side * (p.side + 1) / 2 * 8);
+    p.alpha = take(size_t(batch) * 4);
+    p.norm = take(size_t(batch) * kNormBlocks * 8);
+    if (p.tile == 64) {
+        p.x_lo = take(rect);
+        p.lo1 = take(rect);
+        p.a_lo = take(sq);
+        p.d_lo = take(sq);
+    }
+    p.total = at;
+    return p;
+}
+
+static e8q_status_t ortho_check(const void* g, e8q_dtype_t dtype, int64_t batch, int64_t rows, int64_t cols,
+                                int32_t steps, float ca, float cb, float cc, const uint32_t* status) {
+    if (!g || !status || batch <= 0 || rows <= 0 || cols <= 0 || cols % 8) return E8Q_ERR_INVALID;
+    if (dtype != E8Q_F32 && dtype != E8Q_BF16) return E8Q_ERR_INVALID;
+    if (reinterpret_cast<uintptr_t>(g) % 16) return E8Q_ERR_INVALID;
+    if (!std::isfinite(ca) || !std::isfinite(cb) || !std::isfinite(cc)) return E8Q_ERR_INVALID;
+    if (steps < 1 || steps > 16 || rows > 65536 || cols > 65536 || batch > 65535) return E8Q_ERR_UNSUPPORTED;
+    // largest singular value after each step, from [0, 1]: the polynomial at the
+    // ends and where its derivative a + 3 b s^2 + 5 c s^4 vanishes
+    double top = 1.0;
+    for (int32_t i = 0; i < steps; ++i) {
+        const double a = ca, b = cb, c = cc;
+        double at[4] = {top, 0.0, 0.0, 0.0}, next = 0.0, gain = std::fabs(a);
+        const double disc = 9.0 * b * b - 20.0 * a * c;
+        if (c != 0.0 && disc >= 0.0) {
+            at[1] = (-3.0 * b + std::sqrt(disc)) / (10.0 * c);
+            at[2] = (-3.0 * b - std::sqrt(disc)) / (10.0 * c);
+        } else if (c == 0.0 && b != 0.0) {
+            at[1] = -a / (3.0 * b);
+        }
+        at[3] = c != 0.0 ? -b / (2.0 * c) : 0.0;                 // square where the gain is extreme
+        for (int j = 0; j < 4; ++j) {
+            const double x2 = j == 0 ? top * top : at[j];
+            if (x2 < 0.0 || x2 > top * top) continue;
+            const double f = a + b * x2 + c * x2 * x2;
+            gain = std::fmax(gain, std::fabs(f));
+            next = std::fmax(next, std::fabs(f) * std::sqrt(x2));
+        }
+        if (gain > 7.0 || next > 1.5) return E8Q_ERR_UNSUPPORTED;
+        top = next;
+    }
+    return E8Q_OK;
+}
+
+template <int B, int WP, int WQ, bool SPLIT>
+static void ortho_steps(const OrthoPlan& p, OrthoMul a, int64_t batch, int32_t steps, char* ws, hipStream_t st) {
+    half_t* x = reinterpret_cast<half_t*>(ws + p.x);
+    half_t* lo[2] = {reinterpret_cast<half_t*>(ws + p.lo), reinterpret_cast<half_t*>(ws + (SPLIT ? p.lo1 : p.lo))};
+    half_t* x_lo = SPLIT ? reinterpret_cast<half_t*>(ws + p.x_lo) : nullptr;
+    half_t* a_lo = SPLIT ? reinterpret_cast<half_t*>(ws + p.a_lo) : nullptr;
+    half_t* d_lo = SPLIT ? reinterpret_cast<half_t*>(ws + p.d_lo) : nullptr;
+    half_t* xt[2] = {reinterpret_cast<half_t*>(ws + p.xt0), reinterpret_cast<half_t*>(ws + p.xt1)};
+    half_t *ma = reinterpret_cast<half_t*>(ws + p.a), *md = reinterpret_cast<half_t*>(ws + p.d);
+    const uint32_t tri = p.side * (p.side + 1) / 2, tq = p.mp / p.tile;
+    const uint64_t rect = uint64_t(p.np) * p.mp, sq = uint64_t(p.np) * p.np;
+    const dim3 block(WP * WQ * 64);
+    a.n = p.n;
+    a.np = p.np;
+    a.mp = p.mp;
+    a.s = p.s;
+    a.sums = reinterpret_cast<float*>(ws + p.sums);
+    a.sum_tiles = tri;
+    a.alpha = reinterpret_cast<float*>(ws + p.alpha);
+    a.a = ma;
+    a.a_lo = a_lo;
+    for (int32_t i = 0; i < steps; ++i) {
+        a.tiles_p = p.side;
+        a.per_item = tri;
+        a.p = a.q = x;
+        a.p_lo = a.q_lo = x_lo;
+        a.p_item = a.q_item = rect;
+        a.k = p.mp;
+        a.out = ma;
+        a.out_lo = a_lo;
+        launch(ortho_mul_kernel<B, WP, WQ, SPLIT, kGram>, dim3(uint32_t(batch) * tri), block, 0, st, a);
+        a.p = a.q = ma;
+        a.p_lo = a.q_lo = a_lo;
+        a.p_item = a.q_item = sq;
+        a.k = p.np;
+        a.out = md;
+        a.out_lo = d_lo;
+        launch(ortho_mul_kernel<B, WP, WQ, SPLIT, kPoly>, dim3(uint32_t(batch) * tri), block, 0, st, a);
+        a.p = md;
+        a.p_lo = d_lo;
+        a.q = a.xt = xt[i & 1];
+        a.q_lo = a.xt_lo = lo[i & 1];
+        a.q_item = rect;
+        a.tiles_q = tq;
+        a.per_item = p.side * tq;
+        a.out = x;
+        a.out_lo = x_lo;
+        a.xt_out = xt[(i & 1) ^ 1];
+        a.xt_lo_out = lo[(i & 1) ^ 1];
+        if (i + 1 < steps)
+            launch(ortho_mul_kernel<B, WP, WQ, SPLIT, kApply>, dim3(uint32_t(batch) * a.per_item), block, 0, st, a);
+        else
+            launch(ortho_mul_kernel<B, WP, WQ, SPLIT, kLast>, dim3(uint32_t(batch) * a.per_item), block, 0, st, a);
+    }
+}
+
+static void ortho_run(const OrthoPlan& p, OrthoIn in, const OrthoMul& mul, int64_t batch, int64_t rows, int64_t cols,
+                      int32_t steps, char* ws, hipStream_t st) {
+    in.cells = uint64_t(rows) * uint64_t(cols);
+    in.rows = uint32_t(rows);
+    in.cols = uint32_t(cols);
+    in.np = p.np;
+    in.mp = p.mp;
+    in.tall = p.tall;
+    in.s = p.s;
+    in.x = reinterpret_cast<half_t*>(ws + p.x);
+    in.xt = reinterpret_cast<half_t*>(ws + p.xt0);
+    in.xt_lo = reinterpret_cast<half_t*>(ws + p.lo);
+    in.x_lo = p.tile == 64 ? reinterpret_cast<half_t*>(ws + p.x_lo) : nullptr;
+    in.norm = reinterpret_cast<double*>(ws + p.norm);
+    const uint32_t pr = p.tall ? p.mp : p.np, pc = p.tall ? p.np : p.mp;
+    launch(ortho_norm_kernel, dim3(kNormBlocks, uint32_t(batch)), dim3(256), 0, st, in);
+    launch(ortho_split_kernel, dim3(pc / 64, pr / 64, uint32_t(batch)), dim3(256), 0, st, in);
+    if (p.tile == 256) ortho_steps<256, 2, 4, false>(p, mul, batch, steps, ws, st);
+    else if (p.tile == 128) ortho_steps<128, 2, 2, false>(p, mul, batch, steps, ws, st);
+    else ortho_steps<64, 2, 2, true>(p, mul, batch, steps, ws, st);
+}
+
+// The workspace holds the plan, and no launch has 2^32 threads.
+static e8q_status_t ortho_fits(const OrthoPlan& p, int64_t batch, const void* ws, size_t bytes) {
+    if (double(batch) * p.side * (p.mp / p.tile) >= double(1 << 22)) return E8Q_ERR_UNSUPPORTED;
+    return ws && bytes >= p.total && reinterpret_cast<uintptr_t>(ws) % 256 == 0 ? E8Q_OK : E8Q_ERR_INVALID;
+}
+
+}  // namespace e8q
+
+extern "C" size_t e8q_orthogonalize_workspace_size(int64_t batch, int64_t rows, int64_t cols) {
+    if (batch <= 0 || batch > 65535 || rows <= 0 || rows > 65536 || cols <= 0 || cols > 65536 || cols % 8) return 0;
+    return e8q::ortho_plan(batch, rows, cols).total;
+}
+
+extern "C" e8q_status_t e8q_orthogonalize(const void* g, e8q_dtype_t g_dtype, int64_t batch, int64_t rows,
+                                          int64_t cols, int32_t steps, float coeff_a, float coeff_b, float coeff_c,
+                                          void* update_out, void* workspace, size_t workspace_bytes,
+                                          uint32_t* status_dev, void* stream) {
+    using namespace e8q;
+    const e8q_status_t c = ortho_check(g, g_dtype, batch, rows, cols, steps, coeff_a, coeff_b, coeff_c, status_dev);
+    if (c != E8Q_OK) return c;
+    if (!update_out || reinterpret_cast<uintptr_t>(update_out) % 16) return E8Q_ERR_INVALID;
+    const OrthoPlan p = ortho_plan(batch, rows, cols);
+    const e8q_status_t f = ortho_fits(p, batch, workspace, workspace_bytes);
+    if (f != E8Q_OK) return f;
+    OrthoIn in{};
+    in.g = g;
+    in.g_f32 = g_dtype == E8Q_F32;
+    in.status = status_dev;
+    OrthoMul mul{};
+    mul.ca = coeff_a;
+    mul.cb = coeff_b;
+    mul.cc = coeff_c;
+    mul.rows = uint32_t(rows);
+    mul.cols = uint32_t(cols);
+    mul.tall = p.tall;
+    mul.update = static_cast<uint16_t*>(update_out);
+    ortho_run(p, in, mul, batch, rows, cols, steps, static_cast<char*>(workspace), reinterpret_cast<hipStream_t>(stream));
+    return launch_status();
+}
+
+extern "C" e8q_status_t e8q_orthogonal_step(const void* w, void* w_out, const void* grad, e8q_dtype_t grad_dtype,
+                                            const float* momentum, float* momentum_out, float mu, int32_t nesterov,
+                                            float lr, float decay, float gamma, int64_t batch, int64_t rows,
+                                            int64_t cols, int32_t steps, float coeff_a, float coeff_b, float coeff_c,
+                                            void* workspace, size_t workspace_bytes, uint32_t* status_dev,
+                                            void* stream) {
+    using namespace e8q;
+    const e8q_status_t c =
+        ortho_check(grad, grad_dtype, batch, rows, cols, steps, coeff_a, coeff_b, coeff_c, status_dev);
+    if (c != E8Q_OK) return c;
+    if (!w || !w_out || !momentum || !momentum_out) return E8Q_ERR_INVALID;
+    for (const void* q : {w, static_cast<const void*>(w_out), static_cast<const void*>(momentum),
+                          static_cast<const void*>(momentum_out)})
+        if (reinterpret_cast<uintptr_t>(q) % 16) return E8Q_ERR_INVALID;
+    if (w_out == grad || momentum_out == grad || static_cast<void*>(momentum_out) == w_out ||
+        static_cast<const void*>(momentum_out) == w || static_cast<const void*>(momentum) == w_out)
+        return E8Q_ERR_INVALID;
+    if (!std::isfinite(mu) || !std::isfinite(lr) || !std::isfinite(decay) || !std::isfinite(gamma))
+        return E8Q_ERR_INVALID;
+    const OrthoPlan p = ortho_plan(batch, rows, cols);
+    const e8q_status_t f = ortho_fits(p, batch, workspace, workspace_bytes);
+    if (f != E8Q_OK) return f;
+    OrthoIn in{};
+    in.g = grad;
+    in.g_f32 = grad_dtype == E8Q_F32;
+    in.mom_in = momentum;
+    in.mom_out = momentum_out;
+    in.mu = mu;
+    in.nesterov = nesterov != 0;
+    in.status = status_dev;
+    OrthoMul mul{};
+    mul.ca = coeff_a;
+    mul.cb = coeff_b;
+    mul.cc = coeff_c;
+    mul.rows = uint32_t(rows);
+    mul.cols = uint32_t(cols);
+    mul.tall = p.tall;
+    mul.w = static_cast<const uint16_t*>(w);
+    mul.w_out = static_cast<uint16_t*>(w_out);
+    mul.keep = 1.0f - lr * decay;
+    mul.step = lr * gamma;
+    ortho_run(p, in, mul, batch, rows, cols, steps, static_cast<char*>(workspace), reinterpret_cast<hipStream_t>(stream));
+    return launch_status();
+}

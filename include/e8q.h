@@ -98,6 +98,10 @@ enum {
 typedef int32_t e8q_dtype_t;
 enum { E8Q_F32 = 0, E8Q_BF16 = 1 };
 
+/* Integer type codes of token ids (e8q_token_logprobs, e8q_embed and their gradients). */
+typedef int32_t e8q_index_t;
+enum { E8Q_I32 = 0, E8Q_I64 = 1 };
+
 /* One escape record, 20 bytes.  E8-QAT stores groups outside the core exactly
  * as 20-byte coordinate records (Table 10; Figure 6(c): payload 2 + 20 rho
  * bits per weight).  Field layout (a reading; the pages give only the size):
@@ -528,6 +532,182 @@ e8q_status_t e8q_ptq_init(const void* w, e8q_dtype_t w_dtype,
 
 /* Workspace bytes e8q_ptq_init needs (0 on bad sizes). */
 size_t e8q_ptq_workspace_size(int64_t batch, int64_t rows, int64_t cols);
+
+/* ---------------------------------------------------------------------------
+ * The ends of a training step around the projected matrices, and the step of
+ * the latents: log probabilities of a model's output logits with their
+ * gradient, the embedding lookup with its gradient, and the update along the
+ * orthogonalized momentum.  Conventions as above (device pointers, stream
+ * order, no allocation, status bits); results do not depend on scheduling.
+ * ------------------------------------------------------------------------- */
+
+/* ---------------------------------------------------------------------------
+ * e8q_token_logprobs -- per row of logits x, with y = scale * x:
+ *   lse = log sum_i exp(y_i),  logprob_j = y_{t_j} - lse,
+ *   entropy = -sum_i p_i log p_i  (p_i = exp(y_i - lse); a term with p_i = 0 is 0),
+ *   the top_k largest logits, equal ones in the order of their index.
+ *   logits       [rows, vocab] in dtype, rows `row_stride` elements apart
+ *                (>= vocab), each row contiguous, element-aligned
+ *   scale        positive finite (1 / temperature)
+ *   tokens       [rows, n_tokens] token ids (index_type E8Q_I32 or E8Q_I64), or
+ *                NULL with n_tokens = 0.  A negative id is an ignored position
+ *                (logprob 0, no gradient); an id >= vocab is treated the same
+ *                and sets E8Q_STATUS_BAD_INDEX
+ *   logprob_out  [rows, n_tokens] float32, or NULL
+ *   lse_out, entropy_out   [rows] float32, or NULL
+ *   top_idx_out  [rows, top_k] int32, top_logprob_out [rows, top_k] float32:
+ *                either may be NULL; top_k in [0, 64], <= vocab
+ *   workspace    e8q_token_logprobs_workspace_size(rows, vocab, top_k) bytes,
+ *                256-byte aligned (may be NULL if that is 0)
+ * Masked logits are -inf (or the type's lowest value).  A row of -inf only has
+ * lse = -inf, log probabilities -inf and entropy 0.  A row holding a NaN or
+ * +inf has NaN outputs (E8Q_STATUS_NONFINITE); among its alternatives NaN is
+ * the largest value.  exp, sums and the running maximum are float32.
+ * Limits: vocab < 2^31 - 16, rows < 2^24, n_tokens <= 1024.
+ * ------------------------------------------------------------------------- */
+e8q_status_t e8q_token_logprobs(const void* logits, e8q_dtype_t dtype,
+                                int64_t rows, int64_t vocab, int64_t row_stride, float scale,
+                                const void* tokens, e8q_index_t index_type, int64_t n_tokens,
+                                float* logprob_out, float* lse_out, float* entropy_out,
+                                int64_t top_k, int32_t* top_idx_out, float* top_logprob_out,
+                                void* workspace, size_t workspace_bytes,
+                                uint32_t* status_dev, void* stream);
+
+/* Workspace bytes e8q_token_logprobs needs (0 on bad sizes, and where it needs
+ * none).  The size for top_k = 0 also serves e8q_token_logprobs_grad. */
+size_t e8q_token_logprobs_workspace_size(int64_t rows, int64_t vocab, int64_t top_k);
+
+/* ---------------------------------------------------------------------------
+ * e8q_token_logprobs_backward -- the gradient with respect to the logits of
+ * sum grad_logprob * logprob + sum grad_entropy * entropy:
+ *   dx_i = scale * ( sum_j g_j [i = t_j] - p_i sum_j g_j - g_H p_i (log p_i + entropy) )
+ * with the j over the row's positions that are not ignored.
+ *   logits, dtype, rows, vocab, row_stride, scale, tokens, index_type,
+ *   n_tokens     as e8q_token_logprobs
+ *   lse          [rows] float32, as e8q_token_logprobs wrote it
+ *   grad_logprob [rows, n_tokens] float32 (required with n_tokens > 0)
+ *   entropy, grad_entropy   [rows] float32, both or neither
+ *   grad_logits  [rows, vocab] in dtype (bf16: nearest even), rows
+ *                grad_stride elements apart; may be logits itself (with
+ *                grad_stride = row_stride)
+ * A row whose lse is -inf has gradient 0.
+ * ------------------------------------------------------------------------- */
+e8q_status_t e8q_token_logprobs_backward(const void* logits, e8q_dtype_t dtype,
+                                         int64_t rows, int64_t vocab, int64_t row_stride, float scale,
+                                         const void* tokens, e8q_index_t index_type, int64_t n_tokens,
+                                         const float* lse, const float* grad_logprob,
+                                         const float* entropy, const float* grad_entropy,
+                                         void* grad_logits, int64_t grad_stride,
+                                         uint32_t* status_dev, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * e8q_token_logprobs_grad -- both in one call, for upstream gradients that are
+ * known beforehand (a loss with given token weights: grad_logprob = -weight):
+ * the outputs of e8q_token_logprobs (no alternatives) and the gradient of
+ * e8q_token_logprobs_backward (grad_entropy may be NULL).  Arguments as there;
+ * logprob_out, lse_out, entropy_out may be NULL, and grad_logits may be logits
+ * itself (with grad_stride = row_stride).
+ * ------------------------------------------------------------------------- */
+e8q_status_t e8q_token_logprobs_grad(const void* logits, e8q_dtype_t dtype,
+                                     int64_t rows, int64_t vocab, int64_t row_stride, float scale,
+                                     const void* tokens, e8q_index_t index_type, int64_t n_tokens,
+                                     const float* grad_logprob, const float* grad_entropy,
+                                     float* logprob_out, float* lse_out, float* entropy_out,
+                                     void* grad_logits, int64_t grad_stride,
+                                     void* workspace, size_t workspace_bytes,
+                                     uint32_t* status_dev, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * e8q_embed -- out[t] = scale * table[tokens[t]], one rounding.
+ *   table        [vocab, dim] in table_dtype
+ *   tokens       [n] ids (index_type); a negative id is a padded position and
+ *                gives a row of zeros; an id >= vocab likewise, and sets
+ *                E8Q_STATUS_BAD_INDEX
+ *   out          [n, dim] in out_dtype (BF16: nearest even)
+ * Limits: n, vocab, dim < 2^31.
+ * ------------------------------------------------------------------------- */
+e8q_status_t e8q_embed(const void* table, e8q_dtype_t table_dtype, int64_t vocab, int64_t dim,
+                       const void* tokens, e8q_index_t index_type, int64_t n, float scale,
+                       void* out, e8q_dtype_t out_dtype,
+                       uint32_t* status_dev, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * e8q_embed_backward -- the gradient of the table, by sorted tokens:
+ *   dE[v] = scale * sum_{t: tokens[t] = v} grad_out[t]   (float32 sums, in
+ * blocks of consecutive occurrences of v joined in order), written for every
+ * row (0 where v does not occur), and/or applied to the latents at once by the
+ * rule of e8q_ste_backward, rows that do not occur left as they are:
+ *   w_latent[v] <- bf16_RNE(fl32(w) - fl32(lr * dE[v]))     (NaN -> 0x7FC0).
+ *   grad_out     [n, dim] in grad_dtype
+ *   tokens       [n] as e8q_embed (padded positions contribute nothing)
+ *   grad_table   [vocab, dim] in table_dtype, or NULL
+ *   w_latent     [vocab, dim] bf16, updated in place, or NULL
+ *   workspace    e8q_embed_backward_workspace_size(n, vocab, dim) bytes, 256-byte aligned
+ * At least one of grad_table, w_latent.  The latents take the float32 dE, also
+ * when a bf16 grad_table is written.  Limits: n, vocab, dim < 2^31.
+ * ------------------------------------------------------------------------- */
+e8q_status_t e8q_embed_backward(const void* grad_out, e8q_dtype_t grad_dtype, int64_t n, int64_t dim,
+                                const void* tokens, e8q_index_t index_type, int64_t vocab, float scale,
+                                void* grad_table, e8q_dtype_t table_dtype,
+                                void* w_latent, float lr,
+                                void* workspace, size_t workspace_bytes,
+                                uint32_t* status_dev, void* stream);
+
+/* Workspace bytes e8q_embed_backward needs (0 on bad sizes). */
+size_t e8q_embed_backward_workspace_size(int64_t n, int64_t vocab, int64_t dim);
+
+/* ---------------------------------------------------------------------------
+ * e8q_orthogonalize -- every matrix G of the batch towards its orthogonal
+ * factor by Newton-Schulz products: X <- G / |G|_F, then `steps` times
+ *   X <- a X + (b A + c A^2) X,  A = X X^T   (A = X^T X for rows > cols:
+ * the same polynomial of the singular values, sigma -> a s + b s^3 + c s^5).
+ *   g            [batch, rows, cols] in g_dtype
+ *   coeff_a, coeff_b, coeff_c   finite; the polynomial must keep [0, 1] within
+ *                [0, 1.5] over all steps and |a + b s^2 + c s^4| <= 7 there
+ *                (E8Q_ERR_UNSUPPORTED otherwise: fixed-point ranges below)
+ *   steps        in [1, 16]
+ *   update_out   [batch, rows, cols] bf16, nearest even
+ *   workspace    e8q_orthogonalize_workspace_size(batch, rows, cols) bytes, 256-byte aligned
+ * Arithmetic: |G|_F in float64; X is held to 22 significant bits (two float16
+ * parts, scaled by a power of two); the products run on the matrix cores on
+ * float16 operands with float32 sums: X and A rounded to nearest, and
+ * M - alpha I, alpha the mean of the diagonal of M = aI + bA + cA^2, so that
+ * the rounding of the operands does not touch alpha X.  |O - exact|_F is about
+ * 1e-3 |O|_F before the last rounding, for any spectrum.
+ * A zero matrix gives zeros; one with a NaN or infinity gives NaN everywhere
+ * (E8Q_STATUS_NONFINITE), the others of the batch are not affected.
+ * Limits: cols a multiple of 8; rows, cols <= 65536; batch <= 65535.
+ * ------------------------------------------------------------------------- */
+e8q_status_t e8q_orthogonalize(const void* g, e8q_dtype_t g_dtype,
+                               int64_t batch, int64_t rows, int64_t cols,
+                               int32_t steps, float coeff_a, float coeff_b, float coeff_c,
+                               void* update_out,
+                               void* workspace, size_t workspace_bytes,
+                               uint32_t* status_dev, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * e8q_orthogonal_step -- the latents' optimizer step along the orthogonalized
+ * momentum:
+ *   m' = mu m + g (float32),  u = g + mu m' (nesterov != 0) or m',
+ *   w' = bf16_RNE( w (1 - lr * decay) - lr * gamma * O(u) ),  O as e8q_orthogonalize
+ * with float32 O(u).  The updated latents go to the next projection.
+ *   w, w_out     [batch, rows, cols] bf16; w_out may be w
+ *   grad         [batch, rows, cols] in grad_dtype; may alias nothing written
+ *   momentum, momentum_out   [batch, rows, cols] float32; may be the same
+ *   mu, lr, decay, gamma     finite
+ *   other arguments as e8q_orthogonalize
+ * ------------------------------------------------------------------------- */
+e8q_status_t e8q_orthogonal_step(const void* w, void* w_out,
+                                 const void* grad, e8q_dtype_t grad_dtype,
+                                 const float* momentum, float* momentum_out,
+                                 float mu, int32_t nesterov, float lr, float decay, float gamma,
+                                 int64_t batch, int64_t rows, int64_t cols,
+                                 int32_t steps, float coeff_a, float coeff_b, float coeff_c,
+                                 void* workspace, size_t workspace_bytes,
+                                 uint32_t* status_dev, void* stream);
+
+/* Workspace bytes e8q_orthogonalize / e8q_orthogonal_step need (0 on bad sizes). */
+size_t e8q_orthogonalize_workspace_size(int64_t batch, int64_t rows, int64_t cols);
 
 /* |C(core_bound)|, the number of core points; -1 if core_bound is outside [0, 40].
  * Host-only. */

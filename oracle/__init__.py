@@ -80,3 +80,6 @@ from .roots import (  # noqa: F401
 )
 from .ptq import core_search_two_z, core_project_two_z, exact_row_errors, ptq_init  # noqa: F401
 from .brute import brute_nearest_e8  # noqa: F401
+from .logprobs import logprobs, logprobs_grad  # noqa: F401
+from .embed import embed, embed_grad  # noqa: F401
+from .orthogonal import orthogonalize, orthogonal_step  # noqa: F401
