@@ -30,7 +30,9 @@
 // are padded with zeros to whole tiles, which every step maps to zeros.  The
 // two symmetric products compute the tiles on and below the diagonal and write
 // each twice.
+#include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "e8q_device.hpp"
 #include "e8q_host.hpp"
@@ -44,7 +46,7 @@ typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 
 constexpr int kBK = 64;                 // elements of k per stage
 constexpr int kScaleA = 14, kScaleD = 12;
-constexpr int kNormBlocks = 64;         // partial sums of |G|^2 per matrix
+constexpr int kNormBlocks = 1024;       // most partial sums of |G|^2 per matrix
 
 // ------------------------------------------------------------ input
 
@@ -64,7 +66,8 @@ struct OrthoIn {
     half_t* xt;                // [batch, mp, np]
     half_t* xt_lo;
     half_t* x_lo;              // or null
-    double* norm;              // [batch, kNormBlocks]
+    double* norm;              // [batch, norm_blocks]
+    uint32_t norm_blocks;
     uint32_t* status;
 };
 
@@ -126,7 +129,7 @@ __global__ __launch_bounds__(256) void ortho_norm_kernel(OrthoIn a) {
     if ((threadIdx.x & 63u) == 0u) s_sum[threadIdx.x >> 6] = sum;
     __syncthreads();
     if (threadIdx.x == 0)
-        a.norm[uint64_t(blockIdx.y) * kNormBlocks + blockIdx.x] = (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
+        a.norm[uint64_t(blockIdx.y) * a.norm_blocks + blockIdx.x] = (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
 }
 
 // X = U / |U| as float16 parts in both layouts, by tiles of 64 x 64 of U's own
@@ -137,7 +140,8 @@ __global__ __launch_bounds__(256) void ortho_split_kernel(OrthoIn a) {
     __shared__ double s_scale;
     const uint32_t tid = threadIdx.x, item = blockIdx.z;
     if (tid < 64u) {
-        double sum = tid < uint32_t(kNormBlocks) ? a.norm[uint64_t(item) * kNormBlocks + tid] : 0.0;
+        double sum = 0.0;
+        for (uint32_t i = tid; i < a.norm_blocks; i += 64u) sum += a.norm[uint64_t(item) * a.norm_blocks + i];
 #pragma unroll
         for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
         if (tid == 0u) {
@@ -230,20 +234,46 @@ struct OrthoMul {
     float keep, step;          // w_out = w * keep - step * O
 };
 
-typedef __attribute__((address_space(3))) void lds_void;
-typedef const __attribute__((address_space(1))) void global_void;
-
-// 64 lanes x 16 bytes straight to LDS at `to` (wave-uniform) + 16 * lane.
-__device__ __forceinline__ void load_lds16(const half_t* from, half_t* to) {
-    __builtin_amdgcn_global_load_lds((global_void*)from, (lds_void*)to, 16, 0, 0);
+// 64 lanes x 16 bytes straight to LDS at byte `to` (wave-uniform) + 16 * lane,
+// from `base` (wave-uniform) + `offset`.  Written in assembly so that the
+// compiler does not wait for it at the next LDS read: the stage that it fills
+// is read only after wait_loads() and a barrier.  It has no result register, and
+// nothing else in this file uses m0.
+__device__ __forceinline__ void load_lds16(const half_t* base, uint32_t offset, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory");
 }
 
-__device__ __forceinline__ void tri_tile(uint32_t t, uint32_t& ti, uint32_t& tj) {
-    uint32_t i = uint32_t((sqrtf(8.0f * float(t) + 1.0f) - 1.0f) * 0.5f);
-    while ((i + 1u) * (i + 2u) / 2u <= t) ++i;
-    while (i * (i + 1u) / 2u > t) --i;
-    ti = i;
-    tj = t - i * (i + 1u) / 2u;
+__device__ __forceinline__ uint32_t lds_address(const half_t* p) {
+    return uint32_t(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) half_t*)p));
+}
+
+// This wave's loads to LDS have landed and its LDS reads have returned.
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
+
+__device__ __forceinline__ void block_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// Tile t of the lower triangle of side x side tiles: four rows of tiles at a
+// time, column by column, so that tiles that run together share their operands.
+__device__ __forceinline__ void tri_tile(uint32_t t, uint32_t side, uint32_t& ti, uint32_t& tj) {
+    uint32_t g = uint32_t(sqrtf(float(t) * 0.125f));                 // 8 g^2 + 2 g tiles lie before group g
+    while (8u * (g + 1u) * (g + 1u) + 2u * (g + 1u) <= t) ++g;
+    while (8u * g * g + 2u * g > t) --g;
+    uint32_t r = t - (8u * g * g + 2u * g);
+    const uint32_t rows = min(4u, side - 4u * g);
+    if (r < 4u * g * rows) {
+        tj = r / rows;
+        ti = 4u * g + r - tj * rows;
+        return;
+    }
+    r -= 4u * g * rows;
+    uint32_t d = 0u;
+    while (r >= rows - d) r -= rows - d++;
+    tj = 4u * g + d;
+    ti = tj + r;
 }
 
 // Workgroups are dealt to the 8 XCDs in turn; this gives each XCD a contiguous
@@ -266,70 +296,117 @@ __global__ __launch_bounds__(WP* WQ * 64) void ortho_mul_kernel(OrthoMul a) {
     const uint32_t item = tile / a.per_item, t = tile - item * a.per_item;
     uint32_t ti, tj;
     if constexpr (MODE == kGram || MODE == kPoly) {
-        tri_tile(t, ti, tj);
+        tri_tile(t, a.tiles_p, ti, tj);
     } else {
-        tj = t / a.tiles_p;
-        ti = t - tj * a.tiles_p;
+        // four columns of tiles at a time, row by row
+        const uint32_t g = t / (4u * a.tiles_p), cols = min(4u, a.tiles_q - 4u * g), r = t - g * 4u * a.tiles_p;
+        ti = r / cols;
+        tj = 4u * g + r - ti * cols;
     }
-    // stage loads: a wave load fills 8 rows of 128 bytes; the 16-byte chunk c of
-    // row r sits at position c ^ (r & 7), so that the fragments' reads (16 rows,
-    // one chunk) spread over all banks
-    const uint32_t lrow = lane >> 3, lchunk = (lane & 7u) ^ lrow;
-    const uint64_t op = uint64_t(item) * a.p_item + uint64_t(ti * B + wave * (kLoads * 8) + lrow) * a.k + lchunk * 8u;
-    const uint64_t oq = uint64_t(item) * a.q_item + uint64_t(tj * B + wave * (kLoads * 8) + lrow) * a.k + lchunk * 8u;
-    auto stage = [&](int buf, uint32_t k) {
+    // Rows of a wave's fragments.  A lane's results are rows 4 (lane >> 4) .. + 3
+    // of each P fragment and row lane & 15 of each Q fragment.  Row r of P
+    // fragment i stands for row 32 (i / 2) + 8 (r / 4) + 4 (i % 2) + r % 4 of the
+    // wave's P rows, and row r of Q fragment j for its Q row FQ r + j: two P
+    // fragments give a lane 8 neighbours along P, the FQ Q fragments FQ
+    // neighbours along Q, and both orders of the result go to memory in whole
+    // vectors without passing through LDS again.
+    // In LDS, the 16-byte chunk c of row r sits at position c ^ f(r), f chosen so
+    // that 8 lanes that read one chunk of 8 fragment rows meet all banks.
+    const uint32_t lrow = lane >> 3;                 // a wave load fills 8 rows of 128 bytes
+    auto fp_of = [](uint32_t r) { return (r & 3u) | ((r >> 1) & 4u); };
+    auto fq_of = [](uint32_t r) { return (r / FQ) & 7u; };
+    const uint64_t op = uint64_t(item) * a.p_item + uint64_t(ti * B + wave * (kLoads * 8)) * a.k;
+    const uint64_t oq = uint64_t(item) * a.q_item + uint64_t(tj * B + wave * (kLoads * 8)) * a.k;
+    uint32_t off_p[kLoads], off_q[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        const uint32_t r = (wave * kLoads + i) * 8u + lrow;
+        off_p[i] = (lrow * a.k + ((lane & 7u) ^ fp_of(r)) * 8u) * 2u;
+        off_q[i] = (lrow * a.k + ((lane & 7u) ^ fq_of(r)) * 8u) * 2u;
+    }
+    const uint32_t to_p = lds_address(&s_p[0][0][0]) + wave * (kLoads * 8 * kBK * 2);
+    const uint32_t to_q = lds_address(&s_q[0][0][0]) + wave * (kLoads * 8 * kBK * 2);
+    auto stage = [&](uint32_t buf, uint32_t k) {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const uint64_t at = uint64_t(i * 8) * a.k + k;
-            const int to = (wave * kLoads + i) * 8 * kBK;
-            load_lds16(a.p + op + at, &s_p[buf][0][to]);
-            load_lds16(a.q + oq + at, &s_q[buf][0][to]);
-            if constexpr (SPLIT) {
-                load_lds16(a.p_lo + op + at, &s_p[buf][1][to]);
-                load_lds16(a.q_lo + oq + at, &s_q[buf][1][to]);
+#pragma unroll
+            for (int h = 0; h < kParts; ++h) {
+                const uint32_t to = (buf * kParts + h) * (B * kBK * 2) + i * (8 * kBK * 2);
+                load_lds16((h ? a.p_lo : a.p) + op + at, off_p[i], to_p + to);
+                load_lds16((h ? a.q_lo : a.q) + oq + at, off_q[i], to_q + to);
             }
         }
     };
     const uint32_t wp = wave / WQ, wq = wave - wp * WQ;
     const uint32_t frow = lane & 15u, fk = lane >> 4;
-    f32x4_t acc[FP][FQ] = {};
-    stage(0, 0u);
-    int buf = 0;
-    for (uint32_t k = 0; k < a.k; k += kBK) {
-        __syncthreads();                    // stage k has landed; stage k - 1 is no longer read
-        if (k + kBK < a.k) stage(buf ^ 1, k + kBK);
+    struct Frags {
+        half8_t p[kParts][FP], q[kParts][FQ];
+    };
+    // the fragments of half kk (32 of 64) of a stage
+    auto read = [&](Frags& f, uint32_t buf, int kk) {
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            half8_t fp[kParts][FP], fq[kParts][FQ];
-            const uint32_t chunk = ((kk * 4 + fk) ^ (frow & 7u)) * 8u;
+        for (int h = 0; h < kParts; ++h) {
 #pragma unroll
-            for (int h = 0; h < kParts; ++h) {
-#pragma unroll
-                for (int i = 0; i < FP; ++i)
-                    fp[h][i] = *reinterpret_cast<const half8_t*>(&s_p[buf][h][((wp * FP + i) * 16 + frow) * kBK + chunk]);
-#pragma unroll
-                for (int j = 0; j < FQ; ++j)
-                    fq[h][j] = *reinterpret_cast<const half8_t*>(&s_q[buf][h][((wq * FQ + j) * 16 + frow) * kBK + chunk]);
+            for (int i = 0; i < FP; ++i) {
+                const uint32_t r = wp * (FP * 16) + (i / 2) * 32 + (frow >> 2) * 8 + (i % 2) * 4 + (frow & 3u);
+                f.p[h][i] = *reinterpret_cast<const half8_t*>(&s_p[buf][h][r * kBK + ((kk * 4 + fk) ^ fp_of(r)) * 8]);
             }
 #pragma unroll
-            for (int i = 0; i < FP; ++i)
-#pragma unroll
-                for (int j = 0; j < FQ; ++j) {
-                    if constexpr (SPLIT) {
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fp[1][i], fq[0][j], acc[i][j], 0, 0, 0);
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fp[0][i], fq[1][j], acc[i][j], 0, 0, 0);
-                    }
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fp[0][i], fq[0][j], acc[i][j], 0, 0, 0);
-                }
+            for (int j = 0; j < FQ; ++j) {
+                const uint32_t r = wq * (FQ * 16) + frow * FQ + j;
+                f.q[h][j] = *reinterpret_cast<const half8_t*>(&s_q[buf][h][r * kBK + ((kk * 4 + fk) ^ fq_of(r)) * 8]);
+            }
         }
-        buf ^= 1;
+    };
+    f32x4_t acc[FP][FQ] = {};
+    auto multiply = [&](const Frags& f) {
+#pragma unroll
+        for (int i = 0; i < FP; ++i)
+#pragma unroll
+            for (int j = 0; j < FQ; ++j) {
+                if constexpr (SPLIT) {
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f.p[1][i], f.q[0][j], acc[i][j], 0, 0, 0);
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f.p[0][i], f.q[1][j], acc[i][j], 0, 0, 0);
+                }
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f.p[0][i], f.q[0][j], acc[i][j], 0, 0, 0);
+            }
+    };
+    // Two stages in LDS and two fragment sets in registers: each half of a
+    // stage is multiplied while the next half is read, and a stage is loaded
+    // during the stage before it.  One barrier per stage, between its halves:
+    // there the stage's second half has been read by every wave (its buffer can
+    // be filled again) and the next stage has landed.
+    auto interleave = [&]() {
+        constexpr int kReads = (FP + FQ) * kParts, kMul = FP * FQ * (SPLIT ? 3 : 1), kEach = kMul / kReads;
+#pragma unroll
+        for (int i = 0; i < kReads; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);        // an LDS read
+            __builtin_amdgcn_sched_group_barrier(0x008, kEach, 0);    // matrix products
+        }
+    };
+    Frags f0, f1;
+    stage(0u, 0u);
+    wait_loads();
+    block_barrier();
+    if (a.k > uint32_t(kBK)) stage(1u, kBK);
+    read(f0, 0u, 0);
+    uint32_t buf = 0u;
+    for (uint32_t k = 0; k < a.k; k += kBK) {
+        read(f1, buf, 1);
+        multiply(f0);
+        interleave();
+        __builtin_amdgcn_sched_barrier(0);      // the products stay before the wait
+        wait_loads();
+        block_barrier();
+        if (k + 2 * kBK < a.k) stage(buf, k + 2 * kBK);
+        buf ^= 1u;
+        read(f0, buf, 0);                       // after the last stage: old values, not used
+        multiply(f1);
+        interleave();
+        __builtin_amdgcn_sched_barrier(0);
     }
-    __syncthreads();
-    constexpr int kStrip = FQ * 16 + 8;     // a wave's 16 x 16 FQ strip on its way to rows (kStrip halfs per row)
-    half_t* strip = &s_p[0][0][0] + wave * kParts * 16 * kStrip;
-    half_t* strip_lo = strip + 16 * kStrip;
-
-    // lane: rows p0 + 0..3 of P, row q of Q, for fragment (i, j)
+    // the tile's first P and Q rows of this wave
     const uint32_t pw = ti * B + wp * FP * 16, qw = tj * B + wq * FQ * 16;
 
     float alpha = 0.0f;
@@ -363,97 +440,116 @@ __global__ __launch_bounds__(WP* WQ * 64) void ortho_mul_kernel(OrthoMul a) {
     }
     if constexpr (MODE == kApply || MODE == kLast) alpha = a.alpha[item];
 
-    const float to_a = ldexpf(1.0f, kScaleA - 2 * a.s);
+    // (i, j): this lane's 8 results along P, from p0 on, at row q of Q
+    const float to_a = ldexpf(1.0f, kScaleA - 2 * a.s), back = ldexpf(1.0f, -a.s);
+    const uint64_t item_out = uint64_t(item) * a.np * (MODE == kGram || MODE == kPoly ? a.np : a.mp);
     float tr = 0.0f, sq = 0.0f;
-#pragma unroll
-    for (int i = 0; i < FP; ++i) {
+    auto value = [&](int u, int j, int e) { return acc[2 * u + e / 4][j][e % 4]; };
+    half8_t in_hi[2][FQ], in_lo[2][FQ];       // what the results are added to, one pair of fragments ahead
+    auto fetch = [&](int u) {
+        const half_t *hi = MODE == kPoly ? a.a : a.xt, *lo = MODE == kPoly ? a.a_lo : a.xt_lo;
+        const uint32_t p0 = pw + u * 32u + fk * 8u;
 #pragma unroll
         for (int j = 0; j < FQ; ++j) {
-            const uint32_t p0 = pw + i * 16u + fk * 4u, q = qw + j * 16u + frow;
-            f32x4_t v = acc[i][j];
-            half4_t h, l;
-            if constexpr (MODE == kGram) {
-                const uint64_t at = uint64_t(item) * a.np * a.np + uint64_t(q) * a.np + p0;
+            const uint64_t at = item_out + uint64_t(qw + frow * FQ + j) * a.np + p0;
+            in_hi[u & 1][j] = *reinterpret_cast<const half8_t*>(hi + at);
+            if constexpr (MODE != kPoly || SPLIT) in_lo[u & 1][j] = *reinterpret_cast<const half8_t*>(lo + at);
+            else in_lo[u & 1][j] = half8_t{};
+        }
+    };
+    if constexpr (MODE != kGram) fetch(0);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float r = v[e] * to_a;
-                    h[e] = half_t(r);
-                    l[e] = half_t(r - float(h[e]));
+    for (int u = 0; u < FP / 2; ++u) {
+        const uint32_t p0 = pw + u * 32u + fk * 8u;
+        if constexpr (MODE != kGram) {
+            if (u + 1 < FP / 2) fetch(u + 1);
+        }
+        half8_t h[FQ], l[FQ];
+        float v[FQ][8];
+#pragma unroll
+        for (int j = 0; j < FQ; ++j) {
+            const uint32_t q = qw + frow * FQ + j;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float r = value(u, j, e);
+                if constexpr (MODE == kGram) {
+                    r *= to_a;
                     sq = fmaf(r, r, sq);
                     if (p0 + e == q) tr += r;
-                }
-                *reinterpret_cast<half4_t*>(a.out + at) = h;
-                if constexpr (SPLIT) *reinterpret_cast<half4_t*>(a.out_lo + at) = l;
-            }
-            if constexpr (MODE == kPoly) {
-                const uint64_t at = uint64_t(item) * a.np * a.np + uint64_t(q) * a.np + p0;
-                const half4_t av = *reinterpret_cast<const half4_t*>(a.a + at);
-                half4_t al = {};
-                if constexpr (SPLIT) al = *reinterpret_cast<const half4_t*>(a.a_lo + at);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float d = fmaf(a.cc * 0x1p-28f, v[e], a.cb * 0x1p-14f * (float(av[e]) + float(al[e])));
-                    if (p0 + e == q) d += a.ca - alpha;
-                    d *= 0x1p12f;
-                    h[e] = half_t(d);
-                    l[e] = half_t(d - float(h[e]));
-                }
-                *reinterpret_cast<half4_t*>(a.out + at) = h;
-                if constexpr (SPLIT) *reinterpret_cast<half4_t*>(a.out_lo + at) = l;
-            }
-            if constexpr (MODE == kApply || MODE == kLast) {
-                const uint64_t at = uint64_t(item) * a.np * a.mp + uint64_t(q) * a.np + p0;
-                const half4_t hi = *reinterpret_cast<const half4_t*>(a.xt + at);
-                const half4_t lo = *reinterpret_cast<const half4_t*>(a.xt_lo + at);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    v[e] = fmaf(alpha, float(hi[e]) + float(lo[e]), v[e] * 0x1p-12f);
-                    h[e] = half_t(v[e]);
-                    l[e] = half_t(v[e] - float(h[e]));
-                }
-                if constexpr (MODE == kApply) {
-                    *reinterpret_cast<half4_t*>(a.xt_out + at) = h;
-                    *reinterpret_cast<half4_t*>(a.xt_lo_out + at) = l;
                 } else {
-                    const float back = ldexpf(1.0f, -a.s);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t r = a.tall ? q : p0 + e, c = a.tall ? p0 + e : q;
-                        if (r >= a.rows || c >= a.cols) continue;
-                        const uint64_t o = (uint64_t(item) * a.rows + r) * a.cols + c;
-                        const float x = v[e] * back;
-                        if (a.update) a.update[o] = narrow<uint16_t>(x);
-                        else a.w_out[o] = narrow<uint16_t>(fmaf(-a.step, x, widen(a.w[o]) * a.keep));
+                    const float x = float(in_hi[u & 1][j][e]) + float(in_lo[u & 1][j][e]);
+                    if constexpr (MODE == kPoly) {
+                        r = fmaf(a.cc * 0x1p-28f, r, a.cb * 0x1p-14f * x);
+                        if (p0 + e == q) r += a.ca - alpha;
+                        r *= 0x1p12f;
+                    } else {
+                        r = fmaf(alpha, x, r * 0x1p-12f);
                     }
                 }
-            }
-            if constexpr (MODE != kLast) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    strip[(fk * 4 + e) * kStrip + j * 16 + frow] = h[e];
-                    if constexpr (SPLIT) strip_lo[(fk * 4 + e) * kStrip + j * 16 + frow] = l[e];
-                }
+                v[j][e] = r;
+                h[j][e] = half_t(r);
+                l[j][e] = half_t(r - float(h[j][e]));
             }
         }
-        if constexpr (MODE != kLast) {
-            // rows of the strip, 16 bytes a lane; the wave's own LDS, in order
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            constexpr int kPerRow = FQ * 2;                    // 16-byte pieces
-            const uint32_t width = MODE == kApply ? a.mp : a.np;
-            const uint64_t out = uint64_t(item) * a.np * width + uint64_t(pw + i * 16u) * width + qw;
+        if constexpr (MODE == kLast) {
+            // whole vectors of the result's rows lie inside or outside it: its columns are a multiple of 8
+            auto put = [&](uint64_t o, const float* x, int stride, auto count) {
+                constexpr int N = decltype(count)::value;
+                uint32_t out[(N + 1) / 2];
 #pragma unroll
-            for (int c = 0; c < 16 * kPerRow; c += 64) {
-                const uint32_t r = (c + lane) / kPerRow, x = (c + lane) % kPerRow;
-                if (MODE == kApply || ti != tj) {
-                    const uint64_t at = out + uint64_t(r) * width + x * 8u;
-                    *reinterpret_cast<half8_t*>(a.out + at) =
-                        *reinterpret_cast<const half8_t*>(&strip[r * kStrip + x * 8]);
-                    if constexpr (SPLIT)
-                        *reinterpret_cast<half8_t*>(a.out_lo + at) =
-                            *reinterpret_cast<const half8_t*>(&strip_lo[r * kStrip + x * 8]);
+                for (int e = 0; e < N; e += 2) {
+                    float r0 = x[e * stride] * back, r1 = x[(e + 1) * stride] * back;
+                    if (!a.update) {
+                        const uint32_t w2 = *reinterpret_cast<const uint32_t*>(a.w + o + e);
+                        r0 = fmaf(-a.step, r0, __uint_as_float(w2 << 16) * a.keep);
+                        r1 = fmaf(-a.step, r1, __uint_as_float(w2 & 0xFFFF0000u) * a.keep);
+                    }
+                    out[e / 2] = cvt_bf16x2(r0, r1);
+                }
+                uint16_t* to = (a.update ? a.update : a.w_out) + o;
+                struct alignas(2 * N) Out { uint32_t w[N / 2]; };
+                *reinterpret_cast<Out*>(to) = *reinterpret_cast<const Out*>(out);
+            };
+            if (a.tall) {
+#pragma unroll
+                for (int j = 0; j < FQ; ++j) {
+                    const uint32_t q = qw + frow * FQ + j;
+                    if (q < a.rows && p0 < a.cols)
+                        put((uint64_t(item) * a.rows + q) * a.cols + p0, &v[j][0], 1, std::integral_constant<int, 8>{});
+                }
+            } else {
+                const uint32_t q = qw + frow * FQ;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (p0 + e < a.rows && q < a.cols)
+                        put((uint64_t(item) * a.rows + p0 + e) * a.cols + q, &v[0][e], 8, std::integral_constant<int, FQ>{});
+            }
+        } else {
+            // rows of Q: A and D (the mirrored tile), or X^T
+            half_t *turned = MODE == kApply ? a.xt_out : a.out, *turned_lo = MODE == kApply ? a.xt_lo_out : a.out_lo;
+#pragma unroll
+            for (int j = 0; j < FQ; ++j) {
+                const uint64_t at = item_out + uint64_t(qw + frow * FQ + j) * a.np + p0;
+                *reinterpret_cast<half8_t*>(turned + at) = h[j];
+                if constexpr (MODE == kApply || SPLIT) *reinterpret_cast<half8_t*>(turned_lo + at) = l[j];
+            }
+            // rows of P
+            if (MODE == kApply || ti != tj) {
+                typedef _Float16 row_t __attribute__((ext_vector_type(FQ)));
+                const uint32_t width = MODE == kApply ? a.mp : a.np;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    row_t rh, rl;
+#pragma unroll
+                    for (int j = 0; j < FQ; ++j) {
+                        rh[j] = h[j][e];
+                        rl[j] = l[j][e];
+                    }
+                    const uint64_t at = item_out + uint64_t(p0 + e) * width + qw + frow * FQ;
+                    *reinterpret_cast<row_t*>(a.out + at) = rh;
+                    if constexpr (SPLIT) *reinterpret_cast<row_t*>(a.out_lo + at) = rl;
                 }
             }
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         }
     }
     if constexpr (MODE == kGram) {
@@ -488,6 +584,7 @@ __global__ __launch_bounds__(WP* WQ * 64) void ortho_mul_kernel(OrthoMul a) {
 
 struct OrthoPlan {
     uint32_t n, m, np, mp, tile, side;     // side: tiles along n
+    uint32_t norm_blocks;
     int tall, s;
     size_t x, xt0, xt1, lo, a, d, sums, alpha, norm, total;
     size_t x_lo, lo1, a_lo, d_lo;           // 64-wide tiles only
@@ -519,7 +616,11 @@ static OrthoPlan ortho_plan(int64_t batch, int64_t rows, int64_t cols) {
     p.d = take(sq);
     p.sums = take(size_t(batch) * p.side * (p.side + 1) / 2 * 8);
     p.alpha = take(size_t(batch) * 4);
-    p.norm = take(size_t(batch) * kNormBlocks * 8);
+    // four vectors of 8 per thread and block, while that leaves blocks for every CU
+    const uint64_t cells = uint64_t(p.n) * p.m, most = (cus * 8 + batch - 1) / uint64_t(batch);
+    const uint64_t want = (cells + 8191) / 8192;
+    p.norm_blocks = uint32_t(std::min<uint64_t>(std::min<uint64_t>(want, most), kNormBlocks));
+    p.norm = take(size_t(batch) * p.norm_blocks * 8);
     if (p.tile == 64) {
         p.x_lo = take(rect);
         p.lo1 = take(rect);
@@ -633,9 +734,10 @@ static void ortho_run(const OrthoPlan& p, OrthoIn in, const OrthoMul& mul, int64
     in.xt = reinterpret_cast<half_t*>(ws + p.xt0);
     in.xt_lo = reinterpret_cast<half_t*>(ws + p.lo);
     in.x_lo = p.tile == 64 ? reinterpret_cast<half_t*>(ws + p.x_lo) : nullptr;
+    in.norm_blocks = p.norm_blocks;
     in.norm = reinterpret_cast<double*>(ws + p.norm);
     const uint32_t pr = p.tall ? p.mp : p.np, pc = p.tall ? p.np : p.mp;
-    launch(ortho_norm_kernel, dim3(kNormBlocks, uint32_t(batch)), dim3(256), 0, st, in);
+    launch(ortho_norm_kernel, dim3(p.norm_blocks, uint32_t(batch)), dim3(256), 0, st, in);
     launch(ortho_split_kernel, dim3(pc / 64, pr / 64, uint32_t(batch)), dim3(256), 0, st, in);
     if (p.tile == 256) ortho_steps<256, 2, 4, false>(p, mul, batch, steps, ws, st);
     else if (p.tile == 128) ortho_steps<128, 2, 2, false>(p, mul, batch, steps, ws, st);
