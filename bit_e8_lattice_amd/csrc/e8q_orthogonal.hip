@@ -44,7 +44,8 @@ typedef _Float16 half_t;
 typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 
-constexpr int kBK = 64;                 // elements of k per stage
+constexpr int kBK = 32;                 // elements of k per stage: one matrix product's
+constexpr int kRing = 5;                // stages in LDS
 constexpr int kScaleA = 14, kScaleD = 12;
 constexpr int kNormBlocks = 1024;       // most partial sums of |G|^2 per matrix
 
@@ -247,8 +248,12 @@ __device__ __forceinline__ uint32_t lds_address(const half_t* p) {
     return uint32_t(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) half_t*)p));
 }
 
-// This wave's loads to LDS have landed and its LDS reads have returned.
-__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
+// All but this wave's last N loads to LDS have landed, and its LDS reads have
+// returned.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
 
 __device__ __forceinline__ void block_barrier() {
     asm volatile("" ::: "memory");
@@ -286,10 +291,9 @@ __device__ __forceinline__ uint32_t xcd_order(uint32_t b, uint32_t total) {
 template <int B, int WP, int WQ, bool SPLIT, int MODE>
 __global__ __launch_bounds__(WP* WQ * 64) void ortho_mul_kernel(OrthoMul a) {
     constexpr int kWaves = WP * WQ, FP = B / WP / 16, FQ = B / WQ / 16;
-    constexpr int kLoads = B / 8 / kWaves;           // wave loads per operand and stage
+    constexpr int kLoads = B / 16 / kWaves;          // wave loads per operand and stage
     constexpr int kParts = SPLIT ? 2 : 1;
-    __shared__ half_t s_p[2][kParts][B * kBK];
-    __shared__ half_t s_q[2][kParts][B * kBK];
+    __shared__ half_t s_op[kRing][2][kParts][B * kBK];     // P and Q
     const uint32_t tid = threadIdx.x, lane = tid & 63u;
     const uint32_t wave = uint32_t(__builtin_amdgcn_readfirstlane(int(tid >> 6)));
     const uint32_t tile = xcd_order(blockIdx.x, gridDim.x);
@@ -310,109 +314,104 @@ __global__ __launch_bounds__(WP* WQ * 64) void ortho_mul_kernel(OrthoMul a) {
     // fragments give a lane 8 neighbours along P, the FQ Q fragments FQ
     // neighbours along Q, and both orders of the result go to memory in whole
     // vectors without passing through LDS again.
-    // In LDS, the 16-byte chunk c of row r sits at position c ^ f(r), f chosen so
-    // that 8 lanes that read one chunk of 8 fragment rows meet all banks.
-    const uint32_t lrow = lane >> 3;                 // a wave load fills 8 rows of 128 bytes
-    auto fp_of = [](uint32_t r) { return (r & 3u) | ((r >> 1) & 4u); };
-    auto fq_of = [](uint32_t r) { return (r / FQ) & 7u; };
-    const uint64_t op = uint64_t(item) * a.p_item + uint64_t(ti * B + wave * (kLoads * 8)) * a.k;
-    const uint64_t oq = uint64_t(item) * a.q_item + uint64_t(tj * B + wave * (kLoads * 8)) * a.k;
+    // LDS holds the rows in fragment order (row 16 i + r for row r of fragment i),
+    // and the 16-byte chunk c of LDS row r at position c ^ f(r), f = 0, 3, 2, 1 for
+    // r / 4 mod 4: the 16 lanes that a fragment read serves at a time (rows 0-3
+    // and 12-15 of one chunk, 4-11 of its neighbour, or the other way round) then
+    // meet all 64 banks.
+    const uint32_t lrow = lane >> 2;                 // a wave load fills 16 rows of 64 bytes
+    auto place = [](uint32_t r) { return (0u - (r >> 2)) & 3u; };
+    const uint64_t op = uint64_t(item) * a.p_item + uint64_t(ti * B) * a.k;
+    const uint64_t oq = uint64_t(item) * a.q_item + uint64_t(tj * B) * a.k;
     uint32_t off_p[kLoads], off_q[kLoads];
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-        const uint32_t r = (wave * kLoads + i) * 8u + lrow;
-        off_p[i] = (lrow * a.k + ((lane & 7u) ^ fp_of(r)) * 8u) * 2u;
-        off_q[i] = (lrow * a.k + ((lane & 7u) ^ fq_of(r)) * 8u) * 2u;
+        const uint32_t r = (wave * kLoads + i) * 16u + lrow, c = (lane & 3u) ^ place(lrow);
+        const uint32_t rp = (r & ~31u) | ((r << 1) & 24u) | ((r >> 2) & 4u) | (r & 3u);
+        const uint32_t rq = r / (FQ * 16) * (FQ * 16) + (r & 15u) * FQ + (r >> 4) % FQ;
+        off_p[i] = (rp * a.k + c * 8u) * 2u;
+        off_q[i] = (rq * a.k + c * 8u) * 2u;
     }
-    const uint32_t to_p = lds_address(&s_p[0][0][0]) + wave * (kLoads * 8 * kBK * 2);
-    const uint32_t to_q = lds_address(&s_q[0][0][0]) + wave * (kLoads * 8 * kBK * 2);
-    auto stage = [&](uint32_t buf, uint32_t k) {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const uint64_t at = uint64_t(i * 8) * a.k + k;
-#pragma unroll
-            for (int h = 0; h < kParts; ++h) {
-                const uint32_t to = (buf * kParts + h) * (B * kBK * 2) + i * (8 * kBK * 2);
-                load_lds16((h ? a.p_lo : a.p) + op + at, off_p[i], to_p + to);
-                load_lds16((h ? a.q_lo : a.q) + oq + at, off_q[i], to_q + to);
-            }
-        }
+    const uint32_t to = lds_address(&s_op[0][0][0][0]) + wave * (kLoads * 16 * kBK * 2);
+    // load `l` of this wave's loads of the stage at k
+    constexpr int kStageLoads = 2 * kLoads * kParts;
+    auto load = [&](uint32_t slot, uint32_t k, int l) {
+        const int q = l % 2, h = l / 2 % kParts, i = l / (2 * kParts);
+        const half_t* from = q ? (h ? a.q_lo : a.q) + oq : (h ? a.p_lo : a.p) + op;
+        load_lds16(from + k, q ? off_q[i] : off_p[i],
+                   to + ((slot * 2 + q) * kParts + h) * (B * kBK * 2) + i * (16 * kBK * 2));
     };
     const uint32_t wp = wave / WQ, wq = wave - wp * WQ;
     const uint32_t frow = lane & 15u, fk = lane >> 4;
     struct Frags {
         half8_t p[kParts][FP], q[kParts][FQ];
     };
-    // the fragments of half kk (32 of 64) of a stage
-    auto read = [&](Frags& f, uint32_t buf, int kk) {
-#pragma unroll
-        for (int h = 0; h < kParts; ++h) {
-#pragma unroll
-            for (int i = 0; i < FP; ++i) {
-                const uint32_t r = wp * (FP * 16) + (i / 2) * 32 + (frow >> 2) * 8 + (i % 2) * 4 + (frow & 3u);
-                f.p[h][i] = *reinterpret_cast<const half8_t*>(&s_p[buf][h][r * kBK + ((kk * 4 + fk) ^ fp_of(r)) * 8]);
-            }
-#pragma unroll
-            for (int j = 0; j < FQ; ++j) {
-                const uint32_t r = wq * (FQ * 16) + frow * FQ + j;
-                f.q[h][j] = *reinterpret_cast<const half8_t*>(&s_q[buf][h][r * kBK + ((kk * 4 + fk) ^ fq_of(r)) * 8]);
-            }
-        }
+    // fragment `r` of the (FP + FQ) kParts fragments of a stage
+    constexpr int kReads = (FP + FQ) * kParts;
+    const uint32_t at_p = (wp * FP * 16 + frow) * kBK + (fk ^ place(frow)) * 8;
+    const uint32_t at_q = (wq * FQ * 16 + frow) * kBK + (fk ^ place(frow)) * 8;
+    auto read = [&](Frags& f, uint32_t slot, int r) {
+        const int h = r % kParts, n = r / kParts;
+        if (n < FQ) f.q[h][n] = *reinterpret_cast<const half8_t*>(&s_op[slot][1][h][at_q + n * 16 * kBK]);
+        else f.p[h][n - FQ] = *reinterpret_cast<const half8_t*>(&s_op[slot][0][h][at_p + (n - FQ) * 16 * kBK]);
     };
     f32x4_t acc[FP][FQ] = {};
-    auto multiply = [&](const Frags& f) {
+    auto multiply_row = [&](const Frags& f, int i) {
 #pragma unroll
-        for (int i = 0; i < FP; ++i)
-#pragma unroll
-            for (int j = 0; j < FQ; ++j) {
-                if constexpr (SPLIT) {
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f.p[1][i], f.q[0][j], acc[i][j], 0, 0, 0);
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f.p[0][i], f.q[1][j], acc[i][j], 0, 0, 0);
-                }
-                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f.p[0][i], f.q[0][j], acc[i][j], 0, 0, 0);
+        for (int j = 0; j < FQ; ++j) {
+            if constexpr (SPLIT) {
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f.p[1][i], f.q[0][j], acc[i][j], 0, 0, 0);
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f.p[0][i], f.q[1][j], acc[i][j], 0, 0, 0);
             }
-    };
-    // Two stages in LDS and two fragment sets in registers: each half of a
-    // stage is multiplied while the next half is read, and a stage is loaded
-    // during the stage before it.  One barrier per stage, between its halves:
-    // there the stage's second half has been read by every wave (its buffer can
-    // be filled again) and the next stage has landed.
-    auto interleave = [&]() {
-        constexpr int kReads = (FP + FQ) * kParts, kMul = FP * FQ * (SPLIT ? 3 : 1), kEach = kMul / kReads;
-#pragma unroll
-        for (int i = 0; i < kReads; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);        // an LDS read
-            __builtin_amdgcn_sched_group_barrier(0x008, kEach, 0);    // matrix products
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f.p[0][i], f.q[0][j], acc[i][j], 0, 0, 0);
         }
     };
-    Frags f0, f1;
-    stage(0u, 0u);
-    wait_loads();
-    block_barrier();
-    if (a.k > uint32_t(kBK)) stage(1u, kBK);
-    read(f0, 0u, 0);
-    uint32_t buf = 0u;
-    for (uint32_t k = 0; k < a.k; k += kBK) {
-        read(f1, buf, 1);
-        multiply(f0);
-        interleave();
-        __builtin_amdgcn_sched_barrier(0);      // the products stay before the wait
-        wait_loads();
+    // A ring of stages in LDS and two fragment sets in registers.  In step s the
+    // products of stage s run while the fragments of s + 1 are read and stage
+    // s + kRing is loaded into the slot of stage s, which every wave has read
+    // (its fragments) before the barrier that opens step s.  A stage is so
+    // loaded kRing - 1 steps before it is read, and one barrier is met per step.
+    // Past the end the last stage is loaded again and not used: no branch
+    // stands between the products.
+    auto step = [&](const Frags& f, Frags& next, uint32_t s, uint32_t slot) {
+        wait_loads<(kRing - 2) * kStageLoads>();
         block_barrier();
-        if (k + 2 * kBK < a.k) stage(buf, k + 2 * kBK);
-        buf ^= 1u;
-        read(f0, buf, 0);                       // after the last stage: old values, not used
-        multiply(f1);
-        interleave();
-        __builtin_amdgcn_sched_barrier(0);
+        const uint32_t k = min((s + kRing) * kBK, a.k - kBK), read_slot = slot + 1 == kRing ? 0 : slot + 1;
+#pragma unroll
+        for (int i = 0; i < FP; ++i) {
+            multiply_row(f, i);
+#pragma unroll
+            for (int l = kStageLoads * i / FP; l < kStageLoads * (i + 1) / FP; ++l) load(slot, k, l);
+#pragma unroll
+            for (int r = kReads * i / FP; r < kReads * (i + 1) / FP; ++r) read(next, read_slot, r);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        return read_slot;
+    };
+    Frags f0, f1;
+#pragma unroll
+    for (int s = 0; s < kRing; ++s)
+#pragma unroll
+        for (int l = 0; l < kStageLoads; ++l) load(s, min(uint32_t(s * kBK), a.k - kBK), l);
+    wait_loads<(kRing - 1) * kStageLoads>();
+    block_barrier();
+#pragma unroll
+    for (int r = 0; r < kReads; ++r) read(f0, 0u, r);
+    uint32_t slot = 0u;
+    for (uint32_t s = 0; s * kBK < a.k; s += 2) {        // k is a multiple of two stages
+        slot = step(f0, f1, s, slot);
+        slot = step(f1, f0, s + 1, slot);
     }
+    wait_loads<0>();
+
     // the tile's first P and Q rows of this wave
     const uint32_t pw = ti * B + wp * FP * 16, qw = tj * B + wq * FQ * 16;
 
     float alpha = 0.0f;
     if constexpr (MODE == kPoly) {
         // every block of a matrix adds the tiles' sums up in the same order
-        __shared__ float s_sum[2][kWaves];
+        block_barrier();
+        float* s_sum = reinterpret_cast<float*>(&s_op[0][0][0][0]);
         const float* sums = a.sums + uint64_t(item) * a.sum_tiles * 2u;
         float tr = 0.0f, sq = 0.0f;
         for (uint32_t i = tid; i < a.sum_tiles; i += kWaves * 64u) {
@@ -425,15 +424,15 @@ __global__ __launch_bounds__(WP* WQ * 64) void ortho_mul_kernel(OrthoMul a) {
             sq += __shfl_xor(sq, off, 64);
         }
         if (lane == 0u) {
-            s_sum[0][wave] = tr;
-            s_sum[1][wave] = sq;
+            s_sum[wave] = tr;
+            s_sum[kWaves + wave] = sq;
         }
         __syncthreads();
         tr = sq = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-            tr += s_sum[0][w];
-            sq += s_sum[1][w];
+            tr += s_sum[w];
+            sq += s_sum[kWaves + w];
         }
         alpha = a.ca + (a.cb * tr + a.cc * sq) / float(a.n);
         if (t == 0u && tid == 0u) a.alpha[item] = alpha;
@@ -553,7 +552,8 @@ __global__ __launch_bounds__(WP* WQ * 64) void ortho_mul_kernel(OrthoMul a) {
         }
     }
     if constexpr (MODE == kGram) {
-        __shared__ float s_sum[2][kWaves];
+        block_barrier();
+        float* s_sum = reinterpret_cast<float*>(&s_op[0][0][0][0]);
         tr *= 0x1p-14f;
         sq *= ti != tj ? 0x1p-27f : 0x1p-28f;              // an entry off the diagonal stands for two
 #pragma unroll
@@ -562,16 +562,16 @@ __global__ __launch_bounds__(WP* WQ * 64) void ortho_mul_kernel(OrthoMul a) {
             sq += __shfl_xor(sq, off, 64);
         }
         if (lane == 0u) {
-            s_sum[0][wave] = tr;
-            s_sum[1][wave] = sq;
+            s_sum[wave] = tr;
+            s_sum[kWaves + wave] = sq;
         }
         __syncthreads();
         if (tid == 0u) {
             tr = sq = 0.0f;
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) {
-                tr += s_sum[0][w];
-                sq += s_sum[1][w];
+                tr += s_sum[w];
+                sq += s_sum[kWaves + w];
             }
             float* out = a.sums + (uint64_t(item) * a.sum_tiles + t) * 2u;
             out[0] = tr;
