@@ -20,8 +20,15 @@
 // rounding of the result (a small matrix has few entries for errors to average
 // over: 9e-3 of |O|_F for a rank-1 8 x 8 without the low parts).
 //
-// Ranges.  X is stored times 2^s, s = floor(log2(sqrt(n m))) <= 15, A times
-// 2^14, D times 2^12: the entries' bounds (singular values <= 1.5) stay below
+// Two steps at once.  Where m is well above n, two steps take one A = X X^T and
+// one product with X instead of two each: with M, M' the two steps' polynomials
+// of A, A' = M A M and M' M are n x n and symmetric (all commute):
+//   T = M A,  A' = T M,  X <- M' M X,
+// three symmetric products of n^3 for 3 n^2 m saved.  More than two would lose
+// accuracy (A' holds the squares of the singular values).
+//
+// Ranges.  X is stored times 2^s, s = floor(log2(sqrt(n m))) <= 15, A and T times
+// 2^14, D times 2^12, E times 2^9: the entries' bounds (singular values <= 1.5) stay below
 // 65504 and typical entries well above float16's smallest normal number.
 //
 // Layout.  Every product is C[p][q] = sum_k P[p][k] Q[q][k] with k contiguous
@@ -46,7 +53,7 @@ typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 
 constexpr int kBK = 32;                 // elements of k per stage: one matrix product's
 constexpr int kRing = 5;                // stages in LDS
-constexpr int kScaleA = 14, kScaleD = 12;
+constexpr int kScaleA = 14, kScaleD = 12, kScaleE = 9;
 constexpr int kNormBlocks = 1024;       // most partial sums of |G|^2 per matrix
 
 // ------------------------------------------------------------ input
@@ -201,7 +208,17 @@ __global__ __launch_bounds__(256) void ortho_split_kernel(OrthoIn a) {
 
 // ------------------------------------------------------------ products
 
-enum { kGram = 0, kPoly = 1, kApply = 2, kLast = 3 };
+// What a launch computes from C = P Q^T; the symmetric ones on the lower
+// triangle's tiles.
+//   kGram     A  = X X^T                                (P = Q = X)
+//   kPoly     D  = (a - alpha) I + b A + c A^2          (P = Q = A)
+//   kApply    X <- gain X + E X                         (P = E, Q = X^T; E = D or a pair's)
+//   kLast     the same, as the result or the latents' step
+// and for two steps at once
+//   kMix      T  = alpha A + D A = M A                  (P = D, Q = A)
+//   kMixSum   A' = alpha T + T D = M A M                (P = T, Q = D)
+//   kJoin     E  = M' M - alpha alpha' I = alpha' D + alpha D' + D' D   (P = D', Q = D)
+enum { kGram, kPoly, kMix, kMixSum, kJoin, kApply, kLast };
 
 struct OrthoMul {
     const half_t* p;           // [batch, np, k]
@@ -217,15 +234,16 @@ struct OrthoMul {
     int s;
     half_t* out;               // kGram: A; kPoly: D; kApply: X [np, mp]
     half_t* out_lo;            // its low part (SPLIT)
-    const half_t* a;           // kPoly: A
-    const half_t* a_lo;
+    const half_t* in;          // added to C (kPoly: A, kMix: A, kMixSum: T, kJoin: D; kApply, kLast: X^T)
+    const half_t* in_lo;       // its low part (kApply, kLast, SPLIT); kJoin: D'
     float* sums;               // [batch, per-item tiles of the triangle, 2]: tr A, |A|^2 of a tile
     uint32_t sum_tiles;
-    float* alpha;              // [batch]
-    const half_t* xt;          // kApply, kLast: X^T before the step, and its low part
-    const half_t* xt_lo;
-    half_t* xt_out;
-    half_t* xt_lo_out;         // may be xt_lo (without SPLIT, where it is no operand)
+    float* alpha;              // [2, batch]: of the first and of the second step of a pair
+    uint32_t batch;
+    int second;                // kPoly: the pair's second step
+    int pair;                  // kApply, kLast: E stands for two steps
+    half_t* xt_out;            // kApply: X^T
+    half_t* xt_lo_out;         // may be in_lo (without SPLIT, where it is no operand)
     // kLast
     uint32_t rows, cols;
     int tall;
@@ -299,7 +317,8 @@ __global__ __launch_bounds__(WP* WQ * 64) void ortho_mul_kernel(OrthoMul a) {
     const uint32_t tile = xcd_order(blockIdx.x, gridDim.x);
     const uint32_t item = tile / a.per_item, t = tile - item * a.per_item;
     uint32_t ti, tj;
-    if constexpr (MODE == kGram || MODE == kPoly) {
+    constexpr bool kSquare = MODE != kApply && MODE != kLast;
+    if constexpr (kSquare) {
         tri_tile(t, a.tiles_p, ti, tj);
     } else {
         // four columns of tiles at a time, row by row
@@ -407,6 +426,7 @@ __global__ __launch_bounds__(WP* WQ * 64) void ortho_mul_kernel(OrthoMul a) {
     // the tile's first P and Q rows of this wave
     const uint32_t pw = ti * B + wp * FP * 16, qw = tj * B + wq * FQ * 16;
 
+    const float *alpha1 = a.alpha + item, *alpha2 = a.alpha + a.batch + item;
     float alpha = 0.0f;
     if constexpr (MODE == kPoly) {
         // every block of a matrix adds the tiles' sums up in the same order
@@ -435,25 +455,47 @@ __global__ __launch_bounds__(WP* WQ * 64) void ortho_mul_kernel(OrthoMul a) {
             sq += s_sum[kWaves + w];
         }
         alpha = a.ca + (a.cb * tr + a.cc * sq) / float(a.n);
-        if (t == 0u && tid == 0u) a.alpha[item] = alpha;
+        if (t == 0u && tid == 0u) a.alpha[a.second * a.batch + item] = alpha;
     }
-    if constexpr (MODE == kApply || MODE == kLast) alpha = a.alpha[item];
 
-    // (i, j): this lane's 8 results along P, from p0 on, at row q of Q
-    const float to_a = ldexpf(1.0f, kScaleA - 2 * a.s), back = ldexpf(1.0f, -a.s);
-    const uint64_t item_out = uint64_t(item) * a.np * (MODE == kGram || MODE == kPoly ? a.np : a.mp);
+    // result = by_c C + by_hi in + by_lo in_lo + on_diagonal I, all in the scales
+    // of what is stored
+    const float back = ldexpf(1.0f, -a.s);
+    float by_c = 0.0f, by_hi = 0.0f, by_lo = 0.0f, on_diagonal = 0.0f;
+    if constexpr (MODE == kGram) by_c = ldexpf(1.0f, kScaleA - 2 * a.s);
+    if constexpr (MODE == kPoly) {
+        by_c = ldexpf(a.cc, kScaleD - 2 * kScaleA);
+        by_hi = by_lo = ldexpf(a.cb, kScaleD - kScaleA);
+        on_diagonal = ldexpf(a.ca - alpha, kScaleD);
+    }
+    if constexpr (MODE == kMix || MODE == kMixSum) {
+        by_c = ldexpf(1.0f, -kScaleD);
+        by_hi = *alpha1;
+    }
+    if constexpr (MODE == kJoin) {
+        by_c = ldexpf(1.0f, kScaleE - 2 * kScaleD);
+        by_hi = ldexpf(*alpha2, kScaleE - kScaleD);
+        by_lo = ldexpf(*alpha1, kScaleE - kScaleD);
+    }
+    if constexpr (MODE == kApply || MODE == kLast) {
+        by_c = ldexpf(1.0f, a.pair ? -kScaleE : -kScaleD);
+        by_hi = by_lo = a.pair ? *alpha1 * *alpha2 : *alpha1;
+    }
+    constexpr bool kUseLo = MODE == kApply || MODE == kLast || MODE == kJoin || (MODE == kPoly && SPLIT);
+    constexpr bool kSums = MODE == kGram || MODE == kMixSum;
+
+    // (u, j): this lane's 8 results along P, from p0 on, at row q of Q
+    const uint64_t item_out = uint64_t(item) * a.np * (kSquare ? a.np : a.mp);
     float tr = 0.0f, sq = 0.0f;
     auto value = [&](int u, int j, int e) { return acc[2 * u + e / 4][j][e % 4]; };
     half8_t in_hi[2][FQ], in_lo[2][FQ];       // what the results are added to, one pair of fragments ahead
     auto fetch = [&](int u) {
-        const half_t *hi = MODE == kPoly ? a.a : a.xt, *lo = MODE == kPoly ? a.a_lo : a.xt_lo;
         const uint32_t p0 = pw + u * 32u + fk * 8u;
 #pragma unroll
         for (int j = 0; j < FQ; ++j) {
             const uint64_t at = item_out + uint64_t(qw + frow * FQ + j) * a.np + p0;
-            in_hi[u & 1][j] = *reinterpret_cast<const half8_t*>(hi + at);
-            if constexpr (MODE != kPoly || SPLIT) in_lo[u & 1][j] = *reinterpret_cast<const half8_t*>(lo + at);
-            else in_lo[u & 1][j] = half8_t{};
+            in_hi[u & 1][j] = *reinterpret_cast<const half8_t*>(a.in + at);
+            if constexpr (kUseLo) in_lo[u & 1][j] = *reinterpret_cast<const half8_t*>(a.in_lo + at);
         }
     };
     if constexpr (MODE != kGram) fetch(0);
@@ -470,20 +512,13 @@ __global__ __launch_bounds__(WP* WQ * 64) void ortho_mul_kernel(OrthoMul a) {
             const uint32_t q = qw + frow * FQ + j;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                float r = value(u, j, e);
-                if constexpr (MODE == kGram) {
-                    r *= to_a;
+                float r = by_c * value(u, j, e);
+                if constexpr (MODE != kGram) r = fmaf(by_hi, float(in_hi[u & 1][j][e]), r);
+                if constexpr (kUseLo) r = fmaf(by_lo, float(in_lo[u & 1][j][e]), r);
+                if constexpr (MODE == kPoly) r += p0 + e == q ? on_diagonal : 0.0f;
+                if constexpr (kSums) {
                     sq = fmaf(r, r, sq);
-                    if (p0 + e == q) tr += r;
-                } else {
-                    const float x = float(in_hi[u & 1][j][e]) + float(in_lo[u & 1][j][e]);
-                    if constexpr (MODE == kPoly) {
-                        r = fmaf(a.cc * 0x1p-28f, r, a.cb * 0x1p-14f * x);
-                        if (p0 + e == q) r += a.ca - alpha;
-                        r *= 0x1p12f;
-                    } else {
-                        r = fmaf(alpha, x, r * 0x1p-12f);
-                    }
+                    tr += p0 + e == q ? r : 0.0f;
                 }
                 v[j][e] = r;
                 h[j][e] = half_t(r);
@@ -524,7 +559,7 @@ __global__ __launch_bounds__(WP* WQ * 64) void ortho_mul_kernel(OrthoMul a) {
                         put((uint64_t(item) * a.rows + p0 + e) * a.cols + q, &v[0][e], 8, std::integral_constant<int, FQ>{});
             }
         } else {
-            // rows of Q: A and D (the mirrored tile), or X^T
+            // rows of Q: the mirrored tile, or X^T
             half_t *turned = MODE == kApply ? a.xt_out : a.out, *turned_lo = MODE == kApply ? a.xt_lo_out : a.out_lo;
 #pragma unroll
             for (int j = 0; j < FQ; ++j) {
@@ -551,7 +586,7 @@ __global__ __launch_bounds__(WP* WQ * 64) void ortho_mul_kernel(OrthoMul a) {
             }
         }
     }
-    if constexpr (MODE == kGram) {
+    if constexpr (kSums) {
         block_barrier();
         float* s_sum = reinterpret_cast<float*>(&s_op[0][0][0][0]);
         tr *= 0x1p-14f;
@@ -588,6 +623,8 @@ struct OrthoPlan {
     int tall, s;
     size_t x, xt0, xt1, lo, a, d, sums, alpha, norm, total;
     size_t x_lo, lo1, a_lo, d_lo;           // 64-wide tiles only
+    int pair;                               // two steps at once
+    size_t t, d2;
 };
 
 static size_t ortho_align(size_t v) { return (v + 255) / 256 * 256; }
@@ -615,12 +652,17 @@ static OrthoPlan ortho_plan(int64_t batch, int64_t rows, int64_t cols) {
     p.a = take(sq);
     p.d = take(sq);
     p.sums = take(size_t(batch) * p.side * (p.side + 1) / 2 * 8);
-    p.alpha = take(size_t(batch) * 4);
+    p.alpha = take(size_t(batch) * 8);
     // four vectors of 8 per thread and block, while that leaves blocks for every CU
     const uint64_t cells = uint64_t(p.n) * p.m, most = (cus * 8 + batch - 1) / uint64_t(batch);
     const uint64_t want = (cells + 8191) / 8192;
     p.norm_blocks = uint32_t(std::min<uint64_t>(std::min<uint64_t>(want, most), kNormBlocks));
     p.norm = take(size_t(batch) * p.norm_blocks * 8);
+    p.pair = p.tile != 64 && uint64_t(p.m) * 5 >= uint64_t(p.n) * 6;
+    if (p.pair) {
+        p.t = take(sq);
+        p.d2 = take(sq);
+    }
     if (p.tile == 64) {
         p.x_lo = take(rect);
         p.lo1 = take(rect);
@@ -684,40 +726,59 @@ static void ortho_steps(const OrthoPlan& p, OrthoMul a, int64_t batch, int32_t s
     a.sums = reinterpret_cast<float*>(ws + p.sums);
     a.sum_tiles = tri;
     a.alpha = reinterpret_cast<float*>(ws + p.alpha);
-    a.a = ma;
-    a.a_lo = a_lo;
-    for (int32_t i = 0; i < steps; ++i) {
-        a.tiles_p = p.side;
+    a.batch = uint32_t(batch);
+    a.tiles_p = p.side;
+    auto square = [&](auto kernel, const half_t* pp, const half_t* pp_lo, const half_t* qq, const half_t* qq_lo,
+                      const half_t* in, const half_t* in_lo, half_t* out, half_t* out_lo) {
+        a.p = pp;
+        a.p_lo = pp_lo;
+        a.q = qq;
+        a.q_lo = qq_lo;
+        a.p_item = a.q_item = pp == x ? rect : sq;
+        a.k = pp == x ? p.mp : p.np;
+        a.in = in;
+        a.in_lo = in_lo;
+        a.out = out;
+        a.out_lo = out_lo;
         a.per_item = tri;
-        a.p = a.q = x;
-        a.p_lo = a.q_lo = x_lo;
-        a.p_item = a.q_item = rect;
-        a.k = p.mp;
-        a.out = ma;
-        a.out_lo = a_lo;
-        launch(ortho_mul_kernel<B, WP, WQ, SPLIT, kGram>, dim3(uint32_t(batch) * tri), block, 0, st, a);
-        a.p = a.q = ma;
-        a.p_lo = a.q_lo = a_lo;
-        a.p_item = a.q_item = sq;
-        a.k = p.np;
-        a.out = md;
-        a.out_lo = d_lo;
-        launch(ortho_mul_kernel<B, WP, WQ, SPLIT, kPoly>, dim3(uint32_t(batch) * tri), block, 0, st, a);
-        a.p = md;
-        a.p_lo = d_lo;
-        a.q = a.xt = xt[i & 1];
-        a.q_lo = a.xt_lo = lo[i & 1];
+        launch(kernel, dim3(uint32_t(batch) * tri), block, 0, st, a);
+    };
+    int at = 0;                              // which of xt, lo holds X^T
+    for (int32_t i = 0; i < steps;) {
+        a.second = 0;
+        a.pair = p.pair && i + 1 < steps;
+        const half_t *e = md, *e_lo = d_lo;
+        square(ortho_mul_kernel<B, WP, WQ, SPLIT, kGram>, x, x_lo, x, x_lo, nullptr, nullptr, ma, a_lo);
+        square(ortho_mul_kernel<B, WP, WQ, SPLIT, kPoly>, ma, a_lo, ma, a_lo, ma, a_lo, md, d_lo);
+        if constexpr (!SPLIT) {
+            if (a.pair) {
+                half_t *mt = reinterpret_cast<half_t*>(ws + p.t), *md2 = reinterpret_cast<half_t*>(ws + p.d2);
+                square(ortho_mul_kernel<B, WP, WQ, SPLIT, kMix>, md, nullptr, ma, nullptr, ma, nullptr, mt, nullptr);
+                square(ortho_mul_kernel<B, WP, WQ, SPLIT, kMixSum>, mt, nullptr, md, nullptr, mt, nullptr, ma, nullptr);
+                a.second = 1;
+                square(ortho_mul_kernel<B, WP, WQ, SPLIT, kPoly>, ma, nullptr, ma, nullptr, ma, nullptr, md2, nullptr);
+                square(ortho_mul_kernel<B, WP, WQ, SPLIT, kJoin>, md2, nullptr, md, nullptr, md, md2, mt, nullptr);
+                e = mt;
+            }
+        }
+        i += a.pair ? 2 : 1;
+        a.p = e;
+        a.p_lo = e_lo;
+        a.q = a.in = xt[at];
+        a.q_lo = a.in_lo = lo[at];
+        a.p_item = sq;
         a.q_item = rect;
+        a.k = p.np;
         a.tiles_q = tq;
         a.per_item = p.side * tq;
         a.out = x;
         a.out_lo = x_lo;
-        a.xt_out = xt[(i & 1) ^ 1];
-        a.xt_lo_out = lo[(i & 1) ^ 1];
-        if (i + 1 < steps)
-            launch(ortho_mul_kernel<B, WP, WQ, SPLIT, kApply>, dim3(uint32_t(batch) * a.per_item), block, 0, st, a);
-        else
-            launch(ortho_mul_kernel<B, WP, WQ, SPLIT, kLast>, dim3(uint32_t(batch) * a.per_item), block, 0, st, a);
+        at ^= 1;
+        a.xt_out = xt[at];
+        a.xt_lo_out = lo[at];
+        const dim3 grid(uint32_t(batch) * a.per_item);
+        if (i < steps) launch(ortho_mul_kernel<B, WP, WQ, SPLIT, kApply>, grid, block, 0, st, a);
+        else launch(ortho_mul_kernel<B, WP, WQ, SPLIT, kLast>, grid, block, 0, st, a);
     }
 }
 
