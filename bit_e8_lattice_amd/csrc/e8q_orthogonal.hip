@@ -2,30 +2,30 @@
 // matrix cores.
 //
 // With n the smaller and m the larger side, X is n x m.  One step is three
-// products: A = X X^T, then D = (a - alpha) I + b A + c A^2, then
-// X <- alpha X + D X, alpha = a + b tr(A)/n + c tr(A^2)/n the mean of the
-// diagonal of M = aI + bA + cA^2.
+// products: A = X X^T, then M = a I + b A + c A^2, then X <- M X.
 //
-// Why alpha is taken out.  The operands of the matrix cores are float16.  With
-// X <- M X the rounding of X (2^-12) lands on every singular direction alike
-// and grows with the small singular values (up to a^steps = 485 times), so a
-// gradient of low rank would come out with errors of several percent.  With
-// alpha X kept to 22 bits (two float16 parts) the rounding only passes through
-// D, which is small where the singular values are near each other and which
-// maps the strong directions' error back onto the strong directions.  Measured
-// against float64: 6e-4 to 1.2e-3 of |O|_F, for flat, falling and low-rank
-// spectra alike.  Problems too small to fill the chip (64-wide tiles) wait for
-// memory and launches, not for the matrix cores: there every operand has its
-// low part too and a product is three (hi hi, hi lo, lo hi), which leaves the
-// rounding of the result (a small matrix has few entries for errors to average
-// over: 9e-3 of |O|_F for a rank-1 8 x 8 without the low parts).
+// Rounding.  The operands of the matrix cores are float16.  Were X float16 too,
+// its rounding (2^-12 of an entry) would land on every singular direction alike
+// and grow with the small singular values (up to a^steps = 485 times): a
+// gradient of low rank would come out with errors of 2 to 4 percent.  So X is
+// kept to 22 bits, X_hi + X_lo, and the new X is M X_hi + alpha X_lo, alpha the
+// mean of the diagonal of M = aI + bA + cA^2 (M X_lo would differ from it by far
+// less than a rounding of M X_hi).  The rounding of M acts on the strong
+// directions' columns alone.  Measured against float64, of |O|_F: 0.8e-3 to
+// 1.7e-3 for flat, falling and low-rank spectra, 3.3e-3 for a random matrix of
+// rank 16.  Problems too small to fill the chip (64-wide tiles) wait for memory
+// and launches, not for the matrix cores: there every operand has its low part
+// and a product is three (hi hi, hi lo, lo hi), which leaves the rounding of the
+// result.
 //
 // Two steps at once.  Where m is well above n, two steps take one A = X X^T and
 // one product with X instead of two each: with M, M' the two steps' polynomials
 // of A, A' = M A M and M' M are n x n and symmetric (all commute):
 //   T = M A,  A' = T M,  X <- M' M X,
-// three symmetric products of n^3 for 3 n^2 m saved.  More than two would lose
-// accuracy (A' holds the squares of the singular values).
+// three symmetric products of n^3 for 3 n^2 m saved.  These products are made of
+// D = M - alpha I, the rest added in float32: a diagonal rounded with the rest
+// would cost half as much again in accuracy.  More than two steps would lose
+// more (A' holds the squares of the singular values).
 //
 // Ranges.  X is stored times 2^s, s = floor(log2(sqrt(n m))) <= 15, A and T times
 // 2^14, D times 2^12, E times 2^9: the entries' bounds (singular values <= 1.5) stay below
@@ -52,7 +52,6 @@ typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 
 constexpr int kBK = 32;                 // elements of k per stage: one matrix product's
-constexpr int kRing = 5;                // stages in LDS
 constexpr int kScaleA = 14, kScaleD = 12, kScaleE = 9;
 constexpr int kNormBlocks = 1024;       // most partial sums of |G|^2 per matrix
 
@@ -211,13 +210,13 @@ __global__ __launch_bounds__(256) void ortho_split_kernel(OrthoIn a) {
 // What a launch computes from C = P Q^T; the symmetric ones on the lower
 // triangle's tiles.
 //   kGram     A  = X X^T                                (P = Q = X)
-//   kPoly     D  = (a - alpha) I + b A + c A^2          (P = Q = A)
-//   kApply    X <- gain X + E X                         (P = E, Q = X^T; E = D or a pair's)
+//   kPoly     M  = a I + b A + c A^2, or D = M - alpha I for a pair   (P = Q = A)
+//   kApply    X <- E X_hi + gain X_lo                   (P = E, Q = X^T; E = M or a pair's)
 //   kLast     the same, as the result or the latents' step
 // and for two steps at once
 //   kMix      T  = alpha A + D A = M A                  (P = D, Q = A)
 //   kMixSum   A' = alpha T + T D = M A M                (P = T, Q = D)
-//   kJoin     E  = M' M - alpha alpha' I = alpha' D + alpha D' + D' D   (P = D', Q = D)
+//   kJoin     E  = M' M = alpha alpha' I + alpha' D + alpha D' + D' D   (P = D', Q = D)
 enum { kGram, kPoly, kMix, kMixSum, kJoin, kApply, kLast };
 
 struct OrthoMul {
@@ -234,16 +233,16 @@ struct OrthoMul {
     int s;
     half_t* out;               // kGram: A; kPoly: D; kApply: X [np, mp]
     half_t* out_lo;            // its low part (SPLIT)
-    const half_t* in;          // added to C (kPoly: A, kMix: A, kMixSum: T, kJoin: D; kApply, kLast: X^T)
-    const half_t* in_lo;       // its low part (kApply, kLast, SPLIT); kJoin: D'
+    const half_t* in;          // added to C (kPoly: A, kMix: A, kMixSum: T, kJoin: D; kApply, kLast: low part of X^T)
+    const half_t* in_lo;       // its low part (SPLIT); kJoin: D'
     float* sums;               // [batch, per-item tiles of the triangle, 2]: tr A, |A|^2 of a tile
     uint32_t sum_tiles;
     float* alpha;              // [2, batch]: of the first and of the second step of a pair
     uint32_t batch;
     int second;                // kPoly: the pair's second step
-    int pair;                  // kApply, kLast: E stands for two steps
+    int pair;                  // two steps at once
     half_t* xt_out;            // kApply: X^T
-    half_t* xt_lo_out;         // may be in_lo (without SPLIT, where it is no operand)
+    half_t* xt_lo_out;         // may be in (without SPLIT, where it is no operand)
     // kLast
     uint32_t rows, cols;
     int tall;
@@ -306,12 +305,14 @@ __device__ __forceinline__ uint32_t xcd_order(uint32_t b, uint32_t total) {
     return x * each + min(x, rest) + i;
 }
 
-template <int B, int WP, int WQ, bool SPLIT, int MODE>
-__global__ __launch_bounds__(WP* WQ * 64) void ortho_mul_kernel(OrthoMul a) {
-    constexpr int kWaves = WP * WQ, FP = B / WP / 16, FQ = B / WQ / 16;
-    constexpr int kLoads = B / 16 / kWaves;          // wave loads per operand and stage
+// A tile of BP x BQ by WP x WQ waves, RING stages in LDS.
+template <int BP, int BQ, int WP, int WQ, int RING, bool SPLIT, int MODE>
+__global__ __launch_bounds__(WP* WQ * 64, 2) void ortho_mul_kernel(OrthoMul a) {
+    constexpr int kWaves = WP * WQ, FP = BP / WP / 16, FQ = BQ / WQ / 16;
+    constexpr int kLoadsP = BP / 16 / kWaves, kLoadsQ = BQ / 16 / kWaves;    // wave loads per stage
     constexpr int kParts = SPLIT ? 2 : 1;
-    __shared__ half_t s_op[kRing][2][kParts][B * kBK];     // P and Q
+    constexpr int kSlot = kParts * (BP + BQ) * kBK;          // P's parts, then Q's
+    __shared__ half_t s_op[RING * kSlot];
     const uint32_t tid = threadIdx.x, lane = tid & 63u;
     const uint32_t wave = uint32_t(__builtin_amdgcn_readfirstlane(int(tid >> 6)));
     const uint32_t tile = xcd_order(blockIdx.x, gridDim.x);
@@ -340,25 +341,33 @@ __global__ __launch_bounds__(WP* WQ * 64) void ortho_mul_kernel(OrthoMul a) {
     // meet all 64 banks.
     const uint32_t lrow = lane >> 2;                 // a wave load fills 16 rows of 64 bytes
     auto place = [](uint32_t r) { return (0u - (r >> 2)) & 3u; };
-    const uint64_t op = uint64_t(item) * a.p_item + uint64_t(ti * B) * a.k;
-    const uint64_t oq = uint64_t(item) * a.q_item + uint64_t(tj * B) * a.k;
-    uint32_t off_p[kLoads], off_q[kLoads];
+    const uint64_t op = uint64_t(item) * a.p_item + uint64_t(ti * BP) * a.k;
+    const uint64_t oq = uint64_t(item) * a.q_item + uint64_t(tj * BQ) * a.k;
+    const uint32_t chunk = ((lane & 3u) ^ place(lrow)) * 8u;
+    uint32_t off_p[kLoadsP], off_q[kLoadsQ];
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-        const uint32_t r = (wave * kLoads + i) * 16u + lrow, c = (lane & 3u) ^ place(lrow);
-        const uint32_t rp = (r & ~31u) | ((r << 1) & 24u) | ((r >> 2) & 4u) | (r & 3u);
-        const uint32_t rq = r / (FQ * 16) * (FQ * 16) + (r & 15u) * FQ + (r >> 4) % FQ;
-        off_p[i] = (rp * a.k + c * 8u) * 2u;
-        off_q[i] = (rq * a.k + c * 8u) * 2u;
+    for (int i = 0; i < kLoadsP; ++i) {
+        const uint32_t r = (wave * kLoadsP + i) * 16u + lrow;
+        off_p[i] = (((r & ~31u) | ((r << 1) & 24u) | ((r >> 2) & 4u) | (r & 3u)) * a.k + chunk) * 2u;
     }
-    const uint32_t to = lds_address(&s_op[0][0][0][0]) + wave * (kLoads * 16 * kBK * 2);
+#pragma unroll
+    for (int i = 0; i < kLoadsQ; ++i) {
+        const uint32_t r = (wave * kLoadsQ + i) * 16u + lrow;
+        off_q[i] = ((r / (FQ * 16) * (FQ * 16) + (r & 15u) * FQ + (r >> 4) % FQ) * a.k + chunk) * 2u;
+    }
+    const uint32_t lds = lds_address(s_op);
+    const uint32_t to_p = lds + wave * (kLoadsP * 16 * kBK * 2);
+    const uint32_t to_q = lds + kParts * (BP * kBK * 2) + wave * (kLoadsQ * 16 * kBK * 2);
     // load `l` of this wave's loads of the stage at k
-    constexpr int kStageLoads = 2 * kLoads * kParts;
+    constexpr int kStageLoads = (kLoadsP + kLoadsQ) * kParts;
     auto load = [&](uint32_t slot, uint32_t k, int l) {
-        const int q = l % 2, h = l / 2 % kParts, i = l / (2 * kParts);
-        const half_t* from = q ? (h ? a.q_lo : a.q) + oq : (h ? a.p_lo : a.p) + op;
-        load_lds16(from + k, q ? off_q[i] : off_p[i],
-                   to + ((slot * 2 + q) * kParts + h) * (B * kBK * 2) + i * (16 * kBK * 2));
+        const int h = l % kParts, i = l / kParts;
+        if (i < kLoadsP)
+            load_lds16((h ? a.p_lo : a.p) + op + k, off_p[i],
+                       to_p + slot * (kSlot * 2) + h * (BP * kBK * 2) + i * (16 * kBK * 2));
+        else
+            load_lds16((h ? a.q_lo : a.q) + oq + k, off_q[i - kLoadsP],
+                       to_q + slot * (kSlot * 2) + h * (BQ * kBK * 2) + (i - kLoadsP) * (16 * kBK * 2));
     };
     const uint32_t wp = wave / WQ, wq = wave - wp * WQ;
     const uint32_t frow = lane & 15u, fk = lane >> 4;
@@ -371,8 +380,11 @@ __global__ __launch_bounds__(WP* WQ * 64) void ortho_mul_kernel(OrthoMul a) {
     const uint32_t at_q = (wq * FQ * 16 + frow) * kBK + (fk ^ place(frow)) * 8;
     auto read = [&](Frags& f, uint32_t slot, int r) {
         const int h = r % kParts, n = r / kParts;
-        if (n < FQ) f.q[h][n] = *reinterpret_cast<const half8_t*>(&s_op[slot][1][h][at_q + n * 16 * kBK]);
-        else f.p[h][n - FQ] = *reinterpret_cast<const half8_t*>(&s_op[slot][0][h][at_p + (n - FQ) * 16 * kBK]);
+        const half_t* at = s_op + slot * kSlot;
+        if (n < FQ)
+            f.q[h][n] = *reinterpret_cast<const half8_t*>(at + (kParts * BP + h * BQ + n * 16) * kBK + at_q);
+        else
+            f.p[h][n - FQ] = *reinterpret_cast<const half8_t*>(at + (h * BP + (n - FQ) * 16) * kBK + at_p);
     };
     f32x4_t acc[FP][FQ] = {};
     auto multiply_row = [&](const Frags& f, int i) {
@@ -387,15 +399,15 @@ __global__ __launch_bounds__(WP* WQ * 64) void ortho_mul_kernel(OrthoMul a) {
     };
     // A ring of stages in LDS and two fragment sets in registers.  In step s the
     // products of stage s run while the fragments of s + 1 are read and stage
-    // s + kRing is loaded into the slot of stage s, which every wave has read
+    // s + RING is loaded into the slot of stage s, which every wave has read
     // (its fragments) before the barrier that opens step s.  A stage is so
-    // loaded kRing - 1 steps before it is read, and one barrier is met per step.
+    // loaded RING - 1 steps before it is read, and one barrier is met per step.
     // Past the end the last stage is loaded again and not used: no branch
     // stands between the products.
     auto step = [&](const Frags& f, Frags& next, uint32_t s, uint32_t slot) {
-        wait_loads<(kRing - 2) * kStageLoads>();
+        wait_loads<(RING - 2) * kStageLoads>();
         block_barrier();
-        const uint32_t k = min((s + kRing) * kBK, a.k - kBK), read_slot = slot + 1 == kRing ? 0 : slot + 1;
+        const uint32_t k = min((s + RING) * kBK, a.k - kBK), read_slot = slot + 1 == RING ? 0 : slot + 1;
 #pragma unroll
         for (int i = 0; i < FP; ++i) {
             multiply_row(f, i);
@@ -409,10 +421,10 @@ __global__ __launch_bounds__(WP* WQ * 64) void ortho_mul_kernel(OrthoMul a) {
     };
     Frags f0, f1;
 #pragma unroll
-    for (int s = 0; s < kRing; ++s)
+    for (int s = 0; s < RING; ++s)
 #pragma unroll
         for (int l = 0; l < kStageLoads; ++l) load(s, min(uint32_t(s * kBK), a.k - kBK), l);
-    wait_loads<(kRing - 1) * kStageLoads>();
+    wait_loads<(RING - 1) * kStageLoads>();
     block_barrier();
 #pragma unroll
     for (int r = 0; r < kReads; ++r) read(f0, 0u, r);
@@ -424,14 +436,14 @@ __global__ __launch_bounds__(WP* WQ * 64) void ortho_mul_kernel(OrthoMul a) {
     wait_loads<0>();
 
     // the tile's first P and Q rows of this wave
-    const uint32_t pw = ti * B + wp * FP * 16, qw = tj * B + wq * FQ * 16;
+    const uint32_t pw = ti * BP + wp * FP * 16, qw = tj * BQ + wq * FQ * 16;
 
     const float *alpha1 = a.alpha + item, *alpha2 = a.alpha + a.batch + item;
     float alpha = 0.0f;
     if constexpr (MODE == kPoly) {
         // every block of a matrix adds the tiles' sums up in the same order
         block_barrier();
-        float* s_sum = reinterpret_cast<float*>(&s_op[0][0][0][0]);
+        float* s_sum = reinterpret_cast<float*>(s_op);
         const float* sums = a.sums + uint64_t(item) * a.sum_tiles * 2u;
         float tr = 0.0f, sq = 0.0f;
         for (uint32_t i = tid; i < a.sum_tiles; i += kWaves * 64u) {
@@ -466,7 +478,7 @@ __global__ __launch_bounds__(WP* WQ * 64) void ortho_mul_kernel(OrthoMul a) {
     if constexpr (MODE == kPoly) {
         by_c = ldexpf(a.cc, kScaleD - 2 * kScaleA);
         by_hi = by_lo = ldexpf(a.cb, kScaleD - kScaleA);
-        on_diagonal = ldexpf(a.ca - alpha, kScaleD);
+        on_diagonal = ldexpf(a.pair ? a.ca - alpha : a.ca, kScaleD);
     }
     if constexpr (MODE == kMix || MODE == kMixSum) {
         by_c = ldexpf(1.0f, -kScaleD);
@@ -476,12 +488,14 @@ __global__ __launch_bounds__(WP* WQ * 64) void ortho_mul_kernel(OrthoMul a) {
         by_c = ldexpf(1.0f, kScaleE - 2 * kScaleD);
         by_hi = ldexpf(*alpha2, kScaleE - kScaleD);
         by_lo = ldexpf(*alpha1, kScaleE - kScaleD);
+        on_diagonal = ldexpf(*alpha1 * *alpha2, kScaleE);
     }
     if constexpr (MODE == kApply || MODE == kLast) {
         by_c = ldexpf(1.0f, a.pair ? -kScaleE : -kScaleD);
-        by_hi = by_lo = a.pair ? *alpha1 * *alpha2 : *alpha1;
+        by_hi = SPLIT ? 0.0f : a.pair ? *alpha1 * *alpha2 : *alpha1;
     }
-    constexpr bool kUseLo = MODE == kApply || MODE == kLast || MODE == kJoin || (MODE == kPoly && SPLIT);
+    constexpr bool kUseHi = MODE != kGram && !(SPLIT && !kSquare);    // with SPLIT the product has X_lo
+    constexpr bool kUseLo = MODE == kJoin || (MODE == kPoly && SPLIT);
     constexpr bool kSums = MODE == kGram || MODE == kMixSum;
 
     // (u, j): this lane's 8 results along P, from p0 on, at row q of Q
@@ -498,11 +512,11 @@ __global__ __launch_bounds__(WP* WQ * 64) void ortho_mul_kernel(OrthoMul a) {
             if constexpr (kUseLo) in_lo[u & 1][j] = *reinterpret_cast<const half8_t*>(a.in_lo + at);
         }
     };
-    if constexpr (MODE != kGram) fetch(0);
+    if constexpr (kUseHi) fetch(0);
 #pragma unroll
     for (int u = 0; u < FP / 2; ++u) {
         const uint32_t p0 = pw + u * 32u + fk * 8u;
-        if constexpr (MODE != kGram) {
+        if constexpr (kUseHi) {
             if (u + 1 < FP / 2) fetch(u + 1);
         }
         half8_t h[FQ], l[FQ];
@@ -513,9 +527,9 @@ __global__ __launch_bounds__(WP* WQ * 64) void ortho_mul_kernel(OrthoMul a) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 float r = by_c * value(u, j, e);
-                if constexpr (MODE != kGram) r = fmaf(by_hi, float(in_hi[u & 1][j][e]), r);
+                if constexpr (kUseHi) r = fmaf(by_hi, float(in_hi[u & 1][j][e]), r);
                 if constexpr (kUseLo) r = fmaf(by_lo, float(in_lo[u & 1][j][e]), r);
-                if constexpr (MODE == kPoly) r += p0 + e == q ? on_diagonal : 0.0f;
+                if constexpr (MODE == kPoly || MODE == kJoin) r += p0 + e == q ? on_diagonal : 0.0f;
                 if constexpr (kSums) {
                     sq = fmaf(r, r, sq);
                     tr += p0 + e == q ? r : 0.0f;
@@ -588,7 +602,7 @@ __global__ __launch_bounds__(WP* WQ * 64) void ortho_mul_kernel(OrthoMul a) {
     }
     if constexpr (kSums) {
         block_barrier();
-        float* s_sum = reinterpret_cast<float*>(&s_op[0][0][0][0]);
+        float* s_sum = reinterpret_cast<float*>(s_op);
         tr *= 0x1p-14f;
         sq *= ti != tj ? 0x1p-27f : 0x1p-28f;              // an entry off the diagonal stands for two
 #pragma unroll
@@ -707,8 +721,18 @@ static e8q_status_t ortho_check(const void* g, e8q_dtype_t dtype, int64_t batch,
     return E8Q_OK;
 }
 
-template <int B, int WP, int WQ, bool SPLIT>
+template <int BP, int BQ, int WP, int WQ, int RING, bool SPLIT>
+struct OrthoTile {
+    static constexpr int kBP = BP, kBQ = BQ, kThreads = WP * WQ * 64;
+    static constexpr bool kSplit = SPLIT;
+    template <int MODE>
+    static constexpr auto kernel = ortho_mul_kernel<BP, BQ, WP, WQ, RING, SPLIT, MODE>;
+};
+
+// SQ: the kernels of the square products, RE: those of the products with X.
+template <class SQ, class RE>
 static void ortho_steps(const OrthoPlan& p, OrthoMul a, int64_t batch, int32_t steps, char* ws, hipStream_t st) {
+    constexpr bool SPLIT = SQ::kSplit;
     half_t* x = reinterpret_cast<half_t*>(ws + p.x);
     half_t* lo[2] = {reinterpret_cast<half_t*>(ws + p.lo), reinterpret_cast<half_t*>(ws + (SPLIT ? p.lo1 : p.lo))};
     half_t* x_lo = SPLIT ? reinterpret_cast<half_t*>(ws + p.x_lo) : nullptr;
@@ -716,9 +740,8 @@ static void ortho_steps(const OrthoPlan& p, OrthoMul a, int64_t batch, int32_t s
     half_t* d_lo = SPLIT ? reinterpret_cast<half_t*>(ws + p.d_lo) : nullptr;
     half_t* xt[2] = {reinterpret_cast<half_t*>(ws + p.xt0), reinterpret_cast<half_t*>(ws + p.xt1)};
     half_t *ma = reinterpret_cast<half_t*>(ws + p.a), *md = reinterpret_cast<half_t*>(ws + p.d);
-    const uint32_t tri = p.side * (p.side + 1) / 2, tq = p.mp / p.tile;
+    const uint32_t tri = p.side * (p.side + 1) / 2, tq = p.mp / RE::kBQ;
     const uint64_t rect = uint64_t(p.np) * p.mp, sq = uint64_t(p.np) * p.np;
-    const dim3 block(WP * WQ * 64);
     a.n = p.n;
     a.np = p.np;
     a.mp = p.mp;
@@ -727,7 +750,6 @@ static void ortho_steps(const OrthoPlan& p, OrthoMul a, int64_t batch, int32_t s
     a.sum_tiles = tri;
     a.alpha = reinterpret_cast<float*>(ws + p.alpha);
     a.batch = uint32_t(batch);
-    a.tiles_p = p.side;
     auto square = [&](auto kernel, const half_t* pp, const half_t* pp_lo, const half_t* qq, const half_t* qq_lo,
                       const half_t* in, const half_t* in_lo, half_t* out, half_t* out_lo) {
         a.p = pp;
@@ -740,45 +762,47 @@ static void ortho_steps(const OrthoPlan& p, OrthoMul a, int64_t batch, int32_t s
         a.in_lo = in_lo;
         a.out = out;
         a.out_lo = out_lo;
+        a.tiles_p = p.side;
         a.per_item = tri;
-        launch(kernel, dim3(uint32_t(batch) * tri), block, 0, st, a);
+        launch(kernel, dim3(uint32_t(batch) * tri), dim3(SQ::kThreads), 0, st, a);
     };
     int at = 0;                              // which of xt, lo holds X^T
     for (int32_t i = 0; i < steps;) {
         a.second = 0;
         a.pair = p.pair && i + 1 < steps;
         const half_t *e = md, *e_lo = d_lo;
-        square(ortho_mul_kernel<B, WP, WQ, SPLIT, kGram>, x, x_lo, x, x_lo, nullptr, nullptr, ma, a_lo);
-        square(ortho_mul_kernel<B, WP, WQ, SPLIT, kPoly>, ma, a_lo, ma, a_lo, ma, a_lo, md, d_lo);
+        square(SQ::template kernel<kGram>, x, x_lo, x, x_lo, nullptr, nullptr, ma, a_lo);
+        square(SQ::template kernel<kPoly>, ma, a_lo, ma, a_lo, ma, a_lo, md, d_lo);
         if constexpr (!SPLIT) {
             if (a.pair) {
                 half_t *mt = reinterpret_cast<half_t*>(ws + p.t), *md2 = reinterpret_cast<half_t*>(ws + p.d2);
-                square(ortho_mul_kernel<B, WP, WQ, SPLIT, kMix>, md, nullptr, ma, nullptr, ma, nullptr, mt, nullptr);
-                square(ortho_mul_kernel<B, WP, WQ, SPLIT, kMixSum>, mt, nullptr, md, nullptr, mt, nullptr, ma, nullptr);
+                square(SQ::template kernel<kMix>, md, nullptr, ma, nullptr, ma, nullptr, mt, nullptr);
+                square(SQ::template kernel<kMixSum>, mt, nullptr, md, nullptr, mt, nullptr, ma, nullptr);
                 a.second = 1;
-                square(ortho_mul_kernel<B, WP, WQ, SPLIT, kPoly>, ma, nullptr, ma, nullptr, ma, nullptr, md2, nullptr);
-                square(ortho_mul_kernel<B, WP, WQ, SPLIT, kJoin>, md2, nullptr, md, nullptr, md, md2, mt, nullptr);
+                square(SQ::template kernel<kPoly>, ma, nullptr, ma, nullptr, ma, nullptr, md2, nullptr);
+                square(SQ::template kernel<kJoin>, md2, nullptr, md, nullptr, md, md2, mt, nullptr);
                 e = mt;
             }
         }
         i += a.pair ? 2 : 1;
         a.p = e;
         a.p_lo = e_lo;
-        a.q = a.in = xt[at];
-        a.q_lo = a.in_lo = lo[at];
+        a.q = xt[at];
+        a.q_lo = a.in = lo[at];
         a.p_item = sq;
         a.q_item = rect;
         a.k = p.np;
+        a.tiles_p = p.np / RE::kBP;
         a.tiles_q = tq;
-        a.per_item = p.side * tq;
+        a.per_item = (p.np / RE::kBP) * tq;
         a.out = x;
         a.out_lo = x_lo;
         at ^= 1;
         a.xt_out = xt[at];
         a.xt_lo_out = lo[at];
         const dim3 grid(uint32_t(batch) * a.per_item);
-        if (i < steps) launch(ortho_mul_kernel<B, WP, WQ, SPLIT, kApply>, grid, block, 0, st, a);
-        else launch(ortho_mul_kernel<B, WP, WQ, SPLIT, kLast>, grid, block, 0, st, a);
+        if (i < steps) launch(RE::template kernel<kApply>, grid, dim3(RE::kThreads), 0, st, a);
+        else launch(RE::template kernel<kLast>, grid, dim3(RE::kThreads), 0, st, a);
     }
 }
 
@@ -800,9 +824,12 @@ static void ortho_run(const OrthoPlan& p, OrthoIn in, const OrthoMul& mul, int64
     const uint32_t pr = p.tall ? p.mp : p.np, pc = p.tall ? p.np : p.mp;
     launch(ortho_norm_kernel, dim3(p.norm_blocks, uint32_t(batch)), dim3(256), 0, st, in);
     launch(ortho_split_kernel, dim3(pc / 64, pr / 64, uint32_t(batch)), dim3(256), 0, st, in);
-    if (p.tile == 256) ortho_steps<256, 2, 4, false>(p, mul, batch, steps, ws, st);
-    else if (p.tile == 128) ortho_steps<128, 2, 2, false>(p, mul, batch, steps, ws, st);
-    else ortho_steps<64, 2, 2, true>(p, mul, batch, steps, ws, st);
+    typedef OrthoTile<256, 256, 2, 4, 5, false> T256;
+    typedef OrthoTile<128, 128, 2, 2, 5, false> T128;
+    typedef OrthoTile<64, 64, 2, 2, 5, true> T64;
+    if (p.tile == 256) ortho_steps<T256, T256>(p, mul, batch, steps, ws, st);
+    else if (p.tile == 128) ortho_steps<T128, T128>(p, mul, batch, steps, ws, st);
+    else ortho_steps<T64, T64>(p, mul, batch, steps, ws, st);
 }
 
 // The workspace holds the plan, and no launch has 2^32 threads.
