@@ -144,11 +144,11 @@ def lib():
 # ------------------------------------------------------------------ marshalling
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _dev(t, name, dtypes=None):
-    if t is None:
+    if t is None or (type(t) is torch.Tensor and t.is_cuda and t.dtype in (dtypes or (t.dtype,)) and t.is_contiguous()):
         return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a device tensor")
@@ -172,8 +172,8 @@ def _shape3(w):
 
 def _stream(t, stream):
     if stream is None:
-        stream = torch.cuda.current_stream(t.device)
-    return ctypes.c_void_p(stream.cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return stream.cuda_stream
 
 
 def _check(fn, code):

@@ -28,8 +28,8 @@
 
 namespace e8q {
 
-constexpr int kLpBlock = 256;
-constexpr int kLpWaves = kLpBlock / kWave;
+constexpr int kLpBlock = 256;         // threads per row, or per part of a row
+constexpr int kLpWide = 1024;         // threads per row of the two-pass gradient
 constexpr int kLpUnroll = 4;          // vectors in flight per thread
 constexpr int kTopMax = 64;           // one key per lane
 constexpr int kMaxTokens = 1024;
@@ -115,14 +115,20 @@ __device__ __forceinline__ void stat_add(Stat& st, const float (&v)[N], float k)
     st.t += t0 + t1;
 }
 
+template <int MASK>
+__device__ __forceinline__ void stat_xor(Stat& st, float k) {
+    const Stat o = {lane_xor<MASK>(st.m), lane_xor<MASK>(st.s), lane_xor<MASK>(st.t)};
+    // in the order of the lanes, so that both partners get the same bits
+    st = (__lane_id() & uint32_t(MASK)) ? stat_join(o, st, k) : stat_join(st, o, k);
+}
+
 __device__ __forceinline__ Stat stat_wave(Stat st, float k) {
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) {
-        const Stat o = {__shfl_xor(st.m, off, 64), __shfl_xor(st.s, off, 64), __shfl_xor(st.t, off, 64)};
-        // in the order of the lanes, so that both partners get the same bits
-        const bool hi = (__lane_id() & uint32_t(off)) != 0u;
-        st = hi ? stat_join(o, st, k) : stat_join(st, o, k);
-    }
+    stat_xor<32>(st, k);
+    stat_xor<16>(st, k);
+    stat_xor<8>(st, k);
+    stat_xor<4>(st, k);
+    stat_xor<2>(st, k);
+    stat_xor<1>(st, k);
     return st;
 }
 
@@ -135,49 +141,81 @@ __device__ __forceinline__ uint64_t key_of(float v, uint32_t idx) {
     return (uint64_t(h) << 32) | uint32_t(~idx);
 }
 
-__device__ __forceinline__ uint64_t shfl_xor64(uint64_t v, int mask) {
-    const uint32_t lo = __shfl_xor(uint32_t(v), mask, 64), hi = __shfl_xor(uint32_t(v >> 32), mask, 64);
-    return (uint64_t(hi) << 32) | lo;
+__device__ __forceinline__ float value_of(uint64_t key) {
+    const uint32_t h = uint32_t(key >> 32);
+    return __uint_as_float(h & 0x80000000u ? h & 0x7FFFFFFFu : ~h);
 }
 
-__device__ __forceinline__ uint64_t shfl64(uint64_t v, int lane) {
-    const uint32_t lo = __shfl(uint32_t(v), lane, 64), hi = __shfl(uint32_t(v >> 32), lane, 64);
-    return (uint64_t(hi) << 32) | lo;
+// Lane l gets lane l ^ 15.
+__device__ __forceinline__ uint64_t row_mirror(uint64_t v) {
+    const int lo = __builtin_amdgcn_mov_dpp(int(uint32_t(v)), 0x140, 0xF, 0xF, true);
+    const int hi = __builtin_amdgcn_mov_dpp(int(uint32_t(v >> 32)), 0x140, 0xF, 0xF, true);
+    return (uint64_t(uint32_t(hi)) << 32) | uint32_t(lo);
 }
 
 __device__ __forceinline__ uint64_t keep(uint64_t a, uint64_t b, bool larger) { return (a > b) == larger ? a : b; }
 
+// One stage of a bitonic network: blocks of `block` lanes descend and ascend in turn.
+template <int J>
+__device__ __forceinline__ void exchange(uint64_t& v, uint32_t lane, uint32_t block) {
+    v = keep(v, lane_xor<J>(v), ((lane & uint32_t(J)) == 0u) == ((lane & block) == 0u));
+}
+
+template <int J>
+__device__ __forceinline__ void merge_stages(uint64_t& v, uint32_t lane, uint32_t block) {
+    exchange<J>(v, lane, block);
+    if constexpr (J > 1) merge_stages<J / 2>(v, lane, block);
+}
+
 // Descending over the lanes.
 __device__ __forceinline__ uint64_t sort_desc(uint64_t v, uint32_t lane) {
-#pragma unroll
-    for (uint32_t k = 2; k <= 64; k <<= 1)
-#pragma unroll
-        for (uint32_t j = k >> 1; j > 0; j >>= 1)
-            v = keep(v, shfl_xor64(v, int(j)), ((lane & j) == 0u) == ((lane & k) == 0u));
+    merge_stages<1>(v, lane, 2u);
+    merge_stages<2>(v, lane, 4u);
+    merge_stages<4>(v, lane, 8u);
+    merge_stages<8>(v, lane, 16u);
+    merge_stages<16>(v, lane, 32u);
+    merge_stages<32>(v, lane, 64u);
     return v;
 }
 
 // The 64 largest of two descending lists, descending.
 __device__ __forceinline__ uint64_t merge_desc(uint64_t a, uint64_t b, uint32_t lane) {
-    const uint64_t r = shfl64(b, int(63u - lane));
-    uint64_t v = a > r ? a : r;
-#pragma unroll
-    for (uint32_t j = 32; j > 0; j >>= 1) v = keep(v, shfl_xor64(v, int(j)), (lane & j) == 0u);
+    uint64_t v = lane_xor<32>(lane_xor<16>(row_mirror(b)));          // lane 63 - l
+    v = a > v ? a : v;
+    merge_stages<32>(v, lane, 64u);
     return v;
+}
+
+// The k-th largest of the lanes' values, by the bits of the answer from the top.
+__device__ __forceinline__ uint32_t kth_largest(uint32_t v, uint32_t k) {
+    uint32_t t = 0u;
+    for (int b = 31; b >= 0; --b) {
+        const uint32_t c = t | (1u << b);
+        if (uint32_t(__popcll(__ballot(v >= c))) >= k) t = c;
+    }
+    return t;
 }
 
 // A wave's alternatives: its 64 best keys so far, and candidates not merged yet.
 struct TopList {
     uint64_t best;        // lane's place in the descending list
-    uint64_t thr;         // k-th best key (wave-uniform)
+    uint64_t thr;         // k-th best key, at least (wave-uniform)
+    float floor;          // its value; a NaN's lets everything pass to the keys
     uint32_t count;       // candidates in LDS (wave-uniform, < 64 between vectors)
     uint64_t* buf;        // [128] of this wave
+
+    __device__ __forceinline__ void set(uint64_t key) {
+        thr = key;
+        floor = value_of(key);
+    }
 
     __device__ __forceinline__ void flush(uint32_t n, uint32_t k, uint32_t lane) {
         const uint64_t c = lane < n ? buf[lane] : 0ull;
         best = merge_desc(best, sort_desc(c, lane), lane);
-        const uint64_t kth = shfl64(best, int(k - 1));
-        thr = kth > thr ? kth : thr;
+        const uint32_t lo = uint32_t(__builtin_amdgcn_readlane(int(uint32_t(best)), int(k - 1)));
+        const uint32_t hi = uint32_t(__builtin_amdgcn_readlane(int(uint32_t(best >> 32)), int(k - 1)));
+        const uint64_t kth = (uint64_t(hi) << 32) | lo;
+        if (kth > thr) set(kth);
     }
 
     // Appends the lanes' keys above the threshold.
@@ -221,23 +259,50 @@ __device__ __forceinline__ void load_logits(const T* row, uint32_t vocab, uint32
     }
 }
 
+// The block's statistics, in every thread.  Opens with no barrier: `s` is this
+// call's own LDS.
+template <int BLOCK>
+__device__ __forceinline__ Stat stat_block(Stat st, float k2, Stat* s) {
+    st = stat_wave(st, k2);
+    if ((threadIdx.x & 63u) == 0u) s[threadIdx.x >> 6] = st;
+    __syncthreads();
+    st = s[0];
+#pragma unroll
+    for (int w = 1; w < BLOCK / kWave; ++w) st = stat_join(st, s[w], k2);
+    return st;
+}
+
+// The waves' lists (in `s`, STRIDE keys apart, and in `best`) in pairs; wave 0
+// ends with the block's.
+template <int BLOCK, int STRIDE>
+__device__ __forceinline__ void merge_block(uint64_t& best, uint64_t* s, uint32_t wave, uint32_t lane) {
+#pragma unroll
+    for (int gap = 1; gap < BLOCK / kWave; gap *= 2) {
+        if (wave % (2 * gap) == 0) {
+            best = merge_desc(best, s[(wave + gap) * STRIDE + lane], lane);
+            s[wave * STRIDE + lane] = best;
+        }
+        __syncthreads();
+    }
+}
+
 // Statistics (all waves end with the block's) and alternatives (wave 0 ends
 // with the block's) of the vectors [lo, hi) of a row.
-template <typename T, bool TOP>
+template <typename T, bool TOP, int BLOCK>
 __device__ __forceinline__ Stat row_part(const T* row, uint32_t vocab, uint32_t lo, uint32_t hi,
                                          float k2, uint32_t top_k, uint64_t& best) {
-    constexpr int VE = kVec<T>;
-    __shared__ Stat s_stat[kLpWaves];
-    __shared__ uint64_t s_keys[TOP ? kLpWaves * 128 : 1];
+    constexpr int VE = kVec<T>, kWaves = BLOCK / kWave;
+    __shared__ Stat s_stat[kWaves];
+    __shared__ uint64_t s_keys[TOP ? kWaves * 128 : 1];
     const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
     Stat st = stat_empty();
-    TopList top{0ull, 0ull, 0u, s_keys + (TOP ? wave * 128 : 0)};
+    TopList top{0ull, 0ull, -INFINITY, 0u, s_keys + (TOP ? wave * 128 : 0)};
     bool first = true;
-    for (uint32_t base = lo; base < hi; base += kLpBlock * kLpUnroll) {
+    for (uint32_t base = lo; base < hi; base += BLOCK * kLpUnroll) {
         float v[kLpUnroll * VE];
 #pragma unroll
         for (int u = 0; u < kLpUnroll; ++u) {
-            const uint32_t j = base + u * kLpBlock + tid;
+            const uint32_t j = base + u * BLOCK + tid;
             float w[VE];
             if (j < hi) {
                 load_logits<T>(row, vocab, j, w);
@@ -250,34 +315,38 @@ __device__ __forceinline__ Stat row_part(const T* row, uint32_t vocab, uint32_t 
         }
         stat_add(st, v, k2);
         if constexpr (TOP) {
+            // per vector: its largest element, and whether it holds a NaN
+            float most[kLpUnroll];
+            bool nan[kLpUnroll];
+#pragma unroll
+            for (int u = 0; u < kLpUnroll; ++u) {
+                most[u] = v[u * VE];
+                nan[u] = false;
+#pragma unroll
+                for (int i = 1; i < VE; ++i) most[u] = fmaxf(most[u], v[u * VE + i]);
+#pragma unroll
+                for (int i = 0; i < VE; i += 2) nan[u] |= __builtin_isunordered(v[u * VE + i], v[u * VE + i + 1]);
+            }
             if (first) {
-                uint64_t mine = 0ull;
+                float m = most[0];
+                bool any = nan[0];
 #pragma unroll
-                for (int u = 0; u < kLpUnroll; ++u) {
-                    const uint32_t j = base + u * kLpBlock + tid;
-#pragma unroll
-                    for (int i = 0; i < VE; ++i) {
-                        const uint64_t key = key_of(v[u * VE + i], 0xFFFFFFFFu);     // value alone
-                        if (j < hi && j * VE + i < vocab) mine = key > mine ? key : mine;
-                    }
+                for (int u = 1; u < kLpUnroll; ++u) {
+                    m = fmaxf(m, most[u]);
+                    any |= nan[u];
                 }
-                top.thr = shfl64(sort_desc(mine, lane), int(top_k - 1));
+                const uint32_t mine = any ? 0xFFFFFFFFu : uint32_t(key_of(m, 0u) >> 32);
+                top.set(uint64_t(kth_largest(mine, top_k)) << 32);
                 first = false;
             }
 #pragma unroll
             for (int u = 0; u < kLpUnroll; ++u) {
-                const uint32_t j = base + u * kLpBlock + tid;
-                uint64_t most = 0ull;
-                uint64_t key[VE];
+                if (!__ballot(nan[u] || !(most[u] < top.floor))) continue;
+                const uint32_t j = base + u * BLOCK + tid;
 #pragma unroll
                 for (int i = 0; i < VE; ++i) {
                     const uint32_t e = j * VE + i;
-                    key[i] = j < hi && e < vocab ? key_of(v[u * VE + i], e) : 0ull;
-                    most = key[i] > most ? key[i] : most;
-                }
-                if (__ballot(most > top.thr)) {
-#pragma unroll
-                    for (int i = 0; i < VE; ++i) top.offer(key[i], top_k, lane);
+                    top.offer(j < hi && e < vocab ? key_of(v[u * VE + i], e) : 0ull, top_k, lane);
                 }
             }
         }
@@ -286,20 +355,14 @@ __device__ __forceinline__ Stat row_part(const T* row, uint32_t vocab, uint32_t 
         __builtin_amdgcn_wave_barrier();
         if (top.count) top.flush(top.count, top_k, lane);
     }
-    st = stat_wave(st, k2);
-    if (lane == 0) s_stat[wave] = st;
     if constexpr (TOP) {
         __builtin_amdgcn_wave_barrier();
         top.buf[lane] = top.best;
     }
-    __syncthreads();
-    st = s_stat[0];
-#pragma unroll
-    for (int w = 1; w < kLpWaves; ++w) st = stat_join(st, s_stat[w], k2);
+    st = stat_block<BLOCK>(st, k2, s_stat);
     if constexpr (TOP) {
+        merge_block<BLOCK, 128>(top.best, s_keys, wave, lane);
         best = top.best;
-        if (wave == 0)
-            for (int w = 1; w < kLpWaves; ++w) best = merge_desc(best, s_keys[w * 128 + lane], lane);
     }
     return st;
 }
@@ -320,9 +383,27 @@ __device__ __forceinline__ float logprob_of(float x, const Stat& st, const RowEn
     return st.s == 0.0f ? -INFINITY : scale * (x - st.m) - e.ln_s;
 }
 
+// A thread's given token (the first of blockDim) and its logit, read ahead of
+// the statistics.
+struct OneToken {
+    int64_t id;
+    float x;
+};
+
+template <typename T>
+__device__ __forceinline__ OneToken first_token(const LpArgs& a, uint32_t row, const T* x) {
+    OneToken t = {-1, 0.0f};
+    if (threadIdx.x < a.ntok) {
+        t.id = token_at(a, uint64_t(row) * a.ntok + threadIdx.x);
+        if (t.id >= 0 && t.id < int64_t(a.vocab)) t.x = widen(x[t.id]);
+    }
+    return t;
+}
+
 // Outputs of one row, by one block; `best` is wave 0's list.
 template <typename T, bool TOP>
-__device__ __forceinline__ void write_row(const LpArgs& a, uint32_t row, const T* x, const Stat& st, uint64_t best) {
+__device__ __forceinline__ void write_row(const LpArgs& a, uint32_t row, const T* x, const Stat& st, uint64_t best,
+                                          OneToken tok) {
     const uint32_t tid = threadIdx.x;
     const RowEnd e = row_end(st, a.scale);
     uint32_t flags = 0u;
@@ -332,17 +413,19 @@ __device__ __forceinline__ void write_row(const LpArgs& a, uint32_t row, const T
         if (st.s != st.s) flags |= E8Q_STATUS_NONFINITE;
     }
     for (uint32_t j = tid; j < a.ntok; j += blockDim.x) {
-        const int64_t t = token_at(a, uint64_t(row) * a.ntok + j);
-        if (t >= int64_t(a.vocab)) flags |= E8Q_STATUS_BAD_INDEX;
+        if (j != tid) {
+            tok.id = token_at(a, uint64_t(row) * a.ntok + j);
+            tok.x = tok.id >= 0 && tok.id < int64_t(a.vocab) ? widen(x[tok.id]) : 0.0f;
+        }
+        if (tok.id >= int64_t(a.vocab)) flags |= E8Q_STATUS_BAD_INDEX;
         if (a.logprob)
             a.logprob[uint64_t(row) * a.ntok + j] =
-                t >= 0 && t < int64_t(a.vocab) ? logprob_of(widen(x[t]), st, e, a.scale) : 0.0f;
+                tok.id >= 0 && tok.id < int64_t(a.vocab) ? logprob_of(tok.x, st, e, a.scale) : 0.0f;
     }
     if constexpr (TOP) {
         if (tid < a.k) {
-            const uint32_t idx = ~uint32_t(best);
-            if (a.top_idx) a.top_idx[uint64_t(row) * a.k + tid] = int32_t(idx);
-            if (a.top_lp) a.top_lp[uint64_t(row) * a.k + tid] = logprob_of(widen(x[idx]), st, e, a.scale);
+            if (a.top_idx) a.top_idx[uint64_t(row) * a.k + tid] = int32_t(~uint32_t(best));
+            if (a.top_lp) a.top_lp[uint64_t(row) * a.k + tid] = logprob_of(value_of(best), st, e, a.scale);
         }
     }
     flush_status(flags, a.status);
@@ -356,9 +439,11 @@ __global__ __launch_bounds__(kLpBlock) void logprobs_kernel(LpArgs a) {
     const uint32_t nvec = (a.vocab + kVec<T> - 1) / kVec<T>;
     const uint32_t lo = min(sp * a.per_split, nvec), hi = min(lo + a.per_split, nvec);
     uint64_t best = 0ull;
-    const Stat st = row_part<T, TOP>(x, a.vocab, lo, hi, a.scale * kLog2e, a.k, best);
+    OneToken tok = {-1, 0.0f};
+    if (a.splits == 1) tok = first_token(a, row, x);
+    const Stat st = row_part<T, TOP, kLpBlock>(x, a.vocab, lo, hi, a.scale * kLog2e, a.k, best);
     if (a.splits == 1) {
-        write_row<T, TOP>(a, row, x, st, best);
+        write_row<T, TOP>(a, row, x, st, best, tok);
         return;
     }
     if (threadIdx.x == 0) a.part[blockIdx.x] = make_float4(st.m, st.s, st.t, 0.0f);
@@ -370,11 +455,12 @@ __global__ __launch_bounds__(kLpBlock) void logprobs_kernel(LpArgs a) {
 // Joins the parts of one row.
 template <typename T, bool TOP>
 __global__ __launch_bounds__(kLpBlock) void logprobs_join_kernel(LpArgs a) {
-    __shared__ Stat s_stat[kLpWaves];
-    __shared__ uint64_t s_keys[TOP ? kLpWaves * kTopMax : 1];
+    constexpr int BLOCK = kLpBlock, kWaves = BLOCK / kWave;
+    __shared__ Stat s_stat[kWaves];
+    __shared__ uint64_t s_keys[TOP ? kWaves * kTopMax : 1];
     const uint32_t row = blockIdx.x, tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
     const T* x = static_cast<const T*>(a.x) + int64_t(row) * a.stride;
-    const float k2 = a.scale * kLog2e;
+    const OneToken tok = first_token(a, row, x);
     Stat st = stat_empty();
     if (tid < a.splits) {
         const float4 p = a.part[uint64_t(row) * a.splits + tid];
@@ -383,20 +469,13 @@ __global__ __launch_bounds__(kLpBlock) void logprobs_join_kernel(LpArgs a) {
     uint64_t best = 0ull;
     if constexpr (TOP) {
         const uint64_t* keys = a.part_keys + uint64_t(row) * a.splits * kTopMax + lane;
-        for (uint32_t i = wave; i < a.splits; i += kLpWaves) best = merge_desc(best, keys[i * kTopMax], lane);
+        if (wave < a.splits) best = keys[wave * kTopMax];
+        for (uint32_t i = wave + kWaves; i < a.splits; i += kWaves) best = merge_desc(best, keys[i * kTopMax], lane);
         s_keys[tid] = best;
     }
-    st = stat_wave(st, k2);
-    if (lane == 0) s_stat[wave] = st;
-    __syncthreads();
-    st = s_stat[0];
-#pragma unroll
-    for (int w = 1; w < kLpWaves; ++w) st = stat_join(st, s_stat[w], k2);
-    if constexpr (TOP) {
-        if (wave == 0)
-            for (int w = 1; w < kLpWaves; ++w) best = merge_desc(best, s_keys[w * kTopMax + lane], lane);
-    }
-    write_row<T, TOP>(a, row, x, st, best);
+    st = stat_block<BLOCK>(st, a.scale * kLog2e, s_stat);
+    if constexpr (TOP) merge_block<BLOCK, kTopMax>(best, s_keys, wave, lane);
+    write_row<T, TOP>(a, row, x, st, best, tok);
 }
 
 // ------------------------------------------------------------ gradient
@@ -411,15 +490,21 @@ __device__ __forceinline__ float grad_at(float x, const GradRow& g) {
     return exp2_fast(d) * fmaf(g.c1, fmaxf(d, kFloor), g.c0);
 }
 
-// The row's live tokens, their logits and upstream gradients in LDS.
+// The row's live tokens, their logits and upstream gradients in (dynamic) LDS.
 struct RowTokens {
-    int32_t id[kMaxTokens];
-    float g[kMaxTokens];
-    float x[kMaxTokens];
+    int32_t* id;
+    float* g;
+    float* x;
 };
 
+__device__ __forceinline__ RowTokens row_tokens(uint32_t ntok) {
+    extern __shared__ uint32_t s_tokens[];
+    return {reinterpret_cast<int32_t*>(s_tokens), reinterpret_cast<float*>(s_tokens + ntok),
+            reinterpret_cast<float*>(s_tokens + 2u * ntok)};
+}
+
 template <typename T>
-__device__ __forceinline__ float load_tokens(const LpArgs& a, uint32_t row, const T* x, RowTokens& s) {
+__device__ __forceinline__ float load_tokens(const LpArgs& a, uint32_t row, const T* x, const RowTokens& s) {
     uint32_t flags = 0u;
     for (uint32_t j = threadIdx.x; j < a.ntok; j += blockDim.x) {
         const int64_t t = token_at(a, uint64_t(row) * a.ntok + j);
@@ -436,41 +521,52 @@ __device__ __forceinline__ float load_tokens(const LpArgs& a, uint32_t row, cons
     return sum;
 }
 
-// The vectors [lo, hi) of the gradient row, then its given tokens among them
-// (the logits of the tokens were read before the first store: dx may be x).
 template <typename T>
-__device__ __forceinline__ void grad_part(const LpArgs& a, const T* x, T* dx, uint32_t lo, uint32_t hi,
-                                          const GradRow& g, bool zero, const RowTokens& s) {
-    constexpr int VE = kVec<T>;
-    for (uint32_t j = lo + threadIdx.x; j < hi; j += blockDim.x) {
-        float v[VE], d[VE];
-        load_logits<T>(x, a.vocab, j, v);
+__device__ __forceinline__ void store_grad(T* dx, uint32_t vocab, uint32_t e0, const float (&d)[kVec<T>]) {
+    if (e0 + kVec<T> <= vocab) {
+        // past the caches: it would push the rows' logits out, which are read again
+        __builtin_nontemporal_store(pack(d), &reinterpret_cast<RowVec<T>*>(dx + e0)->v);
+    } else {
 #pragma unroll
-        for (int i = 0; i < VE; ++i) d[i] = zero ? 0.0f : grad_at(v[i], g);
-        const uint32_t e0 = j * VE;
-        if (e0 + VE <= a.vocab) {
-            reinterpret_cast<RowVec<T>*>(dx + e0)->v = pack(d);
-        } else {
-#pragma unroll
-            for (int i = 0; i < VE; ++i)
-                if (e0 + i < a.vocab) dx[e0 + i] = narrow<T>(d[i]);
-        }
+        for (int i = 0; i < kVec<T>; ++i)
+            if (e0 + i < vocab) dx[e0 + i] = narrow<T>(d[i]);
     }
-    if (!a.ntok) return;
+}
+
+// The given tokens among the elements [first, last), which this block has
+// written (the logits of the tokens were read before: dx may be x).
+template <typename T>
+__device__ __forceinline__ void grad_tokens(const LpArgs& a, T* dx, int64_t first, int64_t last, const GradRow& g,
+                                            bool zero, const RowTokens& s) {
+    if (!a.ntok || zero) return;
     __syncthreads();
-    const int64_t first = int64_t(lo) * VE, last = int64_t(hi) * VE;
     for (uint32_t j = threadIdx.x; j < a.ntok; j += blockDim.x) {
         const int32_t t = s.id[j];
-        if (t < 0 || t < first || t >= last || zero) continue;
+        if (t < 0 || t < first || t >= last) continue;
         float sum = 0.0f;                                  // equal tokens: the same sum for each
         for (uint32_t i = 0; i < a.ntok; ++i) sum += s.id[i] == t ? s.g[i] : 0.0f;
         dx[t] = narrow<T>(fmaf(a.scale, sum, grad_at(s.x[j], g)));
     }
 }
 
+// The vectors [lo, hi) of the gradient row.
+template <typename T>
+__device__ __forceinline__ void grad_part(const LpArgs& a, const T* x, T* dx, uint32_t lo, uint32_t hi,
+                                          const GradRow& g, bool zero, const RowTokens& s) {
+    constexpr int VE = kVec<T>;
+    for (uint32_t j = lo + threadIdx.x; j < hi; j += blockDim.x) {
+        float v[VE];
+        load_logits<T>(x, a.vocab, j, v);
+#pragma unroll
+        for (int i = 0; i < VE; ++i) v[i] = zero ? 0.0f : grad_at(v[i], g);
+        store_grad<T>(dx, a.vocab, j * VE, v);
+    }
+    grad_tokens<T>(a, dx, int64_t(lo) * VE, int64_t(hi) * VE, g, zero, s);
+}
+
 template <typename T>
 __global__ __launch_bounds__(kLpBlock) void logprobs_backward_kernel(LpArgs a) {
-    __shared__ RowTokens s_tok;
+    const RowTokens s_tok = row_tokens(a.ntok);
     const uint32_t row = a.splits == 1 ? blockIdx.x : blockIdx.x / a.splits;
     const uint32_t sp = blockIdx.x - row * a.splits;
     const T* x = static_cast<const T*>(a.x) + int64_t(row) * a.stride;
@@ -484,31 +580,97 @@ __global__ __launch_bounds__(kLpBlock) void logprobs_backward_kernel(LpArgs a) {
     grad_part<T>(a, x, dx, lo, hi, g, lse == -INFINITY, s_tok);
 }
 
-// Statistics and gradient of a whole row by one block (the second reading of
-// the row is served by the caches).
+// The gradient's constants from the row's statistics.
+__device__ __forceinline__ GradRow grad_row(const LpArgs& a, const Stat& st, float sum, float gh) {
+    const RowEnd e = row_end(st, a.scale);
+    const float c = a.scale / st.s;
+    return {1.0f, st.m, a.scale * kLog2e, -c * (sum + gh * (e.ent - e.ln_s)), -c * gh * kLn2};
+}
+
+// Statistics and gradient of a row that fits the registers of one block, NV
+// vectors a thread: the row is read once.
+template <typename T, int BLOCK, int NV>
+__global__ __launch_bounds__(BLOCK) void logprobs_grad_kernel(LpArgs a) {
+    constexpr int VE = kVec<T>, kGroup = 2;      // vectors unpacked at a time
+    __shared__ Stat s_stat[BLOCK / kWave];
+    const RowTokens s_tok = row_tokens(a.ntok);
+    const uint32_t row = blockIdx.x;
+    const T* x = static_cast<const T*>(a.x) + int64_t(row) * a.stride;
+    T* dx = static_cast<T*>(a.dx) + int64_t(row) * a.dx_stride;
+    const uint32_t nvec = (a.vocab + VE - 1) / VE;
+    const uint32_t wave0 = uint32_t(__builtin_amdgcn_readfirstlane(int(threadIdx.x & ~63u)));
+    u32x4_t raw[NV];
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+        const uint32_t e0 = (n * BLOCK + threadIdx.x) * VE;
+        if (e0 + VE <= a.vocab) {
+            raw[n] = reinterpret_cast<const RowVec<T>*>(x + e0)->v;
+        } else {
+            float v[VE];
+#pragma unroll
+            for (int i = 0; i < VE; ++i) v[i] = e0 + i < a.vocab ? widen(x[e0 + i]) : -INFINITY;
+            raw[n] = pack(v);
+        }
+    }
+    const float sum = load_tokens<T>(a, row, x, s_tok);
+    const float k2 = a.scale * kLog2e;
+    Stat st = stat_empty();
+#pragma unroll
+    for (int n = 0; n < NV; n += kGroup) {
+        if (uint32_t(n * BLOCK) + wave0 >= nvec) break;        // nothing of the row for this wave any more
+        float v[kGroup * VE];
+#pragma unroll
+        for (int u = 0; u < kGroup; ++u) {
+            float w[VE];
+            unpack(raw[n + u], w);
+#pragma unroll
+            for (int i = 0; i < VE; ++i) v[u * VE + i] = w[i];
+        }
+        stat_add(st, v, k2);
+        __builtin_amdgcn_sched_barrier(0);       // one group unpacked at a time
+    }
+    st = stat_block<BLOCK>(st, k2, s_stat);
+    write_row<T, false>(a, row, x, st, 0ull, first_token(a, row, x));
+    __syncthreads();                 // the tokens' logits are read before dx (maybe x) is written
+    const GradRow g = grad_row(a, st, sum, a.g_ent ? a.g_ent[row] : 0.0f);
+    const bool zero = st.s == 0.0f;
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+        if (uint32_t(n * BLOCK) + wave0 >= nvec) break;
+        const uint32_t e0 = (n * BLOCK + threadIdx.x) * VE;
+        float v[VE];
+        unpack(raw[n], v);
+#pragma unroll
+        for (int i = 0; i < VE; ++i) v[i] = zero ? 0.0f : grad_at(v[i], g);
+        store_grad<T>(dx, a.vocab, e0, v);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    grad_tokens<T>(a, dx, 0, int64_t(a.vocab), g, zero, s_tok);
+}
+
+// The same for longer rows: two passes over the row.
 template <typename T>
-__global__ __launch_bounds__(kLpBlock) void logprobs_grad_kernel(LpArgs a) {
-    __shared__ RowTokens s_tok;
+__global__ __launch_bounds__(kLpWide) void logprobs_grad_long_kernel(LpArgs a) {
+    const RowTokens s_tok = row_tokens(a.ntok);
     const uint32_t row = blockIdx.x;
     const T* x = static_cast<const T*>(a.x) + int64_t(row) * a.stride;
     T* dx = static_cast<T*>(a.dx) + int64_t(row) * a.dx_stride;
     const uint32_t nvec = (a.vocab + kVec<T> - 1) / kVec<T>;
     const float sum = load_tokens<T>(a, row, x, s_tok);
     uint64_t none = 0ull;
-    const Stat st = row_part<T, false>(x, a.vocab, 0u, nvec, a.scale * kLog2e, 0u, none);
-    write_row<T, false>(a, row, x, st, 0ull);
+    const Stat st = row_part<T, false, kLpWide>(x, a.vocab, 0u, nvec, a.scale * kLog2e, 0u, none);
+    write_row<T, false>(a, row, x, st, 0ull, first_token(a, row, x));
     __syncthreads();                 // the tokens' logits are read before dx (maybe x) is written
-    const RowEnd e = row_end(st, a.scale);
-    const float inv = 1.0f / st.s, gh = a.g_ent ? a.g_ent[row] : 0.0f;
-    const float c = a.scale * inv;
-    const GradRow g = {1.0f, st.m, a.scale * kLog2e, -c * (sum + gh * (e.ent - e.ln_s)), -c * gh * kLn2};
+    const GradRow g = grad_row(a, st, sum, a.g_ent ? a.g_ent[row] : 0.0f);
     grad_part<T>(a, x, dx, 0u, nvec, g, st.s == 0.0f, s_tok);
 }
 
 // ------------------------------------------------------------ host
 
-// Blocks per row: enough blocks for every CU to hold several, each with at
-// least `kLpBlock * kLpUnroll` vectors to read.
+// Blocks per row: enough blocks for every CU to hold about four, each with
+// kLpUnroll vectors a thread to read (one row of 131072 bf16 logits with 8
+// alternatives: 14.4 us with 16 parts, 14.7 with 32, 16.4 with 32 joined by 1024
+// threads).
 static uint32_t lp_splits(int64_t rows, int64_t vocab, size_t esz, uint32_t& per_split) {
     const uint64_t ve = 16 / esz, nvec = (uint64_t(vocab) + ve - 1) / ve;
     const uint64_t want = (uint64_t(device_cu_count()) * 4 + uint64_t(rows) - 1) / uint64_t(rows);
@@ -569,13 +731,35 @@ static void lp_forward(LpArgs& a, void* ws, hipStream_t st) {
     a.part = static_cast<float4*>(ws);
     a.part_keys = reinterpret_cast<uint64_t*>(static_cast<char*>(ws) + lp_part_bytes(uint64_t(a.rows) * a.splits));
     launch(logprobs_kernel<T, TOP>, dim3(a.rows * a.splits), dim3(kLpBlock), 0, st, a);
-    if (a.splits > 1) launch(logprobs_join_kernel<T, TOP>, dim3(a.rows), dim3(kLpBlock), 0, st, a);
+    if (a.splits == 1) return;
+    launch(logprobs_join_kernel<T, TOP>, dim3(a.rows), dim3(kLpBlock), 0, st, a);
 }
 
 template <typename T>
 static void lp_backward(LpArgs& a, hipStream_t st) {
     a.splits = lp_splits(a.rows, a.vocab, sizeof(T), a.per_split);
-    launch(logprobs_backward_kernel<T>, dim3(a.rows * a.splits), dim3(kLpBlock), 0, st, a);
+    launch(logprobs_backward_kernel<T>, dim3(a.rows * a.splits), dim3(kLpBlock), a.ntok * 12u, st, a);
+}
+
+// Whole rows: the smallest block whose registers hold one, while that leaves
+// several rows to a CU.  Longer rows are read twice by blocks of kLpWide threads,
+// two to a CU: their rows (512 at a time, 128 MiB at 131072 bf16 logits) stay in
+// the last-level cache until the second reading.  Measured, 2^28 logits, bytes
+// read and written once: bf16 2048 wide 5.0 TB/s, 16384 5.4, 32768 4.7, 65536
+// 4.2 (3.9 in the registers of 512 threads), 131072 4.4; float32 8192 wide 5.4,
+// 32768 5.4 (4.7 read twice), 131072 4.3.  A copy reaches 4.9.
+template <typename T>
+static void lp_grad(LpArgs& a, hipStream_t st) {
+    a.splits = 1;
+    const uint32_t nvec = (a.vocab + kVec<T> - 1) / kVec<T>;
+    auto go = [&](auto kernel, unsigned block) { launch(kernel, dim3(a.rows), dim3(block), a.ntok * 12u, st, a); };
+    if (nvec <= 64 * 4) go(logprobs_grad_kernel<T, 64, 4>, 64);
+    else if (nvec <= 128 * 4) go(logprobs_grad_kernel<T, 128, 4>, 128);
+    else if (nvec <= 256 * 4) go(logprobs_grad_kernel<T, 256, 4>, 256);
+    else if (nvec <= 256 * 8) go(logprobs_grad_kernel<T, 256, 8>, 256);
+    else if (nvec <= 256 * 16) go(logprobs_grad_kernel<T, 256, 16>, 256);
+    else if (sizeof(T) == 4 && nvec <= 512 * 16) go(logprobs_grad_kernel<T, 512, 16>, 512);
+    else go(logprobs_grad_long_kernel<T>, kLpWide);
 }
 
 }  // namespace e8q
@@ -684,9 +868,8 @@ extern "C" e8q_status_t e8q_token_logprobs_grad(const void* logits, e8q_dtype_t 
     a.dx_stride = grad_stride;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     if (!need) {
-        a.splits = 1;
-        if (dtype == E8Q_BF16) launch(logprobs_grad_kernel<uint16_t>, dim3(a.rows), dim3(kLpBlock), 0, s, a);
-        else launch(logprobs_grad_kernel<float>, dim3(a.rows), dim3(kLpBlock), 0, s, a);
+        if (dtype == E8Q_BF16) lp_grad<uint16_t>(a, s);
+        else lp_grad<float>(a, s);
         return launch_status();
     }
     // few rows: the two split passes, with the rows' statistics in the workspace where no output takes them

@@ -55,4 +55,36 @@ __device__ __forceinline__ u32x4_t pack(const float (&v)[8]) {
     return r;
 }
 
+// Value of the lane whose number differs by the bits of MASK (a power of two),
+// by register moves between lanes (no LDS).
+template <int MASK>
+__device__ __forceinline__ uint32_t lane_xor(uint32_t v) {
+    if constexpr (MASK == 1) return uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0xB1, 0xF, 0xF, true));        // quad 1 0 3 2
+    else if constexpr (MASK == 2) return uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0x4E, 0xF, 0xF, true));   // quad 2 3 0 1
+    else if constexpr (MASK == 4) {                                                // mirror of 8 (^ 7), quad 3 2 1 0 (^ 3)
+        const int m = __builtin_amdgcn_mov_dpp(int(v), 0x141, 0xF, 0xF, true);
+        return uint32_t(__builtin_amdgcn_mov_dpp(m, 0x1B, 0xF, 0xF, true));
+    } else if constexpr (MASK == 8) {
+        return uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0x128, 0xF, 0xF, true));  // rotate 16 by 8
+    } else if constexpr (MASK == 16) {
+        // rows 1 and 3 of the first result, 0 and 2 of the second come from their partner
+        const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        return (__lane_id() & 16u) ? r[0] : r[1];
+    } else {
+        static_assert(MASK == 32, "a power of two below 64");
+        const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        return (__lane_id() & 32u) ? r[0] : r[1];
+    }
+}
+
+template <int MASK>
+__device__ __forceinline__ float lane_xor(float v) {
+    return __uint_as_float(lane_xor<MASK>(__float_as_uint(v)));
+}
+
+template <int MASK>
+__device__ __forceinline__ uint64_t lane_xor(uint64_t v) {
+    return (uint64_t(lane_xor<MASK>(uint32_t(v >> 32))) << 32) | lane_xor<MASK>(uint32_t(v));
+}
+
 }  // namespace e8q
