@@ -32,14 +32,14 @@
 // 65504 and typical entries well above float16's smallest normal number.
 //
 // Layout.  Every product is C[p][q] = sum_k P[p][k] Q[q][k] with k contiguous
-// in both operands: A = (X, X), A^2 = (A, A) (symmetric), D X = (D, X^T).  So
-// X is kept as X [n, m] and X^T [m, n]; the last product writes both.  Sides
-// are padded with zeros to whole tiles, which every step maps to zeros.  The
+// in both operands: A = (X, X), A^2 = (A, A), M A = (M, A) (all symmetric).  Only
+// M X = (M, X^T) has its second operand the other way round: its fragments are
+// read out of X's rows by LDS reads that turn them, so X is kept (and moved)
+// once, as [n, m].  Sides are padded with zeros to whole tiles, which every step maps to zeros.  The
 // two symmetric products compute the tiles on and below the diagonal and write
 // each twice.
 #include <algorithm>
 #include <cmath>
-#include <type_traits>
 
 #include "e8q_device.hpp"
 #include "e8q_host.hpp"
@@ -67,12 +67,9 @@ struct OrthoIn {
     uint64_t cells;            // per matrix
     uint32_t rows, cols;
     uint32_t np, mp;
-    int tall;
     int s;                     // X is scaled by 2^s
     half_t* x;                 // [batch, np, mp]
-    half_t* xt;                // [batch, mp, np]
-    half_t* xt_lo;
-    half_t* x_lo;              // or null
+    half_t* x_lo;
     double* norm;              // [batch, norm_blocks]
     uint32_t norm_blocks;
     uint32_t* status;
@@ -139,11 +136,12 @@ __global__ __launch_bounds__(256) void ortho_norm_kernel(OrthoIn a) {
         a.norm[uint64_t(blockIdx.y) * a.norm_blocks + blockIdx.x] = (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
 }
 
-// X = U / |U| as float16 parts in both layouts, by tiles of 64 x 64 of U's own
-// layout; cells outside U are zeros.
+// X = U / |U| (of U^T for a tall U) as float16 parts, by tiles of 64 x 64 of U's
+// own layout; cells outside U are zeros.
+template <bool TALL>
 __global__ __launch_bounds__(256) void ortho_split_kernel(OrthoIn a) {
-    __shared__ half_t s_hi[64][72];
-    __shared__ half_t s_lo[64][72];
+    __shared__ half_t s_hi[TALL ? 64 : 1][72];
+    __shared__ half_t s_lo[TALL ? 64 : 1][72];
     __shared__ double s_scale;
     const uint32_t tid = threadIdx.x, item = blockIdx.z;
     if (tid < 64u) {
@@ -160,10 +158,7 @@ __global__ __launch_bounds__(256) void ortho_split_kernel(OrthoIn a) {
     __syncthreads();
     const double scale = s_scale;
     const uint32_t r0 = blockIdx.y * 64u, c0 = blockIdx.x * 64u;
-    const uint32_t prows = a.tall ? a.mp : a.np, pcols = a.tall ? a.np : a.mp;    // padded sides of U
     const uint64_t item_g = uint64_t(item) * a.cells, item_x = uint64_t(item) * a.np * a.mp;
-    half_t* same_hi = (a.tall ? a.xt : a.x) + item_x;
-    half_t* turn_hi = (a.tall ? a.x : a.xt) + item_x;
     const uint32_t c = (tid & 7u) * 8u;
 #pragma unroll
     for (uint32_t it = 0; it < 2; ++it) {
@@ -181,37 +176,50 @@ __global__ __launch_bounds__(256) void ortho_split_kernel(OrthoIn a) {
                 lo[j] = half_t(x - float(hi[j]));
             }
         }
-        *reinterpret_cast<half8_t*>(&s_hi[r][c]) = hi;
-        *reinterpret_cast<half8_t*>(&s_lo[r][c]) = lo;
-        const uint64_t at = uint64_t(r0 + r) * pcols + c0 + c;
-        *reinterpret_cast<half8_t*>(same_hi + at) = hi;
-        half_t* same_lo = a.tall ? a.xt_lo : a.x_lo;
-        if (same_lo) *reinterpret_cast<half8_t*>(same_lo + item_x + at) = lo;
-    }
-    __syncthreads();
-#pragma unroll
-    for (uint32_t it = 0; it < 2; ++it) {
-        const uint32_t r = (tid >> 3) + it * 32u;        // row of the turned tile
-        half8_t hi, lo;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            hi[j] = s_hi[c + j][r];
-            lo[j] = s_lo[c + j][r];
+        if constexpr (TALL) {
+            *reinterpret_cast<half8_t*>(&s_hi[r][c]) = hi;
+            *reinterpret_cast<half8_t*>(&s_lo[r][c]) = lo;
+        } else {
+            const uint64_t at = item_x + uint64_t(r0 + r) * a.mp + c0 + c;
+            *reinterpret_cast<half8_t*>(a.x + at) = hi;
+            *reinterpret_cast<half8_t*>(a.x_lo + at) = lo;
         }
-        const uint64_t at = uint64_t(c0 + r) * prows + r0 + c;
-        *reinterpret_cast<half8_t*>(turn_hi + at) = hi;
-        half_t* turn_lo = a.tall ? a.x_lo : a.xt_lo;
-        if (turn_lo) *reinterpret_cast<half8_t*>(turn_lo + item_x + at) = lo;
+    }
+    if constexpr (TALL) {
+        __syncthreads();
+#pragma unroll
+        for (uint32_t it = 0; it < 2; ++it) {
+            const uint32_t r = (tid >> 3) + it * 32u;        // row of the turned tile
+            half8_t hi, lo;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                hi[j] = s_hi[c + j][r];
+                lo[j] = s_lo[c + j][r];
+            }
+            const uint64_t at = item_x + uint64_t(c0 + r) * a.mp + r0 + c;
+            *reinterpret_cast<half8_t*>(a.x + at) = hi;
+            *reinterpret_cast<half8_t*>(a.x_lo + at) = lo;
+        }
     }
 }
 
 // ------------------------------------------------------------ products
 
+// The 4 x 4 halves of four neighbouring lanes (two words each), turned: lane e
+// gets half e of every lane, in the order of the lanes.
+__device__ __forceinline__ uint2 quad_turn(uint2 v) {
+    const uint32_t lane = __lane_id(), sel = lane & 1u ? 0x03020706u : 0x05040100u;
+    const uint32_t a = __builtin_amdgcn_perm(lane_xor<1>(v.x), v.x, sel);
+    const uint32_t b = __builtin_amdgcn_perm(lane_xor<1>(v.y), v.y, sel);
+    const uint32_t got = lane_xor<2>(lane & 2u ? a : b);
+    return lane & 2u ? make_uint2(got, b) : make_uint2(a, got);
+}
+
 // What a launch computes from C = P Q^T; the symmetric ones on the lower
 // triangle's tiles.
 //   kGram     A  = X X^T                                (P = Q = X)
 //   kPoly     M  = a I + b A + c A^2, or D = M - alpha I for a pair   (P = Q = A)
-//   kApply    X <- E X_hi + gain X_lo                   (P = E, Q = X^T; E = M or a pair's)
+//   kApply    X <- E X_hi + gain X_lo                   (P = E, Q = X turned; E = M or a pair's)
 //   kLast     the same, as the result or the latents' step
 // and for two steps at once
 //   kMix      T  = alpha A + D A = M A                  (P = D, Q = A)
@@ -221,7 +229,7 @@ enum { kGram, kPoly, kMix, kMixSum, kJoin, kApply, kLast };
 
 struct OrthoMul {
     const half_t* p;           // [batch, np, k]
-    const half_t* q;           // [batch, (np or mp), k]
+    const half_t* q;           // [batch, np, k]; kApply, kLast: X [batch, k = np, mp]
     const half_t* p_lo;        // low parts (SPLIT)
     const half_t* q_lo;
     uint64_t p_item, q_item;   // elements per matrix
@@ -232,8 +240,8 @@ struct OrthoMul {
     float ca, cb, cc;
     int s;
     half_t* out;               // kGram: A; kPoly: D; kApply: X [np, mp]
-    half_t* out_lo;            // its low part (SPLIT)
-    const half_t* in;          // added to C (kPoly: A, kMix: A, kMixSum: T, kJoin: D; kApply, kLast: low part of X^T)
+    half_t* out_lo;            // its low part (kApply, SPLIT); kApply: may be in, where that is no operand
+    const half_t* in;          // added to C (kPoly: A, kMix: A, kMixSum: T, kJoin: D; kApply, kLast: X's low part)
     const half_t* in_lo;       // its low part (SPLIT); kJoin: D'
     float* sums;               // [batch, per-item tiles of the triangle, 2]: tr A, |A|^2 of a tile
     uint32_t sum_tiles;
@@ -241,8 +249,6 @@ struct OrthoMul {
     uint32_t batch;
     int second;                // kPoly: the pair's second step
     int pair;                  // two steps at once
-    half_t* xt_out;            // kApply: X^T
-    half_t* xt_lo_out;         // may be in (without SPLIT, where it is no operand)
     // kLast
     uint32_t rows, cols;
     int tall;
@@ -263,6 +269,14 @@ __device__ __forceinline__ void load_lds16(const half_t* base, uint32_t offset, 
 
 __device__ __forceinline__ uint32_t lds_address(const half_t* p) {
     return uint32_t(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) half_t*)p));
+}
+
+// Lane (t, c) of 16 reads 4 halves and lane (c, e) gets element e of the 4 that
+// lanes (0, c) .. (3, c) read.
+__device__ __forceinline__ half4_t read_turned(const half_t* p) {
+    typedef short short4_t __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) short4_t lds_short4;
+    return __builtin_bit_cast(half4_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4*)p));
 }
 
 // All but this wave's last N loads to LDS have landed, and its LDS reads have
@@ -307,7 +321,8 @@ __device__ __forceinline__ uint32_t xcd_order(uint32_t b, uint32_t total) {
 
 // A tile of BP x BQ by WP x WQ waves, RING stages in LDS.
 template <int BP, int BQ, int WP, int WQ, int RING, bool SPLIT, int MODE>
-__global__ __launch_bounds__(WP* WQ * 64, 2) void ortho_mul_kernel(OrthoMul a) {
+__global__ __launch_bounds__(WP* WQ * 64, WP* WQ >= 4 ? 2 : 1) void ortho_mul_kernel(OrthoMul a) {
+    constexpr bool kSquare = MODE != kApply && MODE != kLast;
     constexpr int kWaves = WP * WQ, FP = BP / WP / 16, FQ = BQ / WQ / 16;
     constexpr int kLoadsP = BP / 16 / kWaves, kLoadsQ = BQ / 16 / kWaves;    // wave loads per stage
     constexpr int kParts = SPLIT ? 2 : 1;
@@ -318,7 +333,6 @@ __global__ __launch_bounds__(WP* WQ * 64, 2) void ortho_mul_kernel(OrthoMul a) {
     const uint32_t tile = xcd_order(blockIdx.x, gridDim.x);
     const uint32_t item = tile / a.per_item, t = tile - item * a.per_item;
     uint32_t ti, tj;
-    constexpr bool kSquare = MODE != kApply && MODE != kLast;
     if constexpr (kSquare) {
         tri_tile(t, a.tiles_p, ti, tj);
     } else {
@@ -342,7 +356,15 @@ __global__ __launch_bounds__(WP* WQ * 64, 2) void ortho_mul_kernel(OrthoMul a) {
     const uint32_t lrow = lane >> 2;                 // a wave load fills 16 rows of 64 bytes
     auto place = [](uint32_t r) { return (0u - (r >> 2)) & 3u; };
     const uint64_t op = uint64_t(item) * a.p_item + uint64_t(ti * BP) * a.k;
-    const uint64_t oq = uint64_t(item) * a.q_item + uint64_t(tj * BQ) * a.k;
+    const uint64_t oq = uint64_t(item) * a.q_item + (kSquare ? uint64_t(tj * BQ) * a.k : uint64_t(tj * BQ));
+    // The products with X take Q's fragments out of rows of X by LDS reads that
+    // turn 4 x 4 blocks (read_turned).  Fragment j's column c = (c', e) is column
+    // 32 (c' / 2) + 8 j + 4 (c' % 2) + e of the wave's, so that after a turn among
+    // four lanes each holds 4 neighbours; turn() spreads the 8 rows and 4 places
+    // that 32 lanes read over all banks.
+    auto turn = [](uint32_t r) {
+        return BQ >= 128 ? (r & 3u) | (r & 8u) : ((r >> 1) & 1u) | ((r >> 2) & 2u);
+    };
     const uint32_t chunk = ((lane & 3u) ^ place(lrow)) * 8u;
     uint32_t off_p[kLoadsP], off_q[kLoadsQ];
 #pragma unroll
@@ -352,8 +374,14 @@ __global__ __launch_bounds__(WP* WQ * 64, 2) void ortho_mul_kernel(OrthoMul a) {
     }
 #pragma unroll
     for (int i = 0; i < kLoadsQ; ++i) {
-        const uint32_t r = (wave * kLoadsQ + i) * 16u + lrow;
-        off_q[i] = ((r / (FQ * 16) * (FQ * 16) + (r & 15u) * FQ + (r >> 4) % FQ) * a.k + chunk) * 2u;
+        if constexpr (kSquare) {
+            const uint32_t r = (wave * kLoadsQ + i) * 16u + lrow;
+            off_q[i] = ((r / (FQ * 16) * (FQ * 16) + (r & 15u) * FQ + (r >> 4) % FQ) * a.k + chunk) * 2u;
+        } else {
+            // rows of X are Q's columns: whole rows of BQ elements, chunk c at c ^ turn(row)
+            const uint32_t r = (wave * kLoadsQ + i) * (512 / BQ) + lane / (BQ / 8);
+            off_q[i] = (r * a.mp + ((lane % (BQ / 8)) ^ turn(r)) * 8u) * 2u;
+        }
     }
     const uint32_t lds = lds_address(s_op);
     const uint32_t to_p = lds + wave * (kLoadsP * 16 * kBK * 2);
@@ -366,7 +394,7 @@ __global__ __launch_bounds__(WP* WQ * 64, 2) void ortho_mul_kernel(OrthoMul a) {
             load_lds16((h ? a.p_lo : a.p) + op + k, off_p[i],
                        to_p + slot * (kSlot * 2) + h * (BP * kBK * 2) + i * (16 * kBK * 2));
         else
-            load_lds16((h ? a.q_lo : a.q) + oq + k, off_q[i - kLoadsP],
+            load_lds16((h ? a.q_lo : a.q) + oq + (kSquare ? uint64_t(k) : uint64_t(k) * a.mp), off_q[i - kLoadsP],
                        to_q + slot * (kSlot * 2) + h * (BQ * kBK * 2) + (i - kLoadsP) * (16 * kBK * 2));
     };
     const uint32_t wp = wave / WQ, wq = wave - wp * WQ;
@@ -378,13 +406,28 @@ __global__ __launch_bounds__(WP* WQ * 64, 2) void ortho_mul_kernel(OrthoMul a) {
     constexpr int kReads = (FP + FQ) * kParts;
     const uint32_t at_p = (wp * FP * 16 + frow) * kBK + (fk ^ place(frow)) * 8;
     const uint32_t at_q = (wq * FQ * 16 + frow) * kBK + (fk ^ place(frow)) * 8;
+    // (products with X) this lane's part of the rows for fragment j
+    uint32_t turn_q[FQ];
+    if constexpr (!kSquare) {
+#pragma unroll
+        for (int j = 0; j < FQ; ++j) {
+            const uint32_t r = fk * 8u + (frow >> 2), c = frow & 3u;
+            turn_q[j] = r * BQ + ((wq * (FQ * 2) + (c >> 1) * 4u + j) ^ turn(r)) * 8u + (c & 1u) * 4u;
+        }
+    }
     auto read = [&](Frags& f, uint32_t slot, int r) {
         const int h = r % kParts, n = r / kParts;
         const half_t* at = s_op + slot * kSlot;
-        if (n < FQ)
-            f.q[h][n] = *reinterpret_cast<const half8_t*>(at + (kParts * BP + h * BQ + n * 16) * kBK + at_q);
-        else
+        if (n < FQ) {
+            if constexpr (kSquare) {
+                f.q[h][n] = *reinterpret_cast<const half8_t*>(at + (kParts * BP + h * BQ + n * 16) * kBK + at_q);
+            } else {
+                const half_t* q = at + (kParts * BP + h * BQ) * kBK + turn_q[n];
+                f.q[h][n] = __builtin_shufflevector(read_turned(q), read_turned(q + 4 * BQ), 0, 1, 2, 3, 4, 5, 6, 7);
+            }
+        } else {
             f.p[h][n - FQ] = *reinterpret_cast<const half8_t*>(at + (h * BP + (n - FQ) * 16) * kBK + at_p);
+        }
     };
     f32x4_t acc[FP][FQ] = {};
     auto multiply_row = [&](const Frags& f, int i) {
@@ -494,7 +537,6 @@ __global__ __launch_bounds__(WP* WQ * 64, 2) void ortho_mul_kernel(OrthoMul a) {
         by_c = ldexpf(1.0f, a.pair ? -kScaleE : -kScaleD);
         by_hi = SPLIT ? 0.0f : a.pair ? *alpha1 * *alpha2 : *alpha1;
     }
-    constexpr bool kUseHi = MODE != kGram && !(SPLIT && !kSquare);    // with SPLIT the product has X_lo
     constexpr bool kUseLo = MODE == kJoin || (MODE == kPoly && SPLIT);
     constexpr bool kSums = MODE == kGram || MODE == kMixSum;
 
@@ -502,100 +544,142 @@ __global__ __launch_bounds__(WP* WQ * 64, 2) void ortho_mul_kernel(OrthoMul a) {
     const uint64_t item_out = uint64_t(item) * a.np * (kSquare ? a.np : a.mp);
     float tr = 0.0f, sq = 0.0f;
     auto value = [&](int u, int j, int e) { return acc[2 * u + e / 4][j][e % 4]; };
-    half8_t in_hi[2][FQ], in_lo[2][FQ];       // what the results are added to, one pair of fragments ahead
-    auto fetch = [&](int u) {
-        const uint32_t p0 = pw + u * 32u + fk * 8u;
-#pragma unroll
-        for (int j = 0; j < FQ; ++j) {
-            const uint64_t at = item_out + uint64_t(qw + frow * FQ + j) * a.np + p0;
-            in_hi[u & 1][j] = *reinterpret_cast<const half8_t*>(a.in + at);
-            if constexpr (kUseLo) in_lo[u & 1][j] = *reinterpret_cast<const half8_t*>(a.in_lo + at);
-        }
-    };
-    if constexpr (kUseHi) fetch(0);
-#pragma unroll
-    for (int u = 0; u < FP / 2; ++u) {
-        const uint32_t p0 = pw + u * 32u + fk * 8u;
-        if constexpr (kUseHi) {
-            if (u + 1 < FP / 2) fetch(u + 1);
-        }
-        half8_t h[FQ], l[FQ];
-        float v[FQ][8];
-#pragma unroll
-        for (int j = 0; j < FQ; ++j) {
-            const uint32_t q = qw + frow * FQ + j;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float r = by_c * value(u, j, e);
-                if constexpr (kUseHi) r = fmaf(by_hi, float(in_hi[u & 1][j][e]), r);
-                if constexpr (kUseLo) r = fmaf(by_lo, float(in_lo[u & 1][j][e]), r);
-                if constexpr (MODE == kPoly || MODE == kJoin) r += p0 + e == q ? on_diagonal : 0.0f;
-                if constexpr (kSums) {
-                    sq = fmaf(r, r, sq);
-                    tr += p0 + e == q ? r : 0.0f;
-                }
-                v[j][e] = r;
-                h[j][e] = half_t(r);
-                l[j][e] = half_t(r - float(h[j][e]));
-            }
-        }
-        if constexpr (MODE == kLast) {
-            // whole vectors of the result's rows lie inside or outside it: its columns are a multiple of 8
-            auto put = [&](uint64_t o, const float* x, int stride, auto count) {
-                constexpr int N = decltype(count)::value;
-                uint32_t out[(N + 1) / 2];
-#pragma unroll
-                for (int e = 0; e < N; e += 2) {
-                    float r0 = x[e * stride] * back, r1 = x[(e + 1) * stride] * back;
-                    if (!a.update) {
-                        const uint32_t w2 = *reinterpret_cast<const uint32_t*>(a.w + o + e);
-                        r0 = fmaf(-a.step, r0, __uint_as_float(w2 << 16) * a.keep);
-                        r1 = fmaf(-a.step, r1, __uint_as_float(w2 & 0xFFFF0000u) * a.keep);
-                    }
-                    out[e / 2] = cvt_bf16x2(r0, r1);
-                }
-                uint16_t* to = (a.update ? a.update : a.w_out) + o;
-                struct alignas(2 * N) Out { uint32_t w[N / 2]; };
-                *reinterpret_cast<Out*>(to) = *reinterpret_cast<const Out*>(out);
-            };
-            if (a.tall) {
-#pragma unroll
-                for (int j = 0; j < FQ; ++j) {
-                    const uint32_t q = qw + frow * FQ + j;
-                    if (q < a.rows && p0 < a.cols)
-                        put((uint64_t(item) * a.rows + q) * a.cols + p0, &v[j][0], 1, std::integral_constant<int, 8>{});
-                }
-            } else {
-                const uint32_t q = qw + frow * FQ;
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (p0 + e < a.rows && q < a.cols)
-                        put((uint64_t(item) * a.rows + p0 + e) * a.cols + q, &v[0][e], 8, std::integral_constant<int, FQ>{});
-            }
-        } else {
-            // rows of Q: the mirrored tile, or X^T
-            half_t *turned = MODE == kApply ? a.xt_out : a.out, *turned_lo = MODE == kApply ? a.xt_lo_out : a.out_lo;
+    if constexpr (kSquare) {
+        half8_t in_hi[2][FQ], in_lo[2][FQ];       // what the results are added to, one pair of fragments ahead
+        auto fetch = [&](int u) {
+            const uint32_t p0 = pw + u * 32u + fk * 8u;
 #pragma unroll
             for (int j = 0; j < FQ; ++j) {
                 const uint64_t at = item_out + uint64_t(qw + frow * FQ + j) * a.np + p0;
-                *reinterpret_cast<half8_t*>(turned + at) = h[j];
-                if constexpr (MODE == kApply || SPLIT) *reinterpret_cast<half8_t*>(turned_lo + at) = l[j];
+                in_hi[u & 1][j] = *reinterpret_cast<const half8_t*>(a.in + at);
+                if constexpr (kUseLo) in_lo[u & 1][j] = *reinterpret_cast<const half8_t*>(a.in_lo + at);
             }
-            // rows of P
-            if (MODE == kApply || ti != tj) {
-                typedef _Float16 row_t __attribute__((ext_vector_type(FQ)));
-                const uint32_t width = MODE == kApply ? a.mp : a.np;
+        };
+        if constexpr (MODE != kGram) fetch(0);
+#pragma unroll
+        for (int u = 0; u < FP / 2; ++u) {
+            const uint32_t p0 = pw + u * 32u + fk * 8u;
+            if constexpr (MODE != kGram) {
+                if (u + 1 < FP / 2) fetch(u + 1);
+            }
+            half8_t h[FQ], l[FQ];
+#pragma unroll
+            for (int j = 0; j < FQ; ++j) {
+                const uint32_t q = qw + frow * FQ + j;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    row_t rh, rl;
+                    float r = by_c * value(u, j, e);
+                    if constexpr (MODE != kGram) r = fmaf(by_hi, float(in_hi[u & 1][j][e]), r);
+                    if constexpr (kUseLo) r = fmaf(by_lo, float(in_lo[u & 1][j][e]), r);
+                    if constexpr (MODE == kPoly || MODE == kJoin) r += p0 + e == q ? on_diagonal : 0.0f;
+                    if constexpr (kSums) {
+                        sq = fmaf(r, r, sq);
+                        tr += p0 + e == q ? r : 0.0f;
+                    }
+                    h[j][e] = half_t(r);
+                    l[j][e] = half_t(r - float(h[j][e]));
+                }
+                // rows of Q: the mirrored tile
+                const uint64_t at = item_out + uint64_t(q) * a.np + p0;
+                *reinterpret_cast<half8_t*>(a.out + at) = h[j];
+                if constexpr (SPLIT) *reinterpret_cast<half8_t*>(a.out_lo + at) = l[j];
+            }
+            if (ti == tj) continue;
+            typedef _Float16 row_t __attribute__((ext_vector_type(FQ)));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                row_t rh, rl;
+#pragma unroll
+                for (int j = 0; j < FQ; ++j) {
+                    rh[j] = h[j][e];
+                    rl[j] = l[j][e];
+                }
+                const uint64_t at = item_out + uint64_t(p0 + e) * a.np + qw + frow * FQ;
+                *reinterpret_cast<row_t*>(a.out + at) = rh;
+                if constexpr (SPLIT) *reinterpret_cast<row_t*>(a.out_lo + at) = rl;
+            }
+        }
+    } else {
+        static_assert(FQ == 4, "columns turned four by four");
+        // after a turn: columns m0 .. m0 + 3; before: column mj + 8 j in slot j
+        const uint32_t quad = qw + (frow >> 3) * 32u + ((frow >> 2) & 1u) * 4u;
+        const uint32_t m0 = quad + (frow & 3u) * 8u, mj = quad + (frow & 3u);
+        uint2 in[2][8];                           // X's low part, one pair of fragments ahead
+        auto fetch = [&](int u) {
+            const uint64_t at = item_out + uint64_t(pw + u * 32u + fk * 8u) * a.mp + m0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) in[u & 1][e] = *reinterpret_cast<const uint2*>(a.in + at + uint64_t(e) * a.mp);
+        };
+        constexpr bool kAddLow = !SPLIT;          // with SPLIT the product has it
+        if constexpr (kAddLow) fetch(0);
+#pragma unroll
+        for (int u = 0; u < FP / 2; ++u) {
+            const uint32_t p0 = pw + u * 32u + fk * 8u;
+            if constexpr (kAddLow) {
+                if (u + 1 < FP / 2) fetch(u + 1);
+            }
+            float v[FQ][8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                half4_t low = {};
+                if constexpr (kAddLow) low = __builtin_bit_cast(half4_t, quad_turn(in[u & 1][e]));
+#pragma unroll
+                for (int j = 0; j < FQ; ++j) {
+                    float r = by_c * value(u, j, e);
+                    if constexpr (kAddLow) r = fmaf(by_hi, float(low[j]), r);
+                    v[j][e] = r;
+                }
+            }
+            if constexpr (MODE == kApply) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    half4_t h, l;
 #pragma unroll
                     for (int j = 0; j < FQ; ++j) {
-                        rh[j] = h[j][e];
-                        rl[j] = l[j][e];
+                        h[j] = half_t(v[j][e]);
+                        l[j] = half_t(v[j][e] - float(h[j]));
                     }
-                    const uint64_t at = item_out + uint64_t(p0 + e) * width + qw + frow * FQ;
-                    *reinterpret_cast<row_t*>(a.out + at) = rh;
-                    if constexpr (SPLIT) *reinterpret_cast<row_t*>(a.out_lo + at) = rl;
+                    const uint64_t at = item_out + uint64_t(p0 + e) * a.mp + m0;
+                    *reinterpret_cast<uint2*>(a.out + at) = quad_turn(__builtin_bit_cast(uint2, h));
+                    *reinterpret_cast<uint2*>(a.out_lo + at) = quad_turn(__builtin_bit_cast(uint2, l));
+                }
+            } else if (a.tall) {
+                // whole vectors of the result's rows lie inside or outside it: its columns are a multiple of 8
+#pragma unroll
+                for (int j = 0; j < FQ; ++j) {
+                    const uint32_t q = mj + 8u * j;
+                    if (q >= a.rows || p0 >= a.cols) continue;
+                    const uint64_t o = (uint64_t(item) * a.rows + q) * a.cols + p0;
+                    float r[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) r[e] = v[j][e] * back;
+                    if (!a.update) {
+                        float w[8];
+                        unpack(*reinterpret_cast<const u32x4_t*>(a.w + o), w);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) r[e] = fmaf(-a.step, r[e], w[e] * a.keep);
+                    }
+                    *reinterpret_cast<u32x4_t*>((a.update ? a.update : a.w_out) + o) = pack(r);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const bool in_range = p0 + e < a.rows && m0 < a.cols;
+                    const uint64_t o = (uint64_t(item) * a.rows + p0 + e) * a.cols + m0;
+                    float r[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) r[j] = v[j][e] * back;
+                    if (!a.update) {
+                        uint2 w = make_uint2(0u, 0u);
+                        if (in_range) w = *reinterpret_cast<const uint2*>(a.w + o);
+                        w = quad_turn(w);
+                        r[0] = fmaf(-a.step, r[0], __uint_as_float(w.x << 16) * a.keep);
+                        r[1] = fmaf(-a.step, r[1], __uint_as_float(w.x & 0xFFFF0000u) * a.keep);
+                        r[2] = fmaf(-a.step, r[2], __uint_as_float(w.y << 16) * a.keep);
+                        r[3] = fmaf(-a.step, r[3], __uint_as_float(w.y & 0xFFFF0000u) * a.keep);
+                    }
+                    const uint2 b = quad_turn(make_uint2(cvt_bf16x2(r[0], r[1]), cvt_bf16x2(r[2], r[3])));
+                    if (in_range) *reinterpret_cast<uint2*>((a.update ? a.update : a.w_out) + o) = b;
                 }
             }
         }
@@ -635,8 +719,8 @@ struct OrthoPlan {
     uint32_t n, m, np, mp, tile, side;     // side: tiles along n
     uint32_t norm_blocks;
     int tall, s;
-    size_t x, xt0, xt1, lo, a, d, sums, alpha, norm, total;
-    size_t x_lo, lo1, a_lo, d_lo;           // 64-wide tiles only
+    size_t x0, x1, lo, a, d, sums, alpha, norm, total;
+    size_t lo1, a_lo, d_lo;                 // 64-wide tiles only
     int pair;                               // two steps at once
     size_t t, d2;
 };
@@ -659,9 +743,8 @@ static OrthoPlan ortho_plan(int64_t batch, int64_t rows, int64_t cols) {
     const size_t rect = size_t(batch) * p.np * p.mp * 2, sq = size_t(batch) * p.np * p.np * 2;
     size_t at = 0;
     auto take = [&](size_t bytes) { const size_t o = at; at += ortho_align(bytes); return o; };
-    p.x = take(rect);
-    p.xt0 = take(rect);
-    p.xt1 = take(rect);
+    p.x0 = take(rect);
+    p.x1 = take(rect);
     p.lo = take(rect);
     p.a = take(sq);
     p.d = take(sq);
@@ -678,7 +761,6 @@ static OrthoPlan ortho_plan(int64_t batch, int64_t rows, int64_t cols) {
         p.d2 = take(sq);
     }
     if (p.tile == 64) {
-        p.x_lo = take(rect);
         p.lo1 = take(rect);
         p.a_lo = take(sq);
         p.d_lo = take(sq);
@@ -733,12 +815,10 @@ struct OrthoTile {
 template <class SQ, class RE>
 static void ortho_steps(const OrthoPlan& p, OrthoMul a, int64_t batch, int32_t steps, char* ws, hipStream_t st) {
     constexpr bool SPLIT = SQ::kSplit;
-    half_t* x = reinterpret_cast<half_t*>(ws + p.x);
+    half_t* x[2] = {reinterpret_cast<half_t*>(ws + p.x0), reinterpret_cast<half_t*>(ws + p.x1)};
     half_t* lo[2] = {reinterpret_cast<half_t*>(ws + p.lo), reinterpret_cast<half_t*>(ws + (SPLIT ? p.lo1 : p.lo))};
-    half_t* x_lo = SPLIT ? reinterpret_cast<half_t*>(ws + p.x_lo) : nullptr;
     half_t* a_lo = SPLIT ? reinterpret_cast<half_t*>(ws + p.a_lo) : nullptr;
     half_t* d_lo = SPLIT ? reinterpret_cast<half_t*>(ws + p.d_lo) : nullptr;
-    half_t* xt[2] = {reinterpret_cast<half_t*>(ws + p.xt0), reinterpret_cast<half_t*>(ws + p.xt1)};
     half_t *ma = reinterpret_cast<half_t*>(ws + p.a), *md = reinterpret_cast<half_t*>(ws + p.d);
     const uint32_t tri = p.side * (p.side + 1) / 2, tq = p.mp / RE::kBQ;
     const uint64_t rect = uint64_t(p.np) * p.mp, sq = uint64_t(p.np) * p.np;
@@ -756,8 +836,8 @@ static void ortho_steps(const OrthoPlan& p, OrthoMul a, int64_t batch, int32_t s
         a.p_lo = pp_lo;
         a.q = qq;
         a.q_lo = qq_lo;
-        a.p_item = a.q_item = pp == x ? rect : sq;
-        a.k = pp == x ? p.mp : p.np;
+        a.p_item = a.q_item = in ? sq : rect;
+        a.k = in ? p.np : p.mp;
         a.in = in;
         a.in_lo = in_lo;
         a.out = out;
@@ -766,12 +846,12 @@ static void ortho_steps(const OrthoPlan& p, OrthoMul a, int64_t batch, int32_t s
         a.per_item = tri;
         launch(kernel, dim3(uint32_t(batch) * tri), dim3(SQ::kThreads), 0, st, a);
     };
-    int at = 0;                              // which of xt, lo holds X^T
+    int at = 0;                              // which of x, lo holds X
     for (int32_t i = 0; i < steps;) {
         a.second = 0;
         a.pair = p.pair && i + 1 < steps;
         const half_t *e = md, *e_lo = d_lo;
-        square(SQ::template kernel<kGram>, x, x_lo, x, x_lo, nullptr, nullptr, ma, a_lo);
+        square(SQ::template kernel<kGram>, x[at], lo[at], x[at], lo[at], nullptr, nullptr, ma, a_lo);
         square(SQ::template kernel<kPoly>, ma, a_lo, ma, a_lo, ma, a_lo, md, d_lo);
         if constexpr (!SPLIT) {
             if (a.pair) {
@@ -787,7 +867,7 @@ static void ortho_steps(const OrthoPlan& p, OrthoMul a, int64_t batch, int32_t s
         i += a.pair ? 2 : 1;
         a.p = e;
         a.p_lo = e_lo;
-        a.q = xt[at];
+        a.q = x[at];
         a.q_lo = a.in = lo[at];
         a.p_item = sq;
         a.q_item = rect;
@@ -795,11 +875,9 @@ static void ortho_steps(const OrthoPlan& p, OrthoMul a, int64_t batch, int32_t s
         a.tiles_p = p.np / RE::kBP;
         a.tiles_q = tq;
         a.per_item = (p.np / RE::kBP) * tq;
-        a.out = x;
-        a.out_lo = x_lo;
         at ^= 1;
-        a.xt_out = xt[at];
-        a.xt_lo_out = lo[at];
+        a.out = x[at];
+        a.out_lo = lo[at];
         const dim3 grid(uint32_t(batch) * a.per_item);
         if (i < steps) launch(RE::template kernel<kApply>, grid, dim3(RE::kThreads), 0, st, a);
         else launch(RE::template kernel<kLast>, grid, dim3(RE::kThreads), 0, st, a);
@@ -813,20 +891,19 @@ static void ortho_run(const OrthoPlan& p, OrthoIn in, const OrthoMul& mul, int64
     in.cols = uint32_t(cols);
     in.np = p.np;
     in.mp = p.mp;
-    in.tall = p.tall;
     in.s = p.s;
-    in.x = reinterpret_cast<half_t*>(ws + p.x);
-    in.xt = reinterpret_cast<half_t*>(ws + p.xt0);
-    in.xt_lo = reinterpret_cast<half_t*>(ws + p.lo);
-    in.x_lo = p.tile == 64 ? reinterpret_cast<half_t*>(ws + p.x_lo) : nullptr;
+    in.x = reinterpret_cast<half_t*>(ws + p.x0);
+    in.x_lo = reinterpret_cast<half_t*>(ws + p.lo);
     in.norm_blocks = p.norm_blocks;
     in.norm = reinterpret_cast<double*>(ws + p.norm);
     const uint32_t pr = p.tall ? p.mp : p.np, pc = p.tall ? p.np : p.mp;
     launch(ortho_norm_kernel, dim3(p.norm_blocks, uint32_t(batch)), dim3(256), 0, st, in);
-    launch(ortho_split_kernel, dim3(pc / 64, pr / 64, uint32_t(batch)), dim3(256), 0, st, in);
+    const dim3 split(pc / 64, pr / 64, uint32_t(batch));
+    if (p.tall) launch(ortho_split_kernel<true>, split, dim3(256), 0, st, in);
+    else launch(ortho_split_kernel<false>, split, dim3(256), 0, st, in);
     typedef OrthoTile<256, 256, 2, 4, 5, false> T256;
     typedef OrthoTile<128, 128, 2, 2, 5, false> T128;
-    typedef OrthoTile<64, 64, 2, 2, 5, true> T64;
+    typedef OrthoTile<64, 64, 2, 1, 3, true> T64;
     if (p.tile == 256) ortho_steps<T256, T256>(p, mul, batch, steps, ws, st);
     else if (p.tile == 128) ortho_steps<T128, T128>(p, mul, batch, steps, ws, st);
     else ortho_steps<T64, T64>(p, mul, batch, steps, ws, st);
