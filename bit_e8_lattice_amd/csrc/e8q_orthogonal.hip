@@ -716,7 +716,8 @@ __global__ __launch_bounds__(WP* WQ * 64, WP* WQ >= 4 ? 2 : 1) void ortho_mul_ke
 // ------------------------------------------------------------ host
 
 struct OrthoPlan {
-    uint32_t n, m, np, mp, tile, side;     // side: tiles along n
+    uint32_t n, m, np, mp;
+    uint32_t square, rect, side;           // tiles of the square products and of those with X; square tiles along n
     uint32_t norm_blocks;
     int tall, s;
     size_t x0, x1, lo, a, d, sums, alpha, norm, total;
@@ -727,17 +728,33 @@ struct OrthoPlan {
 
 static size_t ortho_align(size_t v) { return (v + 255) / 256 * 256; }
 
+// 256-wide tiles, one a CU, or 128-wide ones, two a CU: whichever takes fewer
+// rounds, a round of 128-wide tiles (half the work) counting 0.66, or 0.33 if
+// there is at most one to a CU.  Five steps, square / rectangular products by
+// 256 / 256, 128 / 256 and 128 / 128: 4096 x 4096 1.48, 1.68, 1.78 ms; 2048 x 8192
+// 1.16, 0.65, 0.68 ms; 16 x 768 x 2048 0.70, 0.60, 0.58 ms; 1024 x 4096 0.66, 0.34,
+// 0.30 ms (64 / 64 with low parts 0.48 ms).
+static uint32_t ortho_tile(uint64_t of256, uint64_t of128, uint64_t cus) {
+    const double wide = double((of256 + cus - 1) / cus);
+    const double small = of128 <= cus ? 0.33 : 0.66 * double((of128 + 2 * cus - 1) / (2 * cus));
+    return wide <= small ? 256u : 128u;
+}
+
 static OrthoPlan ortho_plan(int64_t batch, int64_t rows, int64_t cols) {
     OrthoPlan p{};
     p.tall = rows > cols;
     p.n = uint32_t(p.tall ? cols : rows);
     p.m = uint32_t(p.tall ? rows : cols);
-    auto tiles = [&](uint32_t t) { return uint64_t(batch) * ((p.n + t - 1) / t) * ((p.m + t - 1) / t); };
     const uint64_t cus = uint64_t(device_cu_count());
-    p.tile = tiles(256) * 4 >= cus * 3 ? 256u : tiles(128) >= cus ? 128u : 64u;
-    p.np = (p.n + p.tile - 1) / p.tile * p.tile;
-    p.mp = (p.m + p.tile - 1) / p.tile * p.tile;
-    p.side = p.np / p.tile;
+    auto along = [](uint32_t v, uint32_t tile) { return uint64_t((v + tile - 1) / tile); };
+    auto squares = [&](uint32_t tile) { const uint64_t s = along(p.n, tile); return batch * (s * (s + 1) / 2); };
+    auto rects = [&](uint32_t tile) { return batch * along(p.n, tile) * along(p.m, tile); };
+    p.rect = rects(128) < cus ? 64u : ortho_tile(rects(256), rects(128), cus);
+    p.square = p.rect < 256u ? p.rect : ortho_tile(squares(256), squares(128), cus);
+    const uint32_t pad = std::max(p.square, p.rect);
+    p.np = (p.n + pad - 1) / pad * pad;
+    p.mp = (p.m + pad - 1) / pad * pad;
+    p.side = p.np / p.square;
     p.s = int(std::floor(0.5 * std::log2(double(p.n) * double(p.m))));
     if (p.s > 15) p.s = 15;
     const size_t rect = size_t(batch) * p.np * p.mp * 2, sq = size_t(batch) * p.np * p.np * 2;
@@ -755,12 +772,12 @@ static OrthoPlan ortho_plan(int64_t batch, int64_t rows, int64_t cols) {
     const uint64_t want = (cells + 8191) / 8192;
     p.norm_blocks = uint32_t(std::min<uint64_t>(std::min<uint64_t>(want, most), kNormBlocks));
     p.norm = take(size_t(batch) * p.norm_blocks * 8);
-    p.pair = p.tile != 64 && uint64_t(p.m) * 5 >= uint64_t(p.n) * 6;
+    p.pair = p.rect != 64 && uint64_t(p.m) * 5 >= uint64_t(p.n) * 6;
     if (p.pair) {
         p.t = take(sq);
         p.d2 = take(sq);
     }
-    if (p.tile == 64) {
+    if (p.rect == 64) {
         p.lo1 = take(rect);
         p.a_lo = take(sq);
         p.d_lo = take(sq);
@@ -904,14 +921,16 @@ static void ortho_run(const OrthoPlan& p, OrthoIn in, const OrthoMul& mul, int64
     typedef OrthoTile<256, 256, 2, 4, 5, false> T256;
     typedef OrthoTile<128, 128, 2, 2, 5, false> T128;
     typedef OrthoTile<64, 64, 2, 1, 3, true> T64;
-    if (p.tile == 256) ortho_steps<T256, T256>(p, mul, batch, steps, ws, st);
-    else if (p.tile == 128) ortho_steps<T128, T128>(p, mul, batch, steps, ws, st);
-    else ortho_steps<T64, T64>(p, mul, batch, steps, ws, st);
+    if (p.rect == 64) ortho_steps<T64, T64>(p, mul, batch, steps, ws, st);
+    else if (p.rect == 128) ortho_steps<T128, T128>(p, mul, batch, steps, ws, st);
+    else if (p.square == 128) ortho_steps<T128, T256>(p, mul, batch, steps, ws, st);
+    else ortho_steps<T256, T256>(p, mul, batch, steps, ws, st);
 }
 
 // The workspace holds the plan, and no launch has 2^32 threads.
 static e8q_status_t ortho_fits(const OrthoPlan& p, int64_t batch, const void* ws, size_t bytes) {
-    if (double(batch) * p.side * (p.mp / p.tile) >= double(1 << 22)) return E8Q_ERR_UNSUPPORTED;
+    const double tiles = std::max(double(p.side) * (p.side + 1) / 2, double(p.np / p.rect) * (p.mp / p.rect));
+    if (double(batch) * tiles >= double(1 << 22)) return E8Q_ERR_UNSUPPORTED;
     return ws && bytes >= p.total && reinterpret_cast<uintptr_t>(ws) % 256 == 0 ? E8Q_OK : E8Q_ERR_INVALID;
 }
 
