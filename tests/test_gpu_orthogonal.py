@@ -90,6 +90,22 @@ def test_large_tiles(shape):
         _near([got[i].double().cpu().numpy()], [y.cpu().numpy()])
 
 
+def test_long_matrix_with_small_square_tiles():
+    """One side much longer: the square products take smaller tiles than those with X."""
+    test_large_tiles((1, 1537, 6144))
+
+
+def test_nonfinite_and_zero_matrices_in_large_batches():
+    for shape in ((40, 136, 264), (20, 769, 1280)):
+        x = _gradient((1,) + shape[1:], 6, "flat").expand(shape).contiguous().to(device())
+        x[1] = 0
+        x[2, 100, 4] = float("-inf")
+        got, st = _run(x)
+        assert st == e8q.STATUS_BITS["NONFINITE"]
+        assert not got[1].any() and torch.isnan(got[2]).all()
+        assert torch.equal(got[3], got[0]) and torch.equal(got[-1], got[0]) and torch.isfinite(got[0]).all()
+
+
 @pytest.mark.parametrize("steps,coeffs", [(1, e8q.NEWTON_SCHULZ), (2, e8q.NEWTON_SCHULZ), (9, (1.5, -0.5, 0.0)),
                                           (4, (1.875, -1.25, 0.375))])
 def test_steps_and_coefficients(steps, coeffs):
