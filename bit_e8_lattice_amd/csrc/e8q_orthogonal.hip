@@ -555,6 +555,13 @@ __global__ __launch_bounds__(WP* WQ * 64, WP* WQ >= 4 ? 2 : 1) void ortho_mul_ke
                 if constexpr (kUseLo) in_lo[u & 1][j] = *reinterpret_cast<const half8_t*>(a.in_lo + at);
             }
         };
+        // The mirrored tile goes through LDS (a part of its own for each wave, rows of
+        // Q, chunk c of row r at c ^ (r / FQ)) to memory in rows of FP * 32 bytes:
+        // stored from the registers, 64 bytes of a row at a time, it took three times
+        // as long as the tile itself.
+        constexpr uint32_t kChunks = FP * 2;
+        half_t* mirror = s_op + wave * (kParts * FQ * 16 * FP * 16);
+        block_barrier();                          // the operands are no longer read
         if constexpr (MODE != kGram) fetch(0);
 #pragma unroll
         for (int u = 0; u < FP / 2; ++u) {
@@ -579,12 +586,10 @@ __global__ __launch_bounds__(WP* WQ * 64, WP* WQ >= 4 ? 2 : 1) void ortho_mul_ke
                     h[j][e] = half_t(r);
                     l[j][e] = half_t(r - float(h[j][e]));
                 }
-                // rows of Q: the mirrored tile
-                const uint64_t at = item_out + uint64_t(q) * a.np + p0;
-                *reinterpret_cast<half8_t*>(a.out + at) = h[j];
-                if constexpr (SPLIT) *reinterpret_cast<half8_t*>(a.out_lo + at) = l[j];
+                half_t* at = mirror + (frow * FQ + j) * (FP * 16) + ((u * 4u + fk) ^ (frow & (kChunks - 1u))) * 8u;
+                *reinterpret_cast<half8_t*>(at) = h[j];
+                if constexpr (SPLIT) *reinterpret_cast<half8_t*>(at + FQ * 16 * FP * 16) = l[j];
             }
-            if (ti == tj) continue;
             typedef _Float16 row_t __attribute__((ext_vector_type(FQ)));
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -597,6 +602,19 @@ __global__ __launch_bounds__(WP* WQ * 64, WP* WQ >= 4 ? 2 : 1) void ortho_mul_ke
                 const uint64_t at = item_out + uint64_t(p0 + e) * a.np + qw + frow * FQ;
                 *reinterpret_cast<row_t*>(a.out + at) = rh;
                 if constexpr (SPLIT) *reinterpret_cast<row_t*>(a.out_lo + at) = rl;
+            }
+        }
+        if (ti != tj) {
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+            for (int n = 0; n < FP * FQ / 2; ++n) {
+                const uint32_t r = n * (64u / kChunks) + lane / kChunks, c = lane % kChunks;
+                const half_t* from = mirror + r * (FP * 16) + (c ^ ((r / FQ) & (kChunks - 1u))) * 8u;
+                const uint64_t at = item_out + uint64_t(qw + r) * a.np + pw + c * 8u;
+                *reinterpret_cast<half8_t*>(a.out + at) = *reinterpret_cast<const half8_t*>(from);
+                if constexpr (SPLIT)
+                    *reinterpret_cast<half8_t*>(a.out_lo + at) =
+                        *reinterpret_cast<const half8_t*>(from + FQ * 16 * FP * 16);
             }
         }
     } else {
@@ -729,14 +747,14 @@ struct OrthoPlan {
 static size_t ortho_align(size_t v) { return (v + 255) / 256 * 256; }
 
 // 256-wide tiles, one a CU, or 128-wide ones, two a CU: whichever takes fewer
-// rounds, a round of 128-wide tiles (half the work) counting 0.66, or 0.33 if
+// rounds, a round of 128-wide tiles (half the work) counting 0.75, or 0.33 if
 // there is at most one to a CU.  Five steps, square / rectangular products by
 // 256 / 256, 128 / 256 and 128 / 128: 4096 x 4096 1.48, 1.68, 1.78 ms; 2048 x 8192
 // 1.16, 0.65, 0.68 ms; 16 x 768 x 2048 0.70, 0.60, 0.58 ms; 1024 x 4096 0.66, 0.34,
 // 0.30 ms (64 / 64 with low parts 0.48 ms).
 static uint32_t ortho_tile(uint64_t of256, uint64_t of128, uint64_t cus) {
     const double wide = double((of256 + cus - 1) / cus);
-    const double small = of128 <= cus ? 0.33 : 0.66 * double((of128 + 2 * cus - 1) / (2 * cus));
+    const double small = of128 <= cus ? 0.33 : 0.75 * double((of128 + 2 * cus - 1) / (2 * cus));
     return wide <= small ? 256u : 128u;
 }
 
