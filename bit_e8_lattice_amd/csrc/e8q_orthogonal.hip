@@ -286,10 +286,18 @@ __device__ __forceinline__ void wait_loads() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
 }
 
+// Waits for no memory operation of its own: after wait_loads() only.
 __device__ __forceinline__ void block_barrier() {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
+}
+
+// A barrier where LDS is about to be used for something else: what this wave read
+// and wrote there is done (the writes too: a diagonal tile never reads its mirror).
+__device__ __forceinline__ void reuse_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    block_barrier();
 }
 
 // Tile t of the lower triangle of side x side tiles: four rows of tiles at a
@@ -561,7 +569,7 @@ __global__ __launch_bounds__(WP* WQ * 64, WP* WQ >= 4 ? 2 : 1) void ortho_mul_ke
         // as long as the tile itself.
         constexpr uint32_t kChunks = FP * 2;
         half_t* mirror = s_op + wave * (kParts * FQ * 16 * FP * 16);
-        block_barrier();                          // the operands are no longer read
+        reuse_barrier();                          // operands and (kPoly) sums are no longer read
         if constexpr (MODE != kGram) fetch(0);
 #pragma unroll
         for (int u = 0; u < FP / 2; ++u) {
@@ -703,7 +711,7 @@ __global__ __launch_bounds__(WP* WQ * 64, WP* WQ >= 4 ? 2 : 1) void ortho_mul_ke
         }
     }
     if constexpr (kSums) {
-        block_barrier();
+        reuse_barrier();
         float* s_sum = reinterpret_cast<float*>(s_op);
         tr *= 0x1p-14f;
         sq *= ti != tj ? 0x1p-27f : 0x1p-28f;              // an entry off the diagonal stands for two

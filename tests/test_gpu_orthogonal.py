@@ -95,6 +95,14 @@ def test_long_matrix_with_small_square_tiles():
     test_large_tiles((1, 1537, 6144))
 
 
+@pytest.mark.parametrize("shape", [(20, 769, 1280), (2, 1025, 1032), (5, 200, 328)])
+def test_runs_agree_bit_for_bit(shape):
+    x = _gradient(shape, 5, "fall").to(torch.bfloat16).to(device())
+    first, _ = _run(x)
+    for _ in range(10):
+        assert torch.equal(_run(x)[0], first)
+
+
 def test_nonfinite_and_zero_matrices_in_large_batches():
     for shape in ((40, 136, 264), (20, 769, 1280)):
         x = _gradient((1,) + shape[1:], 6, "flat").expand(shape).contiguous().to(device())
