@@ -11,9 +11,9 @@
 // kept to 22 bits, X_hi + X_lo, and the new X is M X_hi + alpha X_lo, alpha the
 // mean of the diagonal of M = aI + bA + cA^2 (M X_lo would differ from it by far
 // less than a rounding of M X_hi).  The rounding of M acts on the strong
-// directions' columns alone.  Measured against float64, of |O|_F: 0.8e-3 to
-// 1.7e-3 for flat, falling and low-rank spectra, 3.3e-3 for a random matrix of
-// rank 16.  Problems too small to fill the chip (64-wide tiles) wait for memory
+// directions' columns alone.  Measured against float64, of |O|_F, for flat, falling
+// and low-rank (an eighth) spectra at 20 x 769 x 1280: 1.1e-3, 1.1e-3 and 1.4e-3;
+// with two steps at once (below) 1.1e-3, 2.9e-3 and 3.5e-3.  Problems too small to fill the chip (64-wide tiles) wait for memory
 // and launches, not for the matrix cores: there every operand has its low part
 // and a product is three (hi hi, hi lo, lo hi), which leaves the rounding of the
 // result.
@@ -21,23 +21,33 @@
 // Two steps at once.  Where m is well above n, two steps take one A = X X^T and
 // one product with X instead of two each: with M, M' the two steps' polynomials
 // of A, A' = M A M and M' M are n x n and symmetric (all commute):
-//   T = M A,  A' = T M,  X <- M' M X,
+//   T = A M,  A' = M T,  X <- M' M X,
 // three symmetric products of n^3 for 3 n^2 m saved.  These products are made of
 // D = M - alpha I, the rest added in float32: a diagonal rounded with the rest
 // would cost half as much again in accuracy.  More than two steps would lose
 // more (A' holds the squares of the singular values).
 //
 // Ranges.  X is stored times 2^s, s = floor(log2(sqrt(n m))) <= 15, A and T times
-// 2^14, D times 2^12, E times 2^9: the entries' bounds (singular values <= 1.5) stay below
-// 65504 and typical entries well above float16's smallest normal number.
+// 2^14, M and D times 2^12, E times 2^9: the entries' bounds (singular values
+// <= 1.5, |M| <= 7) stay below 65504 and typical entries well above float16's
+// smallest normal number.
 //
 // Layout.  Every product is C[p][q] = sum_k P[p][k] Q[q][k] with k contiguous
 // in both operands: A = (X, X), A^2 = (A, A), M A = (M, A) (all symmetric).  Only
 // M X = (M, X^T) has its second operand the other way round: its fragments are
 // read out of X's rows by LDS reads that turn them, so X is kept (and moved)
-// once, as [n, m].  Sides are padded with zeros to whole tiles, which every step maps to zeros.  The
-// two symmetric products compute the tiles on and below the diagonal and write
-// each twice.
+// once, as [n, m].  Sides are padded with zeros to whole tiles, which every step
+// maps to zeros.  The symmetric products compute the tiles on and below the
+// diagonal and write each twice.
+//
+// What bounds it.  The inner loop of a 256 x 256 tile keeps the matrix cores 85%
+// busy; random operands then run the chip into its power limit (about 1.85
+// PFLOP/s of bare products, 1.3 for the library's float16 product of 8192^3).  At
+// 4096 x 14336 the product with X (481 GFLOP) takes 440 us, X X^T (half a product)
+// 290 us and a square product 86 us: its 136 tiles leave 120 of 256 CUs idle, and
+// 528 tiles of 128 are as many rounds.  At 128 x 768 x 2048 a tile's sum is 24
+// stages long and the moving of X (2 + 2 + 2 bytes an entry of a product) counts
+// as much: 490 us for 309 GFLOP.
 #include <algorithm>
 #include <cmath>
 
@@ -105,7 +115,8 @@ __device__ __forceinline__ void load_f8(const float* p, float (&v)[8]) {
     for (int j = 0; j < 4; ++j) v[4 + j] = w[j];
 }
 
-// New momentum, and partial sums of |U|^2 (float64: any magnitude of G).
+// New momentum, and partial sums of |U|^2 (float64: any magnitude of G).  A
+// stream: 95 us for the momentum of 4096 x 14336 (6.2 TB/s).
 __global__ __launch_bounds__(256) void ortho_norm_kernel(OrthoIn a) {
     __shared__ double s_sum[4];
     const uint64_t base = uint64_t(blockIdx.y) * a.cells;
@@ -137,7 +148,8 @@ __global__ __launch_bounds__(256) void ortho_norm_kernel(OrthoIn a) {
 }
 
 // X = U / |U| (of U^T for a tall U) as float16 parts, by tiles of 64 x 64 of U's
-// own layout; cells outside U are zeros.
+// own layout; cells outside U are zeros.  A stream: 226 us for 128 x 768 x 2048 in
+// bf16 (5.3 TB/s).
 template <bool TALL>
 __global__ __launch_bounds__(256) void ortho_split_kernel(OrthoIn a) {
     __shared__ half_t s_hi[TALL ? 64 : 1][72];
@@ -222,8 +234,8 @@ __device__ __forceinline__ uint2 quad_turn(uint2 v) {
 //   kApply    X <- E X_hi + gain X_lo                   (P = E, Q = X turned; E = M or a pair's)
 //   kLast     the same, as the result or the latents' step
 // and for two steps at once
-//   kMix      T  = alpha A + D A = M A                  (P = D, Q = A)
-//   kMixSum   A' = alpha T + T D = M A M                (P = T, Q = D)
+//   kMix      T  = alpha A + A D = A M                  (P = A, Q = D)
+//   kMixSum   A' = alpha T + D T = M A M                (P = D, Q = T)
 //   kJoin     E  = M' M = alpha alpha' I + alpha' D + alpha D' + D' D   (P = D', Q = D)
 enum { kGram, kPoly, kMix, kMixSum, kJoin, kApply, kLast };
 
@@ -624,6 +636,30 @@ __global__ __launch_bounds__(WP* WQ * 64, WP* WQ >= 4 ? 2 : 1) void ortho_mul_ke
                     *reinterpret_cast<half8_t*>(a.out_lo + at) =
                         *reinterpret_cast<const half8_t*>(from + FQ * 16 * FP * 16);
             }
+        } else if constexpr (MODE == kMix || MODE == kMixSum) {
+            // Rounded factors commute only nearly, so these two products are not
+            // symmetric by themselves, as X X^T and A^2 are, and what reads them takes
+            // rows for columns: left so inside the diagonal tiles they gave errors of
+            // 4.5e-3 to 5.6e-3.  The entries above the diagonal are overwritten with those below.
+            static_assert(BP == BQ && !SPLIT, "square tiles");
+            wait_loads<0>();                      // this wave's stores too
+            block_barrier();
+            constexpr uint32_t kRowChunks = BP / 8;
+            for (uint32_t i = tid; i < BQ * kRowChunks; i += kWaves * 64u) {
+                const uint32_t q = i / kRowChunks, p = i % kRowChunks * 8u;
+                if (p + 7u <= q) continue;
+                const uint32_t part = p / (FP * 16) * WQ + q / (FQ * 16), r = q % (FQ * 16), c = p % (FP * 16) / 8u;
+                const half8_t v = *reinterpret_cast<const half8_t*>(
+                    s_op + (part * (FQ * 16) + r) * (FP * 16) + (c ^ ((r / FQ) & (kChunks - 1u))) * 8u);
+                half_t* to = a.out + item_out + uint64_t(tj * BQ + q) * a.np + ti * BP + p;
+                if (p > q) {
+                    *reinterpret_cast<half8_t*>(to) = v;
+                } else {
+#pragma unroll
+                    for (uint32_t e = 1; e < 8; ++e)
+                        if (p + e > q) to[e] = v[e];
+                }
+            }
         }
     } else {
         static_assert(FQ == 4, "columns turned four by four");
@@ -899,8 +935,8 @@ static void ortho_steps(const OrthoPlan& p, OrthoMul a, int64_t batch, int32_t s
         if constexpr (!SPLIT) {
             if (a.pair) {
                 half_t *mt = reinterpret_cast<half_t*>(ws + p.t), *md2 = reinterpret_cast<half_t*>(ws + p.d2);
-                square(SQ::template kernel<kMix>, md, nullptr, ma, nullptr, ma, nullptr, mt, nullptr);
-                square(SQ::template kernel<kMixSum>, mt, nullptr, md, nullptr, mt, nullptr, ma, nullptr);
+                square(SQ::template kernel<kMix>, ma, nullptr, md, nullptr, ma, nullptr, mt, nullptr);
+                square(SQ::template kernel<kMixSum>, md, nullptr, mt, nullptr, mt, nullptr, ma, nullptr);
                 a.second = 1;
                 square(SQ::template kernel<kPoly>, ma, nullptr, ma, nullptr, ma, nullptr, md2, nullptr);
                 square(SQ::template kernel<kJoin>, md2, nullptr, md, nullptr, md, md2, mt, nullptr);

@@ -644,7 +644,8 @@ e8q_status_t e8q_embed(const void* table, e8q_dtype_t table_dtype, int64_t vocab
  *   w_latent     [vocab, dim] bf16, updated in place, or NULL
  *   workspace    e8q_embed_backward_workspace_size(n, vocab, dim) bytes, 256-byte aligned
  * At least one of grad_table, w_latent.  The latents take the float32 dE, also
- * when a bf16 grad_table is written.  Limits: n, vocab, dim < 2^31.
+ * when a bf16 grad_table is written.  Limits: n, vocab, dim < 2^31, and
+ * (n / 128) (dim / 256) + vocab / 16 < 2^24 (E8Q_ERR_UNSUPPORTED past them).
  * ------------------------------------------------------------------------- */
 e8q_status_t e8q_embed_backward(const void* grad_out, e8q_dtype_t grad_dtype, int64_t n, int64_t dim,
                                 const void* tokens, e8q_index_t index_type, int64_t vocab, float scale,
@@ -663,17 +664,18 @@ size_t e8q_embed_backward_workspace_size(int64_t n, int64_t vocab, int64_t dim);
  * the same polynomial of the singular values, sigma -> a s + b s^3 + c s^5).
  *   g            [batch, rows, cols] in g_dtype
  *   coeff_a, coeff_b, coeff_c   finite; the polynomial must keep [0, 1] within
- *                [0, 1.5] over all steps and |a + b s^2 + c s^4| <= 7 there
- *                (E8Q_ERR_UNSUPPORTED otherwise: fixed-point ranges below)
+ *                [-1.5, 1.5] over all steps and |a + b s^2 + c s^4| <= 7 there
+ *                (E8Q_ERR_UNSUPPORTED otherwise: the operands are float16)
  *   steps        in [1, 16]
  *   update_out   [batch, rows, cols] bf16, nearest even
  *   workspace    e8q_orthogonalize_workspace_size(batch, rows, cols) bytes, 256-byte aligned
  * Arithmetic: |G|_F in float64; X is held to 22 significant bits (two float16
  * parts, scaled by a power of two); the products run on the matrix cores on
- * float16 operands with float32 sums: X and A rounded to nearest, and
- * M - alpha I, alpha the mean of the diagonal of M = aI + bA + cA^2, so that
- * the rounding of the operands does not touch alpha X.  |O - exact|_F is about
- * 1e-3 |O|_F before the last rounding, for any spectrum.
+ * float16 operands with float32 sums, and the part of X below float16 is carried
+ * beside them, so that the small singular values of a gradient of low rank are
+ * not drowned by rounding.  |O - exact|_F is about 1e-3 of |O|_F for a flat spectrum and
+ * up to 3.5e-3 for one of low rank, before the last rounding; problems too small
+ * to fill the chip multiply both parts, and only the last rounding is left.
  * A zero matrix gives zeros; one with a NaN or infinity gives NaN everywhere
  * (E8Q_STATUS_NONFINITE), the others of the batch are not affected.
  * Limits: cols a multiple of 8; rows, cols <= 65536; batch <= 65535.

@@ -95,6 +95,17 @@ def test_long_matrix_with_small_square_tiles():
     test_large_tiles((1, 1537, 6144))
 
 
+@pytest.mark.parametrize("shape", [(20, 769, 1280), (40, 257, 1280)])
+def test_rounding_spares_no_rows(shape):
+    """Errors of products taken for symmetric would gather in some tiles' rows."""
+    x = _gradient((1,) + shape[1:], 5, "fall").to(torch.bfloat16).expand(shape).contiguous().to(device())
+    got, _ = _run(x)
+    want = oracle.orthogonalize(_f64(x[:1]))[0]
+    err = np.linalg.norm(_f64(got[:1])[0] - want, axis=1) / np.linalg.norm(want, axis=1)
+    blocks = [err[i:i + 64].mean() for i in range(0, shape[1] - shape[1] % 64, 64)]
+    assert max(blocks) <= 1.25 * min(blocks)
+
+
 @pytest.mark.parametrize("shape", [(20, 769, 1280), (2, 1025, 1032), (5, 200, 328)])
 def test_runs_agree_bit_for_bit(shape):
     x = _gradient(shape, 5, "fall").to(torch.bfloat16).to(device())
@@ -120,6 +131,16 @@ def test_steps_and_coefficients(steps, coeffs):
     x = _gradient((2, 96, 200), 9, "fall").to(device())
     got, _ = _run(x, steps, coeffs)
     _near(_f64(got), oracle.orthogonalize(_f64(x), steps, coeffs))
+
+
+@pytest.mark.parametrize("steps,coeffs", [(2, e8q.NEWTON_SCHULZ), (4, e8q.NEWTON_SCHULZ), (1, e8q.NEWTON_SCHULZ),
+                                          (9, (1.5, -0.5, 0.0))])
+def test_steps_in_pairs(steps, coeffs):
+    """Batches that fill the chip take two steps at a time where one side is longer."""
+    x = _gradient((1, 136, 264), 9, "fall").expand(40, 136, 264).contiguous().to(device())
+    got, _ = _run(x, steps, coeffs)
+    _near(_f64(got[:1]), oracle.orthogonalize(_f64(x[:1]), steps, coeffs))
+    assert torch.equal(got[0], got[39])
 
 
 @pytest.mark.parametrize("size", [1e-30, 1e30, 1.0])
