@@ -14,6 +14,10 @@
 //
 // Sort: least significant digit first, with a digit count and a stable
 // placement per tile of 1024 ids; up to 4096 ids take one launch of one block.
+//
+// What bounds it: writing the table's gradient.  32768 x 4096 bf16 into 131072
+// float32 rows: 433 us for the sums and zeros (2.4 GB, 5.6 TB/s), 32 us for the
+// sort, 11 us for the joins, 97 us for the lookup (5.5 TB/s).
 #include "e8q_device.hpp"
 #include "e8q_host.hpp"
 #include "e8q_vec.hpp"

@@ -20,6 +20,11 @@
 //
 // Few rows are split over blocks (partial m, s, t and keys in the workspace)
 // and joined by a second kernel.
+//
+// What bounds it.  Long batches: memory, with about 11 vector instruction slots
+// per logit close behind (v_exp_f32 takes four): 4096 x 32768 bf16 52 us, 5.1 TB/s.
+// One row: two launches and their latencies (11 + 5 us for 131072 logits with 8
+// alternatives, while the host needs 12 us to issue them).
 #include <float.h>
 
 #include "e8q_device.hpp"
