@@ -6,7 +6,8 @@
 //   lse = scale m + ln s,   entropy = ln s - ln 2 * t / s,
 //   logprob = scale (x_t - m) - ln s,
 // so every exponent is formed from a difference of logits, exact where it
-// matters (near the maximum), and not from scale x - lse.
+// matters (near the maximum), and not from scale x - lse.  So is the gradient's,
+// but for one that is handed a stored lse of moderate size (kLseMost).
 //
 // Alternatives.  Each wave keeps the 64 best keys of its part of the row,
 // sorted, one per lane.  A key orders by value, then by lower index:
@@ -64,6 +65,7 @@ struct LpArgs {
     uint32_t per_split;         // vectors per block
     float4* part;               // [rows, splits] m, s, t
     uint64_t* part_keys;        // [rows, splits, 64]
+    float4* joined;             // [rows] m, s, t of whole rows: joined for the gradient, or null
     const float* g_lp;
     const float* g_ent;
     const float* lse_in;
@@ -479,6 +481,7 @@ __global__ __launch_bounds__(kLpBlock) void logprobs_join_kernel(LpArgs a) {
         s_keys[tid] = best;
     }
     st = stat_block<BLOCK>(st, a.scale * kLog2e, s_stat);
+    if (a.joined && tid == 0u) a.joined[row] = make_float4(st.m, st.s, st.t, 0.0f);
     if constexpr (TOP) merge_block<BLOCK, kTopMax>(best, s_keys, wave, lane);
     write_row<T, TOP>(a, row, x, st, best, tok);
 }
@@ -569,8 +572,25 @@ __device__ __forceinline__ void grad_part(const LpArgs& a, const T* x, T* dx, ui
     grad_tokens<T>(a, dx, int64_t(lo) * VE, int64_t(hi) * VE, g, zero, s);
 }
 
-template <typename T>
-__global__ __launch_bounds__(kLpBlock) void logprobs_backward_kernel(LpArgs a) {
+// The gradient's constants from the row's statistics.
+__device__ __forceinline__ GradRow grad_row(const LpArgs& a, const Stat& st, float sum, float gh) {
+    const RowEnd e = row_end(st, a.scale);
+    const float c = a.scale / st.s;
+    return {1.0f, st.m, a.scale * kLog2e, -c * (sum + gh * (e.ent - e.ln_s)), -c * gh * kLn2};
+}
+
+// Rows up to this |lse| take their p from lse.  It is stored to 24 bits, so p is
+// off by a factor of at most 1 + |lse| 2^-24: here 2^-20 of itself (16 < |lse| <= 32),
+// about what the rounding of an exponent of that size costs.  Past it the error would
+// grow with whatever all logits of a row have in common (a row of the type's lowest
+// value would have p = 1 everywhere), so the row's maximum and sum are formed
+// again.  301 x 32003 float32: 14 us, with the second reading (by every part of a
+// row) 35 us; 8192 x 32768 bf16: 202 and 240 us.
+constexpr float kLseMost = 32.0f;
+
+// Statistics as they were joined (`joined`), or from lse as stored.
+template <typename T, int BLOCK>
+__global__ __launch_bounds__(BLOCK) void logprobs_backward_kernel(LpArgs a) {
     const RowTokens s_tok = row_tokens(a.ntok);
     const uint32_t row = a.splits == 1 ? blockIdx.x : blockIdx.x / a.splits;
     const uint32_t sp = blockIdx.x - row * a.splits;
@@ -579,17 +599,30 @@ __global__ __launch_bounds__(kLpBlock) void logprobs_backward_kernel(LpArgs a) {
     const uint32_t nvec = (a.vocab + kVec<T> - 1) / kVec<T>;
     const uint32_t lo = min(sp * a.per_split, nvec), hi = min(lo + a.per_split, nvec);
     const float sum = load_tokens<T>(a, row, x, s_tok);
-    const float lse = a.lse_in[row];
-    const float gh = a.g_ent ? a.g_ent[row] : 0.0f, h = a.g_ent ? a.ent_in[row] : 0.0f;
-    const GradRow g = {a.scale, lse, kLog2e, -a.scale * (sum + gh * h), -a.scale * gh * kLn2};
-    grad_part<T>(a, x, dx, lo, hi, g, lse == -INFINITY, s_tok);
-}
-
-// The gradient's constants from the row's statistics.
-__device__ __forceinline__ GradRow grad_row(const LpArgs& a, const Stat& st, float sum, float gh) {
-    const RowEnd e = row_end(st, a.scale);
-    const float c = a.scale / st.s;
-    return {1.0f, st.m, a.scale * kLog2e, -c * (sum + gh * (e.ent - e.ln_s)), -c * gh * kLn2};
+    const float gh = a.g_ent ? a.g_ent[row] : 0.0f;
+    GradRow g;
+    bool zero;
+    if (a.joined) {
+        const float4 p = a.joined[row];
+        const Stat st = {p.x, p.y, p.z};
+        g = grad_row(a, st, sum, gh);
+        zero = st.s == 0.0f;
+    } else {
+        const float lse = a.lse_in[row];
+        zero = lse == -INFINITY;
+        if (fabsf(lse) > kLseMost && !zero) {
+            // in place only with one block per row, whose threads have all read here
+            // (a barrier joins the statistics) before one of them writes
+            uint64_t none = 0ull;
+            const Stat st = row_part<T, false, BLOCK>(x, a.vocab, 0u, nvec, a.scale * kLog2e, 0u, none);
+            g = grad_row(a, st, sum, gh);
+            zero = st.s == 0.0f;
+        } else {
+            const float h = a.g_ent ? a.ent_in[row] : 0.0f;
+            g = {a.scale, lse, kLog2e, -a.scale * (sum + gh * h), -a.scale * gh * kLn2};
+        }
+    }
+    grad_part<T>(a, x, dx, lo, hi, g, zero, s_tok);
 }
 
 // Statistics and gradient of a row that fits the registers of one block, NV
@@ -724,9 +757,9 @@ static size_t lp_workspace(int64_t rows, int64_t vocab, size_t esz, int64_t top_
     uint32_t per = 0;
     const uint64_t splits = lp_splits(rows, vocab, esz, per);
     if (splits == 1) return 0;
-    // without alternatives: room for the rows' lse and entropy (e8q_token_logprobs_grad)
+    // without alternatives: room for the rows' statistics (e8q_token_logprobs_grad)
     return lp_part_bytes(uint64_t(rows) * splits) +
-           (top_k ? size_t(uint64_t(rows) * splits * kTopMax * 8) : size_t(rows) * 8);
+           (top_k ? size_t(uint64_t(rows) * splits * kTopMax * 8) : size_t(rows) * sizeof(float4));
 }
 
 // Forward launches; the arguments are checked.
@@ -743,7 +776,16 @@ static void lp_forward(LpArgs& a, void* ws, hipStream_t st) {
 template <typename T>
 static void lp_backward(LpArgs& a, hipStream_t st) {
     a.splits = lp_splits(a.rows, a.vocab, sizeof(T), a.per_split);
-    launch(logprobs_backward_kernel<T>, dim3(a.rows * a.splits), dim3(kLpBlock), a.ntok * 12u, st, a);
+    if (a.splits > 1 && a.dx == a.x && !a.joined) {
+        // few rows in place, from lse: a row may have to be read whole before any of it
+        // is written, so one wide block takes it (301 x 32003 float32: 20 us in place,
+        // 14 us into another buffer by four blocks a row)
+        a.splits = 1;
+        a.per_split = (a.vocab + kVec<T> - 1) / kVec<T>;
+        launch(logprobs_backward_kernel<T, kLpWide>, dim3(a.rows), dim3(kLpWide), a.ntok * 12u, st, a);
+        return;
+    }
+    launch(logprobs_backward_kernel<T, kLpBlock>, dim3(a.rows * a.splits), dim3(kLpBlock), a.ntok * 12u, st, a);
 }
 
 // Whole rows: the smallest block whose registers hold one, while that leaves
@@ -877,15 +919,14 @@ extern "C" e8q_status_t e8q_token_logprobs_grad(const void* logits, e8q_dtype_t 
         else lp_grad<float>(a, s);
         return launch_status();
     }
-    // few rows: the two split passes, with the rows' statistics in the workspace where no output takes them
-    float* stats = reinterpret_cast<float*>(static_cast<char*>(workspace) + need - size_t(rows) * 8);
-    if (!a.lse) a.lse = stats;
-    if (grad_entropy && !a.ent) a.ent = stats + rows;
-    if (dtype == E8Q_BF16) lp_forward<uint16_t, false>(a, workspace, s);
-    else lp_forward<float, false>(a, workspace, s);
-    a.lse_in = a.lse;
-    a.ent_in = a.ent;
-    if (dtype == E8Q_BF16) lp_backward<uint16_t>(a, s);
-    else lp_backward<float>(a, s);
+    // few rows: the two split passes, with the rows' statistics in the workspace
+    a.joined = reinterpret_cast<float4*>(static_cast<char*>(workspace) + need - size_t(rows) * sizeof(float4));
+    if (dtype == E8Q_BF16) {
+        lp_forward<uint16_t, false>(a, workspace, s);
+        lp_backward<uint16_t>(a, s);
+    } else {
+        lp_forward<float, false>(a, workspace, s);
+        lp_backward<float>(a, s);
+    }
     return launch_status();
 }

@@ -590,7 +590,9 @@ size_t e8q_token_logprobs_workspace_size(int64_t rows, int64_t vocab, int64_t to
  *   grad_logits  [rows, vocab] in dtype (bf16: nearest even), rows
  *                grad_stride elements apart; may be logits itself (with
  *                grad_stride = row_stride)
- * A row whose lse is -inf has gradient 0.
+ * A row whose lse is -inf has gradient 0.  p_i comes from lse while |lse| <= 32
+ * (off by at most 2^-20 of itself) and from the row's maximum and sum, formed
+ * again, past that.
  * ------------------------------------------------------------------------- */
 e8q_status_t e8q_token_logprobs_backward(const void* logits, e8q_dtype_t dtype,
                                          int64_t rows, int64_t vocab, int64_t row_stride, float scale,
