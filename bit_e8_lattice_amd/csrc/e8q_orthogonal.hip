@@ -8,24 +8,53 @@
 // its rounding (2^-12 of an entry) would land on every singular direction alike
 // and grow with the small singular values (up to a^steps = 485 times): a
 // gradient of low rank would come out with errors of 2 to 4 percent.  So X is
-// kept to 22 bits, X_hi + X_lo, and the new X is M X_hi + alpha X_lo, alpha the
-// mean of the diagonal of M = aI + bA + cA^2 (M X_lo would differ from it by far
-// less than a rounding of M X_hi).  The rounding of M acts on the strong
-// directions' columns alone.  Measured against float64, of |O|_F, for flat, falling
-// and low-rank (an eighth) spectra at 20 x 769 x 1280: 1.1e-3, 1.1e-3 and 1.4e-3;
-// with two steps at once (below) 1.1e-3, 2.9e-3 and 3.5e-3.  Problems too small to fill the chip (64-wide tiles) wait for memory
-// and launches, not for the matrix cores: there every operand has its low part
-// and a product is three (hi hi, hi lo, lo hi), which leaves the rounding of the
-// result.
+// kept to 22 bits, X_hi + X_lo, and the new X is M X_hi + g X_lo with one gain g of
+// M = aI + bA + cA^2 for all directions.  What (M - g I) X_lo leaves out lands on
+// every direction and grows in the weak ones, so g has to be theirs: the
+// polynomial one standard deviation below the mean of the squared singular values
+// (never below 0), both of which the trace and the norm of A give.  That is a for a
+// spectrum of low rank, and the mean gain for a flat one, whose directions are all
+// alike; the last step, after which nothing grows, takes the mean gain alpha.  (With
+// alpha throughout, low rank came out with 1.9e-2 at 8 x 64 and 5e-3 at 257 x 1280; with
+// a throughout, flat spectra with 1.6e-3 instead of 1.2e-3 at 769 x 1280.)  The rounding
+// of M acts on the strong directions' columns alone.  Problems too small to fill the
+// chip (64-wide tiles) wait for memory and launches, not for the matrix cores: there
+// every operand has its low part and a product is three (hi hi, hi lo, lo hi), which
+// leaves the rounding of the result.
 //
-// Two steps at once.  Where m is well above n, two steps take one A = X X^T and
+// Measured against float64, of |O|_F, before the last rounding, five default steps:
+// flat, falling, low-rank (1/8, 1/4, 1/2) and half-weak (1e-3) spectra, and a scan of
+// 37 in clusters (a part at 1, the rest at 0.3 .. 1e-5), power laws and exponentials:
+//                        flat    fall    1/8     1/4     1/2     half    worst
+//   256 x    8 x   64    0.8e-3  0.9e-3  1.6e-3  2.0e-3  2.7e-3  3.3e-3  4.1e-3
+//    64 x   32 x 1024    3.2e-3  1.4e-3  2.2e-3  1.7e-3  1.8e-3  1.8e-3  3.2e-3
+//   140 x  257 x 1280    1.0e-3  0.7e-3  1.6e-3  1.6e-3  1.6e-3  1.7e-3  2.6e-3
+//    20 x  769 x 1280    1.2e-3  1.0e-3  1.4e-3  1.4e-3  1.5e-3  2.4e-3  2.4e-3
+//   128 x  768 x 2048    0.9e-3  2.7e-3  3.2e-3  3.2e-3  2.4e-3  2.3e-3  6.1e-3  in pairs
+//        2048 x 8192     1.1e-3  2.3e-3  2.7e-3  2.2e-3  1.6e-3  1.6e-3  3.9e-3  in pairs
+// Steps amplify roundings; eight default ones: worst of the scan 1.3e-2 at 8 x 64, else
+// 9e-3, half of it below 2e-3.
+//
+// Two steps at once.  Where m is at least 2 n, two steps may take one A = X X^T and
 // one product with X instead of two each: with M, M' the two steps' polynomials
 // of A, A' = M A M and M' M are n x n and symmetric (all commute):
 //   T = A M,  A' = M T,  X <- M' M X,
 // three symmetric products of n^3 for 3 n^2 m saved.  These products are made of
 // D = M - alpha I, the rest added in float32: a diagonal rounded with the rest
-// would cost half as much again in accuracy.  More than two steps would lose
-// more (A' holds the squares of the singular values).
+// would cost half as much again in accuracy.  A' comes out of two more roundings
+// than X X^T of a new X would, which the table above shows; so pairs are kept for
+// sides from 640 on, where those errors have averaged out to 6.4e-3 at worst (5.5e-3 and
+// more for a half-weak spectrum at 64 x 256), and for steps that amplify by no more
+// than five default ones do.  Time of five steps singly and in pairs, ms:
+//   m / n   4096 x ..    128 of 768 x ..   16 of 1024 x ..  24, 32 of 640 x ..
+//   1       1.45, 1.59   2.11, 2.36
+//   1.33    1.86, 1.80   2.43, 2.54
+//   1.5     2.07, 1.99   2.93, 2.82        0.69, 0.74       0.59, 0.67 (1.6)
+//   2                    3.31, 3.09        0.82, 0.82       0.54, 0.55
+//   2.67                 4.03, 3.54
+//   3.5     4.14, 3.22                                      1.06, 0.93 (3.2)
+// Below 2 what pairs gain (7% at most) is not worth their errors.  More than two
+// steps at once would lose more (A' holds the squares of the singular values).
 //
 // Ranges.  X is stored times 2^s, s = floor(log2(sqrt(n m))) <= 15, A and T times
 // 2^14, M and D times 2^12, E times 2^9: the entries' bounds (singular values
@@ -46,8 +75,8 @@
 // of 256 CUs idle (on the others the matrix cores are busy 71% of the time, with
 // no LDS bank conflict), and 528 tiles of 128 are as many rounds.  Random operands
 // run the chip into its power limit: bare matrix instructions reach 1.85 PFLOP/s.
-// At 128 x 768 x 2048 a tile's sum is 24 stages long and the moving of X (2 + 2 + 2
-// bytes an entry of a product) counts as much: 486 us for 309 GFLOP.
+// At 128 x 768 x 2048 a tile's sum is 24 stages long and the moving of X (both
+// parts read and written, 8 bytes an entry) counts as much: 486 us for 309 GFLOP.
 #include <algorithm>
 #include <cmath>
 
@@ -257,7 +286,7 @@ struct OrthoMul {
     const half_t* in_lo;       // its low part (SPLIT); kJoin: D'
     float* sums;               // [batch, per-item tiles of the triangle, 2]: tr A, |A|^2 of a tile
     uint32_t sum_tiles;
-    float* alpha;              // [2, batch]: of the first and of the second step of a pair
+    float* alpha;              // [4, batch]: alpha of the first and of the second step of a pair, then their low gains
     uint32_t batch;
     int second;                // kPoly: the pair's second step
     int pair;                  // two steps at once
@@ -501,7 +530,8 @@ __global__ __launch_bounds__(WP* WQ * 64, WP* WQ >= 4 ? 2 : 1) void ortho_mul_ke
     // the tile's first P and Q rows of this wave
     const uint32_t pw = ti * BP + wp * FP * 16, qw = tj * BQ + wq * FQ * 16;
 
-    const float *alpha1 = a.alpha + item, *alpha2 = a.alpha + a.batch + item;
+    const float *alpha1 = a.alpha + item, *alpha2 = alpha1 + a.batch;
+    const float *gain1 = alpha2 + a.batch, *gain2 = gain1 + a.batch;
     float alpha = 0.0f;
     if constexpr (MODE == kPoly) {
         // every block of a matrix adds the tiles' sums up in the same order
@@ -530,7 +560,13 @@ __global__ __launch_bounds__(WP* WQ * 64, WP* WQ >= 4 ? 2 : 1) void ortho_mul_ke
             sq += s_sum[kWaves + w];
         }
         alpha = a.ca + (a.cb * tr + a.cc * sq) / float(a.n);
-        if (t == 0u && tid == 0u) a.alpha[a.second * a.batch + item] = alpha;
+        if (t == 0u && tid == 0u) {
+            // the gain a standard deviation below the mean of the squared singular values
+            const float mean = tr / float(a.n), spread = sqrtf(fmaxf(sq / float(a.n) - mean * mean, 0.0f));
+            const float low = fmaxf(mean - spread, 0.0f);
+            a.alpha[a.second * a.batch + item] = alpha;
+            a.alpha[(2 + a.second) * a.batch + item] = a.ca + low * (a.cb + a.cc * low);
+        }
     }
 
     // result = by_c C + by_hi in + by_lo in_lo + on_diagonal I, all in the scales
@@ -555,7 +591,9 @@ __global__ __launch_bounds__(WP* WQ * 64, WP* WQ >= 4 ? 2 : 1) void ortho_mul_ke
     }
     if constexpr (MODE == kApply || MODE == kLast) {
         by_c = ldexpf(1.0f, a.pair ? -kScaleE : -kScaleD);
-        by_hi = SPLIT ? 0.0f : a.pair ? *alpha1 * *alpha2 : *alpha1;
+        // the last step takes the mean gain: nothing grows after it
+        const float last = MODE == kLast ? (a.pair ? *alpha2 : *alpha1) : (a.pair ? *gain2 : *gain1);
+        by_hi = SPLIT ? 0.0f : a.pair ? *gain1 * last : last;
     }
     constexpr bool kUseLo = MODE == kJoin || (MODE == kPoly && SPLIT);
     constexpr bool kSums = MODE == kGram || MODE == kMixSum;
@@ -792,17 +830,27 @@ static size_t ortho_align(size_t v) { return (v + 255) / 256 * 256; }
 
 // 256-wide tiles, one a CU, or 128-wide ones, two a CU: whichever takes fewer
 // rounds, a round of 128-wide tiles (half the work) counting 0.75, or 0.33 if
-// there is at most one to a CU.  Five steps, square / rectangular products by
-// 256 / 256, 128 / 256 and 128 / 128: 4096 x 4096 1.48, 1.68, 1.78 ms; 2048 x 8192
-// 1.16, 0.65, 0.68 ms; 16 x 768 x 2048 0.70, 0.60, 0.58 ms; 1024 x 4096 0.66, 0.34,
-// 0.30 ms (64 / 64 with low parts 0.48 ms).
+// there is at most one to a CU.  Five steps, ms, square / rectangular products by
+// 256 / 256, 128 / 256 and 128 / 128, * what this rule takes:
+//   4096 x 4096      1.48*  1.69   1.77     16 x 768 x 2048    0.68   0.58*  0.57
+//   2048 x 8192      1.16   0.66*  0.68     128 x 768 x 2048   3.59*  3.97   4.26
+//   1024 x 4096      0.65   0.34   0.30*    5503 x 4096        2.06*  2.36   2.34
+//   2048 x 2048      0.68   0.44   0.33*    140 x 257 x 1280   1.68   1.74*  1.34
+// (1024 x 4096 by 64 / 64 with low parts 0.46.)  The last is what the rule does not
+// see: rows that a wider tile pads.
 static uint32_t ortho_tile(uint64_t of256, uint64_t of128, uint64_t cus) {
     const double wide = double((of256 + cus - 1) / cus);
     const double small = of128 <= cus ? 0.33 : 0.75 * double((of128 + 2 * cus - 1) / (2 * cus));
     return wide <= small ? 256u : 128u;
 }
 
-static OrthoPlan ortho_plan(int64_t batch, int64_t rows, int64_t cols) {
+// Bounds of the steps taken in pairs (see the top): what the steps can amplify a
+// rounding by, the product of their largest gains |a + b s^2 + c s^4| (3.4445^5 = 485
+// for five default steps), and the smaller side.
+constexpr double kPairGrowth = 512.0;
+constexpr uint32_t kPairSide = 640;
+
+static OrthoPlan ortho_plan(int64_t batch, int64_t rows, int64_t cols, double growth) {
     OrthoPlan p{};
     p.tall = rows > cols;
     p.n = uint32_t(p.tall ? cols : rows);
@@ -828,13 +876,13 @@ static OrthoPlan ortho_plan(int64_t batch, int64_t rows, int64_t cols) {
     p.a = take(sq);
     p.d = take(sq);
     p.sums = take(size_t(batch) * p.side * (p.side + 1) / 2 * 8);
-    p.alpha = take(size_t(batch) * 8);
+    p.alpha = take(size_t(batch) * 16);
     // four vectors of 8 per thread and block, while that leaves blocks for every CU
     const uint64_t cells = uint64_t(p.n) * p.m, most = (cus * 8 + batch - 1) / uint64_t(batch);
     const uint64_t want = (cells + 8191) / 8192;
     p.norm_blocks = uint32_t(std::min<uint64_t>(std::min<uint64_t>(want, most), kNormBlocks));
     p.norm = take(size_t(batch) * p.norm_blocks * 8);
-    p.pair = p.rect != 64 && uint64_t(p.m) * 5 >= uint64_t(p.n) * 6;
+    p.pair = p.rect != 64 && p.n >= kPairSide && p.m >= 2u * p.n && growth <= kPairGrowth;
     if (p.pair) {
         p.t = take(sq);
         p.d2 = take(sq);
@@ -849,7 +897,7 @@ static OrthoPlan ortho_plan(int64_t batch, int64_t rows, int64_t cols) {
 }
 
 static e8q_status_t ortho_check(const void* g, e8q_dtype_t dtype, int64_t batch, int64_t rows, int64_t cols,
-                                int32_t steps, float ca, float cb, float cc, const uint32_t* status) {
+                                int32_t steps, float ca, float cb, float cc, const uint32_t* status, double& growth) {
     if (!g || !status || batch <= 0 || rows <= 0 || cols <= 0 || cols % 8) return E8Q_ERR_INVALID;
     if (dtype != E8Q_F32 && dtype != E8Q_BF16) return E8Q_ERR_INVALID;
     if (reinterpret_cast<uintptr_t>(g) % 16) return E8Q_ERR_INVALID;
@@ -858,6 +906,7 @@ static e8q_status_t ortho_check(const void* g, e8q_dtype_t dtype, int64_t batch,
     // largest singular value after each step, from [0, 1]: the polynomial at the
     // ends and where its derivative a + 3 b s^2 + 5 c s^4 vanishes
     double top = 1.0;
+    growth = 1.0;
     for (int32_t i = 0; i < steps; ++i) {
         const double a = ca, b = cb, c = cc;
         double at[4] = {top, 0.0, 0.0, 0.0}, next = 0.0, gain = std::fabs(a);
@@ -878,6 +927,7 @@ static e8q_status_t ortho_check(const void* g, e8q_dtype_t dtype, int64_t batch,
         }
         if (gain > 7.0 || next > 1.5) return E8Q_ERR_UNSUPPORTED;
         top = next;
+        growth *= gain;
     }
     return E8Q_OK;
 }
@@ -1000,7 +1050,7 @@ static e8q_status_t ortho_fits(const OrthoPlan& p, int64_t batch, const void* ws
 
 extern "C" size_t e8q_orthogonalize_workspace_size(int64_t batch, int64_t rows, int64_t cols) {
     if (batch <= 0 || batch > 65535 || rows <= 0 || rows > 65536 || cols <= 0 || cols > 65536 || cols % 8) return 0;
-    return e8q::ortho_plan(batch, rows, cols).total;
+    return e8q::ortho_plan(batch, rows, cols, 1.0).total;      // with pairs, where the sides allow them
 }
 
 extern "C" e8q_status_t e8q_orthogonalize(const void* g, e8q_dtype_t g_dtype, int64_t batch, int64_t rows,
@@ -1008,10 +1058,12 @@ extern "C" e8q_status_t e8q_orthogonalize(const void* g, e8q_dtype_t g_dtype, in
                                           void* update_out, void* workspace, size_t workspace_bytes,
                                           uint32_t* status_dev, void* stream) {
     using namespace e8q;
-    const e8q_status_t c = ortho_check(g, g_dtype, batch, rows, cols, steps, coeff_a, coeff_b, coeff_c, status_dev);
+    double growth = 1.0;
+    const e8q_status_t c =
+        ortho_check(g, g_dtype, batch, rows, cols, steps, coeff_a, coeff_b, coeff_c, status_dev, growth);
     if (c != E8Q_OK) return c;
     if (!update_out || reinterpret_cast<uintptr_t>(update_out) % 16) return E8Q_ERR_INVALID;
-    const OrthoPlan p = ortho_plan(batch, rows, cols);
+    const OrthoPlan p = ortho_plan(batch, rows, cols, growth);
     const e8q_status_t f = ortho_fits(p, batch, workspace, workspace_bytes);
     if (f != E8Q_OK) return f;
     OrthoIn in{};
@@ -1037,8 +1089,9 @@ extern "C" e8q_status_t e8q_orthogonal_step(const void* w, void* w_out, const vo
                                             void* workspace, size_t workspace_bytes, uint32_t* status_dev,
                                             void* stream) {
     using namespace e8q;
+    double growth = 1.0;
     const e8q_status_t c =
-        ortho_check(grad, grad_dtype, batch, rows, cols, steps, coeff_a, coeff_b, coeff_c, status_dev);
+        ortho_check(grad, grad_dtype, batch, rows, cols, steps, coeff_a, coeff_b, coeff_c, status_dev, growth);
     if (c != E8Q_OK) return c;
     if (!w || !w_out || !momentum || !momentum_out) return E8Q_ERR_INVALID;
     for (const void* q : {w, static_cast<const void*>(w_out), static_cast<const void*>(momentum),
@@ -1049,7 +1102,7 @@ extern "C" e8q_status_t e8q_orthogonal_step(const void* w, void* w_out, const vo
         return E8Q_ERR_INVALID;
     if (!std::isfinite(mu) || !std::isfinite(lr) || !std::isfinite(decay) || !std::isfinite(gamma))
         return E8Q_ERR_INVALID;
-    const OrthoPlan p = ortho_plan(batch, rows, cols);
+    const OrthoPlan p = ortho_plan(batch, rows, cols, growth);
     const e8q_status_t f = ortho_fits(p, batch, workspace, workspace_bytes);
     if (f != E8Q_OK) return f;
     OrthoIn in{};
