@@ -302,10 +302,11 @@ struct OrthoMul {
 // 64 lanes x 16 bytes straight to LDS at byte `to` (wave-uniform) + 16 * lane,
 // from `base` (wave-uniform) + `offset`.  Written in assembly so that the
 // compiler does not wait for it at the next LDS read: the stage that it fills
-// is read only after wait_loads() and a barrier.  It has no result register, and
-// nothing else in this file uses m0.
+// is read only after wait_loads() and a barrier.  It has no result register.  The
+// LDS address goes in m0, as an operand, so that the compiler knows what is there;
+// the load needs a wait state after it is written.
 __device__ __forceinline__ void load_lds16(const half_t* base, uint32_t offset, uint32_t to) {
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory");
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"{m0}"(to), "v"(offset), "s"(base) : "memory");
 }
 
 __device__ __forceinline__ uint32_t lds_address(const half_t* p) {
