@@ -40,7 +40,7 @@ constexpr int kLpUnroll = 4;          // vectors in flight per thread
 constexpr int kTopMax = 64;           // one key per lane
 constexpr int kMaxTokens = 1024;
 constexpr int kMaxSplits = 256;
-constexpr int64_t kMaxRows = int64_t(1) << 24;   // a block per row, fewer than 2^32 threads
+constexpr int64_t kMaxRows = int64_t(1) << 24;   // a block of kLpBlock per row, fewer than 2^32 threads
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 // Stands in for an exponent of -inf where it is multiplied (0 * -inf is NaN):
@@ -795,18 +795,32 @@ static void lp_backward(LpArgs& a, hipStream_t st) {
 // read and written once: bf16 2048 wide 5.0 TB/s, 16384 5.4, 32768 4.7, 65536
 // 4.2 (3.9 in the registers of 512 threads), 131072 4.4; float32 8192 wide 5.4,
 // 32768 5.4 (4.7 read twice), 131072 4.3.  A copy reaches 4.9.
+template <typename T, class Go>
+static void lp_grad_kernel(int64_t vocab, Go&& go) {
+    const uint64_t nvec = (uint64_t(vocab) + kVec<T> - 1) / kVec<T>;
+    if (nvec <= 64 * 4) go(logprobs_grad_kernel<T, 64, 4>, 64u);
+    else if (nvec <= 128 * 4) go(logprobs_grad_kernel<T, 128, 4>, 128u);
+    else if (nvec <= 256 * 4) go(logprobs_grad_kernel<T, 256, 4>, 256u);
+    else if (nvec <= 256 * 8) go(logprobs_grad_kernel<T, 256, 8>, 256u);
+    else if (nvec <= 256 * 16) go(logprobs_grad_kernel<T, 256, 16>, 256u);
+    else if (sizeof(T) == 4 && nvec <= 512 * 16) go(logprobs_grad_kernel<T, 512, 16>, 512u);
+    else go(logprobs_grad_long_kernel<T>, unsigned(kLpWide));
+}
+
 template <typename T>
 static void lp_grad(LpArgs& a, hipStream_t st) {
     a.splits = 1;
-    const uint32_t nvec = (a.vocab + kVec<T> - 1) / kVec<T>;
-    auto go = [&](auto kernel, unsigned block) { launch(kernel, dim3(a.rows), dim3(block), a.ntok * 12u, st, a); };
-    if (nvec <= 64 * 4) go(logprobs_grad_kernel<T, 64, 4>, 64);
-    else if (nvec <= 128 * 4) go(logprobs_grad_kernel<T, 128, 4>, 128);
-    else if (nvec <= 256 * 4) go(logprobs_grad_kernel<T, 256, 4>, 256);
-    else if (nvec <= 256 * 8) go(logprobs_grad_kernel<T, 256, 8>, 256);
-    else if (nvec <= 256 * 16) go(logprobs_grad_kernel<T, 256, 16>, 256);
-    else if (sizeof(T) == 4 && nvec <= 512 * 16) go(logprobs_grad_kernel<T, 512, 16>, 512);
-    else go(logprobs_grad_long_kernel<T>, kLpWide);
+    lp_grad_kernel<T>(a.vocab, [&](auto kernel, unsigned block) {
+        launch(kernel, dim3(a.rows), dim3(block), a.ntok * 12u, st, a);
+    });
+}
+
+// A launch has fewer than 2^32 threads.
+template <typename T>
+static bool lp_grad_fits(int64_t rows, int64_t vocab) {
+    bool fits = false;
+    lp_grad_kernel<T>(vocab, [&](auto, unsigned block) { fits = uint64_t(rows) * block < uint64_t(1) << 32; });
+    return fits;
 }
 
 }  // namespace e8q
@@ -903,6 +917,8 @@ extern "C" e8q_status_t e8q_token_logprobs_grad(const void* logits, e8q_dtype_t 
     st = lp_check_grad(logits, vocab, row_stride, n_tokens, grad_logprob, grad_logits, grad_stride, dtype);
     if (st != E8Q_OK) return st;
     const size_t need = lp_workspace(rows, vocab, dtype == E8Q_BF16 ? 2 : 4, 0);
+    if (!need && !(dtype == E8Q_BF16 ? lp_grad_fits<uint16_t>(rows, vocab) : lp_grad_fits<float>(rows, vocab)))
+        return E8Q_ERR_UNSUPPORTED;
     if (need && (!workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 256))
         return E8Q_ERR_INVALID;
     LpArgs a = lp_args(logits, rows, vocab, row_stride, scale, tokens, index_type, n_tokens, status_dev);

@@ -608,7 +608,8 @@ e8q_status_t e8q_token_logprobs_backward(const void* logits, e8q_dtype_t dtype,
  * the outputs of e8q_token_logprobs (no alternatives) and the gradient of
  * e8q_token_logprobs_backward (grad_entropy may be NULL).  Arguments as there;
  * logprob_out, lse_out, entropy_out may be NULL, and grad_logits may be logits
- * itself (with grad_stride = row_stride).
+ * itself (with grad_stride = row_stride).  Limits as there, and rows < 2^22 for
+ * vocab > 32768, rows < 2^23 for float32 and vocab > 16384 (threads of a launch).
  * ------------------------------------------------------------------------- */
 e8q_status_t e8q_token_logprobs_grad(const void* logits, e8q_dtype_t dtype,
                                      int64_t rows, int64_t vocab, int64_t row_stride, float scale,
