@@ -18,6 +18,8 @@
 // What bounds it: writing the table's gradient.  32768 x 4096 bf16 into 131072
 // float32 rows: 433 us for the sums and zeros (2.4 GB, 5.6 TB/s), 32 us for the
 // sort, 11 us for the joins, 97 us for the lookup (5.5 TB/s).
+#include <algorithm>
+
 #include "e8q_device.hpp"
 #include "e8q_host.hpp"
 #include "e8q_vec.hpp"
@@ -617,8 +619,12 @@ static EmbedPlan embed_plan(int64_t n, int64_t vocab, int64_t dim) {
     }
     p.counts = at;
     at += a256((size_t(p.tiles) << p.bits) * 4);
+    // room for the chunks of every smaller number of ids too (shorter chunks can be
+    // more: 4096 ids make 512, 4104 make 257), so that one workspace serves a last,
+    // smaller batch
+    const uint64_t most = std::min((uint64_t(n) + 7) / 8, 2 * uint64_t(device_cu_count()) + 1);
     p.part = at;
-    at += a256(size_t(p.chunks) * 2 * size_t(dim) * 4);
+    at += a256(size_t(std::max<uint64_t>(p.chunks, most)) * 2 * size_t(dim) * 4);
     p.total = at;
     return p;
 }

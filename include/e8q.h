@@ -574,7 +574,10 @@ e8q_status_t e8q_token_logprobs(const void* logits, e8q_dtype_t dtype,
                                 uint32_t* status_dev, void* stream);
 
 /* Workspace bytes e8q_token_logprobs needs (0 on bad sizes, and where it needs
- * none).  The size for top_k = 0 also serves e8q_token_logprobs_grad. */
+ * none).  The size for top_k = 0 also serves e8q_token_logprobs_grad.  It is the
+ * size for these rows: fewer rows are split over more blocks and can need more
+ * (8192 rows need none, one row of the same length does), so a program with
+ * batches of several sizes takes the largest of theirs. */
 size_t e8q_token_logprobs_workspace_size(int64_t rows, int64_t vocab, int64_t top_k);
 
 /* ---------------------------------------------------------------------------
@@ -657,7 +660,8 @@ e8q_status_t e8q_embed_backward(const void* grad_out, e8q_dtype_t grad_dtype, in
                                 void* workspace, size_t workspace_bytes,
                                 uint32_t* status_dev, void* stream);
 
-/* Workspace bytes e8q_embed_backward needs (0 on bad sizes). */
+/* Workspace bytes e8q_embed_backward needs (0 on bad sizes); it is enough for
+ * every smaller n with the same vocab and dim. */
 size_t e8q_embed_backward_workspace_size(int64_t n, int64_t vocab, int64_t dim);
 
 /* ---------------------------------------------------------------------------
@@ -717,7 +721,9 @@ e8q_status_t e8q_orthogonal_step(const void* w, void* w_out,
                                  void* workspace, size_t workspace_bytes,
                                  uint32_t* status_dev, void* stream);
 
-/* Workspace bytes e8q_orthogonalize / e8q_orthogonal_step need (0 on bad sizes). */
+/* Workspace bytes e8q_orthogonalize / e8q_orthogonal_step need (0 on bad sizes).
+ * For these sizes: a smaller batch can need more, so a program with several takes
+ * the largest of theirs. */
 size_t e8q_orthogonalize_workspace_size(int64_t batch, int64_t rows, int64_t cols);
 
 /* |C(core_bound)|, the number of core points; -1 if core_bound is outside [0, 40].

@@ -26,3 +26,10 @@ def test_rows_past_the_threads_of_a_launch(L, dtype, rows, vocab):
     # status, stream
     args = [FAKE, dtype, rows, vocab, vocab, 1.0, FAKE, 0, 1, FAKE, None, FAKE, None, None, FAKE, vocab, None, 0, FAKE, None]
     assert L.e8q_token_logprobs_grad(*args) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("vocab,dim", [(100, 16), (1024, 300), (131072, 4096)])
+def test_embedding_workspace_serves_smaller_batches(L, vocab, dim):
+    sizes = [L.e8q_embed_backward_workspace_size(n, vocab, dim)
+             for n in list(range(1, 9000, 7)) + list(range(9000, 400000, 997))]
+    assert sizes[0] > 0 and sizes == sorted(sizes)
