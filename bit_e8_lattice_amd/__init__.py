@@ -31,7 +31,8 @@ __all__ = [
 
 F32, BF16 = 0, 1
 I32, I64 = 0, 1
-# sigma -> a sigma + b sigma^3 + c sigma^5: five steps bring singular values in [0.01, 1] into [0.68, 1.21]
+# sigma -> a sigma + b sigma^3 + c sigma^5: five steps bring singular values in [0.01, 1] into [0.68, 1.14]
+# (coefficients published by K. Jordan and others, 2024)
 NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)
 ESCAPE_RECORD_BYTES = 20
 ENCODE_NOALLOC_SCRATCH_BYTES = 64 << 20      # E8Q_ENCODE_NOALLOC_SCRATCH_BYTES
@@ -172,6 +173,8 @@ def _shape3(w):
 
 def _stream(t, stream):
     if stream is None:
+        # the handle that torch.cuda.current_stream(t.device).cuda_stream gives, without the 1.8 us that
+        # making its Stream object takes (a call of a small operator takes 5.6 us in all)
         return torch._C._cuda_getCurrentRawStream(t.get_device())
     return stream.cuda_stream
 

@@ -23,7 +23,8 @@
 // and joined by a second kernel.
 //
 // What bounds it.  Long batches: memory, with about 11 vector instruction slots
-// per logit close behind (v_exp_f32 takes four): 4096 x 32768 bf16 52 us, 5.1 TB/s.
+// per logit close behind (v_exp_f32 takes four): 4096 x 32768 bf16 52 us, 5.1 TB/s;
+// with 20 alternatives the search for them, 103 us.
 // One row: two launches and their latencies (11 + 5 us for 131072 logits with 8
 // alternatives, while the host needs 12 us to issue them).
 #include <float.h>
@@ -792,9 +793,9 @@ static void lp_backward(LpArgs& a, hipStream_t st) {
 // several rows to a CU.  Longer rows are read twice by blocks of kLpWide threads,
 // two to a CU: their rows (512 at a time, 128 MiB at 131072 bf16 logits) stay in
 // the last-level cache until the second reading.  Measured, 2^28 logits, bytes
-// read and written once: bf16 2048 wide 5.0 TB/s, 16384 5.4, 32768 4.7, 65536
-// 4.2 (3.9 in the registers of 512 threads), 131072 4.4; float32 8192 wide 5.4,
-// 32768 5.4 (4.7 read twice), 131072 4.3.  A copy reaches 4.9.
+// read and written once: bf16 2048 wide 4.3 TB/s, 16384 5.2, 32768 5.0, 65536
+// 4.3 (3.9 in the registers of 512 threads), 131072 4.3; float32 8192 wide 5.3,
+// 32768 5.3 (4.7 read twice), 131072 4.3.  A copy reaches 4.9.
 template <typename T, class Go>
 static void lp_grad_kernel(int64_t vocab, Go&& go) {
     const uint64_t nvec = (uint64_t(vocab) + kVec<T> - 1) / kVec<T>;

@@ -69,14 +69,13 @@
 // maps to zeros.  The symmetric products compute the tiles on and below the
 // diagonal and write each twice.
 //
-// What bounds it.  At 4096 x 14336 the product with X (481 GFLOP) takes 442 us
+// What bounds it.  At 4096 x 14336 the product with X (481 GFLOP) takes 443 us
 // (1.09 PFLOP/s; the library's float16 product of 8192^3 runs at 1.30), X X^T
-// (half a product) 290 us and a square product 87 to 91 us: its 136 tiles leave 120
-// of 256 CUs idle (on the others the matrix cores are busy 71% of the time, with
-// no LDS bank conflict), and 528 tiles of 128 are as many rounds.  Random operands
-// run the chip into its power limit: bare matrix instructions reach 1.85 PFLOP/s.
+// (half a product) 300 us and a square product 91 to 96 us: its 136 tiles leave 120
+// of 256 CUs idle (on the others the matrix cores are busy 72% of the time, with
+// no LDS bank conflict), and 528 tiles of 128 are as many rounds.
 // At 128 x 768 x 2048 a tile's sum is 24 stages long and the moving of X (both
-// parts read and written, 8 bytes an entry) counts as much: 486 us for 309 GFLOP.
+// parts read and written, 8 bytes an entry) counts as much: 483 us for 309 GFLOP.
 #include <algorithm>
 #include <cmath>
 
