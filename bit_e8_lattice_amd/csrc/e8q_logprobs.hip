@@ -586,19 +586,19 @@ __device__ __forceinline__ GradRow grad_row(const LpArgs& a, const Stat& st, flo
 // grow with whatever all logits of a row have in common (a row of the type's lowest
 // value would have p = 1 everywhere), so the row's maximum and sum are formed
 // again.  301 x 32003 float32: 14 us, with the second reading (by every part of a
-// row) 35 us; 8192 x 32768 bf16: 202 and 240 us.
+// row) 35 us, in place 13 and 54 us; 8192 x 32768 bf16: 202 and 240 us.
 constexpr float kLseMost = 32.0f;
 
 // Statistics as they were joined (`joined`), or from lse as stored.
-template <typename T, int BLOCK>
-__global__ __launch_bounds__(BLOCK) void logprobs_backward_kernel(LpArgs a) {
+template <typename T>
+__global__ __launch_bounds__(kLpBlock) void logprobs_backward_kernel(LpArgs a) {
     const RowTokens s_tok = row_tokens(a.ntok);
     const uint32_t row = a.splits == 1 ? blockIdx.x : blockIdx.x / a.splits;
     const uint32_t sp = blockIdx.x - row * a.splits;
     const T* x = static_cast<const T*>(a.x) + int64_t(row) * a.stride;
     T* dx = static_cast<T*>(a.dx) + int64_t(row) * a.dx_stride;
     const uint32_t nvec = (a.vocab + kVec<T> - 1) / kVec<T>;
-    const uint32_t lo = min(sp * a.per_split, nvec), hi = min(lo + a.per_split, nvec);
+    uint32_t lo = min(sp * a.per_split, nvec), hi = min(lo + a.per_split, nvec);
     const float sum = load_tokens<T>(a, row, x, s_tok);
     const float gh = a.g_ent ? a.g_ent[row] : 0.0f;
     GradRow g;
@@ -612,10 +612,15 @@ __global__ __launch_bounds__(BLOCK) void logprobs_backward_kernel(LpArgs a) {
         const float lse = a.lse_in[row];
         zero = lse == -INFINITY;
         if (fabsf(lse) > kLseMost && !zero) {
-            // in place only with one block per row, whose threads have all read here
-            // (a barrier joins the statistics) before one of them writes
+            // in place a row is read and written by its first block alone, whose threads
+            // have all read (a barrier joins the statistics) before one of them writes
+            if (a.dx == a.x) {
+                if (sp > 0u) return;
+                lo = 0u;
+                hi = nvec;
+            }
             uint64_t none = 0ull;
-            const Stat st = row_part<T, false, BLOCK>(x, a.vocab, 0u, nvec, a.scale * kLog2e, 0u, none);
+            const Stat st = row_part<T, false, kLpBlock>(x, a.vocab, 0u, nvec, a.scale * kLog2e, 0u, none);
             g = grad_row(a, st, sum, gh);
             zero = st.s == 0.0f;
         } else {
@@ -777,16 +782,7 @@ static void lp_forward(LpArgs& a, void* ws, hipStream_t st) {
 template <typename T>
 static void lp_backward(LpArgs& a, hipStream_t st) {
     a.splits = lp_splits(a.rows, a.vocab, sizeof(T), a.per_split);
-    if (a.splits > 1 && a.dx == a.x && !a.joined) {
-        // few rows in place, from lse: a row may have to be read whole before any of it
-        // is written, so one wide block takes it (301 x 32003 float32: 20 us in place,
-        // 14 us into another buffer by four blocks a row)
-        a.splits = 1;
-        a.per_split = (a.vocab + kVec<T> - 1) / kVec<T>;
-        launch(logprobs_backward_kernel<T, kLpWide>, dim3(a.rows), dim3(kLpWide), a.ntok * 12u, st, a);
-        return;
-    }
-    launch(logprobs_backward_kernel<T, kLpBlock>, dim3(a.rows * a.splits), dim3(kLpBlock), a.ntok * 12u, st, a);
+    launch(logprobs_backward_kernel<T>, dim3(a.rows * a.splits), dim3(kLpBlock), a.ntok * 12u, st, a);
 }
 
 // Whole rows: the smallest block whose registers hold one, while that leaves

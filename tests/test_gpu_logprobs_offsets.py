@@ -156,3 +156,27 @@ def test_a_row_of_lowest_values_is_uniform(rows, dtype):
     for got in (two, both):
         # the entropy's gradient is 0, but for rounding of log p + H: 100 / V * 16 u ln V
         assert (np.abs(_f64(got) - want) <= last * np.abs(want) + 100 / vocab * 16 * U * ln_v).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,vocab", [(1, 40001), (5, 9000), (301, 20011), (1100, 515)])
+def test_in_place_gives_the_same_bits(rows, vocab, dtype):
+    """Rows of moderate and of large lse in one call: the same gradient into another buffer and in place."""
+    d = device()
+    x = _rows("0", rows, vocab, dtype, 9)
+    x[::2] += 1000
+    x[rows - 1] = torch.finfo(dtype).min
+    if rows > 4:
+        x[3] = -float("inf")
+    tok = (torch.arange(rows * 3, device=d) * 997 % vocab).view(rows, 3)
+    g, gh = torch.randn((rows, 3), device=d), torch.randn(rows, device=d)
+    st, lse, h = torch.zeros(1, dtype=torch.int32, device=d), torch.empty(rows, device=d), torch.empty(rows, device=d)
+    ws = torch.empty(e8q.e8q_token_logprobs_workspace_size(rows, vocab), dtype=torch.uint8, device=d)
+    e8q.e8q_token_logprobs(x, ws, st, lse_out=lse, entropy_out=h)
+    other, own = torch.empty_like(x), x.clone()
+    e8q.e8q_token_logprobs_backward(x, lse, other, st, tokens=tok, grad_logprob=g, entropy=h, grad_entropy=gh)
+    for _ in range(3):
+        own.copy_(x)
+        e8q.e8q_token_logprobs_backward(own, lse, own, st, tokens=tok, grad_logprob=g, entropy=h, grad_entropy=gh)
+        assert torch.equal(own, other)
+    assert int(st.item()) == 0 and bool(torch.isfinite(other).all())
