@@ -684,14 +684,15 @@ size_t e8q_embed_backward_workspace_size(int64_t n, int64_t vocab, int64_t dim);
  * float16 operands with float32 sums, and the part of X below float16 is carried
  * beside them, so that the small singular values of a gradient of low rank are
  * not drowned by rounding.  |O - exact|_F / |O|_F before the last rounding, for five
- * steps of the coefficients (3.4445, -4.7750, 2.0315): about 1e-3 for a flat spectrum
- * and 2e-3 for one of low rank (3.3e-3 and 4.1e-3 at most where the smaller side is
- * below 64); where the larger side is at least twice the smaller one of 640 or
- * more, steps may be taken in pairs, and low rank costs 2e-3 to 3.5e-3, a spectrum in
- * clusters up to 6.4e-3.  Every further step amplifies roundings: eight of these, 2e-3
- * as a rule and 9e-3 at worst (1.3e-2 for 8 rows); from twelve on, directions
- * below 1e-4 of the strongest one come up out of the rounding of X (2e-2).  Problems too
- * small to fill the chip multiply both parts: 7e-5 for five steps, 1e-3 for eight.
+ * steps of the coefficients (3.4445, -4.7750, 2.0315): about 1e-3 for a flat spectrum,
+ * 2e-3 for one of low rank and 3e-3 at most for one in clusters (4.1e-3 where the
+ * smaller side is below 64); where the larger side is at least twice the smaller one of
+ * 640 or more, steps may be taken in pairs, and low rank costs 2e-3 to 3.5e-3, clusters up
+ * to 6.4e-3.  Every further step amplifies roundings: eight of these, 2e-3 as a rule
+ * and 9e-3 at worst (1.3e-2 for 8 rows); from twelve on, directions that G hardly has (1e-5
+ * of the strongest one and less) come up out of the rounding of X, 3e-2 of |O|_F for
+ * twelve, all of it for sixteen.  Problems too small to fill the chip multiply both
+ * parts: 7e-5 for five steps, 1.2e-3 for eight.
  * A zero matrix gives zeros; one with a NaN or infinity gives NaN everywhere
  * (E8Q_STATUS_NONFINITE), the others of the batch are not affected.
  * Limits: cols a multiple of 8; rows, cols <= 65536; batch <= 65535.
