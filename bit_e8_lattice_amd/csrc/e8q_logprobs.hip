@@ -65,8 +65,10 @@ struct LpArgs {
     uint32_t splits;            // blocks per row
     uint32_t per_split;         // vectors per block
     float4* part;               // [rows, splits] m, s, t
-    uint64_t* part_keys;        // [rows, splits, 64]
-    float4* joined;             // [rows] m, s, t of whole rows: joined for the gradient, or null
+    union {                     // (one more pointer costs a call of few rows 0.4 us)
+        uint64_t* part_keys;    // with alternatives: [rows, splits, 64]
+        float4* joined;         // without: [rows] m, s, t of whole rows, for the gradient, or null
+    };
     const float* g_lp;
     const float* g_ent;
     const float* lse_in;
@@ -482,7 +484,9 @@ __global__ __launch_bounds__(kLpBlock) void logprobs_join_kernel(LpArgs a) {
         s_keys[tid] = best;
     }
     st = stat_block<BLOCK>(st, a.scale * kLog2e, s_stat);
-    if (a.joined && tid == 0u) a.joined[row] = make_float4(st.m, st.s, st.t, 0.0f);
+    if constexpr (!TOP) {
+        if (a.joined && tid == 0u) a.joined[row] = make_float4(st.m, st.s, st.t, 0.0f);
+    }
     if constexpr (TOP) merge_block<BLOCK, kTopMax>(best, s_keys, wave, lane);
     write_row<T, TOP>(a, row, x, st, best, tok);
 }
@@ -599,8 +603,11 @@ __global__ __launch_bounds__(kLpBlock) void logprobs_backward_kernel(LpArgs a) {
     T* dx = static_cast<T*>(a.dx) + int64_t(row) * a.dx_stride;
     const uint32_t nvec = (a.vocab + kVec<T> - 1) / kVec<T>;
     uint32_t lo = min(sp * a.per_split, nvec), hi = min(lo + a.per_split, nvec);
-    const float sum = load_tokens<T>(a, row, x, s_tok);
+    // read beside the tokens: what branches below depends on it
+    const float lse = a.joined ? 0.0f : a.lse_in[row];
     const float gh = a.g_ent ? a.g_ent[row] : 0.0f;
+    const float h = a.g_ent && !a.joined ? a.ent_in[row] : 0.0f;
+    const float sum = load_tokens<T>(a, row, x, s_tok);
     GradRow g;
     bool zero;
     if (a.joined) {
@@ -609,7 +616,6 @@ __global__ __launch_bounds__(kLpBlock) void logprobs_backward_kernel(LpArgs a) {
         g = grad_row(a, st, sum, gh);
         zero = st.s == 0.0f;
     } else {
-        const float lse = a.lse_in[row];
         zero = lse == -INFINITY;
         if (fabsf(lse) > kLseMost && !zero) {
             // in place a row is read and written by its first block alone, whose threads
@@ -624,7 +630,6 @@ __global__ __launch_bounds__(kLpBlock) void logprobs_backward_kernel(LpArgs a) {
             g = grad_row(a, st, sum, gh);
             zero = st.s == 0.0f;
         } else {
-            const float h = a.g_ent ? a.ent_in[row] : 0.0f;
             g = {a.scale, lse, kLog2e, -a.scale * (sum + gh * h), -a.scale * gh * kLn2};
         }
     }
@@ -773,7 +778,8 @@ template <typename T, bool TOP>
 static void lp_forward(LpArgs& a, void* ws, hipStream_t st) {
     a.splits = lp_splits(a.rows, a.vocab, sizeof(T), a.per_split);
     a.part = static_cast<float4*>(ws);
-    a.part_keys = reinterpret_cast<uint64_t*>(static_cast<char*>(ws) + lp_part_bytes(uint64_t(a.rows) * a.splits));
+    if (TOP)
+        a.part_keys = reinterpret_cast<uint64_t*>(static_cast<char*>(ws) + lp_part_bytes(uint64_t(a.rows) * a.splits));
     launch(logprobs_kernel<T, TOP>, dim3(a.rows * a.splits), dim3(kLpBlock), 0, st, a);
     if (a.splits == 1) return;
     launch(logprobs_join_kernel<T, TOP>, dim3(a.rows), dim3(kLpBlock), 0, st, a);
