@@ -22,7 +22,8 @@ __all__ = [
     "e8q_gemv_core_escape", "e8q_gemv_workspace_size", "e8q_pack_escapes", "e8q_unpack_escapes",
     "e8q_pack_workspace_size", "PACKED_RECORD_BYTES", "e8q_ptq_init", "e8q_ptq_workspace_size",
     "e8q_token_logprobs", "e8q_token_logprobs_workspace_size", "e8q_token_logprobs_backward",
-    "e8q_token_logprobs_grad", "e8q_embed", "e8q_embed_backward", "e8q_embed_backward_workspace_size",
+    "e8q_token_logprobs_grad", "e8q_distill", "e8q_distill_workspace_size", "e8q_distill_backward",
+    "e8q_distill_grad", "TAIL_NONE", "TAIL_RENORM", "TAIL_REST", "e8q_embed", "e8q_embed_backward", "e8q_embed_backward_workspace_size",
     "e8q_orthogonalize", "e8q_orthogonal_step", "e8q_orthogonalize_workspace_size", "NEWTON_SCHULZ",
     "e8q_core_size",
     "e8q_status_string", "e8q_version",
@@ -31,6 +32,7 @@ __all__ = [
 
 F32, BF16 = 0, 1
 I32, I64 = 0, 1
+TAIL_NONE, TAIL_RENORM, TAIL_REST = 0, 1, 2
 # sigma -> a sigma + b sigma^3 + c sigma^5: five steps bring singular values in [0.01, 1] into [0.68, 1.14]
 # (coefficients published by K. Jordan and others, 2024)
 NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)
@@ -119,6 +121,14 @@ def lib():
     L.e8q_token_logprobs_grad.argtypes = [vp, e, i64, i64, i64, f32, vp, e, i64, vp, vp, vp, vp, vp, vp, i64,
                                           vp, sz, vp, vp]
     L.e8q_token_logprobs_grad.restype = e
+    L.e8q_distill.argtypes = [vp, e, i64, i64, i64, f32, vp, e, vp, i64, i32, vp, vp, vp, vp, sz, vp, vp]
+    L.e8q_distill.restype = e
+    L.e8q_distill_workspace_size.argtypes = [i64, i64, i64]
+    L.e8q_distill_workspace_size.restype = sz
+    L.e8q_distill_backward.argtypes = [vp, e, i64, i64, i64, f32, vp, e, vp, i64, i32, vp, vp, vp, i64, vp, vp]
+    L.e8q_distill_backward.restype = e
+    L.e8q_distill_grad.argtypes = [vp, e, i64, i64, i64, f32, vp, e, vp, i64, i32, vp, vp, vp, vp, i64, vp, sz, vp, vp]
+    L.e8q_distill_grad.restype = e
     L.e8q_embed.argtypes = [vp, e, i64, i64, vp, e, i64, f32, vp, e, vp, vp]
     L.e8q_embed.restype = e
     L.e8q_embed_backward.argtypes = [vp, e, i64, i64, vp, e, i64, f32, vp, e, vp, f32, vp, sz, vp, vp]
@@ -571,6 +581,73 @@ def e8q_token_logprobs_grad(logits, tokens, grad_logprob, grad_logits, workspace
                                          _ptr(grad_logits), gstride, _ptr(workspace), _size(workspace), _ptr(status),
                                          _stream(logits, stream))
     _check("e8q_token_logprobs_grad", code)
+
+
+def e8q_distill_workspace_size(rows, vocab, k):
+    return int(lib().e8q_distill_workspace_size(int(rows), int(vocab), int(k)))
+
+
+def _places(logits, teacher_idx, teacher_logprob):
+    """Rows, vocabulary and places of a distillation call."""
+    rows, vocab = logits.shape
+    _dev(teacher_idx, "teacher_idx", _IDX)
+    if teacher_idx.dim() != 2 or teacher_idx.shape[0] != rows:
+        raise ValueError("teacher_idx must be [rows, k]")
+    _sized(teacher_logprob, "teacher_logprob", teacher_idx.numel())
+    return rows, vocab, teacher_idx.shape[1]
+
+
+def e8q_distill(logits, teacher_idx, teacher_logprob, workspace, status, scale=1.0, tail=TAIL_NONE, loss_out=None,
+                logprob_out=None, stats_out=None, stream=None):
+    """``e8q_distill``: the divergence of ``softmax(scale * logits)`` from a
+    teacher's top logits (``teacher_idx`` [rows, k], negative: not used;
+    ``teacher_logprob`` [rows, k]) per row, the student's log probabilities at
+    the places, and the statistics for the backward call (``stats_out``
+    [rows, 4]).  ``tail``: ``TAIL_NONE``, ``TAIL_RENORM`` or ``TAIL_REST``."""
+    stride = _rows(logits, "logits", _WDT)
+    rows, vocab, k = _places(logits, teacher_idx, teacher_logprob)
+    _sized(loss_out, "loss_out", rows); _sized(logprob_out, "logprob_out", rows * k)
+    _sized(stats_out, "stats_out", rows * 4)
+    _dev(workspace, "workspace", (torch.uint8,)); _dev(status, "status", (torch.int32,))
+    code = lib().e8q_distill(_ptr(logits), _dtype_code(logits), rows, vocab, stride, float(scale), _ptr(teacher_idx),
+                             _index_code(teacher_idx), _ptr(teacher_logprob), k, int(tail), _ptr(loss_out),
+                             _ptr(logprob_out), _ptr(stats_out), _ptr(workspace), _size(workspace), _ptr(status),
+                             _stream(logits, stream))
+    _check("e8q_distill", code)
+
+
+def e8q_distill_backward(logits, teacher_idx, teacher_logprob, stats, grad_loss, grad_logits, status, scale=1.0,
+                         tail=TAIL_NONE, stream=None):
+    """``e8q_distill_backward``: the gradient of ``sum(grad_loss * loss)`` with
+    respect to ``logits`` (``grad_logits`` may be ``logits``)."""
+    stride, gstride = _rows(logits, "logits", _WDT), _rows(grad_logits, "grad_logits", (logits.dtype,))
+    rows, vocab, k = _places(logits, teacher_idx, teacher_logprob)
+    if grad_logits.shape != logits.shape:
+        raise ValueError("grad_logits must have the shape of logits")
+    _sized(stats, "stats", rows * 4); _sized(grad_loss, "grad_loss", rows); _dev(status, "status", (torch.int32,))
+    code = lib().e8q_distill_backward(_ptr(logits), _dtype_code(logits), rows, vocab, stride, float(scale),
+                                      _ptr(teacher_idx), _index_code(teacher_idx), _ptr(teacher_logprob), k, int(tail),
+                                      _ptr(stats), _ptr(grad_loss), _ptr(grad_logits), gstride, _ptr(status),
+                                      _stream(logits, stream))
+    _check("e8q_distill_backward", code)
+
+
+def e8q_distill_grad(logits, teacher_idx, teacher_logprob, grad_loss, grad_logits, workspace, status, scale=1.0,
+                     tail=TAIL_NONE, loss_out=None, logprob_out=None, stream=None):
+    """``e8q_distill_grad``: loss and, for row weights known beforehand, the
+    gradient of the logits in one call (``grad_logits`` may be ``logits``)."""
+    stride, gstride = _rows(logits, "logits", _WDT), _rows(grad_logits, "grad_logits", (logits.dtype,))
+    rows, vocab, k = _places(logits, teacher_idx, teacher_logprob)
+    if grad_logits.shape != logits.shape:
+        raise ValueError("grad_logits must have the shape of logits")
+    _sized(grad_loss, "grad_loss", rows); _sized(loss_out, "loss_out", rows)
+    _sized(logprob_out, "logprob_out", rows * k)
+    _dev(workspace, "workspace", (torch.uint8,)); _dev(status, "status", (torch.int32,))
+    code = lib().e8q_distill_grad(_ptr(logits), _dtype_code(logits), rows, vocab, stride, float(scale),
+                                  _ptr(teacher_idx), _index_code(teacher_idx), _ptr(teacher_logprob), k, int(tail),
+                                  _ptr(grad_loss), _ptr(loss_out), _ptr(logprob_out), _ptr(grad_logits), gstride,
+                                  _ptr(workspace), _size(workspace), _ptr(status), _stream(logits, stream))
+    _check("e8q_distill_grad", code)
 
 
 def e8q_embed(table, tokens, out, status, scale=1.0, stream=None):

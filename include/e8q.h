@@ -624,6 +624,83 @@ e8q_status_t e8q_token_logprobs_grad(const void* logits, e8q_dtype_t dtype,
                                      uint32_t* status_dev, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * e8q_distill -- the divergence of a row's distribution from a teacher's top
+ * logits, such as the alternatives that e8q_token_logprobs wrote for it.  With
+ * y = scale * x, q = softmax(y), the row's places (i_j, l_j) and p_j = exp(l_j):
+ *   loss = sum_j w_j (log w_j - log q_{i_j})  [ + w_r (log w_r - log q_r) ]
+ * with, by `tail`,
+ *   E8Q_TAIL_NONE     w_j = p_j (the places' terms only),
+ *   E8Q_TAIL_RENORM   w_j = p_j / sum p,
+ *   E8Q_TAIL_REST     w_j = p_j, and all tokens that no place names as one event more:
+ *                     w_r = max(0, 1 - sum p), q_r = their sum of q.  Where q is 0
+ *                     there (all tokens named, or their logits -inf), w_r is 0.
+ *   logits, dtype, rows, vocab, row_stride, scale   as e8q_token_logprobs
+ *   teacher_idx  [rows, k] token ids (index_type).  A negative id is a place not
+ *                used; an id >= vocab is treated the same and sets E8Q_STATUS_BAD_INDEX.
+ *                A token may be named twice: both terms count, its q once
+ *   teacher_logprob [rows, k] float32 log probabilities (-inf: p = 0, the term is 0)
+ *   loss_out     [rows] float32, or NULL
+ *   logprob_out  [rows, k] float32 log q of the places (0 where not used), or NULL
+ *   stats_out    [rows, 4] float32 for e8q_distill_backward, 16-byte aligned, or NULL
+ *   workspace    e8q_distill_workspace_size(rows, vocab, k) bytes, 256-byte aligned
+ *                (may be NULL if that is 0)
+ * At least one output.  A row without a used place has loss 0 and gradient 0,
+ * whatever its logits.  Otherwise a row holding a NaN or +inf (logit or used
+ * log probability) has NaN outputs (E8Q_STATUS_NONFINITE), and a named token
+ * of logit -inf with p > 0 loss +inf.  exp, sums and the running maximum are float32.
+ * Limits: vocab < 2^31 - 16, rows < 2^24, k <= 1024.
+ * ------------------------------------------------------------------------- */
+enum { E8Q_TAIL_NONE = 0, E8Q_TAIL_RENORM = 1, E8Q_TAIL_REST = 2 };
+
+e8q_status_t e8q_distill(const void* logits, e8q_dtype_t dtype,
+                         int64_t rows, int64_t vocab, int64_t row_stride, float scale,
+                         const void* teacher_idx, e8q_index_t index_type,
+                         const float* teacher_logprob, int64_t k, int32_t tail,
+                         float* loss_out, float* logprob_out, float* stats_out,
+                         void* workspace, size_t workspace_bytes,
+                         uint32_t* status_dev, void* stream);
+
+/* Workspace bytes e8q_distill and e8q_distill_grad need (0 on bad sizes, and where
+ * they need none).  It is the size for these rows: fewer rows can need more. */
+size_t e8q_distill_workspace_size(int64_t rows, int64_t vocab, int64_t k);
+
+/* ---------------------------------------------------------------------------
+ * e8q_distill_backward -- the gradient of sum_r grad_loss[r] * loss[r] with
+ * respect to the logits, from the stored statistics: with K the named tokens and
+ * P = sum_j w_j + w_r,
+ *   dx_i = scale * grad_loss * ( P q_i - sum_{j: i_j = i} w_j )   i in K,
+ *          scale * grad_loss * q_i (P - w_r / q_r)                 otherwise.
+ *   other arguments as e8q_distill (the same as its call's)
+ *   stats        [rows, 4] as e8q_distill wrote it
+ *   grad_loss    [rows] float32
+ *   grad_logits  [rows, vocab] in dtype (bf16: nearest even), rows grad_stride
+ *                elements apart; may be logits itself (with grad_stride = row_stride)
+ * A row whose logits are all -inf has gradient 0.
+ * ------------------------------------------------------------------------- */
+e8q_status_t e8q_distill_backward(const void* logits, e8q_dtype_t dtype,
+                                  int64_t rows, int64_t vocab, int64_t row_stride, float scale,
+                                  const void* teacher_idx, e8q_index_t index_type,
+                                  const float* teacher_logprob, int64_t k, int32_t tail,
+                                  const float* stats, const float* grad_loss,
+                                  void* grad_logits, int64_t grad_stride,
+                                  uint32_t* status_dev, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * e8q_distill_grad -- loss and gradient in one call, for upstream gradients that
+ * are known beforehand (the rows' weights in the loss).  Arguments as above;
+ * loss_out and logprob_out may be NULL.  Limits as above, and rows < 2^22 for
+ * vocab > 32768, rows < 2^23 for float32 and vocab > 16384 (threads of a launch).
+ * ------------------------------------------------------------------------- */
+e8q_status_t e8q_distill_grad(const void* logits, e8q_dtype_t dtype,
+                              int64_t rows, int64_t vocab, int64_t row_stride, float scale,
+                              const void* teacher_idx, e8q_index_t index_type,
+                              const float* teacher_logprob, int64_t k, int32_t tail,
+                              const float* grad_loss, float* loss_out, float* logprob_out,
+                              void* grad_logits, int64_t grad_stride,
+                              void* workspace, size_t workspace_bytes,
+                              uint32_t* status_dev, void* stream);
+
+/* ---------------------------------------------------------------------------
  * e8q_embed -- out[t] = scale * table[tokens[t]], one rounding.
  *   table        [vocab, dim] in table_dtype
  *   tokens       [n] ids (index_type); a negative id is a padded position and

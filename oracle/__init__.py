@@ -83,3 +83,4 @@ from .brute import brute_nearest_e8  # noqa: F401
 from .logprobs import logprobs, logprobs_grad  # noqa: F401
 from .embed import embed, embed_grad  # noqa: F401
 from .orthogonal import orthogonalize, orthogonal_step  # noqa: F401
+from .distill import distill  # noqa: F401
