@@ -22,8 +22,9 @@ __all__ = [
     "e8q_gemv_core_escape", "e8q_gemv_workspace_size", "e8q_pack_escapes", "e8q_unpack_escapes",
     "e8q_pack_workspace_size", "PACKED_RECORD_BYTES", "e8q_ptq_init", "e8q_ptq_workspace_size",
     "e8q_token_logprobs", "e8q_token_logprobs_workspace_size", "e8q_token_logprobs_backward",
-    "e8q_token_logprobs_grad", "e8q_distill", "e8q_distill_workspace_size", "e8q_distill_backward",
-    "e8q_distill_grad", "TAIL_NONE", "TAIL_RENORM", "TAIL_REST", "e8q_embed", "e8q_embed_backward", "e8q_embed_backward_workspace_size",
+    "e8q_token_logprobs_grad", "e8q_adjust_logits", "e8q_distill", "e8q_distill_workspace_size", "e8q_distill_backward",
+    "e8q_distill_grad", "TAIL_NONE", "TAIL_RENORM", "TAIL_REST", "e8q_embed", "e8q_embed_backward",
+    "e8q_embed_backward_workspace_size",
     "e8q_orthogonalize", "e8q_orthogonal_step", "e8q_orthogonalize_workspace_size", "NEWTON_SCHULZ",
     "e8q_core_size",
     "e8q_status_string", "e8q_version",
@@ -121,6 +122,9 @@ def lib():
     L.e8q_token_logprobs_grad.argtypes = [vp, e, i64, i64, i64, f32, vp, e, i64, vp, vp, vp, vp, vp, vp, i64,
                                           vp, sz, vp, vp]
     L.e8q_token_logprobs_grad.restype = e
+    L.e8q_adjust_logits.argtypes = [vp, e, i64, i64, i64, e, vp, i64, i64, vp, vp, vp, vp, vp, vp, vp, i64, i64, vp, i64,
+                                    vp, i64, vp, vp]
+    L.e8q_adjust_logits.restype = e
     L.e8q_distill.argtypes = [vp, e, i64, i64, i64, f32, vp, e, vp, i64, i32, vp, vp, vp, vp, sz, vp, vp]
     L.e8q_distill.restype = e
     L.e8q_distill_workspace_size.argtypes = [i64, i64, i64]
@@ -581,6 +585,61 @@ def e8q_token_logprobs_grad(logits, tokens, grad_logprob, grad_logits, workspace
                                          _ptr(grad_logits), gstride, _ptr(workspace), _size(workspace), _ptr(status),
                                          _stream(logits, stream))
     _check("e8q_token_logprobs_grad", code)
+
+
+def _row_list(t, name, rows, dtypes):
+    """Columns and row stride (0: one list for all rows) of ``t`` [rows, n] or [n] with contiguous rows."""
+    if t is None:
+        return 0, 0
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a device tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} dtype {t.dtype} not in {dtypes}")
+    if t.dim() not in (1, 2) or (t.dim() == 2 and t.shape[0] != rows) or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must be [n] or [rows, n] with contiguous rows")
+    n = t.shape[-1]
+    if t.dim() == 1 or t.shape[0] == 1:
+        return n, 0
+    return n, t.stride(0)
+
+
+def e8q_adjust_logits(logits, out, status, history=None, history_len=None, prompt_len=None, repetition=None,
+                      frequency=None, presence=None, bias_idx=None, bias=None, mask=None, stream=None):
+    """``e8q_adjust_logits``: ``out`` (may be ``logits``) = the logits after
+    repetition, frequency and presence penalties ([rows] float32 each) for the
+    tokens of ``history`` [rows, n] (``history_len`` and ``prompt_len`` [rows]
+    int32), biases (``bias_idx`` and ``bias`` [rows, n], or [n] for all rows) and a
+    mask of allowed tokens (int32 words [rows, words], or [words])."""
+    stride, ostride = _rows(logits, "logits", _WDT), _rows(out, "out", (logits.dtype,))
+    rows, vocab = logits.shape
+    if out.shape != logits.shape:
+        raise ValueError("out must have the shape of logits")
+    if history is not None and history.dim() != 2:
+        raise ValueError("history must be [rows, n]")
+    hcols, hstride = _row_list(history, "history", rows, _IDX)
+    nb, bstride = _row_list(bias_idx, "bias_idx", rows, _IDX)
+    nv, vstride = _row_list(bias, "bias", rows, (torch.float32,))
+    if (nb, bstride) != (nv, vstride) or (bias_idx is None) != (bias is None):
+        raise ValueError("bias_idx and bias must have the same shape and strides")
+    words, mstride = _row_list(mask, "mask", rows, (torch.int32,))
+    if mask is not None and words < (vocab + 31) // 32:
+        raise ValueError(f"mask must have {(vocab + 31) // 32} words a row, has {words}")
+    if history is not None and bias_idx is not None and history.dtype != bias_idx.dtype:
+        raise TypeError("history and bias_idx must have one dtype")
+    _sized(history_len, "history_len", rows, (torch.int32,)); _sized(prompt_len, "prompt_len", rows, (torch.int32,))
+    _sized(repetition, "repetition", rows); _sized(frequency, "frequency", rows); _sized(presence, "presence", rows)
+    _dev(status, "status", (torch.int32,))
+    if repetition is None and frequency is None and presence is None:
+        history = history_len = prompt_len = None
+    if history is not None and hcols == 0:
+        history = history_len = prompt_len = repetition = frequency = presence = None
+    code = lib().e8q_adjust_logits(_ptr(logits), _dtype_code(logits), rows, vocab, stride,
+                                   _index_code(history if history is not None else bias_idx), _ptr(history), hcols,
+                                   max(hstride, hcols), _ptr(history_len), _ptr(prompt_len), _ptr(repetition),
+                                   _ptr(frequency), _ptr(presence), _ptr(bias_idx) if nb else None,
+                                   _ptr(bias) if nb else None, nb, bstride, _ptr(mask), mstride, _ptr(out), ostride,
+                                   _ptr(status), _stream(logits, stream))
+    _check("e8q_adjust_logits", code)
 
 
 def e8q_distill_workspace_size(rows, vocab, k):

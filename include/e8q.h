@@ -624,6 +624,45 @@ e8q_status_t e8q_token_logprobs_grad(const void* logits, e8q_dtype_t dtype,
                                      uint32_t* status_dev, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * e8q_adjust_logits -- a row of logits before a token is chosen from it: penalties
+ * for the tokens of its history, biases of given tokens, a mask of allowed ones.
+ * With c_i the occurrences of token i among the row's made tokens, b_i the sum of its biases:
+ *   y = x / r (x > 0) or x * r      where i is in the history (prompt or made),
+ *   y <- y - (f * c_i + p * [c_i > 0]),   y <- y + b_i,
+ *   out_i = y where the mask's bit i is set, -inf where not (whatever x_i is).
+ *   logits       [rows, vocab] in dtype, rows row_stride elements apart (>= vocab)
+ *   index_type   of history and bias_idx
+ *   history      [rows, history_cols] token ids, rows history_stride apart, or NULL
+ *                (exactly without penalties).  Of row r the first history_len[r] count
+ *                (NULL: all; more than history_cols counts as history_cols), the first
+ *                prompt_len[r] of them as the prompt (NULL: none), the others as made
+ *   repetition, frequency, presence   [rows] float32 r (positive), f, p; each may be NULL
+ *   bias_idx, bias   [rows, n_bias] ids and float32 values, rows bias_stride apart
+ *                (0: one list for all rows); several biases of a token are added in
+ *                their order.  NULL exactly with n_bias = 0
+ *   mask         bit i % 32 of word i / 32 allows token i; rows mask_stride words
+ *                apart (0: one mask for all rows); or NULL
+ *   out          [rows, vocab] in dtype (bf16: nearest even), rows out_stride apart;
+ *                may be logits itself (with out_stride = row_stride), and elements that nothing
+ *                touches are then not rewritten
+ * A negative id is not used; an id >= vocab is not either and sets E8Q_STATUS_BAD_INDEX.
+ * With neither penalties, biases nor mask it is a copy.  Arithmetic is float32, each
+ * operation rounded.
+ * Limits: vocab < 2^31 - 16, rows < 2^24, rows * ceil(vocab / 16384) < 2^22 for vocab > 4096
+ * (threads of a launch), n_bias <= 1024, history_cols < 2^30 - 1.
+ * ------------------------------------------------------------------------- */
+e8q_status_t e8q_adjust_logits(const void* logits, e8q_dtype_t dtype,
+                               int64_t rows, int64_t vocab, int64_t row_stride,
+                               e8q_index_t index_type,
+                               const void* history, int64_t history_cols, int64_t history_stride,
+                               const int32_t* history_len, const int32_t* prompt_len,
+                               const float* repetition, const float* frequency, const float* presence,
+                               const void* bias_idx, const float* bias, int64_t n_bias, int64_t bias_stride,
+                               const uint32_t* mask, int64_t mask_stride,
+                               void* out, int64_t out_stride,
+                               uint32_t* status_dev, void* stream);
+
+/* ---------------------------------------------------------------------------
  * e8q_distill -- the divergence of a row's distribution from a teacher's top
  * logits, such as the alternatives that e8q_token_logprobs wrote for it.  With
  * y = scale * x, q = softmax(y), the row's places (i_j, l_j) and p_j = exp(l_j):

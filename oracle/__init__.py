@@ -84,3 +84,4 @@ from .logprobs import logprobs, logprobs_grad  # noqa: F401
 from .embed import embed, embed_grad  # noqa: F401
 from .orthogonal import orthogonalize, orthogonal_step  # noqa: F401
 from .distill import distill  # noqa: F401
+from .adjust import adjust_logits  # noqa: F401

@@ -69,3 +69,23 @@ def test_distill_gradients_reject(L):
         assert f(*args) == INVALID, args
     # 2^32 threads
     assert f(*_with(base, a2=1 << 22, a3=40000, a4=40000, a15=40000)) == UNSUPPORTED
+
+
+def test_adjust_rejects(L):
+    # logits, dtype, rows, vocab, stride, index, history, cols, hstride, hlen, plen, rep, freq, pres, bias_idx, bias, n, bstride,
+    # mask, mstride, out, ostride, status, stream
+    base = [FAKE, 1, 4, 100, 100, 0, FAKE, 9, 9, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 3, 3, FAKE, 4, FAKE, 100, FAKE, None]
+    f = L.e8q_adjust_logits
+    for args in (_with(base, a0=None), _with(base, a1=2), _with(base, a2=0), _with(base, a3=0), _with(base, a4=99),
+                 _with(base, a5=2), _with(base, a6=None), _with(base, a7=0), _with(base, a8=8),
+                 _with(base, a11=None, a12=None, a13=None), _with(base, a6=None, a11=None, a12=None, a13=None),
+                 _with(base, a14=None), _with(base, a15=None), _with(base, a16=0), _with(base, a16=-1),
+                 _with(base, a17=2), _with(base, a19=3), _with(base, a20=None), _with(base, a21=99),
+                 _with(base, a21=101), _with(base, a22=None), _with(base, a0=ODD), _with(base, a20=ODD),
+                 _with(base, a5=1, a6=ctypes.c_void_p(0x10004)), _with(base, a11=ODD), _with(base, a18=ODD)):
+        assert f(*args) == INVALID, args
+    big = _with(base, a6=None, a9=None, a10=None, a11=None, a12=None, a13=None)
+    for args in (_with(base, a16=1025, a17=1025), _with(base, a2=1 << 24), _with(base, a7=1 << 30, a8=1 << 30),
+                 _with(base, a4=1 << 40, a21=1 << 40), _with(big, a2=1 << 22, a3=16384, a4=16384, a19=0, a21=16384),
+                 _with(base, a3=(1 << 31) - 16, a4=1 << 31, a19=0, a21=1 << 31)):
+        assert f(*args) == UNSUPPORTED, args
