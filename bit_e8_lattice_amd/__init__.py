@@ -19,7 +19,8 @@ __all__ = [
     "e8q_encode_core_escape", "e8q_encode_workspace_size", "e8q_encode_core_escape_noalloc",
     "ENCODE_NOALLOC_SCRATCH_BYTES", "e8q_ste_backward",
     "e8q_ste_backward_hadamard", "e8q_decode_core_escape", "e8q_decode_workspace_size",
-    "e8q_gemv_core_escape", "e8q_gemv_workspace_size", "e8q_pack_escapes", "e8q_unpack_escapes",
+    "e8q_gemv_core_escape", "e8q_gemv_workspace_size", "Experts", "e8q_moe_core_escape", "e8q_moe_workspace_size",
+    "ACT_SILU", "ACT_GELU_TANH", "e8q_pack_escapes", "e8q_unpack_escapes",
     "e8q_pack_workspace_size", "PACKED_RECORD_BYTES", "e8q_ptq_init", "e8q_ptq_workspace_size",
     "e8q_token_logprobs", "e8q_token_logprobs_workspace_size", "e8q_token_logprobs_backward",
     "e8q_token_logprobs_grad", "e8q_adjust_logits", "e8q_distill", "e8q_distill_workspace_size", "e8q_distill_backward",
@@ -34,6 +35,7 @@ __all__ = [
 F32, BF16 = 0, 1
 I32, I64 = 0, 1
 TAIL_NONE, TAIL_RENORM, TAIL_REST = 0, 1, 2
+ACT_SILU, ACT_GELU_TANH = 0, 1
 # sigma -> a sigma + b sigma^3 + c sigma^5: five steps bring singular values in [0.01, 1] into [0.68, 1.14]
 # (coefficients published by K. Jordan and others, 2024)
 NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)
@@ -85,6 +87,11 @@ def lib():
     L.e8q_gemv_core_escape.restype = e
     L.e8q_gemv_workspace_size.argtypes = [i64, i64, i64, i64]
     L.e8q_gemv_workspace_size.restype = sz
+    L.e8q_moe_core_escape.argtypes = [vp, vp, vp, i64, i64, i64, i32, vp, i32, vp, i32, i32, vp, e, i64, vp, e, i64, i32,
+                                      vp, vp, vp, e, vp, sz, vp, vp]
+    L.e8q_moe_core_escape.restype = e
+    L.e8q_moe_workspace_size.argtypes = [i64, i64, i64, i64, i64]
+    L.e8q_moe_workspace_size.restype = sz
     L.e8q_pack_escapes.argtypes = [vp, i64, i32, vp, vp, i64, vp, vp, sz, vp, vp]
     L.e8q_pack_escapes.restype = e
     L.e8q_unpack_escapes.argtypes = [vp, i64, vp, i64, i32, vp, vp, sz, vp, vp]
@@ -424,6 +431,65 @@ def e8q_gemv_core_escape(core_idx, esc, esc_count, shape, core_bound, row_scale,
         int(had_block), _ptr(x), _dtype_code(x), x.shape[1], _ptr(y_out), _ptr(workspace), workspace.numel(),
         _ptr(status), _stream(core_idx, stream))
     _check("e8q_gemv_core_escape", code)
+
+
+class _ExpertsStruct(ctypes.Structure):
+    _fields_ = [("core_idx", ctypes.c_void_p), ("esc", ctypes.c_void_p), ("esc_capacity", ctypes.c_int64),
+                ("esc_count", ctypes.c_void_p), ("row_scale", ctypes.c_void_p)]
+
+
+class Experts:
+    """``e8q_experts_t``: the exported form of ``shape = (experts, rows, cols)``
+    matrices, as ``e8q_encode_core_escape`` writes it for that batch (the
+    tensors are kept and must stay as they are)."""
+
+    def __init__(self, core_idx, esc, esc_count, row_scale, shape, esc_records=None):
+        experts, rows, cols = shape
+        _sized(core_idx, "core_idx", experts * rows * cols // 8, (torch.int16,)); _dev(esc, "esc", (torch.uint8,))
+        _sized(esc_count, "esc_count", experts, (torch.int64,)); _sized(row_scale, "row_scale", experts * rows)
+        cap = 0 if esc is None else esc.numel() // ESCAPE_RECORD_BYTES
+        if esc_records is not None:
+            cap = min(cap, int(esc_records))
+        self.shape, self.tensors = tuple(shape), (core_idx, esc, esc_count, row_scale)
+        self.struct = _ExpertsStruct(_ptr(core_idx), _ptr(esc), cap, _ptr(esc_count), _ptr(row_scale))
+        self.ref = ctypes.addressof(self.struct)
+
+
+def e8q_moe_workspace_size(experts, hidden, inter, tokens, top_k):
+    return int(lib().e8q_moe_workspace_size(int(experts), int(hidden), int(inter), int(tokens), int(top_k)))
+
+
+def e8q_moe_core_escape(gate, up, down, core_bound, x, expert_idx, expert_weight, y_out, workspace, status, router=None,
+                        signs_in=None, had_block_in=0, signs_down=None, had_block_down=0, activation=ACT_SILU,
+                        normalize=True, stream=None):
+    """``e8q_moe_core_escape``: a mixture-of-experts layer of ``x`` [tokens,
+    hidden] from the exported form.  ``gate`` and ``up`` are ``Experts`` of
+    shape (experts, inter, hidden), ``down`` of (experts, hidden, inter).  With
+    ``router`` [experts, hidden] the ``expert_idx`` (int32) and
+    ``expert_weight`` [tokens, k] are written; without it they are read."""
+    experts, inter, hidden = gate.shape
+    if up.shape != gate.shape or down.shape != (experts, hidden, inter):
+        raise ValueError("gate and up must be (experts, inter, hidden), down (experts, hidden, inter)")
+    _dev(x, "x", _WDT); _dev(router, "router", _WDT); _dev(y_out, "y_out", _WDT)
+    if x.dim() != 2 or x.shape[1] != hidden or y_out.shape != x.shape:
+        raise ValueError("x and y_out must be [tokens, hidden]")
+    if router is not None and tuple(router.shape) != (experts, hidden):
+        raise ValueError("router must be [experts, hidden]")
+    tokens = x.shape[0]
+    _dev(expert_idx, "expert_idx", (torch.int32,))
+    if expert_idx.dim() != 2 or expert_idx.shape[0] != tokens:
+        raise ValueError("expert_idx must be [tokens, k]")
+    k = expert_idx.shape[1]
+    _sized(expert_weight, "expert_weight", tokens * k)
+    _sized(signs_in, "signs_in", hidden, (torch.int8,)); _sized(signs_down, "signs_down", inter, (torch.int8,))
+    _dev(workspace, "workspace", (torch.uint8,)); _dev(status, "status", (torch.int32,))
+    code = lib().e8q_moe_core_escape(gate.ref, up.ref, down.ref, experts, hidden, inter, int(core_bound),
+                                     _ptr(signs_in), int(had_block_in), _ptr(signs_down), int(had_block_down),
+                                     int(activation), _ptr(x), _dtype_code(x), tokens, _ptr(router),
+                                     _dtype_code(router) if router is not None else F32, k, int(bool(normalize)),
+                                     _ptr(expert_idx), _ptr(expert_weight), _ptr(y_out), _dtype_code(y_out),
+                                     _ptr(workspace), _size(workspace), _ptr(status), _stream(x, stream))
+    _check("e8q_moe_core_escape", code)
 
 
 def e8q_pack_workspace_size(n):

@@ -20,7 +20,8 @@ LIB = os.path.join(PKG, "libe8q.so")
 
 SOURCES = ["e8q_common.hip", "e8q_tables.hip", "e8q_project.hip", "e8q_encode.hip", "e8q_ste.hip",
            "e8q_decode.hip", "e8q_roots.hip", "e8q_ptq.hip", "e8q_logprobs.hip", "e8q_embed.hip",
-           "e8q_orthogonal.hip", "e8q_distill.hip", "e8q_adjust.hip"]
+           "e8q_orthogonal.hip", "e8q_distill.hip", "e8q_adjust.hip",
+           "e8q_moe.hip"]
 # host program run before the library is compiled: writes the device table
 # blob and its layout header (embedded by e8q_tables.hip)
 TABLEGEN_SOURCES = ["e8q_tablegen.cpp", "e8q_tables_build.cpp", "e8q_core_table.cpp"]
@@ -35,10 +36,11 @@ FLAGS = [
     "-Wno-unused-command-line-argument",
 ]
 
-# Per-source additions.  The PTQ search and the GEMV keep their MFMA
+# Per-source additions.  The PTQ search, the GEMV and the experts keep their MFMA
 # accumulators in ordinary VGPRs (no copies out of the accumulation registers).
 SOURCE_FLAGS = {"e8q_ptq.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-                "e8q_decode.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+                "e8q_decode.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+                "e8q_moe.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 
 def hipcc():

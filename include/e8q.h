@@ -454,6 +454,71 @@ e8q_status_t e8q_gemv_core_escape(const uint16_t* core_idx,
 size_t e8q_gemv_workspace_size(int64_t batch, int64_t m, int64_t rows, int64_t cols);
 
 /* ---------------------------------------------------------------------------
+ * e8q_moe_core_escape -- a mixture-of-experts layer of a few tokens from the exported
+ * form (E8-QAT Figure 2(c): the exported form; the pages quantize expert weights
+ * too).  Per token, with G, U, D the experts' restored matrices (as
+ * e8q_decode_core_escape's w_hat, before any rounding; they are never formed):
+ *   p = softmax(router x),  e_1 ... e_k the k largest (equal ones by index),
+ *   w_j = p_{e_j}, divided by their sum if `normalize`,
+ *   y = sum_j w_j D_{e_j} ( act(G_{e_j} x) * (U_{e_j} x) ).
+ *   gate, up     host structs: [experts, inter, hidden] in the exported form
+ *   down         host struct: [experts, hidden, inter]
+ *   core_bound   of all three
+ *   signs_in, had_block_in       the rotation of gate and up (NULL: none), over hidden columns
+ *   signs_down, had_block_down   the rotation of down (NULL: none), over inter columns
+ *                (signs 8-byte aligned)
+ *   activation   E8Q_ACT_SILU: g / (1 + exp(-g)); E8Q_ACT_GELU_TANH: g (1 + tanh(
+ *                sqrt(2 / pi) (g + 0.044715 g^3))) / 2
+ *   x            [tokens, hidden] in x_dtype
+ *   router       [experts, hidden] in router_dtype; the logits are float64 sums.  Or NULL: the
+ *                places are the caller's
+ *   expert_idx, expert_weight   [tokens, top_k] int32 and float32: written with a router,
+ *                read without (a negative id is a place not used; an id >= experts is
+ *                not either and sets E8Q_STATUS_BAD_INDEX; an expert may be named twice)
+ *   y_out        [tokens, hidden] in y_dtype (bf16: nearest even); a token without a used
+ *                place has y = 0
+ *   workspace    e8q_moe_workspace_size(...) bytes, 256-byte aligned
+ * Rounding: x~ = R x (float32) is taken in fixed point, off by at most 2^(e-23) with
+ * 2^(e-1) <= max |x~| < 2^e (2^-22 of the largest), the row sums are exact, a product is rounded once to
+ * float32; so is down's, of h = act(g) u.  The sum over the places is float32, in their order.
+ * A token holding a NaN or infinity has NaN outputs, others are not affected
+ * (E8Q_STATUS_NONFINITE); a NaN router logit counts as -inf.  Malformed exports and bad
+ * scales are flagged as in e8q_decode_core_escape (the slot or row is 0); so is a
+ * record with |2z| > 2^14, which no encoder writes (E8Q_STATUS_X_RANGE).
+ * Limits: hidden, inter multiples of 8 and <= 32768; experts <= 1024; top_k <= 64;
+ * tokens * top_k <= 4096.
+ * ------------------------------------------------------------------------- */
+enum { E8Q_ACT_SILU = 0, E8Q_ACT_GELU_TANH = 1 };
+
+/* The exported form of [experts, rows, cols] matrices (device pointers), as
+ * e8q_encode_core_escape writes it for that batch. */
+typedef struct {
+    const uint16_t* core_idx;    /* [experts * rows * cols / 8] */
+    const e8q_escape_t* esc;     /* records; NULL only with esc_capacity == 0 */
+    int64_t esc_capacity;        /* how many records the array holds */
+    const int64_t* esc_count;    /* [experts] */
+    const float* row_scale;      /* [experts * rows] */
+} e8q_experts_t;
+
+e8q_status_t e8q_moe_core_escape(const e8q_experts_t* gate, const e8q_experts_t* up,
+                                 const e8q_experts_t* down,
+                                 int64_t experts, int64_t hidden, int64_t inter, int32_t core_bound,
+                                 const int8_t* signs_in, int32_t had_block_in,
+                                 const int8_t* signs_down, int32_t had_block_down,
+                                 int32_t activation,
+                                 const void* x, e8q_dtype_t x_dtype, int64_t tokens,
+                                 const void* router, e8q_dtype_t router_dtype,
+                                 int64_t top_k, int32_t normalize,
+                                 int32_t* expert_idx, float* expert_weight,
+                                 void* y_out, e8q_dtype_t y_dtype,
+                                 void* workspace, size_t workspace_bytes,
+                                 uint32_t* status_dev, void* stream);
+
+/* Workspace bytes e8q_moe_core_escape needs (0 on bad sizes); enough for fewer tokens too. */
+size_t e8q_moe_workspace_size(int64_t experts, int64_t hidden, int64_t inter, int64_t tokens,
+                              int64_t top_k);
+
+/* ---------------------------------------------------------------------------
  * e8q_pack_escapes -- escape records to root-packed records (E8-QAT Table 3).
  *   esc, n       the 20-byte records (4-byte aligned)
  *   core_bound   the encoder's B

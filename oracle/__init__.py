@@ -85,3 +85,4 @@ from .embed import embed, embed_grad  # noqa: F401
 from .orthogonal import orthogonalize, orthogonal_step  # noqa: F401
 from .distill import distill  # noqa: F401
 from .adjust import adjust_logits  # noqa: F401
+from .moe import exported_two_z, moe_route, moe_layer  # noqa: F401

@@ -89,3 +89,39 @@ def test_adjust_rejects(L):
                  _with(base, a4=1 << 40, a21=1 << 40), _with(big, a2=1 << 22, a3=16384, a4=16384, a19=0, a21=16384),
                  _with(base, a3=(1 << 31) - 16, a4=1 << 31, a19=0, a21=1 << 31)):
         assert f(*args) == UNSUPPORTED, args
+
+
+def test_moe_rejects(L):
+    import bit_e8_lattice_amd as e8q
+    ok = e8q._ExpertsStruct(0x10000, 0x10000, 5, 0x10000, 0x10000)
+    ref = ctypes.addressof
+    P = lambda v: ctypes.c_void_p(v)  # noqa: E731
+    need = L.e8q_moe_workspace_size(8, 256, 64, 4, 2)
+    assert need > 0
+    # gate, up, down, experts, hidden, inter, bound, signs_in, had, signs_down, had, act, x, dtype, tokens, router, dtype, k,
+    # normalize, idx, weight, y, dtype, ws, bytes, status, stream
+    base = [ref(ok), ref(ok), ref(ok), 8, 256, 64, 16, FAKE, 128, FAKE, 64, 0, FAKE, 1, 4, FAKE, 1, 2, 1, FAKE, FAKE, FAKE,
+            1, FAKE, need, FAKE, None]
+    f = L.e8q_moe_core_escape
+    structs = [e8q._ExpertsStruct(*v) for v in ((0, 0x10000, 5, 0x10000, 0x10000), (0x10001, 0x10000, 5, 0x10000, 0x10000),
+                                                (0x10000, 0, 5, 0x10000, 0x10000), (0x10000, 0x10000, -1, 0x10000, 0x10000),
+                                                (0x10000, 0x10002, 5, 0x10000, 0x10000), (0x10000, 0x10000, 5, 0, 0x10000),
+                                                (0x10000, 0x10000, 5, 0x10004, 0x10000), (0x10000, 0x10000, 5, 0x10000, 0))]
+    bad = [_with(base, **{f"a{i}": ref(s)}) for s in structs for i in range(3)]
+    bad += [_with(base, **{f"a{i}": None}) for i in (0, 1, 2, 12, 19, 20, 21, 23, 25)]
+    bad += [_with(base, a3=0), _with(base, a4=0), _with(base, a4=252), _with(base, a5=0), _with(base, a5=60),
+            _with(base, a6=-1), _with(base, a6=41), _with(base, a8=96), _with(base, a8=512), _with(base, a10=128),
+            _with(base, a11=2), _with(base, a13=2), _with(base, a14=0), _with(base, a16=3), _with(base, a17=0),
+            _with(base, a17=9), _with(base, a22=7), _with(base, a24=need - 1), _with(base, a23=P(0x10010)),
+            _with(base, a7=P(0x10004)), _with(base, a9=P(0x10004)), _with(base, a12=ODD), _with(base, a15=ODD),
+            _with(base, a21=ODD), _with(base, a19=P(0x10002)), _with(base, a20=P(0x10002))]
+    for args in bad:
+        assert f(*args) == INVALID, args
+    for args in (_with(base, a3=1025), _with(base, a4=32896), _with(base, a5=32832), _with(base, a14=2049),
+                 _with(base, a3=1024, a17=65)):
+        assert f(*args) == UNSUPPORTED, args
+    for args in ((0, 256, 64, 4, 2), (8, 252, 64, 4, 2), (8, 256, 64, 0, 2), (8, 256, 64, 4, 9), (8, 256, 64, 2049, 2),
+                 (1025, 256, 64, 4, 2), (8, 32776, 64, 4, 2)):
+        assert L.e8q_moe_workspace_size(*args) == 0
+    # host memory is read for the structs only; enough for fewer tokens too
+    assert all(L.e8q_moe_workspace_size(8, 256, 64, t, 2) <= need for t in (1, 2, 3))

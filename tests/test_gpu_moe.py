@@ -1,0 +1,181 @@
+"""e8q_moe_core_escape against float64, within the bounds of oracle/moe.py."""
+
+import numpy as np
+import pytest
+import torch
+
+import bit_e8_lattice_amd as e8q
+import oracle
+from gpu_util import device
+from moe_cases import Layer
+
+pytestmark = pytest.mark.gpu
+
+HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
+U = 2.0 ** -24
+
+
+def inputs(layer, tokens, x_dtype, router_dtype, seed):
+    e, h, _ = layer.shape
+    g = torch.Generator(device=layer.device).manual_seed(seed)
+    x = torch.randn((tokens, h), generator=g, device=layer.device)
+    x[:, torch.randint(0, h, (max(1, h // 100),), generator=g, device=layer.device)] *= 20.0
+    router = torch.randn((e, h), generator=g, device=layer.device) / h ** 0.5
+    return x.to(x_dtype), router.to(router_dtype)
+
+
+def close(y, want, tol):
+    got = y.float().cpu().numpy().astype(np.float64)
+    tol = tol + HALF[y.dtype] * np.abs(want) * (1 + 2.0 ** -10) + 1e-30
+    off = np.abs(got - want)
+    assert (off <= tol).all(), (off.max(), (off / tol).max())
+
+
+def check(layer, tokens, k, seed, normalize=True, act="silu", x_dtype=torch.bfloat16, router_dtype=torch.bfloat16,
+          y_dtype=torch.float32):
+    x, router = inputs(layer, tokens, x_dtype, router_dtype, seed)
+    y, idx, weight, st = layer.run(x, k, router, normalize, act, y_dtype)
+    assert st == 0
+    want_idx, want_w = oracle.moe_route(x.float().cpu().numpy(), router.float().cpu().numpy(), k, normalize)
+    assert np.array_equal(idx.cpu().numpy(), want_idx)
+    assert np.abs(weight.cpu().numpy() - want_w).max() <= 40 * U
+    want, tol = layer.expect(x, want_idx, want_w, act)
+    close(y, want, tol)
+    return x, router, y, idx, weight
+
+
+@pytest.mark.parametrize("experts,hidden,inter,bound,alpha,had_in,had_down,k,act", [
+    (2, 8, 8, 8, 3.0, 8, 8, 1, "silu"),
+    (1, 64, 24, 16, 3.0, 0, 0, 1, "gelu_tanh"),
+    (9, 520, 328, 24, 2.5, 8, 8, 2, "gelu_tanh"),
+    (5, 768, 256, 8, 1.0, 128, 64, 3, "silu"),              # most groups escape
+    (70, 256, 128, 16, 3.0, 32, 16, 8, "silu"),             # more than a wave of experts
+    (4, 2560, 144, 16, 2.0, 512, 16, 2, "silu"),            # digits in two parts
+    (3, 4096, 1024, 40, 3.0, 4096, 1024, 2, "silu"),        # wide rotations; the table in memory
+    (2, 8200, 72, 32, 2.0, 8, 0, 1, "silu"),                # more than 8192 columns
+    (2, 40, 8200, 16, 2.0, 8, 8, 2, "silu"),
+])
+@pytest.mark.parametrize("tokens", [1, 6, 23])
+def test_sizes(experts, hidden, inter, bound, alpha, had_in, had_down, k, act, tokens):
+    layer = Layer(experts, hidden, inter, bound, alpha, had_in, had_down, experts + hidden, device())
+    check(layer, tokens, k, tokens, normalize=tokens != 6, act=act, x_dtype=torch.float32 if tokens == 6 else torch.bfloat16,
+          router_dtype=torch.float32 if tokens == 23 else torch.bfloat16,
+          y_dtype=torch.bfloat16 if tokens == 23 else torch.float32)
+
+
+def test_expert_workload():
+    """The gate, up and down sizes of the expert workload."""
+    layer = Layer(8, 2048, 768, 16, 3.0, 128, 128, 5, device())
+    for tokens in (1, 2, 16):
+        check(layer, tokens, 4, tokens, y_dtype=torch.bfloat16)
+
+
+def test_many_tokens():
+    layer = Layer(3, 128, 64, 16, 3.0, 128, 64, 5, device())
+    check(layer, 700, 2, 1)
+    check(layer, 1365, 3, 2)
+
+
+def test_wide_escapes():
+    """Escaped points of more than eight bits, beside ordinary ones."""
+    layer = Layer(3, 256, 160, 16, 3.0, 32, 32, 8, device(), outliers=400)
+    assert all(np.abs(m[0]).max() > 2000 for m in layer.oracle)
+    check(layer, 7, 2, 3)
+
+
+def test_given_places():
+    """Routes of the caller: unused places, an expert named twice, ids out of range, a token without a place."""
+    layer = Layer(6, 256, 128, 16, 3.0, 128, 128, 9, device())
+    x, _ = inputs(layer, 9, torch.float32, torch.float32, 2)
+    idx = torch.randint(0, 6, (9, 4), dtype=torch.int32, device=x.device)
+    idx[0] = -1
+    idx[1] = 3
+    idx[2, 1:] = -5
+    weight = torch.randn((9, 4), device=x.device)
+    keep, keep_w = idx.clone(), weight.clone()
+    y, _, _, st = layer.run(x, 4, idx=idx, weight=weight)
+    assert st == 0 and torch.equal(idx, keep) and torch.equal(weight, keep_w)
+    want, tol = layer.expect(x, idx.cpu().numpy(), weight.cpu().numpy())
+    close(y, want, tol)
+    assert not y[0].any()
+    idx[4, 2] = 6
+    y, _, _, st = layer.run(x, 4, idx=idx, weight=weight)
+    assert st == e8q.STATUS_BITS["BAD_INDEX"]
+    want, tol = layer.expect(x, idx.cpu().numpy(), weight.cpu().numpy())
+    close(y, want, tol)
+
+
+def test_ties_take_the_lowest_index():
+    layer = Layer(5, 64, 16, 8, 3.0, 0, 0, 9, device())
+    x, router = inputs(layer, 3, torch.float32, torch.float32, 2)
+    router[3] = router[1]
+    router[4] = router[1]
+    x[2] = 0                                               # every logit 0
+    y, idx, weight, st = layer.run(x, 4, router)
+    want_idx, want_w = oracle.moe_route(x.cpu().numpy(), router.cpu().numpy(), 4, True)
+    assert st == 0 and np.array_equal(idx.cpu().numpy(), want_idx) and not y[2].any()
+    assert idx[2].tolist() == [0, 1, 2, 3]
+
+
+def test_malformed_data():
+    """Non-finite tokens, bad scales, indices past the core, missing and impossible records."""
+    layer = Layer(4, 256, 64, 16, 1.5, 128, 64, 10, device())
+    x, router = inputs(layer, 5, torch.float32, torch.float32, 3)
+    clean, idx, weight, _ = layer.run(x, 2, router)
+    bad = x.clone()
+    bad[1, 3] = float("nan")
+    bad[3, 5] = float("inf")
+    y, idx2, _, st = layer.run(bad, 2, router)
+    assert st == e8q.STATUS_BITS["NONFINITE"]
+    assert torch.isnan(y[[1, 3]]).all() and torch.equal(y[[0, 2, 4]], clean[[0, 2, 4]])
+    assert ((idx2 >= 0) & (idx2 < 4)).all()
+    # a scale that is no positive number: the row is 0
+    core, esc, cnt, scale = layer.down.tensors
+    keep = scale.clone()
+    scale[int(idx[0, 0]) * 256 + 7] = float("nan")
+    scale[int(idx[0, 0]) * 256 + 9] = -1.0
+    layer.oracle[2] = (layer.oracle[2][0], scale.cpu().numpy().reshape(4, 256))
+    y, _, _, st = layer.run(x, 2, router)
+    assert st == e8q.STATUS_BITS["BAD_SCALE"]
+    close(y, *layer.expect(x, idx.cpu().numpy(), weight.cpu().numpy()))
+    scale.copy_(keep)
+    layer.oracle[2] = (layer.oracle[2][0], scale.cpu().numpy().reshape(4, 256))
+    # an index past the core and an escaped slot without its record decode to 0; so does an impossible record
+    used = int(idx[0, 0])
+    groups = 256 * 64 // 8
+    slots = core.view(4, groups)
+    z = layer.oracle[2][0].reshape(4, groups, 8)
+    plain = (slots[used] != -1).nonzero()[:2, 0].tolist()
+    keep = core.clone()
+    for value, flag in ((oracle.core_size(16), "BAD_INDEX"), (-1, "ESC_MISSING")):
+        slots[used, plain[0]] = value
+        was = z[used, plain[0]].copy()
+        z[used, plain[0]] = 0
+        y, _, _, st = layer.run(x, 2, router)
+        assert st == e8q.STATUS_BITS[flag]
+        close(y, *layer.expect(x, idx.cpu().numpy(), weight.cpu().numpy()))
+        z[used, plain[0]] = was
+        core.copy_(keep)
+    first = int(cnt[:used].sum())
+    rec = esc.view(-1, 20)[first].view(torch.int16)
+    kept = rec.clone()
+    rec[2 + 3] = 32767
+    group = int(esc.view(-1, 20)[first].view(torch.int32)[0])
+    z[used, group] = 0
+    y, _, _, st = layer.run(x, 2, router)
+    assert st == e8q.STATUS_BITS["X_RANGE"]
+    close(y, *layer.expect(x, idx.cpu().numpy(), weight.cpu().numpy()))
+    rec.copy_(kept)
+
+
+def test_streams_workspaces_and_smaller_batches():
+    layer = Layer(7, 512, 96, 16, 3.0, 128, 32, 11, device())
+    e, h, f = layer.shape
+    ws = torch.zeros(e8q.e8q_moe_workspace_size(e, h, f, 12, 3), dtype=torch.uint8, device=layer.device)
+    x, router = inputs(layer, 12, torch.bfloat16, torch.bfloat16, 4)
+    first = layer.run(x, 3, router, ws=ws)
+    for t in (12, 5, 1):
+        for stream in (None, torch.cuda.Stream()):
+            y, idx, weight, st = layer.run(x[:t].contiguous(), 3, router, ws=ws, stream=stream)
+            assert st == 0 and torch.equal(y, first[0][:t]) and torch.equal(idx, first[1][:t])
+            assert torch.equal(weight, first[2][:t])
