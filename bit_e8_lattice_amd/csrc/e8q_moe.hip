@@ -5,23 +5,27 @@
 //   y = sum_j w_j D_{e_j} ( act(G_{e_j} x) * (U_{e_j} x) ),   G, U, D = R^T (s z).
 //
 // R is orthogonal, so a product with an expert's matrix is s_r sum_g z_g . x~_g with
-// x~ = R x = kappa H (sigma x), as in e8q_gemv_core_escape: x is rotated once, the
-// weights never are.  x~ is held in fixed point, N = rint(x~ 2^(22 - e)) with
-// 2^(e-1) <= max |x~| < 2^e, written as three signed base-256 digits, and the row sums
-// sum 2z N are exact int32 sums on the int8 matrix cores:
+// x~ = R x = kappa H (sigma x), as in e8q_gemv_core_escape: x is rotated, the
+// weights never are.  x~ is held in fixed point, N = rint(x~ S) with S = 8355000 / max |x~|,
+// written as three signed base-256 digits, and the row sums sum 2z N are exact int32
+// sums on the int8 matrix cores:
 //   A (16 x 64): 16 rows x 8 groups of points, a byte for each 2z;
 //   B (64 x 16): the same groups' digits, column 3 j + d holding digit d of token j.
-// So one sweep over an expert's indices serves five tokens.  The rounding to fixed point,
-// |x~ - N 2^(e-22)| <= 2^(e-23) (2^-22 of the largest), is the only one in the product
-// besides the last to float32: it keeps three digits because 2^-14 of the largest (two
-// digits) would be more than a bfloat16 activation's own rounding in a vector with one
-// strong channel.  An escaped slot's 2z has up to 16 bits: its low byte goes into A and,
-// where there is one, its high byte into a second product.
+// So one product serves five tokens, and a sweep over an expert's indices up to three
+// such products (15 tokens).  The rounding to fixed point, half a step of 2^-23 of the largest |x~|, is
+// of the size of float32's own; two digits (2^-15) would be more than a bfloat16 activation's
+// rounding in a vector with one strong channel.
+// An escaped slot's 2z has up to 16 bits: its low byte goes into A, and where one has a
+// high byte the tile is swept once more for those.
 //
-// Launches: router products (float64: a tie or near-tie must not depend on the order of
-// a sum) with the rotation of x beside them; the choice of experts; gate and up of the chosen
-// experts with the activation; the rotation of its result; down; the weighted sum, in
-// the order of the places.
+// Two tiles of 16 rows go together (gate and up of the same rows; two neighbouring
+// tiles of down): they share every read of the digits from LDS.
+//
+// Launches: the router's products (float64: a near-tie must not depend on the
+// order of a sum) beside the digits of x; the choice of experts (a few logits: inside the
+// next); gate and up of the chosen experts with the activation; down, whose blocks rotate h and
+// make its digits (past 2048 columns a launch before it); the weighted sum in the order of
+// the places (up to 16 places: inside down).
 #include <float.h>
 
 #include "e8q_device.hpp"
@@ -32,12 +36,18 @@ namespace e8q {
 
 constexpr uint32_t kMoeThreads = 1024, kMoeWaves = 16;
 constexpr uint32_t kMoeTile = 16;            // rows of a matrix instruction
-constexpr uint32_t kMoeTokens = 5;           // tokens of a sweep: 3 of the 16 columns each
+constexpr uint32_t kMoeTokens = 5;           // tokens of a product: 3 of the 16 columns each
+constexpr uint32_t kMoeGroups = 2;           // products of a sweep, at most
+constexpr uint32_t kMoeVectors = 16;         // vectors whose digits are in LDS, at most
 constexpr uint32_t kMoeSlab = 8;             // chunks of 256 columns whose digits are in LDS at a time
-constexpr uint32_t kMoeTable = 9216;         // points whose table fits LDS beside them
+constexpr uint32_t kMoeSmall = 4096;         // points of a table at a fixed place in LDS
+constexpr uint32_t kMoeOwn = 32 * 1024;      // LDS of the kernels' own, at most
+constexpr uint32_t kMoeLds = 160 * 1024;
+constexpr uint32_t kMoeInline = 256;         // logits that every block of the next launch ranks itself
+constexpr uint32_t kMoeDirect = 16;          // places that down's blocks sum up themselves
 constexpr int64_t kMoeExperts = 1024, kMoeTopK = 64, kMoeRoutes = 4096, kMoeCols = 32768;
-constexpr int kDigitBits = 22;
-constexpr int kBadExponent = 1 << 20;        // the exponent of a vector with a NaN or infinity
+constexpr float kMoeFull = 8355000.0f;       // largest |N|: below 127 (2^16 + 2^8 + 1)
+constexpr float kMoeLeast = 0x1p-100f;       // a vector's largest element, at least (S stays finite)
 
 typedef int moe_i32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned short moe_u16x2 __attribute__((ext_vector_type(2)));
@@ -49,6 +59,11 @@ struct MoeMatrix {
     uint64_t esc_capacity;
     const float* scale;         // [experts, rows]
     const uint64_t* offsets;    // [experts + 1], in the workspace
+};
+
+// One sweep: up to 5 G tokens of an expert, their routes from list[first] on.
+struct MoeItem {
+    uint32_t expert, first, n, pad;
 };
 
 struct MoeArgs {
@@ -67,17 +82,25 @@ struct MoeArgs {
     MoeMatrix gate, up, down;
     uint64_t* offsets;          // [3, experts + 1]
     uint8_t* xd;                // digits of x: [tokens] x 3 bytes a (padded) column
-    int* xe;                    // their exponents
+    struct Vector* xs;          // their steps (NaN: a vector with a NaN or infinity) and sums
     float* h;                   // [tokens k, inter]
     uint8_t* hd;
-    int* he;
+    struct Vector* hs;
     float* part;                // [tokens k, hidden]
     void* y;
     int y_bf16;
     const uint32_t* pts;
     uint32_t npts;
-    uint32_t rows_in, rows_down;     // rows of a block
-    uint32_t parts_in, parts_down;   // blocks of an expert
+    int table;                       // where the point table goes (Points)
+    FastDiv k_div, experts_div;
+    uint32_t split_direct;           // waves of a place
+    int ready_down;                  // the digits of h are in the workspace
+    MoeItem* items;                  // the sweeps
+    uint32_t* n_items;
+    uint16_t* list;                  // [tokens k] routes by expert
+    uint32_t most;                   // tokens of a sweep
+    int choose;                      // the product's blocks choose the experts, without items
+    int direct;                      // down sums over the places
     uint32_t* status;
 };
 
@@ -156,19 +179,21 @@ __device__ __forceinline__ uint32_t abs_bits(const float (&v)[8]) {
     return m;
 }
 
-// e with 2^(e-1) <= max < 2^e from the bits of the largest |value| (0: 0).
-__device__ __forceinline__ int exponent_of(uint32_t bits) {
-    if (bits >= 0x7F800000u) return kBadExponent;
-    return bits == 0u ? 0 : __builtin_amdgcn_frexp_expf(__uint_as_float(bits));
+// S from the bits of the largest |x~|, 0 where a value is not finite.
+__device__ __forceinline__ float scale_of(uint32_t bits) {
+    return bits >= 0x7F800000u ? 0.0f : kMoeFull / fmaxf(__uint_as_float(bits), kMoeLeast);
 }
 
-// The three digits of a group, 8 bytes each.
-__device__ __forceinline__ void digits8(const float (&v)[8], int e, uint2 (&d)[3]) {
+__device__ __forceinline__ double step_of(float s) { return s == 0.0f ? __builtin_nan("") : 1.0 / double(s); }
+
+// The three digits of a group, 8 bytes each (0 where S is 0); returns the sum of N.
+__device__ __forceinline__ int digits8(const float (&v)[8], float s, uint2 (&d)[3]) {
+    int sum = 0;
     uint32_t w[3][2] = {{0u, 0u}, {0u, 0u}, {0u, 0u}};
-    const bool fin = e != kBadExponent;          // digits of a non-finite vector are not used
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        int n = fin ? int(__builtin_rintf(__builtin_ldexpf(v[i], kDigitBits - e))) : 0;
+        int n = s != 0.0f ? int(__builtin_rintf(v[i] * s)) : 0;
+        sum += n;
         const int d2 = int(int8_t(uint8_t(n)));
         n = (n - d2) >> 8;
         const int d1 = int(int8_t(uint8_t(n)));
@@ -180,24 +205,53 @@ __device__ __forceinline__ void digits8(const float (&v)[8], int e, uint2 (&d)[3
     }
 #pragma unroll
     for (int k = 0; k < 3; ++k) d[k] = make_uint2(w[k][0], w[k][1]);
+    return sum;
 }
+
+// What a vector's products need beside its digits: 1 / S, and the sum of N.
+struct Vector {
+    double step, sum;
+};
+
+__device__ __forceinline__ int add_lanes(int v) {
+    v += int(lane_xor<32>(uint32_t(v)));
+    v += int(lane_xor<16>(uint32_t(v)));
+    v += int(lane_xor<8>(uint32_t(v)));
+    v += int(lane_xor<4>(uint32_t(v)));
+    v += int(lane_xor<2>(uint32_t(v)));
+    v += int(lane_xor<1>(uint32_t(v)));
+    return v;
+}
+
+// The sum over a wave of values below 2^28: in halves that stay below 2^31.
+__device__ __forceinline__ double sum_wave(int v) { return double(add_lanes(v >> 12)) * 4096.0 + double(add_lanes(v & 4095)); }
 
 // Digits in the order of the sweep: a lane of quarter q takes groups 32 c + 8 q + 2 s, + 1 at
 // step s of chunk c, so entry ((c 4 + s) 4 + q) holds both groups' digits, 16 bytes for
-// each digit.  Byte offset of a group's half of digit 0 in the vector's entries, `columns` digits apart.
+// each digit.  Byte offset of a group's half of digit 0 in the entries, `columns` digits apart.
 __device__ __forceinline__ uint32_t digit_offset(uint32_t g, uint32_t columns) {
     const uint32_t entry = ((g >> 5) * 4u + ((g >> 1) & 3u)) * 4u + ((g >> 3) & 3u);
     return entry * columns * 16u + (g & 1u) * 8u;
 }
 
-// Rotation and digits of one vector by the block: `load` gives a group's values.
+__device__ __forceinline__ uint32_t max_wave(uint32_t m) {
+    m = max(m, lane_xor<32>(m));
+    m = max(m, lane_xor<16>(m));
+    m = max(m, lane_xor<8>(m));
+    m = max(m, lane_xor<4>(m));
+    m = max(m, lane_xor<2>(m));
+    m = max(m, lane_xor<1>(m));
+    return m;
+}
+
+// Rotation and digits of one vector by the block, into memory: `load` gives a group's values.
 template <class Load>
 __device__ __forceinline__ void vector_digits(Load&& load, uint32_t cols, const int8_t* signs, uint32_t had, float kappa,
-                                              uint8_t* out, int* exponent) {
+                                              uint8_t* out, Vector* vec) {
     constexpr int kPasses = int(kMoeCols / (kMoeThreads * 8));
     __shared__ float4 s_wide4[kMoeThreads * 2];
-    float* s_wide = reinterpret_cast<float*>(s_wide4);
     __shared__ uint32_t s_max[kMoeWaves];
+    float* s_wide = reinterpret_cast<float*>(s_wide4);
     const uint32_t tid = threadIdx.x, groups = cols / 8u, padded = moe_chunks(cols) * 32u;
     float v[kPasses][8];
     uint32_t m = 0u;
@@ -212,82 +266,148 @@ __device__ __forceinline__ void vector_digits(Load&& load, uint32_t cols, const 
             m = max(m, abs_bits(v[p]));
         }
     }
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) m = max(m, uint32_t(__shfl_xor(m, off, 64)));
+    m = max_wave(m);
     if ((tid & 63u) == 0u) s_max[tid >> 6] = m;
     __syncthreads();
 #pragma unroll
     for (uint32_t w = 0; w < kMoeWaves; ++w) m = max(m, s_max[w]);
-    const int e = exponent_of(m);
+    const float s = scale_of(m);
+    int total = 0;
 #pragma unroll
     for (int p = 0; p < kPasses; ++p) {
         const uint32_t g = uint32_t(p) * kMoeThreads + tid;
         if (g < padded) {
             uint2 d[3];
-            digits8(v[p], e, d);
+            total += digits8(v[p], s, d);
 #pragma unroll
             for (uint32_t k = 0; k < 3u; ++k)
                 *reinterpret_cast<uint2*>(out + digit_offset(g, 3u) + k * 16u) = d[k];
         }
     }
-    if (tid == 0u) *exponent = e;
-}
-
-// Digits of x, one block a token; three more blocks scan the matrices' escape counts.
-__global__ __launch_bounds__(kMoeThreads) void moe_prepare_kernel(MoeArgs a) {
-    if (blockIdx.x < a.tokens) {
-        const uint32_t t = blockIdx.x;
-        vector_digits([&](uint32_t g, float (&v)[8]) { load8(a.x, a.x_bf16, uint64_t(t) * a.hidden + g * 8u, v); },
-                      a.hidden, a.signs_in, a.had_in, a.kappa_in, a.xd + t * moe_digit_bytes(a.hidden), a.xe + t);
-        return;
-    }
-    __shared__ uint64_t s_sum[kMoeWaves];
-    const uint32_t which = blockIdx.x - a.tokens, tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
-    const MoeMatrix& m = which == 0u ? a.gate : which == 1u ? a.up : a.down;
-    const int64_t c = tid < a.experts ? m.esc_count[tid] : 0;
-    uint64_t run = c > 0 ? uint64_t(c) : 0ull;
-    const uint64_t own = run;
-    for (uint32_t off = 1u; off < 64u; off *= 2u) {
-        const uint64_t o = __shfl_up(run, off, 64);
-        if (lane >= off) run += o;
-    }
-    if (lane == 63u) s_sum[wave] = run;
+    __shared__ double s_sum[kMoeWaves];
+    const double part = sum_wave(total);
+    if ((tid & 63u) == 0u) s_sum[tid >> 6] = part;
     __syncthreads();
-    for (uint32_t w = 0; w < wave; ++w) run += s_sum[w];
-    uint64_t* out = a.offsets + uint64_t(which) * (a.experts + 1u);
-    if (tid < a.experts) out[tid] = min(run - own, m.esc_capacity);
-    if (tid == a.experts - 1u) out[a.experts] = min(run, m.esc_capacity);
+    if (tid == 0u) {
+        double sum = 0.0;
+        for (uint32_t w = 0; w < kMoeWaves; ++w) sum += s_sum[w];
+        *vec = {step_of(s), sum};
+    }
 }
 
-__global__ __launch_bounds__(kMoeThreads) void moe_digits_kernel(MoeArgs a) {
+__global__ __launch_bounds__(kMoeThreads) void moe_inner_digits_kernel(MoeArgs a) {
     const uint32_t r = blockIdx.x;
     const int32_t e = a.route[r];
     if (e < 0 || uint32_t(e) >= a.experts) return;
     vector_digits([&](uint32_t g, float (&v)[8]) { load8(a.h, 0, uint64_t(r) * a.inter + g * 8u, v); }, a.inter,
-                  a.signs_down, a.had_down, a.kappa_down, a.hd + r * moe_digit_bytes(a.inter), a.he + r);
+                  a.signs_down, a.had_down, a.kappa_down, a.hd + r * moe_digit_bytes(a.inter), a.hs + r);
+}
+
+// The same for `n` vectors of at most 2048 columns and rotations within a wave, into LDS: vector j into columns
+// 3 (j % 5) ... of part j / 5 of `digits`, its numbers into `vec`.  A wave takes 64 groups of a vector, the block as
+// many vectors at a time as it has waves for (a loop, not unrolled: code that runs once costs its fetch).  Ends with a barrier.
+template <class Load>
+__device__ __forceinline__ void vectors_lds(Load&& load, uint32_t n, uint32_t cols, const int8_t* signs, uint32_t had,
+                                            float kappa, uint4* digits, Vector* vec, uint32_t* s_max,
+                                            double* s_sum) {
+    const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t groups = cols / 8u, padded = moe_chunks(cols) * 32u, quarters = (padded + 63u) / 64u;
+    const uint32_t at_once = kMoeWaves / quarters, mine = wave / quarters, first = mine * quarters;
+    const uint32_t g = (wave - first) * 64u + lane, entries = moe_chunks(cols) * 16u;
+#pragma unroll 1
+    for (uint32_t j0 = 0; j0 < n; j0 += at_once) {
+        const uint32_t j = j0 + mine;
+        const bool live = mine < at_once && j < n;
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = 0.0f;
+        if (live && g < groups) load(j, g, v);
+        rotate8(v, signs, had, kappa, g, live && g < groups, nullptr);
+        const uint32_t m = max_wave(abs_bits(v));
+        if (j0 > 0u) __syncthreads();                // the maxima before are read
+        if (lane == 0u) s_max[wave] = m;
+        __syncthreads();
+        uint32_t most = 0u;
+        for (uint32_t q = 0; q < quarters; ++q) most = max(most, s_max[min(first + q, kMoeWaves - 1u)]);
+        const float s = scale_of(most);
+        int total = 0;
+        if (live && g < padded) {
+            uint2 d[3];
+            total = digits8(v, s, d);
+            char* out = reinterpret_cast<char*>(digits) + (j / kMoeTokens) * entries * 256u + (j % kMoeTokens) * 48u +
+                        digit_offset(g, 16u);
+#pragma unroll
+            for (uint32_t k = 0; k < 3u; ++k) *reinterpret_cast<uint2*>(out + k * 16u) = d[k];
+        }
+        const double sum = sum_wave(total);
+        if (lane == 0u) s_sum[wave] = sum;
+        __syncthreads();
+        if (live && g == 0u) {
+            double all = 0.0;
+            for (uint32_t q = 0; q < quarters; ++q) all += s_sum[first + q];
+            vec[j] = {step_of(s), all};
+        }
+    }
+    __syncthreads();
 }
 
 // ------------------------------------------------------------ router
 
-constexpr uint32_t kRouteTokens = 4;     // tokens a wave multiplies with one expert's router row
+constexpr uint32_t kRouteTokens = 2;     // tokens a wave multiplies with one expert's router row
 
-__global__ __launch_bounds__(256) void moe_logits_kernel(MoeArgs a) {
-    const uint32_t lane = threadIdx.x & 63u, e = blockIdx.x * 4u + (threadIdx.x >> 6), t0 = blockIdx.y * kRouteTokens;
+// The first launch.  Blocks [0, 3): running sums of the matrices' escape counts; [3, 3 + tokens): the digits of x; the
+// others: logits, a wave for an expert and up to kRouteTokens tokens.
+__global__ __launch_bounds__(kMoeThreads) void moe_prepare_kernel(MoeArgs a) {
+    __shared__ uint64_t s_sum[kMoeWaves];
+    const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
+    if (blockIdx.x < 3u) {
+        const MoeMatrix& m = blockIdx.x == 0u ? a.gate : blockIdx.x == 1u ? a.up : a.down;
+        const int64_t c = tid < a.experts ? m.esc_count[tid] : 0;
+        const uint64_t own = c > 0 ? uint64_t(c) : 0ull;
+        uint64_t run = own;
+        for (uint32_t off = 1u; off < 64u; off *= 2u) {
+            const uint64_t o = __shfl_up(run, off, 64);
+            if (lane >= off) run += o;
+        }
+        if (lane == 63u) s_sum[wave] = run;
+        __syncthreads();
+        for (uint32_t w = 0; w < wave; ++w) run += s_sum[w];
+        uint64_t* out = a.offsets + uint64_t(blockIdx.x) * (a.experts + 1u);
+        if (tid < a.experts) out[tid] = min(run - own, m.esc_capacity);
+        if (tid == a.experts - 1u) out[a.experts] = min(run, m.esc_capacity);
+        return;
+    }
+    if (blockIdx.x < 3u + a.tokens) {
+        const uint32_t t = blockIdx.x - 3u;
+        vector_digits([&](uint32_t g, float (&v)[8]) { load8(a.x, a.x_bf16, uint64_t(t) * a.hidden + g * 8u, v); },
+                      a.hidden, a.signs_in, a.had_in, a.kappa_in, a.xd + t * moe_digit_bytes(a.hidden), a.xs + t);
+        return;
+    }
+    const uint32_t blocks = (a.experts + kMoeWaves - 1u) / kMoeWaves, b = blockIdx.x - 3u - a.tokens, chunk = b / blocks;
+    const uint32_t e = (b - chunk * blocks) * kMoeWaves + wave, t0 = chunk * kRouteTokens;
     if (e >= a.experts) return;
     const uint32_t nt = min(kRouteTokens, a.tokens - t0);
     double acc[kRouteTokens] = {};
-    for (uint32_t g = lane; g < a.hidden / 8u; g += kWave) {
-        float w[8], x[8];
-        load8(a.router, a.router_bf16, uint64_t(e) * a.hidden + g * 8u, w);
-        double wd[8];
+    constexpr uint32_t kEach = 2u;                   // groups of a lane whose loads go together
+    for (uint32_t g0 = lane; g0 < a.hidden / 8u; g0 += kEach * kWave) {
+        float w[kEach][8], x[kRouteTokens][kEach][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) wd[i] = double(w[i]);
+        for (uint32_t i = 0; i < kEach; ++i) {
+            const uint32_t g = min(g0 + i * kWave, a.hidden / 8u - 1u);
+            load8(a.router, a.router_bf16, uint64_t(e) * a.hidden + g * 8u, w[i]);
 #pragma unroll
-        for (uint32_t t = 0; t < kRouteTokens; ++t) {
-            if (t >= nt) break;
-            load8(a.x, a.x_bf16, uint64_t(t0 + t) * a.hidden + g * 8u, x);
+            for (uint32_t t = 0; t < kRouteTokens; ++t)
+                load8(a.x, a.x_bf16, uint64_t(min(t0 + t, a.tokens - 1u)) * a.hidden + g * 8u, x[t][i]);
+        }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[t] = fma(wd[i], double(x[i]), acc[t]);
+        for (uint32_t i = 0; i < kEach; ++i) {
+            if (g0 + i * kWave >= a.hidden / 8u) break;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const double wd = double(w[i][k]);
+#pragma unroll
+                for (uint32_t t = 0; t < kRouteTokens; ++t) acc[t] = fma(wd, double(x[t][i][k]), acc[t]);
+            }
         }
     }
 #pragma unroll
@@ -298,399 +418,1019 @@ __global__ __launch_bounds__(256) void moe_logits_kernel(MoeArgs a) {
     }
 }
 
-// The k largest logits of a token (equal ones by index, NaN as -inf) and their weights, one wave a token.
-__global__ __launch_bounds__(256) void moe_choose_kernel(MoeArgs a) {
-    constexpr int kEach = int(kMoeExperts / kWave);
-    const uint32_t lane = threadIdx.x & 63u, t = blockIdx.x * 4u + (threadIdx.x >> 6);
-    if (t >= a.tokens) return;
-    const double* row = a.logits + uint64_t(t) * a.experts;
-    double v[kEach];
-    uint32_t taken = 0u, flags = 0u;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-        const uint32_t e = uint32_t(i) * kWave + lane;
-        v[i] = -INFINITY;
-        if (e < a.experts) {
-            v[i] = row[e];
-            if (!(v[i] - v[i] == 0.0)) flags |= E8Q_STATUS_NONFINITE;
-            if (v[i] != v[i]) v[i] = -INFINITY;
-        } else {
-            taken |= 1u << i;
+// A logit's place in the order of the values; NaN below everything.
+__device__ __forceinline__ uint64_t logit_key(double v) {
+    if (v != v) return 0ull;
+    const uint64_t b = uint64_t(__double_as_longlong(v + 0.0));
+    return (b >> 63) ? ~b : b | 0x8000000000000000ull;
+}
+
+// Logits of a token that are greater than that of expert e, or equal and before it: by the keys' high halves, and by
+// the whole keys where another has the same.
+__device__ __forceinline__ uint32_t logit_rank(const uint32_t* high, const uint32_t* low, uint32_t experts, uint32_t e) {
+    const uint32_t own = high[e];
+    uint32_t rank = 0u, same = 0u;
+#pragma unroll 16
+    for (uint32_t j = 0; j < experts; ++j) {
+        const uint32_t h = high[j];
+        rank += h > own ? 1u : 0u;
+        same += h == own ? 1u : 0u;
+    }
+    if (same > 1u) {
+        const uint32_t mine = low[e];
+#pragma unroll 8
+        for (uint32_t j = 0; j < experts; ++j) {
+            const uint32_t l = low[j];
+            rank += high[j] == own && (l > mine || (l == mine && j < e)) ? 1u : 0u;
         }
     }
-    flush_status(flags, a.status);
-    double most = -INFINITY, mine = -INFINITY;       // the largest; the logit of place `lane`
-    int32_t place = -1;
-    for (uint32_t j = 0; j < a.k; ++j) {
-        double best = -INFINITY;
-        uint32_t at = 0xFFFFFFFFu;
-#pragma unroll
-        for (int i = 0; i < kEach; ++i)
-            if (!((taken >> i) & 1u) && (at == 0xFFFFFFFFu || v[i] > best)) {
-                best = v[i];
-                at = uint32_t(i) * kWave + lane;
-            }
-#pragma unroll
-        for (int off = 32; off >= 1; off >>= 1) {
-            const double ob = __shfl_xor(best, off, 64);
-            const uint32_t oa = uint32_t(__shfl_xor(int(at), off, 64));
-            if (oa != 0xFFFFFFFFu && (at == 0xFFFFFFFFu || ob > best || (ob == best && oa < at))) {
-                best = ob;
-                at = oa;
-            }
+    return rank;
+}
+
+// The weights of a token's places from their logits (in LDS, by place), by one wave.
+__device__ __forceinline__ float place_weight(const MoeArgs& a, const double* chosen, const double* logits, uint32_t lane) {
+    const double most = chosen[0];
+    const float own = lane < a.k ? expf(float(chosen[lane] - most)) : 0.0f;
+    float sum = own;
+    if (!a.normalize) {
+        sum = 0.0f;
+        for (uint32_t e = lane; e < a.experts; e += kWave) {
+            const double v = logits[e];
+            sum += v != v ? 0.0f : expf(float(v - most));
         }
-        if ((at & 63u) == lane) taken |= 1u << (at >> 6);
-        if (j == 0u) most = best;
-        if (lane == j) {
-            mine = best;
-            place = int32_t(at);
-        }
-    }
-    float sum = 0.0f;
-    const float own = lane < a.k ? expf(float(mine - most)) : 0.0f;
-    if (a.normalize) {
-        sum = own;
-    } else {
-#pragma unroll
-        for (int i = 0; i < kEach; ++i)
-            if (uint32_t(i) * kWave + lane < a.experts) sum += expf(float(v[i] - most));
     }
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
-    if (lane < a.k) {
-        a.route[uint64_t(t) * a.k + lane] = place;
-        a.weight[uint64_t(t) * a.k + lane] = own / sum;
+    return own / sum;
+}
+
+// The choice of experts, a block a token.
+__global__ __launch_bounds__(256) void moe_choose_kernel(MoeArgs a) {
+    __shared__ uint32_t s_high[kMoeExperts], s_low[kMoeExperts];
+    __shared__ double s_chosen[kMoeTopK];
+    const uint32_t t = blockIdx.x, tid = threadIdx.x, lane = tid & 63u;
+    const double* row = a.logits + uint64_t(t) * a.experts;
+    uint32_t flags = 0u;
+    for (uint32_t e = tid; e < a.experts; e += 256u) {
+        const double v = row[e];
+        if (!(v - v == 0.0)) flags |= E8Q_STATUS_NONFINITE;
+        const uint64_t key = logit_key(v);
+        s_high[e] = uint32_t(key >> 32);
+        s_low[e] = uint32_t(key);
     }
+    flush_status(flags, a.status);
+    __syncthreads();
+    for (uint32_t e = tid; e < a.experts; e += 256u) {
+        const uint32_t rank = logit_rank(s_high, s_low, a.experts, e);
+        if (rank < a.k) {
+            a.route[uint64_t(t) * a.k + rank] = int32_t(e);
+            s_chosen[rank] = row[e];
+        }
+    }
+    __syncthreads();
+    if (tid >= kWave) return;
+    const float w = place_weight(a, s_chosen, row, lane);
+    if (lane < a.k) a.weight[uint64_t(t) * a.k + lane] = w;
+}
+
+// The sweeps: the routes by expert (their order within one has no effect on any result), and an item for every `most` of
+// them; the items past an expert's first come first, so that an expert that many tokens chose does not hold up the end.
+__global__ __launch_bounds__(kMoeThreads) void moe_plan_kernel(MoeArgs a) {
+    __shared__ uint32_t s_count[kMoeExperts], s_first[kMoeExperts], s_wave[3][kMoeWaves];
+    const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6, routes = a.tokens * a.k;
+    constexpr uint32_t kEach = uint32_t(kMoeRoutes) / kMoeThreads;
+    s_count[tid] = 0u;
+    int32_t e[kEach];
+#pragma unroll
+    for (uint32_t i = 0; i < kEach; ++i) {
+        const uint32_t route = i * kMoeThreads + tid;
+        e[i] = route < routes ? a.route[route] : -1;
+        if (e[i] >= int32_t(a.experts)) e[i] = -1;
+    }
+    __syncthreads();
+    uint32_t place[kEach];
+#pragma unroll
+    for (uint32_t i = 0; i < kEach; ++i) place[i] = e[i] >= 0 ? atomicAdd(&s_count[e[i]], 1u) : 0u;
+    __syncthreads();
+    // running sums over the experts: routes, first items, further items
+    const uint32_t n = s_count[tid], sweeps = (n + a.most - 1u) / a.most;
+    uint32_t run[3] = {n, n ? 1u : 0u, n ? sweeps - 1u : 0u};
+    const uint32_t own[3] = {run[0], run[1], run[2]};
+#pragma unroll
+    for (uint32_t off = 1; off < 64u; off *= 2u)
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            const uint32_t o = uint32_t(__shfl_up(int(run[k]), off, 64));
+            if (lane >= off) run[k] += o;
+        }
+    if (lane == 63u)
+#pragma unroll
+        for (int k = 0; k < 3; ++k) s_wave[k][wave] = run[k];
+    __syncthreads();
+    uint32_t total[3] = {0u, 0u, 0u};
+#pragma unroll
+    for (uint32_t w = 0; w < kMoeWaves; ++w)
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            const uint32_t v = s_wave[k][w];
+            run[k] += w < wave ? v : 0u;
+            total[k] += v;
+        }
+    const uint32_t first = run[0] - own[0];
+    s_first[tid] = first;
+    if (n) {
+        a.items[total[2] + run[1] - 1u] = {tid, first, min(n, a.most), 0u};
+        for (uint32_t i = 1; i < sweeps; ++i)
+            a.items[run[2] - own[2] + i - 1u] = {tid, first + i * a.most, min(n - i * a.most, a.most), 0u};
+    }
+    if (tid == 0u) *a.n_items = total[1] + total[2];
+    __syncthreads();
+#pragma unroll
+    for (uint32_t i = 0; i < kEach; ++i)
+        if (e[i] >= 0) a.list[s_first[e[i]] + place[i]] = uint16_t(i * kMoeThreads + tid);
 }
 
 // ------------------------------------------------------------ the experts' products
 
-// 2z of an escaped slot: by halves among the sorted records of its expert; the first probe where an even spread
+// 2z of an escaped slot: by halves among the sorted records of its expert; the first probe about where an even spread
 // would have it.
-__device__ __forceinline__ bool moe_record(const MoeMatrix& m, uint32_t expert, uint32_t group, uint32_t groups,
+__device__ __forceinline__ bool moe_record(const uint32_t* esc, uint64_t lo, uint64_t hi, uint32_t group, uint32_t groups,
                                            uint32_t (&rec)[4]) {
-    uint64_t lo = m.offsets[expert], hi = m.offsets[expert + 1];
-    bool first = true;
+    uint64_t mid = 0ull;
+    if (lo < hi) {
+        const float at = float(group) * __builtin_amdgcn_rcpf(float(groups)) * float(hi - lo);
+        mid = min(lo + uint64_t(at), hi - 1u);
+    }
     while (lo < hi) {
-        const uint64_t mid = first && hi - lo <= 0xFFFFFFFFull ? lo + uint64_t(group) * (hi - lo) / groups
-                                                               : lo + ((hi - lo) >> 1);
-        first = false;
-        const uint32_t key = m.esc[mid * 5];
+        const uint32_t key = esc[mid * 5];
         if (key == group) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) rec[i] = m.esc[mid * 5 + 1 + i];
+            for (int i = 0; i < 4; ++i) rec[i] = esc[mid * 5 + 1 + i];
             return true;
         }
         if (key < group) lo = mid + 1;
         else hi = mid;
+        mid = lo + ((hi - lo) >> 1);
     }
     return false;
 }
 
-// Points as signed bytes from the table's words of 2z + 64 (no borrow across bytes).
-__device__ __forceinline__ uint32_t signed_bytes(uint32_t p) {
-    return ((p | 0x80808080u) - 0x40404040u) ^ 0x80808080u;
+constexpr uint32_t kMoeRecords = 32;         // records of a block's rows that it keeps in LDS
+constexpr uint32_t kManyRecords = 0xFFFFFFFFu;
+
+// The records of an expert whose groups are in [first, last) into LDS (five words each), by one wave; how many, or
+// kManyRecords if they are more than `cap` (64 at most).  Sorted keys: 64 probes at a time find the first one.
+__device__ __forceinline__ uint32_t gather_records(const MoeMatrix& m, uint32_t expert, uint32_t first, uint32_t last,
+                                                   uint32_t* to, uint32_t cap) {
+    const uint32_t lane = threadIdx.x & 63u;
+    uint64_t lo = m.offsets[expert], hi = m.offsets[expert + 1];
+    const uint64_t end = hi;
+    while (hi - lo > uint64_t(kWave)) {                    // keys before lo are below first, from hi on not
+        const uint64_t step = (hi - lo + kWave - 1u) / kWave, at = min(lo + uint64_t(lane) * step, hi - 1u);
+        const uint32_t below = uint32_t(__popcll(__ballot(m.esc[at * 5] < first)));      // of the probes, the first ones
+        if (below == 0u) {
+            hi = lo;
+            break;
+        }
+        const uint64_t from = min(lo + uint64_t(below - 1u) * step, hi - 1u) + 1u;
+        hi = below < uint32_t(kWave) ? min(lo + uint64_t(below) * step, hi) : hi;
+        lo = from;
+    }
+    // (up to 64 keys that may be below, then the ones asked for)
+    const uint64_t mine = lo + lane;
+    const uint32_t key = mine < end ? m.esc[mine * 5] : 0xFFFFFFFFu;
+    const uint32_t skip = uint32_t(__popcll(__ballot(key < first)));
+    uint64_t at = mine;
+    uint32_t own = key;
+    if (skip) {                                            // 64 keys from the first one on
+        at = mine + skip;
+        own = at < end ? m.esc[at * 5] : 0xFFFFFFFFu;
+    }
+    const uint32_t n = uint32_t(__popcll(__ballot(own < last)));
+    if (n > cap) return kManyRecords;
+    if (lane < n) {
+        to[lane * 5u] = own;
+#pragma unroll
+        for (uint32_t i = 1; i < 5u; ++i) to[lane * 5u + i] = m.esc[at * 5 + i];
+    }
+    return n;
 }
 
-// The eight indices of groups 8 n ... 8 n + 7 of a row; past its end 0, whose point meets digits of 0.
-__device__ __forceinline__ u32x4_t load_indices(const uint16_t* row, uint32_t gpr, uint32_t n) {
-    const uint32_t g = n * 8u;
-    if (g + 8u <= gpr) return reinterpret_cast<const Bytes16*>(row + g)->v;
-    u32x4_t w;
-#pragma unroll
-    for (uint32_t i = 0; i < 4u; ++i) {
-        const uint32_t a = g + 2u * i < gpr ? row[g + 2u * i] : 0u, b = g + 2u * i + 1u < gpr ? row[g + 2u * i + 1u] : 0u;
-        w[i] = a | (b << 16);
+// A point's eight 2z + 8 as nibbles (|2z| <= 6 in any core): coordinates 0 ... 3 in the low ones of the bytes, 4 ... 7 in
+// the high ones; from the table's two words of 2z + 64.
+__device__ __forceinline__ uint32_t point_word(const uint2& p) { return (p.x - 0x38383838u) | ((p.y - 0x38383838u) << 4); }
+
+__device__ __forceinline__ uint2 point_bytes(uint32_t w) { return make_uint2(w & 0x0F0F0F0Fu, (w >> 4) & 0x0F0F0F0Fu); }
+
+constexpr uint32_t kZeroPoint = 0x88888888u, kZeroBytes = 0x08080808u;
+
+// The indices of eight groups from `at` on, in a matrix of `total` groups (eight at least): the words past its end are not
+// read.  A row's last ones can be the next row's: they meet digits of 0.
+__device__ __forceinline__ uint4 load_indices(const uint16_t* idx, uint32_t at, uint32_t total) {
+    const uint32_t from = min(at, total - 8u);
+    const u32x4_t v = reinterpret_cast<const Bytes16*>(reinterpret_cast<const char*>(idx) + from * 2u)->v;
+    uint4 w = make_uint4(v[0], v[1], v[2], v[3]);
+    if (at > from) {
+#pragma unroll 1
+        for (uint32_t d = min(at - from, 8u); d > 0u; --d) {
+            w.x = (w.x >> 16) | (w.y << 16);
+            w.y = (w.y >> 16) | (w.z << 16);
+            w.z = (w.z >> 16) | (w.w << 16);
+            w.w >>= 16;
+        }
     }
     return w;
 }
 
-// One wave: chunks [lo, hi) of 16 rows against the digits in LDS (from chunk `base` on).
-template <bool TAB>
-struct Sweep {
-    const uint16_t* row;        // this lane's row
-    uint32_t gpr, npts, expert, groups, row_group;   // groups of a matrix; of the rows before this one
-    bool row_ok;
-    const uint2* table;         // LDS
-    const uint2* pts;           // global
-    const uint4* digits;        // LDS: [entries][16]
-    moe_i32x4 acc, high;
-    bool any_high;
-    uint32_t flags;
+// LDS accesses of one wave, ordered across its lanes.
+__device__ __forceinline__ void moe_wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
 
-    __device__ __forceinline__ uint2 point(uint32_t idx) const {
-        if constexpr (TAB) return table[idx];
-        if (idx >= npts) return make_uint2(0u, 0u);
-        const uint2 p = pts[idx];
-        return make_uint2(signed_bytes(p.x), signed_bytes(p.y));
+// The point table, four bytes a point: 0 read from memory, 1 at a fixed place in LDS (fewer than kMoeSmall points), 2 in
+// LDS.  Four bytes a lane instead of eight halve the banks a read takes; three vector instructions make them operands
+// (2z + 8 in every byte; the sums lose 8 sum N at the end).
+template <int TAB>
+struct Points {
+    const uint32_t* lds;
+    const uint2* mem;
+    uint32_t n;
+
+    __device__ __forceinline__ uint32_t word(uint32_t i) const {
+        if constexpr (TAB == 0) return i < n ? point_word(mem[i]) : kZeroPoint;
+        return lds[i];
     }
-
-    __device__ __forceinline__ void chunk(const MoeMatrix& m, u32x4_t w, uint32_t c, uint32_t base) {
-        const uint32_t lane = threadIdx.x & 63u, q = lane >> 4;
-        uint2 p[8], ph[8];
-        bool wide = false;
-        // (scalars: a bit cast of a vector's element takes its first one)
-        const uint32_t wd[4] = {w[0], w[1], w[2], w[3]};
-        uint32_t cw[4] = {wd[0], wd[1], wd[2], wd[3]};
-        const moe_u16x2 most = __builtin_elementwise_max(
-            __builtin_elementwise_max(__builtin_bit_cast(moe_u16x2, wd[0]), __builtin_bit_cast(moe_u16x2, wd[1])),
-            __builtin_elementwise_max(__builtin_bit_cast(moe_u16x2, wd[2]), __builtin_bit_cast(moe_u16x2, wd[3])));
-        const bool big = uint32_t(most.x > most.y ? most.x : most.y) >= npts;
-        if (big) {
-            const moe_u16x2 lim = {uint16_t(npts), uint16_t(npts)};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                cw[i] = __builtin_bit_cast(uint32_t, __builtin_elementwise_min(__builtin_bit_cast(moe_u16x2, wd[i]), lim));
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            p[2 * i] = point(cw[i] & 0xFFFFu);
-            p[2 * i + 1] = point(cw[i] >> 16);
-        }
-        const uint32_t g0 = c * 32u + q * 8u;
-        if (__ballot(big)) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ph[i] = make_uint2(0u, 0u);
-            if (big && row_ok) {
-#pragma unroll 1
-                for (uint32_t i = 0; i < 8u; ++i) {
-                    const uint32_t word = i < 4u ? (i < 2u ? wd[0] : wd[1]) : (i < 6u ? wd[2] : wd[3]);
-                    const uint32_t id = (i & 1u) ? word >> 16 : word & 0xFFFFu;
-                    if (id < npts) continue;
-                    if (id != 0xFFFFu) {
-                        flags |= E8Q_STATUS_BAD_INDEX;
-                        continue;
-                    }
-                    uint32_t rec[4];
-                    if (!moe_record(m, expert, row_group + g0 + i, groups, rec)) {
-                        flags |= E8Q_STATUS_ESC_MISSING;
-                        continue;
-                    }
-                    // 2z = 256 hi + lo, lo in [-128, 127]; |2z| <= 2^14 in an encoder's records
-                    uint32_t l[2] = {0u, 0u}, h[2] = {0u, 0u};
-                    bool ok = true;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int z = int(int16_t(uint16_t((k & 1) ? rec[k >> 1] >> 16 : rec[k >> 1] & 0xFFFFu)));
-                        const int hi = (z + 128) >> 8;
-                        ok = ok && z >= -16384 && z <= 16384;
-                        l[k >> 2] |= (uint32_t(z) & 0xFFu) << (8 * (k & 3));
-                        h[k >> 2] |= (uint32_t(hi) & 0xFFu) << (8 * (k & 3));
-                    }
-                    if (!ok) {
-                        flags |= E8Q_STATUS_X_RANGE;
-                        continue;
-                    }
-                    wide |= (h[0] | h[1]) != 0u;
-#pragma unroll
-                    for (uint32_t k = 0; k < 8u; ++k)
-                        if (k == i) {
-                            p[k] = make_uint2(l[0], l[1]);
-                            ph[k] = make_uint2(h[0], h[1]);
-                        }
-                }
-            }
-            if (__ballot(wide)) {
-                any_high = true;
-#pragma unroll
-                for (uint32_t s = 0; s < 4u; ++s) {
-                    const uint4 d = digits[(((c - base) * 4u + s) * 4u + q) * 16u + (lane & 15u)];
-                    const moe_i32x4 av = {int(ph[2 * s].x), int(ph[2 * s].y), int(ph[2 * s + 1].x), int(ph[2 * s + 1].y)};
-                    const moe_i32x4 bv = {int(d.x), int(d.y), int(d.z), int(d.w)};
-                    high = __builtin_amdgcn_mfma_i32_16x16x64_i8(av, bv, high, 0, 0, 0);
-                }
-            }
-        }
-#pragma unroll
-        for (uint32_t s = 0; s < 4u; ++s) {
-            const uint4 d = digits[(((c - base) * 4u + s) * 4u + q) * 16u + (lane & 15u)];
-            const moe_i32x4 av = {int(p[2 * s].x), int(p[2 * s].y), int(p[2 * s + 1].x), int(p[2 * s + 1].y)};
-            const moe_i32x4 bv = {int(d.x), int(d.y), int(d.z), int(d.w)};
-            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(av, bv, acc, 0, 0, 0);
+    __device__ __forceinline__ void pair(uint32_t w, uint32_t& a, uint32_t& b) const {
+        if constexpr (TAB == 0) {
+            a = word(w & 0xFFFFu);
+            b = word(w >> 16);
+        } else {
+            const char* t = reinterpret_cast<const char*>(lds);
+            a = *reinterpret_cast<const uint32_t*>(t + ((w << 2) & 0x3FFFCu));
+            b = *reinterpret_cast<const uint32_t*>(t + ((w >> 14) & 0x3FFFCu));
         }
     }
-
-    __device__ __forceinline__ void run(const MoeMatrix& m, uint32_t lo, uint32_t hi, uint32_t base) {
-        constexpr uint32_t kAhead = 4u;
-        const uint32_t q = (threadIdx.x & 63u) >> 4;
-        u32x4_t w[kAhead];
+    // Two points a thread at a time, four loads in flight.
+    __device__ __forceinline__ void fill(uint32_t* to) const {
+        if constexpr (TAB == 0) return;
+        constexpr uint32_t kEach = TAB == 1 ? kMoeSmall / 2u / kMoeThreads : 4u;
+        const uint4* from = reinterpret_cast<const uint4*>(mem);
+        for (uint32_t i0 = threadIdx.x; 2u * i0 <= n; i0 += kEach * kMoeThreads) {
+            uint4 p[kEach];
 #pragma unroll
-        for (uint32_t i = 0; i < kAhead; ++i)
-            if (lo + i < hi) w[i] = load_indices(row, gpr, (lo + i) * 4u + q);
-        for (uint32_t c0 = lo; c0 < hi; c0 += kAhead) {
+            for (uint32_t k = 0; k < kEach; ++k) {
+                const uint32_t i = i0 + k * kMoeThreads;
+                p[k] = make_uint4(0x40404040u, 0x40404040u, 0x40404040u, 0x40404040u);
+                if (2u * i + 1u < n) p[k] = from[i];
+                else if (2u * i < n) {
+                    const uint2 last = mem[2u * i];
+                    p[k].x = last.x;
+                    p[k].y = last.y;
+                }
+            }
 #pragma unroll
-            for (uint32_t i = 0; i < kAhead; ++i) {
-                const uint32_t c = c0 + i;
-                if (c >= hi) break;
-                const u32x4_t now = w[i];
-                if (c + kAhead < hi) w[i] = load_indices(row, gpr, (c + kAhead) * 4u + q);
-                chunk(m, now, c, base);
+            for (uint32_t k = 0; k < kEach; ++k) {
+                const uint32_t i = i0 + k * kMoeThreads;
+                if (2u * i <= n)
+                    reinterpret_cast<uint2*>(to)[i] = make_uint2(point_word(make_uint2(p[k].x, p[k].y)),
+                                                                 point_word(make_uint2(p[k].z, p[k].w)));
             }
         }
     }
 };
 
-__device__ __forceinline__ float activation(float g, int act) {
-    if (act == E8Q_ACT_SILU) return g / (1.0f + expf(-g));
-    return 0.5f * g * (1.0f + tanhf(0.7978845608028654f * (g + 0.044715f * g * g * g)));
+// The same value, but nothing that is formed from it is formed ahead of a loop (no instruction): what all of a kernel's
+// rare paths need, formed at its start, would be spilled.
+__device__ __forceinline__ uint32_t here_only(uint32_t v) {
+    v = __builtin_amdgcn_readfirstlane(v);
+    asm volatile("" : "+s"(v));
+    return v;
 }
 
-// The rows [row0, row0 + n) of one expert for all its tokens.  IN: gate and up, the activation, into h; otherwise
-// down, into part.
-template <bool IN, bool TAB>
-__global__ __launch_bounds__(kMoeThreads) void moe_product_kernel(MoeArgs a) {
-    constexpr uint32_t kMats = IN ? 2u : 1u;
-    extern __shared__ uint4 s_moe[];
-    __shared__ uint32_t s_used[kMoeExperts / 32];
-    __shared__ uint16_t s_list[kMoeRoutes];
-    __shared__ int s_red[kMoeWaves][2][256];
-    __shared__ uint32_t s_high[kMoeWaves], s_n;
-    const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const uint32_t cols = IN ? a.hidden : a.inter, rows = IN ? a.inter : a.hidden;
-    const uint32_t parts = IN ? a.parts_in : a.parts_down, per = IN ? a.rows_in : a.rows_down;
-    const uint32_t nth = blockIdx.x / parts, part = blockIdx.x - nth * parts;
-    const uint32_t routes = a.tokens * a.k;
+template <typename T>
+__device__ __forceinline__ T* here_only(T* p) {
+    asm volatile("" : "+s"(p));
+    return p;
+}
 
-    // the nth expert that some token chose, and its routes in order
-    if (tid < kMoeExperts / 32) s_used[tid] = 0u;
-    __syncthreads();
-    for (uint32_t r = tid; r < routes; r += kMoeThreads) {
-        const int32_t e = a.route[r];
-        if (e >= 0 && uint32_t(e) < a.experts) atomicOr(&s_used[uint32_t(e) >> 5], 1u << (e & 31));
+// What a wave sweeps: two rows a lane, of one expert.
+struct Rows {
+    const uint16_t* idx[2];     // the expert's matrices
+    const uint32_t* esc[2];
+    const uint64_t* offsets[2]; // of its records
+    uint32_t first[2];          // this lane's rows: groups of the matrix before them
+    bool ok[2];
+    uint32_t gpr, groups;
+    const uint32_t* kept[2];    // records in LDS, their number
+    uint32_t n_kept[2];
+};
+
+__device__ __forceinline__ void set_rows(Rows& r, int t, const MoeMatrix& m, uint32_t expert, uint32_t rows, uint32_t gpr,
+                                         uint32_t row, uint32_t row_end) {
+    r.gpr = gpr;
+    r.groups = rows * gpr;
+    r.idx[t] = m.idx + uint64_t(expert) * r.groups;
+    r.esc[t] = m.esc;
+    r.offsets[t] = m.offsets + expert;
+    r.first[t] = min(row, rows - 1u) * gpr;
+    r.ok[t] = row < row_end;
+}
+
+// The operand of one slot that may be escaped: its point, or its record's low bytes (+ 8) or high bytes.
+template <int TAB>
+__device__ __forceinline__ uint2 resolve(const Points<TAB>& pts, const Rows& r, bool second, uint32_t id, uint32_t g, bool high,
+                                         bool& wide, uint32_t& flags) {
+    uint2 out = high ? make_uint2(0u, 0u) : make_uint2(kZeroBytes, kZeroBytes);
+    if (id < pts.n) return high ? out : point_bytes(pts.word(id));
+    if (g >= r.gpr || !(second ? r.ok[1] : r.ok[0])) return out;
+    if (id != 0xFFFFu) {
+        flags |= E8Q_STATUS_BAD_INDEX;
+        return out;
     }
-    __syncthreads();
-    uint32_t expert = 0xFFFFFFFFu, left = nth;
-    for (uint32_t w = 0; w < (a.experts + 31u) / 32u; ++w) {
-        uint32_t bits = s_used[w];
-        const uint32_t n = uint32_t(__popc(bits));
-        if (left >= n) {
-            left -= n;
-            continue;
-        }
-        for (; left; --left) bits &= bits - 1u;
-        expert = w * 32u + uint32_t(__ffs(int(bits)) - 1);
-        break;
+    uint32_t rec[4];
+    const uint32_t group = (second ? r.first[1] : r.first[0]) + g, kept = second ? r.n_kept[1] : r.n_kept[0];
+    bool found = false;
+    if (kept != kManyRecords) {
+        const uint32_t* list = second ? r.kept[1] : r.kept[0];
+        for (uint32_t i = 0; i < kept; ++i)
+            if (list[i * 5u] == group) {
+                found = true;
+#pragma unroll
+                for (uint32_t k = 0; k < 4u; ++k) rec[k] = list[i * 5u + 1u + k];
+                break;
+            }
+    } else {
+        const uint64_t* at = second ? r.offsets[1] : r.offsets[0];
+        found = moe_record(second ? r.esc[1] : r.esc[0], at[0], at[1], group, r.groups, rec);
     }
-    if (expert == 0xFFFFFFFFu) return;             // fewer are used
-    if (wave == 0u) {
-        uint32_t n = 0u;
-        for (uint32_t r0 = 0; r0 < routes; r0 += kWave) {
-            const uint32_t r = r0 + lane;
-            const bool in = r < routes && a.route[r] == int32_t(expert);
-            const uint64_t who = __ballot(in);
-            if (in) s_list[n + uint32_t(__popcll(who & ((1ull << lane) - 1ull)))] = uint16_t(r);
-            n += uint32_t(__popcll(who));
+    if (!found) {
+        flags |= E8Q_STATUS_ESC_MISSING;
+        return out;
+    }
+    // 2z = 256 hi + lo, lo + 8 in [-128, 127]; |2z| <= 2^14 in an encoder's records
+    uint32_t l[2] = {0u, 0u}, h[2] = {0u, 0u};
+    bool ok = true;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const int z = int(int16_t(uint16_t((k & 1) ? rec[k >> 1] >> 16 : rec[k >> 1] & 0xFFFFu)));
+        const int hi = (z + 136) >> 8;
+        ok = ok && z >= -16384 && z <= 16384;
+        l[k >> 2] |= (uint32_t(z + 8) & 0xFFu) << (8 * (k & 3));
+        h[k >> 2] |= (uint32_t(hi) & 0xFFu) << (8 * (k & 3));
+    }
+    if (!ok) {
+        flags |= E8Q_STATUS_X_RANGE;
+        return out;
+    }
+    wide |= (h[0] | h[1]) != 0u;
+    return high ? make_uint2(h[0], h[1]) : make_uint2(l[0], l[1]);
+}
+
+__device__ __forceinline__ uint32_t most_index(const uint4& w) {
+    const moe_u16x2 m = __builtin_elementwise_max(
+        __builtin_elementwise_max(__builtin_bit_cast(moe_u16x2, w.x), __builtin_bit_cast(moe_u16x2, w.y)),
+        __builtin_elementwise_max(__builtin_bit_cast(moe_u16x2, w.z), __builtin_bit_cast(moe_u16x2, w.w)));
+    return uint32_t(m.x > m.y ? m.x : m.y);
+}
+
+template <int G, int N>
+__device__ __forceinline__ void step_products(const uint4* digits, uint32_t part, const uint2 (&p)[2][2],
+                                              moe_i32x4 (&acc)[2][N]) {
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const uint4 d = digits[uint32_t(g) * part];
+        const moe_i32x4 bv = {int(d.x), int(d.y), int(d.z), int(d.w)};
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const moe_i32x4 av = {int(p[t][0].x), int(p[t][0].y), int(p[t][1].x), int(p[t][1].y)};
+            acc[t][g] = __builtin_amdgcn_mfma_i32_16x16x64_i8(av, bv, acc[t][g], 0, 0, 0);
         }
-        if (lane == 0u) s_n = n;
+    }
+}
+
+// One chunk of both tiles, no slot escaped, against G products' digits, `part` apart.
+template <int TAB, int G, int N>
+__device__ __forceinline__ void plain_chunk(const Points<TAB>& pts, const uint4 (&word)[2], const uint4* digits, uint32_t part,
+                                            moe_i32x4 (&acc)[2][N]) {
+    uint32_t p[4][2][2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        pts.pair(word[t].x, p[0][t][0], p[0][t][1]);
+        pts.pair(word[t].y, p[1][t][0], p[1][t][1]);
+        pts.pair(word[t].z, p[2][t][0], p[2][t][1]);
+        pts.pair(word[t].w, p[3][t][0], p[3][t][1]);
+    }
+#pragma unroll
+    for (uint32_t s = 0; s < 4u; ++s) {
+        const uint2 b[2][2] = {{point_bytes(p[s][0][0]), point_bytes(p[s][0][1])},
+                               {point_bytes(p[s][1][0]), point_bytes(p[s][1][1])}};
+        step_products<G>(digits + s * 64u, part, b, acc);
+    }
+}
+
+// One chunk of both tiles against `groups` products' digits (N at most).  With an escaped (or malformed) slot in the
+// wave, or for the high bytes, step by step.
+template <int TAB, int N, bool HIGH>
+__device__ __forceinline__ void sweep_chunk(const Points<TAB>& pts, const Rows& r, const uint4 (&word)[2], uint32_t c,
+                                            const uint4* digits, uint32_t part, uint32_t groups, moe_i32x4 (&acc)[2][N],
+                                            bool& wide, uint32_t& flags) {
+    if (!HIGH && !__ballot(max(most_index(word[0]), most_index(word[1])) >= pts.n)) {
+        if constexpr (N == 1) {
+            plain_chunk<TAB, 1>(pts, word, digits, part, acc);
+        } else {
+            if (groups == 1u) plain_chunk<TAB, 1>(pts, word, digits, part, acc);
+            else plain_chunk<TAB, N>(pts, word, digits, part, acc);
+        }
+        return;
+    }
+    const uint32_t g0 = c * 32u + (here_only(0u) + (threadIdx.x & 63u)) / 16u * 8u;
+    Rows rare = r;
+    rare.gpr = here_only(r.gpr);
+    rare.groups = here_only(r.groups);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        rare.esc[t] = here_only(r.esc[t]);
+        rare.offsets[t] = here_only(r.offsets[t]);
+    }
+#pragma unroll 1
+    for (uint32_t s = 0; s < 4u; ++s) {
+        uint32_t w[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+            w[t] = (s & 2u) ? ((s & 1u) ? word[t].w : word[t].z) : ((s & 1u) ? word[t].y : word[t].x);
+        const uint32_t m = max(max(w[0] & 0xFFFFu, w[0] >> 16), max(w[1] & 0xFFFFu, w[1] >> 16));
+        uint2 p[2][2] = {};
+        if (__ballot(m >= pts.n)) {
+#pragma unroll 1
+            for (uint32_t k = 0; k < 4u; ++k) {            // tile k / 2, slot k % 2
+                const uint32_t v = k < 2u ? w[0] : w[1];
+                const uint2 out = resolve<TAB>(pts, rare, k >= 2u, (k & 1u) ? v >> 16 : v & 0xFFFFu, g0 + 2u * s + (k & 1u), HIGH,
+                                               wide, flags);
+#pragma unroll
+                for (uint32_t i = 0; i < 4u; ++i)
+                    if (k == i) p[i >> 1][i & 1u] = out;
+            }
+        } else if (!HIGH) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                uint32_t a, b;
+                pts.pair(w[t], a, b);
+                p[t][0] = point_bytes(a);
+                p[t][1] = point_bytes(b);
+            }
+        }
+        // (the products of groups that have no digits are left out)
+#pragma unroll
+        for (int g = 0; g < N; ++g) {
+            if (uint32_t(g) >= groups) break;
+            moe_i32x4 one[2][1] = {{acc[0][g]}, {acc[1][g]}};
+            step_products<1>(digits + uint32_t(g) * part + s * 64u, 0u, p, one);
+            acc[0][g] = one[0][0];
+            acc[1][g] = one[1][0];
+        }
+    }
+}
+
+// Index words of both tiles, kAhead chunks ahead.
+struct Words {
+    static constexpr int kAhead = 2;
+    uint4 w[kAhead][2];
+
+    __device__ __forceinline__ static void load(uint4 (&to)[2], const Rows& r, uint32_t c) {
+        const uint32_t q = (threadIdx.x & 63u) >> 4;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) to[t] = load_indices(r.idx[t], r.first[t] + c * 32u + q * 8u, r.groups);
+    }
+    __device__ __forceinline__ void start(const Rows& r, uint32_t lo, uint32_t hi) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (lo + i < hi) load(w[i], r, lo + i);
+    }
+    // The words of chunk c; loads those of chunk c + kAhead.
+    __device__ __forceinline__ void next(uint4 (&now)[2], const Rows& r, uint32_t c, uint32_t hi) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            now[t] = w[0][t];
+#pragma unroll
+            for (int i = 1; i < kAhead; ++i) w[i - 1][t] = w[i][t];
+        }
+        if (c + kAhead < hi) load(w[kAhead - 1], r, c + kAhead);
+    }
+};
+
+// g sigmoid(g), or g (1 + tanh z) / 2 = g sigmoid(2 z) with z = sqrt(2 / pi) (g + 0.044715 g^3).
+__device__ __forceinline__ float activation(float g, int act) {
+    const float arg = act == E8Q_ACT_SILU ? g : 1.5957691216057308f * fmaf(0.044715f * g * g, g, g);
+    return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * arg));
+}
+
+constexpr uint32_t kRedRow = 17;             // (16 columns; an odd stride for the reads by row)
+
+// A wave's accumulators into LDS (added to what other waves put there: integers, in any order); then lane l has row l % 16
+// of tokens l / 16 and l / 16 + 4, as float64 (exact).
+template <bool ADD>
+__device__ __forceinline__ void put_tile(int* red, const moe_i32x4& acc) {
+    const uint32_t lane = threadIdx.x & 63u;
+#pragma unroll
+    for (uint32_t i = 0; i < 4u; ++i) {
+        int* to = red + (4u * (lane >> 4) + i) * kRedRow + (lane & 15u);
+        if constexpr (ADD) atomicAdd(to, acc[i]);
+        else *to = acc[i];
+    }
+}
+
+__device__ __forceinline__ double get_tile(const int* red, uint32_t row, uint32_t token) {
+    const int* s = red + row * kRedRow + 3u * token;
+    return (double(s[0]) * 256.0 + double(s[1])) * 256.0 + double(s[2]);
+}
+
+// A product from its exact sum of (2z + 8) N.
+__device__ __forceinline__ float product_of(double sum, float scale, const Vector& v, uint32_t& flags) {
+    if (!(scale > 0.0f) || __builtin_isinf(scale)) {
+        flags |= E8Q_STATUS_BAD_SCALE;
+        return 0.0f;
+    }
+    if (v.step != v.step) flags |= E8Q_STATUS_NONFINITE;
+    return float((sum - 8.0 * v.sum) * (0.5 * double(scale) * v.step));
+}
+
+// x / y of small numbers (below 2^12), y's reciprocal given.
+__device__ __forceinline__ uint32_t small_div(uint32_t x, float inv) {
+    return __builtin_amdgcn_readfirstlane(uint32_t((float(x) + 0.5f) * inv));
+}
+
+// How a wave takes part in a round.  IN: a unit is 16 rows of gate and up; otherwise 32 rows of down.  Whole rounds
+// have a unit for every wave; in the last one, where there are fewer, `split` waves share a unit's columns.
+struct Round {
+    uint32_t split, unit, kp;           // unit 0xFFFFFFFF: none
+    float inv;
+
+    __device__ __forceinline__ bool busy() const { return unit != 0xFFFFFFFFu; }
+    // this wave's share of n chunks
+    __device__ __forceinline__ uint32_t lo(uint32_t n) const { return small_div(n * kp, inv); }
+    __device__ __forceinline__ uint32_t hi(uint32_t n) const { return small_div(n * (kp + 1u), inv); }
+};
+
+__device__ __forceinline__ Round round_of(uint32_t units, uint32_t first_chunks, uint32_t round) {
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    Round r;
+    const uint32_t left = units - round * kMoeWaves;       // (round * kMoeWaves < units)
+    r.split = left > 8u ? 1u : left > 5u ? 2u : left == 5u ? 3u : left == 4u ? 4u : left == 3u ? 5u : left == 2u ? 8u : 16u;
+    r.split = min(r.split, first_chunks);
+    r.inv = __builtin_amdgcn_rcpf(float(r.split));
+    const uint32_t slot = small_div(wave, r.inv);
+    r.kp = wave - slot * r.split;
+    r.unit = slot < left ? round * kMoeWaves + slot : 0xFFFFFFFFu;
+    return r;
+}
+
+// What a block multiplies: its rows of one expert with `n` tokens.
+struct Job {
+    uint4* digits;
+    const uint16_t* list;       // their routes
+    Vector* vec;                // in LDS
+    int (*red)[16 * kRedRow];
+    const uint32_t* kept;       // records of the block's rows: [2][kMoeRecords][5], and their numbers
+    const uint32_t* n_kept;
+    uint32_t expert, row0, row_end, n;
+};
+
+template <bool IN>
+__device__ __forceinline__ Rows unit_rows(const MoeArgs& a, uint32_t expert, uint32_t row0, uint32_t row_end, uint32_t unit) {
+    const uint32_t gpr = (IN ? a.hidden : a.inter) / 8u, rows = IN ? a.inter : a.hidden, lane = threadIdx.x & 63u;
+    Rows r;
+    const uint32_t row = row0 + unit * (IN ? 16u : 32u) + (lane & 15u);
+    set_rows(r, 0, IN ? a.gate : a.down, expert, rows, gpr, row, row_end);
+    set_rows(r, 1, IN ? a.up : a.down, expert, rows, gpr, IN ? row : row + 16u, row_end);
+    return r;
+}
+
+// The digits of chunks [base, base + here) of the job's tokens from the workspace, a half of the block a vector at a time:
+// first to registers, then to LDS.
+template <bool IN, int G>
+struct Slab {
+    static constexpr uint32_t kEach = (uint32_t(G) * kMoeTokens + 1u) / 2u;
+    uint4 v[kEach];
+    Vector vec;
+
+    __device__ __forceinline__ static uint32_t word() { return threadIdx.x & (kMoeThreads / 2u - 1u); }
+    __device__ __forceinline__ static uint32_t half() { return __builtin_amdgcn_readfirstlane(threadIdx.x / (kMoeThreads / 2u)); }
+    __device__ __forceinline__ static uint32_t index(const MoeArgs& a, const Job& job, uint32_t j) {
+        const uint32_t route = job.list[min(j, job.n - 1u)];
+        return IN ? fdiv(route, a.k_div) : route;
     }
 
-    uint2* table = reinterpret_cast<uint2*>(s_moe);
-    uint4* digits = s_moe + (TAB ? (a.npts + 2u) / 2u : 0u);
-    if constexpr (TAB) {
-        const uint2* src = reinterpret_cast<const uint2*>(a.pts);
-        for (uint32_t i = tid; i <= a.npts; i += kMoeThreads) {
-            const uint2 p = i < a.npts ? src[i] : make_uint2(0x40404040u, 0x40404040u);
-            table[i] = make_uint2(signed_bytes(p.x), signed_bytes(p.y));
+    // (past the last vector or word: the last ones again, which are not stored)
+    __device__ __forceinline__ void load(const MoeArgs& a, const Job& job, uint32_t base, uint32_t here) {
+        static_assert(kMoeSlab * 48u <= kMoeThreads / 2u, "a thread has one word of a vector's slab");
+        const uint64_t vec_bytes = moe_digit_bytes(IN ? a.hidden : a.inter);
+        const uint8_t* from = (IN ? a.xd : a.hd) + (base * 48u + min(word(), here * 48u - 1u)) * 16u;
+#pragma unroll
+        for (uint32_t k = 0; k < kEach; ++k)
+            v[k] = *reinterpret_cast<const uint4*>(from + index(a, job, half() + 2u * k) * vec_bytes);
+        vec = (IN ? a.xs : a.hs)[index(a, job, threadIdx.x)];
+    }
+    __device__ __forceinline__ void store(const Job& job, uint32_t here, uint32_t part) const {
+        const uint32_t i = word(), entry = i / 3u, d = i - entry * 3u;
+#pragma unroll
+        for (uint32_t k = 0; k < kEach; ++k) {
+            const uint32_t j = half() + 2u * k, group = j >= kMoeTokens ? 1u : 0u;
+            if (j < job.n && i < here * 48u) job.digits[group * part + entry * 16u + 3u * (j - group * kMoeTokens) + d] = v[k];
+        }
+        if (threadIdx.x < job.n) job.vec[threadIdx.x] = vec;
+    }
+    // Both, vector by vector.
+    __device__ __forceinline__ static void copy(const MoeArgs& a, const Job& job, uint32_t base, uint32_t here, uint32_t part) {
+        const uint64_t vec_bytes = moe_digit_bytes(IN ? a.hidden : a.inter);
+        const uint32_t i = word(), entry = i / 3u, d = i - entry * 3u;
+#pragma unroll 1
+        for (uint32_t j = half(); j < job.n; j += 2u) {
+            const uint32_t vec = index(a, job, j);
+            const uint32_t group = j >= kMoeTokens ? 1u : 0u;
+            if (i < here * 48u)
+                job.digits[group * part + entry * 16u + 3u * (j - group * kMoeTokens) + d] =
+                    *reinterpret_cast<const uint4*>((IN ? a.xd : a.hd) + vec * vec_bytes + (base * 48u + i) * 16u);
+            if (i == 0u) job.vec[j] = (IN ? a.xs : a.hs)[vec];
         }
     }
-    __syncthreads();
-    const uint32_t n = s_n, gpr = cols / 8u, chunks = moe_chunks(cols);
-    const uint32_t row0 = part * per, row_end = min(rows, row0 + per);
-    const uint32_t tiles = (row_end - row0 + kMoeTile - 1u) / kMoeTile;
-    // waves share a tile's columns where there are fewer tiles than waves
-    const uint32_t slab_chunks = min(chunks, kMoeSlab);
-    uint32_t split = max(1u, kMoeWaves / (kMats * tiles));
-    split = min(split, slab_chunks);
-    const uint32_t at_once = kMoeWaves / (kMats * split);         // tiles of a round
-    const uint8_t* xd = IN ? a.xd : a.hd;
-    const int* xe = IN ? a.xe : a.he;
-    const uint64_t vec_bytes = moe_digit_bytes(cols);
-    uint32_t flags = 0u;
+};
 
-    for (uint32_t g0 = 0; g0 < n; g0 += kMoeTokens) {
-        const uint32_t nt = min(kMoeTokens, n - g0);
-        for (uint32_t t0 = 0; t0 < tiles; t0 += at_once) {
-            const uint32_t item = wave / split, kp = wave - item * split;
-            const uint32_t tile = t0 + item / kMats, mat = item % kMats;
-            const bool busy = item < at_once * kMats && tile < tiles;
-            const MoeMatrix& m = IN ? (mat ? a.up : a.gate) : a.down;
-            const uint32_t r = row0 + tile * kMoeTile + (lane & 15u);
-            const uint32_t rr = min(r, rows - 1u);
-            Sweep<TAB> sw;
-            sw.row = m.idx + (uint64_t(expert) * rows + rr) * gpr;
-            sw.gpr = gpr;
-            sw.npts = a.npts;
-            sw.expert = expert;
-            sw.groups = rows * gpr;
-            sw.row_group = rr * gpr;
-            sw.row_ok = r < row_end;
-            sw.table = table;
-            sw.pts = reinterpret_cast<const uint2*>(a.pts);
-            sw.digits = digits;
-            sw.acc = sw.high = moe_i32x4{0, 0, 0, 0};
-            sw.any_high = false;
-            sw.flags = 0u;
-            for (uint32_t base = 0; base < chunks; base += kMoeSlab) {
-                const uint32_t here = min(kMoeSlab, chunks - base);
-                if (t0 == 0u || chunks > kMoeSlab) {             // (one slab stays for all tiles)
-                    __syncthreads();
-                    for (uint32_t i = tid; i < here * 16u * 3u * nt; i += kMoeThreads) {
-                        const uint32_t j = i / (here * 48u), k = i - j * (here * 48u), entry = k / 3u, d = k - entry * 3u;
-                        const uint32_t route = s_list[g0 + j], vec = IN ? route / a.k : route;
-                        const uint4* src = reinterpret_cast<const uint4*>(xd + vec * vec_bytes) + base * 48u;
-                        digits[entry * 16u + 3u * j + d] = src[k];
+// A unit's chunks of every slab; `words` has the first ones of the first slab, whose digits are in LDS.
+template <bool IN, int TAB, int N, bool HIGH>
+__device__ __forceinline__ void sweep_unit(const MoeArgs& a, const Points<TAB>& pts, const Job& job, const Round& rd,
+                                           uint32_t chunks, const Rows& r, uint32_t group, uint32_t groups, Words& words,
+                                           moe_i32x4 (&acc)[2][N], bool& wide, uint32_t& flags) {
+    const uint32_t part = min(chunks, kMoeSlab) * 256u;
+    const uint4* from = job.digits + group * part + (threadIdx.x & 63u);
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int g = 0; g < N; ++g) acc[t][g] = moe_i32x4{0, 0, 0, 0};
+#pragma unroll 1
+    for (uint32_t base = 0; base < chunks; base += kMoeSlab) {
+        const uint32_t here = min(kMoeSlab, chunks - base);
+        const uint32_t lo = base + rd.lo(here), hi = base + rd.hi(here);
+        if (rd.busy() && (HIGH || base > 0u)) words.start(r, lo, hi);
+        if (chunks > kMoeSlab) {
+            __syncthreads();
+            Slab<IN, 1>::copy(a, job, base, here, part);
+            __syncthreads();
+        }
+        if (!rd.busy()) continue;
+#pragma unroll 1
+        for (uint32_t c = lo; c < hi; ++c) {
+            uint4 now[2];
+            words.next(now, r, c, hi);
+            sweep_chunk<TAB, N, HIGH>(pts, r, now, c, from + (c - base) * 256u, part, groups, acc, wide, flags);
+        }
+    }
+}
+
+// The rows of a block for up to 5 G of its expert's tokens.
+template <bool IN, int TAB, int G>
+__device__ __forceinline__ void multiply(const MoeArgs& a, const Points<TAB>& pts, const Job& whole, uint32_t units,
+                                         uint32_t chunks, uint32_t& flags, uint32_t* s_max, double* s_sum) {
+    Job job = whole;
+    job.expert = here_only(job.expert);
+    job.row0 = here_only(job.row0);
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t rows = IN ? a.inter : a.hidden, first = min(chunks, kMoeSlab), part = first * 256u;
+    const uint32_t groups = job.n > kMoeTokens ? 2u : 1u;
+    const uint32_t rounds = (units + kMoeWaves - 1u) / kMoeWaves;
+    // the digits, with the first indices on their way behind them
+    Round rd = round_of(units, first, 0u);
+    Words words;
+    const auto start = [&](const Round& x) {
+        words.start(unit_rows<IN>(a, job.expert, job.row0, job.row_end, x.unit), x.lo(first), x.hi(first));
+    };
+    if (!IN && !a.ready_down) {
+        if (rd.busy()) start(rd);
+        vectors_lds([&](uint32_t j, uint32_t g, float (&v)[8]) {
+            load8(a.h, 0, uint64_t(job.list[j]) * a.inter + g * 8u, v);
+        }, job.n, a.inter, a.signs_down, a.had_down, a.kappa_down, job.digits, job.vec, s_max, s_sum);
+    } else if (chunks <= kMoeSlab) {
+        Slab<IN, G> slab;
+        slab.load(a, job, 0u, chunks);
+        if (rd.busy()) start(rd);
+        slab.store(job, chunks, part);
+    } else if (rd.busy()) {
+        start(rd);
+    }
+    for (uint32_t i = threadIdx.x; i < kMoeWaves * 16u * kRedRow; i += kMoeThreads) job.red[0][i] = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (uint32_t round = 0; round < rounds; ++round) {
+        Rows r = unit_rows<IN>(a, job.expert, job.row0, job.row_end, rd.busy() ? rd.unit : 0u);
+#pragma unroll
+        for (uint32_t t = 0; t < 2u; ++t) {
+            r.kept[t] = job.kept + (IN ? t * kMoeRecords * 5u : 0u);
+            r.n_kept[t] = __builtin_amdgcn_readfirstlane(job.n_kept[IN ? t : 0u]);
+        }
+        const uint32_t row = job.row0 + (rd.busy() ? rd.unit : 0u) * (IN ? 16u : 32u) + (threadIdx.x & 15u);
+        float scale[2];
+#pragma unroll
+        for (uint32_t t = 0; t < 2u; ++t)
+            scale[t] = (IN ? (t ? a.up : a.gate) : a.down)
+                           .scale[uint64_t(job.expert) * rows + min(IN ? row : row + t * 16u, rows - 1u)];
+        moe_i32x4 acc[2][G];
+        bool wide = false;
+        sweep_unit<IN, TAB, G, false>(a, pts, job, rd, chunks, r, 0u, groups, words, acc, wide, flags);
+        const bool together = rd.split > 1u || chunks > kMoeSlab;      // the block's waves keep step
+        const bool again = together ? __syncthreads_or(wide) != 0 : __ballot(wide) != 0ull;
+        const Round now = rd;
+        const bool more = round + 1u < rounds;
+        if (more) {
+            rd = round_of(units, first, round + 1u);
+            if (rd.busy() && !again) start(rd);
+        }
+        const uint32_t lane = here_only(0u) + (threadIdx.x & 63u), q = lane >> 4;
+#pragma unroll 1
+        for (uint32_t g = 0; g < groups; ++g) {
+            moe_i32x4 tile[2], above[2][1];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                tile[t] = acc[t][0];
+#pragma unroll
+                for (int i = 1; i < G; ++i)
+                    if (g == uint32_t(i)) tile[t] = acc[t][i];
+            }
+            if (again) {
+                bool none = false;
+                Rows same = unit_rows<IN>(a, here_only(job.expert), job.row0, job.row_end, now.busy() ? now.unit : 0u);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    same.kept[t] = r.kept[t];
+                    same.n_kept[t] = r.n_kept[t];
+                }
+                sweep_unit<IN, TAB, 1, true>(a, pts, job, now, chunks, same, here_only(g), 1u, words, above, none, flags);
+            }
+            double sum[2][2] = {{0.0, 0.0}, {0.0, 0.0}};
+#pragma unroll 1
+            for (int pass = 0; pass < (again ? 2 : 1); ++pass) {
+                const double times = pass ? 256.0 : 1.0;
+                if (now.split > 1u) {
+                    // the waves of a unit add up in the places of its first two
+                    int (*red)[16 * kRedRow] = job.red + (wave - now.kp);
+                    if (round + g + uint32_t(pass) > 0u) {
+                        __syncthreads();
+                        for (uint32_t i = threadIdx.x; i < kMoeWaves * 16u * kRedRow; i += kMoeThreads) job.red[0][i] = 0;
+                        __syncthreads();
+                    }
+                    if (now.busy()) {
+                        put_tile<true>(red[0], pass ? above[0][0] : tile[0]);
+                        put_tile<true>(red[1], pass ? above[1][0] : tile[1]);
                     }
                     __syncthreads();
-                }
-                if (busy) sw.run(m, base + here * kp / split, base + here * (kp + 1u) / split, base);
-            }
-            flags |= sw.flags;
-            if (busy) {
+                    if (now.busy() && now.kp == 0u) {
 #pragma unroll
-                for (uint32_t i = 0; i < 4u; ++i) {
-                    s_red[wave][0][(4u * (lane >> 4) + i) * 16u + (lane & 15u)] = sw.acc[i];
-                    if (sw.any_high) s_red[wave][1][(4u * (lane >> 4) + i) * 16u + (lane & 15u)] = sw.high[i];
-                }
-                if (lane == 0u) s_high[wave] = sw.any_high;
-            }
-            __syncthreads();
-            const uint32_t here = min(at_once, tiles - t0);
-            for (uint32_t o = tid; o < here * 16u * nt; o += kMoeThreads) {
-                const uint32_t j = o / (here * 16u), k = o - j * (here * 16u), lt = k / 16u, i = k & 15u;
-                const uint32_t row = row0 + (t0 + lt) * kMoeTile + i;
-                if (row >= row_end) continue;
-                const uint32_t route = s_list[g0 + j], vec = IN ? route / a.k : route;
-                const int e = xe[vec];
-                float v[kMats];
+                        for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (uint32_t mt = 0; mt < kMats; ++mt) {
-                    int64_t sum = 0;
-                    for (uint32_t p = 0; p < split; ++p) {
-                        const uint32_t w = (lt * kMats + mt) * split + p;
-                        const int* s = &s_red[w][0][i * 16u + 3u * j];
-                        sum += (int64_t(s[0]) * 256 + s[1]) * 256 + s[2];
-                        if (s_high[w]) {
-                            s += 256;
-                            sum += ((int64_t(s[0]) * 256 + s[1]) * 256 + s[2]) * 256;
+                            for (uint32_t i = 0; i < 2u; ++i)
+                                if (q + 4u * i < kMoeTokens) sum[t][i] += times * get_tile(red[t], lane & 15u, q + 4u * i);
+                    }
+                } else {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (now.busy()) put_tile<false>(job.red[wave], pass ? above[t][0] : tile[t]);
+                        moe_wave_sync();
+                        if (now.busy()) {
+#pragma unroll
+                            for (uint32_t i = 0; i < 2u; ++i)
+                                if (q + 4u * i < kMoeTokens)
+                                    sum[t][i] += times * get_tile(job.red[wave], lane & 15u, q + 4u * i);
                         }
-                    }
-                    const MoeMatrix& mm = IN ? (mt ? a.up : a.gate) : a.down;
-                    const float scale = mm.scale[uint64_t(expert) * rows + row];
-                    if (!(scale > 0.0f) || __builtin_isinf(scale)) {
-                        flags |= E8Q_STATUS_BAD_SCALE;
-                        v[mt] = 0.0f;
-                    } else if (e == kBadExponent) {
-                        flags |= E8Q_STATUS_NONFINITE;
-                        v[mt] = __uint_as_float(0x7FC00000u);
-                    } else {
-                        v[mt] = float((0.5 * double(scale)) * __builtin_ldexp(double(sum), e - kDigitBits));
+                        moe_wave_sync();
                     }
                 }
-                if constexpr (IN) a.h[uint64_t(route) * a.inter + row] = activation(v[0], a.act) * v[1];
-                else a.part[uint64_t(route) * a.hidden + row] = v[0];
             }
-            __syncthreads();
+            if (!now.busy() || now.kp != 0u) continue;
+#pragma unroll
+            for (uint32_t i = 0; i < 2u; ++i) {
+                const uint32_t j = g * kMoeTokens + q + 4u * i;
+                if (q + 4u * i >= kMoeTokens || j >= job.n) continue;
+                const uint32_t route = job.list[j];
+                float v[2];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) v[t] = r.ok[t] ? product_of(sum[t][i], scale[t], job.vec[j], flags) : 0.0f;
+                if constexpr (IN) {
+                    if (r.ok[0]) a.h[uint64_t(route) * a.inter + row] = activation(v[0], a.act) * v[1];
+                } else {
+                    if (r.ok[0]) a.part[uint64_t(route) * a.hidden + row] = v[0];
+                    if (r.ok[1]) a.part[uint64_t(route) * a.hidden + row + 16u] = v[1];
+                }
+            }
         }
+        if (more && rd.busy() && again) start(rd);
+    }
+}
+
+template <bool IN, int TAB, int G>
+__global__ __launch_bounds__(kMoeThreads) void moe_product_kernel(MoeArgs a) {
+    extern __shared__ uint4 s_moe[];
+    __shared__ uint2 s_table2[TAB == 1 ? kMoeSmall / 2 : 1];
+    __shared__ int s_red[kMoeWaves][16 * kRedRow];
+    __shared__ uint32_t s_max[kMoeWaves];
+    __shared__ Vector s_vec[kMoeVectors];
+    __shared__ double s_sum[kMoeWaves];
+    __shared__ uint32_t s_high[IN ? kMoeInline : 1], s_low[IN ? kMoeInline : 1];
+    __shared__ double s_chosen[IN ? kMoeDirect : 1];
+    __shared__ int32_t s_route[IN ? kMoeDirect : 1];
+    __shared__ uint16_t s_list[kMoeVectors];
+    __shared__ uint32_t s_kept[2][kMoeRecords][5], s_n_kept[2];
+    const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t cols = IN ? a.hidden : a.inter, rows = IN ? a.inter : a.hidden, gpr = cols / 8u;
+    constexpr uint32_t kUnit = IN ? 16u : 32u;
+    uint32_t flags = 0u, n_items;
+    uint32_t* table = TAB == 1 ? reinterpret_cast<uint32_t*>(s_table2) : reinterpret_cast<uint32_t*>(s_moe);
+    const Points<TAB> pts = {table, reinterpret_cast<const uint2*>(a.pts), a.npts};
+    uint4* digits = s_moe + (TAB == 2 ? a.npts / 4u + 1u : 0u);
+    const bool choose = IN && a.choose;
+
+    uint64_t firsts = 0ull;                        // places (of a choosing block) that are an expert's first
+    if (choose) {
+        // a few logits: every block ranks them; the first one writes the places
+        const uint32_t cells = a.tokens * a.experts, routes = a.tokens * a.k;
+        const bool writer = blockIdx.x == 0u;
+        double logit = 0.0;
+        if (tid < cells) {
+            logit = a.logits[tid];
+            if (!(logit - logit == 0.0) && writer) flags |= E8Q_STATUS_NONFINITE;
+            const uint64_t key = logit_key(logit);
+            s_high[tid] = uint32_t(key >> 32);
+            s_low[tid] = uint32_t(key);
+        }
+        pts.fill(table);
+        __syncthreads();
+        if (tid < cells) {
+            const uint32_t t = fdiv(tid, a.experts_div), e = tid - t * a.experts;
+            const uint32_t rank = logit_rank(s_high + t * a.experts, s_low + t * a.experts, a.experts, e);
+            if (rank < a.k) {
+                s_route[t * a.k + rank] = int32_t(e);
+                s_chosen[t * a.k + rank] = logit;
+                if (writer) a.route[t * a.k + rank] = int32_t(e);
+            }
+        }
+        __syncthreads();
+        if (writer) {
+            for (uint32_t t = wave; t < a.tokens; t += kMoeWaves) {
+                const float w = place_weight(a, s_chosen + t * a.k, a.logits + t * a.experts, lane);
+                if (lane < a.k) a.weight[t * a.k + lane] = w;
+            }
+        }
+        bool first = lane < routes;
+        for (uint32_t j = 0; j < routes; ++j) first = first && !(j < lane && s_route[j] == s_route[lane]);
+        firsts = __ballot(first);
+        n_items = uint32_t(__popcll(firsts));
+    } else {
+        n_items = *a.n_items;
+        pts.fill(table);
+    }
+    n_items = __builtin_amdgcn_readfirstlane(n_items);
+
+    // this block's units: a part of an item, where the items' parts fit the grid, or a share of all items' units
+    const uint32_t each = (rows + kUnit - 1u) / kUnit;
+    uint32_t share = (n_items * each + gridDim.x - 1u) / gridDim.x;
+    const uint32_t parts = share ? (each + share - 1u) / share : 1u;
+    uint32_t at, end;
+    if (n_items * parts <= gridDim.x) {
+        const uint32_t item = blockIdx.x / parts, part = blockIdx.x - item * parts;
+        share = (each + parts - 1u) / parts;
+        at = item < n_items ? item * each + min(part * share, each) : n_items * each;
+        end = min(at + share, min(item + 1u, n_items) * each);
+    } else {
+        at = min(blockIdx.x * share, n_items * each);
+        end = min(at + share, n_items * each);
+    }
+#pragma unroll 1
+    while (at < end) {
+        const uint32_t nth = __builtin_amdgcn_readfirstlane(at / each), unit0 = at - nth * each;
+        const uint32_t unit1 = min(each, unit0 + (end - at)), row0 = unit0 * kUnit, row_end = min(rows, unit1 * kUnit);
+        uint32_t expert, n;
+        if (choose) {
+            // the nth first place's expert and its places
+            uint64_t left = firsts;
+            for (uint32_t k = nth; k; --k) left &= left - 1ull;
+            const int32_t own = s_route[__ffsll((unsigned long long)left) - 1];
+            const uint64_t who = __ballot(lane < a.tokens * a.k && s_route[min(lane, kMoeDirect - 1u)] == own);
+            expert = uint32_t(own);
+            n = uint32_t(__popcll(who));
+            if (wave == 0u && ((who >> lane) & 1ull)) s_list[__popcll(who & ((1ull << lane) - 1ull))] = uint16_t(lane);
+        } else {
+            const MoeItem item = a.items[nth];
+            expert = item.expert;
+            n = item.n;
+            if (tid < n) s_list[tid] = a.list[item.first + tid];
+        }
+        expert = __builtin_amdgcn_readfirstlane(expert);
+        n = __builtin_amdgcn_readfirstlane(n);
+        if (wave >= 1u && wave <= (IN ? 2u : 1u)) {
+            // the records of the rows
+            const uint32_t kept = gather_records(IN ? (wave == 1u ? a.gate : a.up) : a.down, expert, row0 * gpr, row_end * gpr,
+                                                 &s_kept[wave - 1u][0][0], kMoeRecords);
+            if (lane == 0u) s_n_kept[wave - 1u] = kept;
+        }
+        __syncthreads();
+        const Job job = {digits, s_list, s_vec, s_red, &s_kept[0][0][0], s_n_kept, expert, row0, row_end, n};
+        multiply<IN, TAB, G>(a, pts, job, unit1 - unit0, moe_chunks(cols), flags, s_max, s_sum);
+        at += unit1 - unit0;
+        if (at < end) __syncthreads();
+    }
+    flush_status(flags, a.status);
+}
+
+// Down and the weighted sum for few places: a block has 32 rows of every place's expert, a wave (or several that share
+// the columns) a place.
+template <int TAB>
+__global__ __launch_bounds__(kMoeThreads) void moe_direct_kernel(MoeArgs a) {
+    extern __shared__ uint4 s_moe[];
+    __shared__ uint2 s_table2[TAB == 1 ? kMoeSmall / 2 : 1];
+    __shared__ int s_red[kMoeWaves][16 * kRedRow];
+    __shared__ uint32_t s_max[kMoeWaves];
+    __shared__ Vector s_vec[kMoeVectors];
+    __shared__ double s_sum[kMoeWaves];
+    __shared__ float s_y[kMoeDirect][32];
+    __shared__ uint32_t s_kept[kMoeWaves][kMoeRecords / 2][5];
+    const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = __builtin_amdgcn_readfirstlane(tid >> 6), q = lane >> 4;
+    const uint32_t routes = a.tokens * a.k, chunks = moe_chunks(a.inter), split = a.split_direct;
+    const float inv = __builtin_amdgcn_rcpf(float(split));
+    const uint32_t place = small_div(wave, inv), kp = wave - place * split;
+    const int32_t chosen = place < routes ? a.route[place] : -1;
+    const bool busy = chosen >= 0 && uint32_t(chosen) < a.experts;
+    const uint32_t expert = __builtin_amdgcn_readfirstlane(busy ? uint32_t(chosen) : 0u), row0 = blockIdx.x * 32u;
+    uint32_t flags = place < routes && chosen >= int32_t(a.experts) ? uint32_t(E8Q_STATUS_BAD_INDEX) : 0u;
+
+    uint32_t* table = TAB == 1 ? reinterpret_cast<uint32_t*>(s_table2) : reinterpret_cast<uint32_t*>(s_moe);
+    const Points<TAB> pts = {table, reinterpret_cast<const uint2*>(a.pts), a.npts};
+    uint4* digits = s_moe + (TAB == 2 ? a.npts / 4u + 1u : 0u);
+    Rows r;
+    float scale[2];
+#pragma unroll
+    for (uint32_t t = 0; t < 2u; ++t) {
+        const uint32_t row = row0 + t * 16u + (lane & 15u);
+        set_rows(r, int(t), a.down, expert, a.hidden, a.inter / 8u, row, a.hidden);
+        scale[t] = a.down.scale[uint64_t(expert) * a.hidden + min(row, a.hidden - 1u)];
+    }
+    const uint32_t lo = small_div(chunks * kp, inv), hi = small_div(chunks * (kp + 1u), inv);
+    Words words;
+    if (busy) words.start(r, lo, hi);
+    const uint32_t gpr = a.inter / 8u;
+    r.n_kept[0] = r.n_kept[1] = busy ? gather_records(a.down, expert, row0 * gpr, min(row0 + 32u, a.hidden) * gpr,
+                                                      &s_kept[wave][0][0], kMoeRecords / 2) : 0u;
+    r.kept[0] = r.kept[1] = &s_kept[wave][0][0];
+    for (uint32_t i = tid; i < kMoeWaves * 16u * kRedRow; i += kMoeThreads) s_red[0][i] = 0;
+    pts.fill(table);
+    // (places that are not used leave what h held: their columns are not read)
+    vectors_lds([&](uint32_t j, uint32_t g, float (&v)[8]) { load8(a.h, 0, uint64_t(j) * a.inter + g * 8u, v); }, routes,
+                a.inter, a.signs_down, a.had_down, a.kappa_down, digits, s_vec, s_max, s_sum);
+    double sum[2] = {0.0, 0.0};
+    const uint4* mine = digits + (place / kMoeTokens) * chunks * 256u + q * 16u + (lane & 15u);
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+        const bool high = pass == 1;
+        bool wide = false;
+        moe_i32x4 acc[2][1] = {{moe_i32x4{0, 0, 0, 0}}, {moe_i32x4{0, 0, 0, 0}}};
+        if (busy) {
+            if (high) words.start(r, lo, hi);
+#pragma unroll 1
+            for (uint32_t c = lo; c < hi; ++c) {
+                uint4 now[2];
+                words.next(now, r, c, hi);
+                if (high) sweep_chunk<TAB, 1, true>(pts, r, now, c, mine + c * 256u, 0u, 1u, acc, wide, flags);
+                else sweep_chunk<TAB, 1, false>(pts, r, now, c, mine + c * 256u, 0u, 1u, acc, wide, flags);
+            }
+        }
+        // the waves of a place add up in one tile's place, one tile after the other
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            if (t || high) {
+                __syncthreads();
+                for (uint32_t i = tid; i < kMoeWaves * 16u * kRedRow; i += kMoeThreads) s_red[0][i] = 0;
+                __syncthreads();
+            }
+            if (busy) put_tile<true>(s_red[place], acc[t][0]);
+            __syncthreads();
+            if (busy && kp == 0u && q == 0u)
+                sum[t] += (high ? 256.0 : 1.0) * get_tile(s_red[place], lane, place % kMoeTokens);
+        }
+        if (!__syncthreads_or(wide)) break;
+    }
+    if (busy && kp == 0u && q == 0u) {
+#pragma unroll
+        for (uint32_t t = 0; t < 2u; ++t)
+            s_y[place][t * 16u + lane] = r.ok[t] ? product_of(sum[t], scale[t], s_vec[place], flags) : 0.0f;
+    }
+    __syncthreads();
+    for (uint32_t o = tid; o < a.tokens * 32u; o += kMoeThreads) {
+        const uint32_t t = o >> 5, row = row0 + (o & 31u);
+        if (row >= a.hidden) continue;
+        float y = 0.0f;
+        for (uint32_t j = t * a.k; j < (t + 1u) * a.k; ++j) {
+            const int32_t e = a.route[j];
+            if (e >= 0 && uint32_t(e) < a.experts) y += a.weight[j] * s_y[j][o & 31u];
+        }
+        if (a.y_bf16) static_cast<uint16_t*>(a.y)[uint64_t(t) * a.hidden + row] = narrow<uint16_t>(y);
+        else static_cast<float*>(a.y)[uint64_t(t) * a.hidden + row] = y;
     }
     flush_status(flags, a.status);
 }
@@ -717,8 +1457,13 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(MoeArgs a) {
 
 static size_t moe_round(uint64_t bytes) { return size_t((bytes + 255) / 256 * 256); }
 
+// Sweeps at most: one for every expert that is met, and one more for every five tokens (the least that a sweep takes).
+static uint64_t moe_items(uint64_t experts, uint64_t routes) {
+    return (routes < experts ? routes : experts) + routes / kMoeTokens;
+}
+
 struct MoeLayout {
-    size_t offsets, logits, xd, xe, h, hd, he, part, total;
+    size_t offsets, logits, items, list, xd, xs, h, hd, hs, part, total;
 };
 
 static MoeLayout moe_layout(int64_t experts, int64_t hidden, int64_t inter, int64_t tokens, int64_t k) {
@@ -732,11 +1477,13 @@ static MoeLayout moe_layout(int64_t experts, int64_t hidden, int64_t inter, int6
     const uint64_t routes = uint64_t(tokens) * uint64_t(k);
     l.offsets = take(3 * uint64_t(experts + 1) * 8);
     l.logits = take(uint64_t(tokens) * uint64_t(experts) * 8);
+    l.items = take((1 + moe_items(experts, routes)) * sizeof(MoeItem));
+    l.list = take(routes * 2);
     l.xd = take(uint64_t(tokens) * moe_digit_bytes(uint32_t(hidden)));
-    l.xe = take(uint64_t(tokens) * 4);
+    l.xs = take(uint64_t(tokens) * sizeof(Vector));
     l.h = take(routes * uint64_t(inter) * 4);
     l.hd = take(routes * moe_digit_bytes(uint32_t(inter)));
-    l.he = take(routes * 4);
+    l.hs = take(routes * sizeof(Vector));
     l.part = take(routes * uint64_t(hidden) * 4);
     l.total = at;
     return l;
@@ -751,20 +1498,64 @@ static bool moe_sizes_fit(int64_t experts, int64_t hidden, int64_t inter, int64_
            tokens * k <= kMoeRoutes;
 }
 
-// Rows of a block: whole tiles, so that the experts met (at most) fill the CUs once.
-static uint32_t moe_rows(uint32_t rows, uint64_t met) {
-    const uint64_t tiles = (rows + kMoeTile - 1) / kMoeTile, cus = uint64_t(device_cu_count());
-    uint64_t parts = (cus + met - 1) / met;
-    if (parts > tiles) parts = tiles;
-    return uint32_t((tiles + parts - 1) / parts) * kMoeTile;
+static size_t moe_group_lds(uint32_t cols) {
+    const uint32_t chunks = moe_chunks(cols);
+    return size_t(chunks < kMoeSlab ? chunks : kMoeSlab) * 4096;
+}
+
+// LDS of a table in it whose place is not fixed.
+static size_t moe_table_bytes(uint32_t npts) { return (size_t(npts) / 4 + 1) * 16; }
+
+// Where the table goes (Points): LDS, if the digits of one product fit beside it.
+static int moe_table(uint32_t npts, uint32_t hidden, uint32_t inter) {
+    if (npts < kMoeSmall) return 1;
+    const size_t group = moe_group_lds(hidden > inter ? hidden : inter);
+    return kMoeOwn + moe_table_bytes(npts) + group <= kMoeLds ? 2 : 0;
+}
+
+static size_t moe_table_lds(const MoeArgs& a) { return a.table == 2 ? moe_table_bytes(a.npts) : 0; }
+
+// The kernels' LDS without the digits.
+static size_t moe_own_lds(const MoeArgs& a) { return kMoeOwn + (a.table == 1 ? kMoeSmall * 4 : 0) + moe_table_lds(a); }
+
+// Products of a sweep at most, where LDS has room for their digits: one for up to five tokens, two for more.
+static uint32_t moe_groups(const MoeArgs& a, uint32_t cols) {
+    return a.tokens > kMoeTokens && moe_own_lds(a) + kMoeGroups * moe_group_lds(cols) <= kMoeLds ? kMoeGroups : 1;
+}
+
+// Whether down's blocks make the digits of h themselves.
+static bool moe_own_digits(uint32_t cols, uint32_t had) { return moe_chunks(cols) <= kMoeSlab && had <= 512; }
+
+template <bool IN, int TAB>
+static void moe_product(const MoeArgs& a, hipStream_t st) {
+    const uint32_t groups = a.most / kMoeTokens;
+    const size_t lds = moe_table_lds(a) + groups * moe_group_lds(IN ? a.hidden : a.inter);
+    const dim3 grid{unsigned(device_cu_count())};          // a block a CU: they share all sweeps' units
+    if (groups == 1) launch(moe_product_kernel<IN, TAB, 1>, grid, dim3(kMoeThreads), lds, st, a);
+    else launch(moe_product_kernel<IN, TAB, int(kMoeGroups)>, grid, dim3(kMoeThreads), lds, st, a);
 }
 
 template <bool IN>
-static void moe_product(const MoeArgs& a, bool tab, unsigned blocks, hipStream_t st) {
-    const uint32_t chunks = moe_chunks(IN ? a.hidden : a.inter);
-    const size_t lds = (tab ? size_t(a.npts + 2) / 2 * 16 : 0) + size_t(chunks < kMoeSlab ? chunks : kMoeSlab) * 16 * 256;
-    if (tab) launch(moe_product_kernel<IN, true>, dim3(blocks), dim3(kMoeThreads), lds, st, a);
-    else launch(moe_product_kernel<IN, false>, dim3(blocks), dim3(kMoeThreads), lds, st, a);
+static void moe_product(const MoeArgs& a, hipStream_t st) {
+    switch (a.table) {
+        case 1: moe_product<IN, 1>(a, st); break;
+        case 2: moe_product<IN, 2>(a, st); break;
+        default: moe_product<IN, 0>(a, st); break;
+    }
+}
+
+static size_t moe_direct_lds(const MoeArgs& a) {
+    return moe_table_lds(a) + (a.tokens * a.k + kMoeTokens - 1) / kMoeTokens * moe_group_lds(a.inter);
+}
+
+static void moe_direct(const MoeArgs& a, hipStream_t st) {
+    const size_t lds = moe_direct_lds(a);
+    const dim3 grid((a.hidden + 31u) / 32u);
+    switch (a.table) {
+        case 1: launch(moe_direct_kernel<1>, grid, dim3(kMoeThreads), lds, st, a); break;
+        case 2: launch(moe_direct_kernel<2>, grid, dim3(kMoeThreads), lds, st, a); break;
+        default: launch(moe_direct_kernel<0>, grid, dim3(kMoeThreads), lds, st, a); break;
+    }
 }
 
 static e8q_status_t moe_matrix(const e8q_experts_t* m, MoeMatrix& out) {
@@ -849,33 +1640,42 @@ extern "C" e8q_status_t e8q_moe_core_escape(const e8q_experts_t* gate, const e8q
     a.up.offsets = a.offsets + (experts + 1);
     a.down.offsets = a.offsets + 2 * (experts + 1);
     a.xd = reinterpret_cast<uint8_t*>(ws + l.xd);
-    a.xe = reinterpret_cast<int*>(ws + l.xe);
+    a.xs = reinterpret_cast<Vector*>(ws + l.xs);
     a.h = reinterpret_cast<float*>(ws + l.h);
     a.hd = reinterpret_cast<uint8_t*>(ws + l.hd);
-    a.he = reinterpret_cast<int*>(ws + l.he);
+    a.hs = reinterpret_cast<Vector*>(ws + l.hs);
     a.part = reinterpret_cast<float*>(ws + l.part);
+    a.n_items = reinterpret_cast<uint32_t*>(ws + l.items);
+    a.items = reinterpret_cast<MoeItem*>(ws + l.items) + 1;
+    a.list = reinterpret_cast<uint16_t*>(ws + l.list);
     a.y = y_out;
     a.y_bf16 = y_dtype == E8Q_BF16;
     a.pts = tab->dpoints;
     a.npts = uint32_t(tab->size);
+    a.table = moe_table(a.npts, a.hidden, a.inter);
     a.status = status_dev;
     const uint64_t routes = uint64_t(tokens) * uint64_t(top_k);
-    const uint64_t met = routes < uint64_t(experts) ? routes : uint64_t(experts);
-    a.rows_in = moe_rows(a.inter, met);
-    a.rows_down = moe_rows(a.hidden, met);
-    a.parts_in = (a.inter + a.rows_in - 1) / a.rows_in;
-    a.parts_down = (a.hidden + a.rows_down - 1) / a.rows_down;
-    const bool lds = a.npts < kMoeTable;
+    a.split_direct = uint32_t(routes >= kMoeWaves ? 1 : kMoeWaves / routes);
+    if (a.split_direct > moe_chunks(a.inter)) a.split_direct = moe_chunks(a.inter);
+    a.k_div = make_fastdiv(a.k);
+    a.experts_div = make_fastdiv(a.experts);
+    a.ready_down = !moe_own_digits(a.inter, a.had_down);
+    const uint32_t groups_in = moe_groups(a, a.hidden), groups_down = moe_groups(a, a.inter);
+    a.most = (groups_in < groups_down ? groups_in : groups_down) * kMoeTokens;
+    a.direct = !a.ready_down && routes <= kMoeDirect && moe_direct_lds(a) + moe_own_lds(a) - moe_table_lds(a) <= kMoeLds;
+    a.choose = router && a.direct && tokens * experts <= int64_t(kMoeInline) && a.tokens <= kMoeTokens;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    launch(moe_prepare_kernel, dim3(a.tokens + 3u), dim3(kMoeThreads), 0, s, a);
-    if (router) {
-        launch(moe_logits_kernel, dim3((a.experts + 3u) / 4u, (a.tokens + kRouteTokens - 1u) / kRouteTokens), dim3(256), 0,
-               s, a);
-        launch(moe_choose_kernel, dim3((a.tokens + 3u) / 4u), dim3(256), 0, s, a);
+    const uint32_t logits = (a.experts + kMoeWaves - 1u) / kMoeWaves * ((a.tokens + kRouteTokens - 1u) / kRouteTokens);
+    launch(moe_prepare_kernel, dim3(3u + a.tokens + (router ? logits : 0u)), dim3(kMoeThreads), 0, s, a);
+    if (router && !a.choose) launch(moe_choose_kernel, dim3(a.tokens), dim3(256), 0, s, a);
+    if (!a.choose) launch(moe_plan_kernel, dim3(1), dim3(kMoeThreads), 0, s, a);
+    moe_product<true>(a, s);
+    if (a.direct) {
+        moe_direct(a, s);
+        return launch_status();
     }
-    moe_product<true>(a, lds, unsigned(met * a.parts_in), s);
-    launch(moe_digits_kernel, dim3(unsigned(routes)), dim3(kMoeThreads), 0, s, a);
-    moe_product<false>(a, lds, unsigned(met * a.parts_down), s);
+    if (a.ready_down) launch(moe_inner_digits_kernel, dim3(unsigned(routes)), dim3(kMoeThreads), 0, s, a);
+    moe_product<false>(a, s);
     launch(moe_combine_kernel, dim3((a.hidden + 255u) / 256u, a.tokens), dim3(256), 0, s, a);
     return launch_status();
 }
