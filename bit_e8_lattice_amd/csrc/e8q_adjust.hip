@@ -6,16 +6,23 @@
 //   out = x''' where the mask's bit is set, -inf where not (whatever x is).
 //
 // A block has a part of a row, and a word in LDS for each of its elements: the
-// count, a bit for "in the history", a bit for "has a bias".  It reads the whole history
-// of the row (from L2: the row's other blocks read it too) and counts the ids of
-// its part with LDS atomics on integers, whose result does not depend on their order.  Then
-// it streams its part.  A vector whose words are all zero is copied; one that the
-// mask empties is written without being read; in place, one that nothing touches
-// is not met at all.  Biases of the part are listed in LDS, and the wave looks a
-// biased element up together; several of one element are added in the order of
-// their places.
+// count, a bit for "in the history", a bit for "has a bias".  Its threads load their vectors
+// of the part, and the first of the row's history, before anything is waited for; then
+// the whole history is read (from L2: the row's other blocks read it too) and the ids of
+// the part are counted with LDS atomics on integers, whose result does not depend on their
+// order.  A vector whose words are all zero is copied; one that the mask empties is
+// written without being read; in place, one that nothing touches is not met at all.
+// Few elements are touched (2048 ids in a vocabulary of 131072), so a lane takes its
+// touched elements one by one: all elements of every vector with a touched one, the wave
+// through, made the arithmetic the bound (512 rows of 131072 bf16 logits with 2048 ids,
+// biases and a mask: 81.5 us so, 68.8 one by one).  Biases of the part are
+// chained in LDS by their elements; a lane walks the chain of its own, and the wave walks
+// all of them together for an element that has very many (483 rows of 930 tokens, 300
+// biases each: 218 us with the wave for every element, 18).  Several of one element
+// are added in the order of their places.
 //
-// The bound is memory: the logits in and out.
+// The bound is memory: the logits in and out, 54 us of the 68.8 at a large copy's
+// rate.  One row takes 4.8 us, the wait for its length, its ids and its logits in turn.
 #include "e8q_rows.hpp"
 
 namespace e8q {
@@ -58,57 +65,161 @@ __device__ __forceinline__ float divide(float x, float r, float inv) {
     return __builtin_isinf(q) ? q : fmaf(fmaf(-q, r, x), inv, q);
 }
 
-// Biases of a part: element | place << 16 and value, `n` of them, in any order.
+// Biases of a part, each in the slot of its place in the row's list: chains of slots by the
+// element's low bits.  A node is the element (kNoElement: not of this part) and the next
+// slot + 1 << 16.
 struct BiasList {
-    uint32_t* key;
+    uint32_t* head;
+    uint32_t* node;
     float* value;
-    uint32_t* n;
+    uint32_t n;
 };
+constexpr uint32_t kHeads = 1024, kNoElement = 0xFFFFu, kChain = 16;
 
-// The sum of the element's biases in the order of their places, by the whole wave.
-__device__ __forceinline__ float bias_of(const BiasList& l, uint32_t local, uint32_t lane) {
-    float sum = 0.0f;
-    uint32_t next = 0u;                                // places below are added
-    for (;;) {
-        uint32_t best = 0xFFFFFFFFu;
-        float v = 0.0f;
-        for (uint32_t j = lane; j < *l.n; j += kWave) {
-            const uint32_t key = l.key[j], place = key >> 16;
-            if ((key & 0xFFFFu) == local && place >= next && place < best) {
-                best = place;
-                v = l.value[j];
-            }
+// The sum of the element's biases in the order of their places, by its own lane; false: its chain is
+// longer than kChain.
+__device__ __forceinline__ bool bias_short(const BiasList& l, uint32_t local, float& sum) {
+    const uint32_t first = l.head[local % kHeads];
+    uint32_t at = first, m = 0u, one = 0u;
+    for (uint32_t steps = 0u; at && steps < kChain; ++steps) {
+        const uint32_t q = l.node[at - 1u];
+        if ((q & 0xFFFFu) == local) {
+            one = at - 1u;
+            ++m;
         }
-        uint32_t first = best;
-        first = min(first, lane_xor<32>(first));
-        first = min(first, lane_xor<16>(first));
-        first = min(first, lane_xor<8>(first));
-        first = min(first, lane_xor<4>(first));
-        first = min(first, lane_xor<2>(first));
-        first = min(first, lane_xor<1>(first));
-        if (first == 0xFFFFFFFFu) return sum;
-        const int src = __ffsll((unsigned long long)__ballot(best == first)) - 1;
-        sum += __uint_as_float(uint32_t(__builtin_amdgcn_readlane(int(__float_as_uint(v)), src)));
-        next = first + 1u;
+        at = q >> 16;
+    }
+    if (at) return false;
+    sum = 0.0f;
+    if (m == 1u) sum += l.value[one];
+    for (uint32_t next = 0u; m > 1u && next < l.n;) {
+        uint32_t best = l.n;
+        for (at = first; at;) {
+            const uint32_t q = l.node[at - 1u];
+            if ((q & 0xFFFFu) == local && at - 1u >= next) best = min(best, at - 1u);
+            at = q >> 16;
+        }
+        if (best < l.n) sum += l.value[best];
+        next = best + 1u;
+    }
+    return true;
+}
+
+// The same by the whole wave, over all slots.
+__device__ __forceinline__ float bias_long(const BiasList& l, uint32_t local, uint32_t lane) {
+    float sum = 0.0f;
+    for (uint32_t base = 0u; base < l.n; base += kWave) {
+        const uint32_t j = base + lane;
+        const float v = j < l.n ? l.value[j] : 0.0f;
+        uint64_t who = __ballot(j < l.n && (l.node[min(j, l.n - 1u)] & 0xFFFFu) == local);
+        while (who) {
+            const int src = __ffsll((unsigned long long)who) - 1;
+            who &= who - 1ull;
+            sum += __uint_as_float(uint32_t(__builtin_amdgcn_readlane(int(__float_as_uint(v)), src)));
+        }
+    }
+    return sum;
+}
+
+// Element i of a vector, i known at run time only.
+template <typename T>
+__device__ __forceinline__ float element(const u32x4_t& raw, uint32_t i) {
+    const uint32_t k = sizeof(T) == 2 ? i >> 1 : i;
+    const uint32_t r0 = raw[0], r1 = raw[1], r2 = raw[2], r3 = raw[3];
+    const uint32_t r = k & 2u ? (k & 1u ? r3 : r2) : (k & 1u ? r1 : r0);
+    if constexpr (sizeof(T) == 4) return __uint_as_float(r);
+    return __uint_as_float(i & 1u ? r & 0xFFFF0000u : r << 16);
+}
+
+template <typename T>
+__device__ __forceinline__ void put_element(u32x4_t& raw, uint32_t i, float y) {
+#pragma unroll
+    for (uint32_t k = 0u; k < 4u; ++k) {
+        const uint32_t r = raw[k];
+        if constexpr (sizeof(T) == 4) {
+            raw[k] = i == k ? __float_as_uint(y) : r;
+        } else {
+            const uint32_t h = narrow<T>(y), with = i & 1u ? (r & 0xFFFFu) | h << 16 : (r & 0xFFFF0000u) | h;
+            raw[k] = i >> 1 == k ? with : r;
+        }
     }
 }
 
+// -inf where the mask has no bit.
+template <typename T>
+__device__ __forceinline__ u32x4_t masked(const u32x4_t& raw, uint32_t bits) {
+    u32x4_t o;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t r = raw[k];
+        if constexpr (sizeof(T) == 4) {
+            o[k] = (bits >> k) & 1u ? r : 0xFF800000u;
+        } else {
+            const uint32_t keep = ((bits >> (2 * k)) & 1u ? 0xFFFFu : 0u) | ((bits >> (2 * k + 1)) & 1u ? 0xFFFF0000u : 0u);
+            o[k] = (r & keep) | (0xFF80FF80u & ~keep);
+        }
+    }
+    return o;
+}
+
+// A thread has kAdjElements of the part, as vectors that it loads before the history is
+// read: their latency and the history's are one.
+constexpr int kAdjElements = 16;
+
 template <typename T, int BLOCK, bool TABLE>
 __global__ __launch_bounds__(BLOCK) void adjust_kernel(AdjArgs a) {
-    constexpr int VE = kVec<T>;
+    constexpr int VE = kVec<T>, NV = kAdjElements / VE;
+    constexpr uint32_t kFull = (1u << VE) - 1u;
     extern __shared__ uint4 s_adjust[];
-    __shared__ uint32_t s_n;
     const uint32_t tid = threadIdx.x, lane = tid & 63u;
     const uint32_t row = blockIdx.x / a.chunks, part = blockIdx.x - row * a.chunks;
     const uint32_t lo = part * a.chunk, n = min(a.chunk, a.vocab - lo);
     const T* x = static_cast<const T*>(a.x) + int64_t(row) * a.stride + lo;
     T* out = static_cast<T*>(a.out) + int64_t(row) * a.out_stride + lo;
     uint32_t* word = reinterpret_cast<uint32_t*>(s_adjust);
-    const BiasList list = {word + a.chunk, reinterpret_cast<float*>(word + a.chunk + a.n_bias), &s_n};
+    const BiasList list = {word + a.chunk, word + a.chunk + kHeads,
+                           reinterpret_cast<float*>(word + a.chunk + kHeads + a.n_bias), a.n_bias};
+    const uint32_t* mask = a.mask ? a.mask + int64_t(row) * a.mask_stride : nullptr;
+    const bool in_place = a.out == a.x;
+    const uint32_t nvec = (n + VE - 1u) / VE;
+    // the mask's bits of the thread's vectors; none where there is no vector
+    uint32_t bits[NV];
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        const uint32_t j = u * BLOCK + tid, e = lo + j * VE;
+        bits[u] = j >= nvec ? 0u : mask ? (mask[e >> 5] >> (e & 31u)) & kFull : kFull;
+    }
+    u32x4_t raw[NV];
+    const auto load = [&](int u) {
+        const uint32_t e0 = (u * BLOCK + tid) * VE;
+        if (e0 + VE <= n) {
+            raw[u] = reinterpret_cast<const RowVec<T>*>(x + e0)->v;
+        } else {
+            float v[VE];
+#pragma unroll
+            for (int i = 0; i < VE; ++i) v[i] = e0 + i < n ? widen(x[e0 + i]) : 0.0f;
+            raw[u] = pack(v);
+        }
+    };
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        raw[u] = u32x4_t{0u, 0u, 0u, 0u};
+        if (bits[u] != 0u && !in_place) load(u);
+    }
     float rep = 1.0f, inv = 1.0f, freq = 0.0f, pres = 0.0f;
     if constexpr (TABLE) {
+        constexpr int kIds = 2;                 // places in flight per thread
+        const int64_t hrow = int64_t(row) * a.hist_stride;
+        int64_t id[kIds];
+        // the first ids before the length is known: they are in the tensor
+#pragma unroll
+        for (int u = 0; u < kIds; ++u) {
+            const int64_t j = u * BLOCK + int64_t(tid);
+            id[u] = j < int64_t(a.hist_cap) ? id_at(a.hist, a.i64, hrow + j) : -1;
+        }
         for (uint32_t i = tid; i < (n + 7u) / 8u * 2u; i += BLOCK) s_adjust[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (tid == 0u) s_n = 0u;
+        if (a.n_bias)
+            for (uint32_t i = tid; i < kHeads; i += BLOCK) list.head[i] = 0u;
         uint32_t flags = 0u;
         int64_t len = 0, prompt = 0;
         if (a.hist) {
@@ -121,42 +232,48 @@ __global__ __launch_bounds__(BLOCK) void adjust_kernel(AdjArgs a) {
             inv = 1.0f / rep;
         }
         __syncthreads();
-        const int64_t hrow = int64_t(row) * a.hist_stride;
         // a prompt counts for the repetition penalty only
-        for (int64_t j = (a.rep ? 0 : prompt) + tid; j < len; j += BLOCK) {
-            const int64_t id = id_at(a.hist, a.i64, hrow + j);
-            if (id >= int64_t(a.vocab)) flags |= E8Q_STATUS_BAD_INDEX;
-            const int64_t e = id - int64_t(lo);
-            if (id < 0 || e < 0 || e >= int64_t(n)) continue;
-            if (j < prompt) atomicOr(&word[e], kSeen);
-            else atomicAdd(&word[e], 1u);
+        const int64_t from = a.rep ? 0 : prompt;
+        for (int64_t base = 0; base < len; base += kIds * BLOCK) {
+#pragma unroll
+            for (int u = 0; u < kIds; ++u) {
+                const int64_t j = base + u * BLOCK + int64_t(tid);
+                if (base > 0) id[u] = j < len ? id_at(a.hist, a.i64, hrow + j) : -1;
+            }
+#pragma unroll
+            for (int u = 0; u < kIds; ++u) {
+                const int64_t j = base + u * BLOCK + int64_t(tid);
+                if (j < from || j >= len) continue;
+                if (id[u] >= int64_t(a.vocab)) flags |= E8Q_STATUS_BAD_INDEX;
+                const int64_t e = id[u] - int64_t(lo);
+                if (id[u] < 0 || e < 0 || e >= int64_t(n)) continue;
+                if (j < prompt) atomicOr(&word[e], kSeen);
+                else atomicAdd(&word[e], 1u);
+            }
         }
         for (uint32_t j = tid; j < a.n_bias; j += BLOCK) {
-            const int64_t at = int64_t(row) * a.bias_stride + j, id = id_at(a.bias_idx, a.i64, at);
-            if (id >= int64_t(a.vocab)) flags |= E8Q_STATUS_BAD_INDEX;
-            const int64_t e = id - int64_t(lo);
-            if (id < 0 || e < 0 || e >= int64_t(n)) continue;
-            atomicOr(&word[e], kBiased);
-            const uint32_t k = atomicAdd(&s_n, 1u);
-            list.key[k] = uint32_t(e) | (j << 16);
-            list.value[k] = a.bias[at];
+            const int64_t at = int64_t(row) * a.bias_stride + j, t = id_at(a.bias_idx, a.i64, at);
+            if (t >= int64_t(a.vocab)) flags |= E8Q_STATUS_BAD_INDEX;
+            const int64_t e = t - int64_t(lo);
+            const bool here = t >= 0 && e >= 0 && e < int64_t(n);
+            uint32_t node = kNoElement;
+            if (here) {
+                atomicOr(&word[e], kBiased);
+                node = uint32_t(e) | atomicExch(&list.head[uint32_t(e) % kHeads], j + 1u) << 16;
+                list.value[j] = a.bias[at];
+            }
+            list.node[j] = node;
         }
         flush_status(flags, a.status);
         __syncthreads();
     }
-    const uint32_t* mask = a.mask ? a.mask + int64_t(row) * a.mask_stride : nullptr;
-    const bool in_place = a.out == a.x;
-    const uint32_t nvec = (n + VE - 1u) / VE;
-    // whole waves: biased elements are looked up by all lanes
-    for (uint32_t base = 0u; base < nvec; base += BLOCK) {
-        const uint32_t j = base + tid, e0 = j * VE;
-        const bool mine = j < nvec;
-        uint32_t bits = (1u << VE) - 1u, w[VE], any = 0u;
-        if (mask && mine) bits = (mask[(lo + e0) >> 5] >> ((lo + e0) & 31u)) & ((1u << VE) - 1u);
 #pragma unroll
-        for (int i = 0; i < VE; ++i) w[i] = 0u;
+    for (int u = 0; u < NV; ++u) {
+        const uint32_t j = u * BLOCK + tid, e0 = j * VE;
+        uint32_t left = 0u;                      // touched elements of the vector
         if constexpr (TABLE) {
-            if (mine) {
+            if (j < nvec) {
+                uint32_t w[VE], any = 0u;
 #pragma unroll
                 for (int i = 0; i < VE; i += 4) {
                     const uint4 q = s_adjust[(e0 + i) / 4u];
@@ -167,41 +284,49 @@ __global__ __launch_bounds__(BLOCK) void adjust_kernel(AdjArgs a) {
                 }
 #pragma unroll
                 for (int i = 0; i < VE; ++i) any |= w[i];
-            }
-        }
-        const bool write = mine && !(in_place && any == 0u && bits == (1u << VE) - 1u);
-        float v[VE];
+                if (any) {
 #pragma unroll
-        for (int i = 0; i < VE; ++i) v[i] = 0.0f;
-        if (write && bits != 0u) load_logits<T>(x, n, j, v);
-        if constexpr (TABLE) {
-            if (any) {
-#pragma unroll
-                for (int i = 0; i < VE; ++i) {
-                    const uint32_t c = w[i] & kCount;
-                    float y = v[i];
-                    if (w[i] & ~kBiased) y = y > 0.0f ? divide(y, rep, inv) : y * rep;
-                    if (c) y -= freq * float(c) + pres;
-                    v[i] = y;
+                    for (int i = 0; i < VE; ++i) left |= w[i] ? 1u << i : 0u;
                 }
             }
-            if (a.n_bias && __ballot((any & kBiased) != 0u)) {
-#pragma unroll
-                for (int i = 0; i < VE; ++i) {
-                    uint64_t who = __ballot((w[i] & kBiased) != 0u);
+        }
+        const bool write = j < nvec && !(in_place && left == 0u && bits[u] == kFull);
+        if (in_place && write && bits[u] != 0u) load(u);
+        if constexpr (TABLE) {
+            left &= bits[u];
+            while (__ballot(left != 0u)) {
+                // every lane its lowest one
+                const uint32_t i0 = left ? uint32_t(__ffs(int(left)) - 1) : 0u, local = e0 + i0;
+                const uint32_t w = left ? word[local] : 0u, c = w & kCount;
+                float y = element<T>(raw[u], i0);
+                if (w & ~kBiased) y = y > 0.0f ? divide(y, rep, inv) : y * rep;
+                if (c) y -= freq * float(c) + pres;
+                if (__ballot((w & kBiased) != 0u)) {
+                    float b = 0.0f;
+                    uint64_t who = __ballot((w & kBiased) && !bias_short(list, local, b));
                     while (who) {
                         const int src = __ffsll((unsigned long long)who) - 1;
                         who &= who - 1ull;
-                        const float b = bias_of(list, uint32_t(__builtin_amdgcn_readlane(int(e0), src)) + i, lane);
-                        if (lane == uint32_t(src)) v[i] += b;
+                        const float all = bias_long(list, uint32_t(__builtin_amdgcn_readlane(int(local), src)), lane);
+                        if (lane == uint32_t(src)) b = all;
                     }
+                    if (w & kBiased) y += b;
                 }
+                if (left) put_element<T>(raw[u], i0, y);
+                left &= left - 1u;
             }
         }
         if (!write) continue;
+        if (mask) raw[u] = masked<T>(raw[u], bits[u]);
+        if (e0 + VE <= n) {
+            __builtin_nontemporal_store(raw[u], &reinterpret_cast<RowVec<T>*>(out + e0)->v);
+        } else {
+            float v[VE];
+            unpack(raw[u], v);
 #pragma unroll
-        for (int i = 0; i < VE; ++i) v[i] = (bits >> i) & 1u ? v[i] : -INFINITY;
-        store_grad<T>(out, n, e0, v);
+            for (int i = 0; i < VE; ++i)
+                if (e0 + i < n) out[e0 + i] = narrow<T>(v[i]);
+        }
     }
 }
 
@@ -216,10 +341,11 @@ static uint32_t adjust_chunk(int64_t rows, int64_t vocab) {
 }
 
 static uint32_t adjust_threads(uint32_t chunk) { return chunk > 4096 ? 1024u : 256u; }
+static_assert(1024 * kAdjElements >= 16384 && 256 * kAdjElements >= 4096, "a block's threads hold its part");
 
 template <typename T, bool TABLE>
 static void adjust_launch(const AdjArgs& a, hipStream_t st) {
-    const size_t lds = TABLE ? size_t(a.chunk) * 4 + size_t(a.n_bias) * 8 : 0;
+    const size_t lds = TABLE ? size_t(a.chunk) * 4 + (a.n_bias ? size_t(kHeads) * 4 + size_t(a.n_bias) * 8 : 0) : 0;
     const dim3 grid(a.rows * a.chunks);
     if (adjust_threads(a.chunk) == 1024u) launch(adjust_kernel<T, 1024, TABLE>, grid, dim3(1024), lds, st, a);
     else launch(adjust_kernel<T, 256, TABLE>, grid, dim3(256), lds, st, a);

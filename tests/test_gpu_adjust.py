@@ -191,3 +191,19 @@ def test_counts_past_16_bits():
     a["prompt_len"][:] = 1
     out, _ = run(x, a)
     check(out, x, a)
+
+
+@pytest.mark.parametrize("vocab,n_bias,same", [(930, 300, 0), (930, 300, 40), (20000, 1024, 1024), (17, 1024, 0),
+                                               (300000, 1024, 12)])
+def test_many_biases_of_a_token(vocab, n_bias, same):
+    """More biases than tokens, one token named more often than a lane looks it up by itself, ids that share their low
+    bits."""
+    x, a = make(300 if vocab < 1000 else 2, vocab, torch.float32, 20, n_bias, False, vocab + same)
+    a["bias_idx"][:, :same] = vocab // 2
+    if same == 12:
+        a["bias_idx"][:, 12:] = torch.arange(n_bias - 12, device=x.device) % 290 * 1024 + 5
+    out, st = run(x, a)
+    assert st == 0
+    check(out, x, a)
+    again, _ = run(x, a)
+    assert torch.equal(out, again)
