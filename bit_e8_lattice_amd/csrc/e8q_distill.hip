@@ -10,19 +10,24 @@
 // P = sum_j w_j + w_r (w_r = 0 but for "rest").
 //
 // q_r is never formed as 1 - sum of q over K, which would lose it where the
-// student is sure of K: a bit for every element of the row (in LDS, a byte for each
-// vector) says whether the teacher names it, and the pass over the row keeps two pairs of a
-// running maximum and a sum, one of the named elements and one of the others.
-// A named element is met once in the row however often the teacher names it.
+// student is sure of K: there are two pairs of a running maximum and a sum.  The others' comes from
+// the pass over the row, where a bit for every element (in LDS, a byte for each vector) says
+// whether the teacher names it; the named elements' from their own logits, gathered by
+// the places, one place for each element however often the teacher names it.
 // Outside K the gradient is exp2((x - m_r) k - log2 s_r) (P q_r - w_r), m_r and
 // s_r the maximum and sum of the others, so its exponential is at most 1 and the
-// division by q_r is gone.  Where no other element is left (all named, or -inf),
-// w_r counts as 0.
+// division by q_r is gone.  It is written for every element, and then, after a barrier, the
+// places write theirs over it: looking the named elements up in the stream took
+// 1268 us where this takes 1015 (8192 rows of 131072 bf16 logits, 64 places).  Where
+// no other element is left (all named, or -inf), w_r counts as 0.
 //
 // Few rows are split over blocks (partial sums in the workspace) and joined by a second
 // kernel; whole rows are kept in registers between the sums and the gradient, or
-// read twice where they do not fit.  The bound is memory: the bytes of the
-// logits, and of the gradient.
+// read twice where they do not fit: the second time from the end, which the caches still
+// hold (8192 rows of 131072: 1015 us from the start, 973 from the end; in the
+// registers of one block of 1024 threads, which has a CU to itself, 1176).  The bound
+// is memory: the bytes of the logits, and of the gradient.  Reached of them:
+// 4.4 TB/s with 32768 and with 131072 bf16 logits a row (4096 rows 122 us), a copy 4.9.
 #include <float.h>
 
 #include "e8q_rows.hpp"
@@ -135,23 +140,24 @@ __device__ __forceinline__ Sums sums_block(Sums st, float k2, Sums* s) {
 // ------------------------------------------------------------ the teacher's places
 
 // A row's places in (dynamic) LDS: ids (-1: not used), probabilities and their logarithms as
-// given, and the marks of the vectors of a part of the row.
+// given, the student's logits, and the marks of the vectors of a part of the row.
 struct Places {
     int32_t* id;
     float* p;
     float* lp;
+    float* x;
     uint32_t* marks;
 };
 
 __device__ __forceinline__ Places places_lds(uint32_t k) {
     extern __shared__ uint32_t s_places[];
-    return {reinterpret_cast<int32_t*>(s_places), reinterpret_cast<float*>(s_places + k),
-            reinterpret_cast<float*>(s_places + 2u * k), s_places + 3u * k};
+    float* f = reinterpret_cast<float*>(s_places + k);
+    return {reinterpret_cast<int32_t*>(s_places), f, f + k, f + 2u * k, s_places + 4u * k};
 }
 
 static size_t places_bytes(uint32_t k, uint32_t vectors) {
     const uint32_t marked = vectors < kSegment ? vectors : kSegment;
-    return size_t(k) * 12 + (marked + 3) / 4 * 4;
+    return size_t(k) * 16 + (marked + 3) / 4 * 4;
 }
 
 __device__ __forceinline__ int64_t place_id(const DsArgs& a, uint64_t i) {
@@ -159,7 +165,8 @@ __device__ __forceinline__ int64_t place_id(const DsArgs& a, uint64_t i) {
 }
 
 // Fills the places; whether one of them is used (a barrier for the whole block).
-__device__ __forceinline__ bool load_places(const DsArgs& a, uint32_t row, const Places& pl) {
+template <typename T>
+__device__ __forceinline__ bool load_places(const DsArgs& a, uint32_t row, const T* x, const Places& pl) {
     uint32_t flags = 0u;
     int any = 0;
     for (uint32_t j = threadIdx.x; j < a.k; j += blockDim.x) {
@@ -170,86 +177,155 @@ __device__ __forceinline__ bool load_places(const DsArgs& a, uint32_t row, const
         pl.id[j] = live ? int32_t(t) : -1;
         pl.p[j] = live ? expf(lp) : 0.0f;
         pl.lp[j] = lp;
+        pl.x[j] = live ? widen(x[t]) : 0.0f;
         any |= int(live);
     }
     flush_status(flags, a.status);
     return __syncthreads_or(any) != 0;
 }
 
-// Marks the named elements of the vectors [lo, hi), at most kSegment of them.
+// Marks the named elements of the vectors [lo, hi), at most kSegment of them; whether places share one.
 template <typename T>
-__device__ __forceinline__ void mark_places(const Places& pl, uint32_t k, uint32_t lo, uint32_t hi) {
+__device__ __forceinline__ bool mark_places(const Places& pl, uint32_t k, uint32_t lo, uint32_t hi) {
     constexpr uint32_t VE = kVec<T>;
     for (uint32_t w = threadIdx.x; w < (hi - lo + 3u) / 4u; w += blockDim.x) pl.marks[w] = 0u;
     __syncthreads();
+    int shared = 0;
     for (uint32_t j = threadIdx.x; j < k; j += blockDim.x) {
         const int32_t id = pl.id[j];
         const uint32_t v = uint32_t(id) / VE;
         if (id < 0 || v < lo || v >= hi) continue;
-        atomicOr(&pl.marks[(v - lo) >> 2], 1u << (((v - lo) & 3u) * 8u + uint32_t(id) % VE));
+        const uint32_t bit = 1u << (((v - lo) & 3u) * 8u + uint32_t(id) % VE);
+        shared |= int((atomicOr(&pl.marks[(v - lo) >> 2], bit) & bit) != 0u);
     }
+    return __syncthreads_or(shared) != 0;
+}
+
+// Whether places share an element, where nothing is marked: they are entered into an open table, in place
+// of the marks.
+__host__ __device__ inline uint32_t places_slots(uint32_t k) {
+    uint32_t n = 4u;
+    while (n < 2u * k) n *= 2u;
+    return n;
+}
+
+__device__ __forceinline__ bool places_share(const Places& pl, uint32_t k) {
+    const uint32_t slots = places_slots(k);
+    for (uint32_t i = threadIdx.x; i < slots; i += blockDim.x) pl.marks[i] = 0u;
     __syncthreads();
+    int shared = 0;
+    for (uint32_t j = threadIdx.x; j < k; j += blockDim.x) {
+        const uint32_t key = uint32_t(pl.id[j]) + 1u;      // 0: not used
+        if (key == 0u) continue;
+        for (uint32_t at = key * 2654435761u >> 16, old = 1u; old != 0u; ++at) {
+            old = atomicCAS(&pl.marks[at % slots], 0u, key);
+            if (old == key) {
+                shared = 1;
+                break;
+            }
+        }
+    }
+    return __syncthreads_or(shared) != 0;
+}
+
+// Whether no place before j names its element.
+__device__ __forceinline__ bool first_of(const Places& pl, uint32_t j) {
+    const int32_t id = pl.id[j];
+    for (uint32_t i = 0u; i < j; ++i)
+        if (pl.id[i] == id) return false;
+    return true;
+}
+
+// Calls go(j) for a place of each named element of the vectors [lo, hi), a thread each.
+template <typename T, class Go>
+__device__ __forceinline__ void each_named(const Places& pl, uint32_t k, uint32_t lo, uint32_t hi, bool shared, Go&& go) {
+    for (uint32_t j = threadIdx.x; j < k; j += blockDim.x) {
+        const int32_t id = pl.id[j];
+        const uint32_t v = uint32_t(id) / kVec<T>;
+        if (id >= 0 && v >= lo && v < hi && !(shared && !first_of(pl, j))) go(j, id);
+    }
 }
 
 __device__ __forceinline__ uint32_t marks_of(const Places& pl, uint32_t v) {
     return reinterpret_cast<const uint8_t*>(pl.marks)[v];
 }
 
-// Adds N vectors' elements; `marks` has a byte for each vector.
+// Adds the elements of N vectors that no place names; `marks` has a byte for each vector.
 template <typename T, int N>
-__device__ __forceinline__ void sums_add(Sums& st, float (&v)[N * kVec<T>], const uint32_t (&marks)[N], float k2) {
+__device__ __forceinline__ void add_others(Sum& st, float (&v)[N * kVec<T>], const uint32_t (&marks)[N], float k2) {
     constexpr int VE = kVec<T>;
-    uint32_t any = 0u;
 #pragma unroll
-    for (int u = 0; u < N; ++u) any |= marks[u];
-    if (__ballot(any != 0u)) {
+    for (int u = 0; u < N; ++u) {
+        if (!__ballot(marks[u] != 0u)) continue;
 #pragma unroll
-        for (int u = 0; u < N; ++u) {
-            if (!__ballot(marks[u] != 0u)) continue;
-            float w[VE];
-#pragma unroll
-            for (int i = 0; i < VE; ++i) {
-                const bool in = (marks[u] >> i) & 1u;
-                w[i] = in ? v[u * VE + i] : -INFINITY;
-                v[u * VE + i] = in ? -INFINITY : v[u * VE + i];
-            }
-            sum_add(st.named, w, k2);
-        }
+        for (int i = 0; i < VE; ++i) v[u * VE + i] = (marks[u] >> i) & 1u ? -INFINITY : v[u * VE + i];
     }
-    sum_add(st.other, v, k2);
+    sum_add(st, v, k2);
+}
+
+// Adds the named elements of the vectors [lo, hi).
+template <typename T>
+__device__ __forceinline__ void add_named(Sum& st, const Places& pl, uint32_t k, uint32_t lo, uint32_t hi, bool shared,
+                                          float k2) {
+    each_named<T>(pl, k, lo, hi, shared, [&](uint32_t j, int32_t) {
+        const float x = pl.x[j], m = fmaxf(st.m, x);
+        st.s = st.s * exp2_fast((st.m - m) * k2) + exp2_fast((x - m) * k2);
+        st.m = m;
+    });
+}
+
+// Vector j of a row; -inf behind its end.
+template <typename T>
+__device__ __forceinline__ u32x4_t load_raw(const T* x, uint32_t vocab, uint32_t j) {
+    constexpr int VE = kVec<T>;
+    const uint32_t e0 = j * VE;
+    if (e0 + VE <= vocab) return reinterpret_cast<const RowVec<T>*>(x + e0)->v;
+    float v[VE];
+#pragma unroll
+    for (int i = 0; i < VE; ++i) v[i] = e0 + i < vocab ? widen(x[e0 + i]) : -INFINITY;
+    return pack(v);
 }
 
 // Both sums of the vectors [lo, hi) of a row (all threads end with the block's).
-template <typename T, int BLOCK>
+template <typename T, int BLOCK, int UNROLL>
 __device__ __forceinline__ Sums row_sums(const DsArgs& a, const T* row, uint32_t lo, uint32_t hi, float k2,
-                                         const Places& pl) {
-    constexpr int VE = kVec<T>;
+                                         const Places& pl, bool& shared) {
+    constexpr int VE = kVec<T>, kGroup = 2;      // vectors unpacked at a time
     __shared__ Sums s_sums[BLOCK / kWave];
+    const uint32_t wave0 = uint32_t(__builtin_amdgcn_readfirstlane(int(threadIdx.x & ~63u)));
     Sums st = {sum_empty(), sum_empty()};
     for (uint32_t seg = lo; seg < hi; seg += kSegment) {
         const uint32_t end = min(hi, seg + kSegment);
         if (seg > lo) __syncthreads();               // the marks before are read
-        mark_places<T>(pl, a.k, seg, end);
-        for (uint32_t base = seg; base < end; base += BLOCK * kLpUnroll) {
-            float v[kLpUnroll * VE];
-            uint32_t marks[kLpUnroll];
+        const bool sh = mark_places<T>(pl, a.k, seg, end);
+        shared |= sh;
+        for (uint32_t base = seg; base < end; base += BLOCK * UNROLL) {
+            u32x4_t raw[UNROLL];
 #pragma unroll
-            for (int u = 0; u < kLpUnroll; ++u) {
-                const uint32_t j = base + u * BLOCK + threadIdx.x;
-                float w[VE];
-                if (j < end) {
-                    load_logits<T>(row, a.vocab, j, w);
-                    marks[u] = marks_of(pl, j - seg);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < VE; ++i) w[i] = -INFINITY;
-                    marks[u] = 0u;
-                }
-#pragma unroll
-                for (int i = 0; i < VE; ++i) v[u * VE + i] = w[i];
+            for (int u = 0; u < UNROLL; ++u) {
+                raw[u] = u32x4_t{0u, 0u, 0u, 0u};
+                if (base + u * BLOCK + wave0 < end)
+                    raw[u] = load_raw<T>(row, a.vocab, min(base + u * BLOCK + threadIdx.x, end - 1u));
             }
-            sums_add<T, kLpUnroll>(st, v, marks, k2);
+#pragma unroll
+            for (int u = 0; u < UNROLL; u += kGroup) {
+                if (base + u * BLOCK + wave0 >= end) break;      // nothing left for this wave
+                float v[kGroup * VE];
+                uint32_t marks[kGroup];
+#pragma unroll
+                for (int g = 0; g < kGroup; ++g) {
+                    const uint32_t j = base + (u + g) * BLOCK + threadIdx.x;
+                    float w[VE];
+                    unpack(raw[u + g], w);
+                    marks[g] = j < end ? marks_of(pl, j - seg) : 0xFFu;
+#pragma unroll
+                    for (int i = 0; i < VE; ++i) v[g * VE + i] = w[i];
+                }
+                add_others<T, kGroup>(st.other, v, marks, k2);
+                __builtin_amdgcn_sched_barrier(0);       // one group unpacked at a time
+            }
         }
+        add_named<T>(st.named, pl, a.k, seg, end, sh, k2);
     }
     return sums_block<BLOCK>(st, k2, s_sums);
 }
@@ -296,9 +372,8 @@ __device__ __forceinline__ float log_rest(const RowStats& st, float scale) {
 }
 
 // Loss and log probabilities of a row, by wave 0 of one block.
-template <typename T>
-__device__ __forceinline__ void write_row(const DsArgs& a, uint32_t row, const T* x, const RowStats& st,
-                                          const Teacher& t, const Places& pl) {
+__device__ __forceinline__ void write_row(const DsArgs& a, uint32_t row, const RowStats& st, const Teacher& t,
+                                          const Places& pl) {
     if (threadIdx.x >= kWave) return;
     const float ln_s = st.l2 * kLn2;
     float loss = 0.0f;
@@ -306,7 +381,7 @@ __device__ __forceinline__ void write_row(const DsArgs& a, uint32_t row, const T
         const int32_t id = pl.id[j];
         float lq = 0.0f;
         if (id >= 0) {
-            lq = st.l2 == -INFINITY ? -INFINITY : (widen(x[id]) - st.m) * a.scale - ln_s;
+            lq = st.l2 == -INFINITY ? -INFINITY : (pl.x[j] - st.m) * a.scale - ln_s;
             const float p = pl.p[j];
             if (!(p == 0.0f)) loss += p * t.factor * (pl.lp[j] + t.log_factor - lq);
         }
@@ -343,17 +418,18 @@ __global__ __launch_bounds__(kLpBlock) void distill_kernel(DsArgs a) {
     const uint32_t nvec = (a.vocab + kVec<T> - 1) / kVec<T>;
     const uint32_t lo = min(sp * a.per_split, nvec), hi = min(lo + a.per_split, nvec);
     const float k2 = a.scale * kLog2e;
-    if (!load_places(a, row, pl)) {
+    if (!load_places<T>(a, row, x, pl)) {
         if (a.splits == 1) write_empty(a, row);
         return;
     }
-    const Sums st = row_sums<T, kLpBlock>(a, x, lo, hi, k2, pl);
+    bool shared = false;
+    const Sums st = row_sums<T, kLpBlock, kLpUnroll>(a, x, lo, hi, k2, pl, shared);
     if (a.splits > 1) {
         if (threadIdx.x == 0u) a.part[blockIdx.x] = make_float4(st.other.m, st.other.s, st.named.m, st.named.s);
         return;
     }
     const RowStats rs = row_stats(st, k2);
-    write_row<T>(a, row, x, rs, teacher_row(a, pl, rs), pl);
+    write_row(a, row, rs, teacher_row(a, pl, rs), pl);
 }
 
 // Joins the parts of one row.
@@ -365,7 +441,7 @@ __global__ __launch_bounds__(kLpBlock) void distill_join_kernel(DsArgs a) {
     const T* x = static_cast<const T*>(a.x) + int64_t(row) * a.stride;
     const float k2 = a.scale * kLog2e;
     Sums st = {sum_empty(), sum_empty()};
-    if (!load_places(a, row, pl)) {
+    if (!load_places<T>(a, row, x, pl)) {
         write_empty(a, row);
         return;
     }
@@ -375,7 +451,7 @@ __global__ __launch_bounds__(kLpBlock) void distill_join_kernel(DsArgs a) {
     }
     st = sums_block<kLpBlock>(st, k2, s_sums);
     const RowStats rs = row_stats(st, k2);
-    write_row<T>(a, row, x, rs, teacher_row(a, pl, rs), pl);
+    write_row(a, row, rs, teacher_row(a, pl, rs), pl);
 }
 
 // ------------------------------------------------------------ gradient
@@ -384,14 +460,14 @@ __global__ __launch_bounds__(kLpBlock) void distill_join_kernel(DsArgs a) {
 // l2_all), scale g (P q - w) inside.
 struct GradRow {
     float c, m, l2, cq, m_all, l2_all, cw, k2;
-    bool none;                  // nothing outside K
 };
 
 __device__ __forceinline__ GradRow grad_row(const DsArgs& a, const RowStats& st, const Teacher& t, float g) {
     const float up = a.scale * g;
-    GradRow r = {up * t.total, st.m, st.l2, up * t.total, st.m, st.l2, up * t.factor, a.scale * kLog2e,
-                 st.l2_other == -INFINITY};
-    if (t.rest > 0.0f) {
+    GradRow r = {up * t.total, st.m, st.l2, up * t.total, st.m, st.l2, up * t.factor, a.scale * kLog2e};
+    if (st.l2_other == -INFINITY) {                    // all others are -inf: exp2 gives their 0
+        r.c = r.m = r.l2 = 0.0f;
+    } else if (t.rest > 0.0f) {
         r.c = up * (t.total * expf(log_rest(st, a.scale)) - t.rest);
         r.m = st.m_other;
         r.l2 = st.l2_other;
@@ -399,64 +475,55 @@ __device__ __forceinline__ GradRow grad_row(const DsArgs& a, const RowStats& st,
     return r;
 }
 
-// The gradient of one vector from its logits, in place.
+// The gradient of one vector, as if no place named an element of it.
 template <typename T>
-__device__ __forceinline__ void grad_vector(const DsArgs& a, float (&v)[kVec<T>], uint32_t e0, uint32_t marks,
-                                            const GradRow& r, const Places& pl) {
-    constexpr int VE = kVec<T>;
-    float d[VE];
+__device__ __forceinline__ void grad_store(const DsArgs& a, T* dx, uint32_t e0, const u32x4_t& raw, const GradRow& r) {
+    float v[kVec<T>];
+    unpack(raw, v);
 #pragma unroll
-    for (int i = 0; i < VE; ++i) d[i] = r.none ? 0.0f : r.c * exp2_fast((v[i] - r.m) * r.k2 - r.l2);
-    if (__ballot(marks != 0u)) {
-        const uint32_t lane = threadIdx.x & 63u;
-#pragma unroll
-        for (int i = 0; i < VE; ++i) {
-            uint64_t who = __ballot((marks >> i) & 1u);
-            while (who) {
-                const int src = __ffsll((unsigned long long)who) - 1;
-                who &= who - 1ull;
-                const int32_t id = __builtin_amdgcn_readlane(int(e0), src) + i;
-                float w = 0.0f;                            // every place that names it
-                for (uint32_t j = lane; j < a.k; j += kWave) w += pl.id[j] == id ? pl.p[j] : 0.0f;
-                w = add_wave(w);
-                if (lane == uint32_t(src)) {
-                    const float q = r.l2_all == -INFINITY ? 0.0f : exp2_fast((v[i] - r.m_all) * r.k2 - r.l2_all);
-                    d[i] = r.l2_all == -INFINITY ? 0.0f : r.cq * q - r.cw * w;
-                }
-            }
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < VE; ++i) v[i] = d[i];
+    for (int i = 0; i < kVec<T>; ++i) v[i] = r.c * exp2_fast((v[i] - r.m) * r.k2 - r.l2);
+    store_grad<T>(dx, a.vocab, e0, v);
 }
 
-// The vectors [lo, hi) of the gradient row; `marked`: the marks of the first segment stand.
+// Then the named elements of the vectors [lo, hi), after a barrier: over what grad_store left there.
 template <typename T>
-__device__ __forceinline__ void grad_part(const DsArgs& a, const T* x, T* dx, uint32_t lo, uint32_t hi,
-                                          const GradRow& r, const Places& pl, bool marked) {
-    constexpr int VE = kVec<T>;
-    for (uint32_t seg = lo; seg < hi; seg += kSegment) {
-        const uint32_t end = min(hi, seg + kSegment);
-        if (!(marked && seg == lo)) {
-            __syncthreads();
-            mark_places<T>(pl, a.k, seg, end);
+__device__ __forceinline__ void grad_named(const DsArgs& a, T* dx, uint32_t lo, uint32_t hi, bool shared,
+                                           const GradRow& r, const Places& pl) {
+    __syncthreads();
+    each_named<T>(pl, a.k, lo, hi, shared, [&](uint32_t j, int32_t id) {
+        float w = pl.p[j];
+        if (shared) {                                      // every place that names it
+            double sum = 0.0;
+            for (uint32_t i = 0u; i < a.k; ++i) sum += pl.id[i] == id ? pl.p[i] : 0.0f;
+            w = float(sum);
         }
-        // whole waves: the named elements are looked up by all lanes
-        for (uint32_t base = seg; base < end; base += blockDim.x) {
-            const uint32_t j = base + threadIdx.x;
-            float v[VE];
-            uint32_t marks = 0u;
-            if (j < end) {
-                load_logits<T>(x, a.vocab, j, v);
-                marks = marks_of(pl, j - seg);
-            } else {
+        const float q = exp2_fast((pl.x[j] - r.m_all) * r.k2 - r.l2_all);
+        dx[id] = narrow<T>(r.l2_all == -INFINITY ? 0.0f : r.cq * q - r.cw * w);
+    });
+}
+
+// The vectors [lo, hi) of the gradient row.
+template <typename T, int UNROLL>
+__device__ __forceinline__ void grad_part(const DsArgs& a, const T* x, T* dx, uint32_t lo, uint32_t hi,
+                                          const GradRow& r, const Places& pl, bool shared) {
+    const uint32_t step = blockDim.x * UNROLL;
+    for (uint32_t left = (hi - lo + step - 1u) / step; left-- > 0u;) {
+        const uint32_t base = lo + left * step;
+        u32x4_t raw[UNROLL];
 #pragma unroll
-                for (int i = 0; i < VE; ++i) v[i] = 0.0f;
-            }
-            grad_vector<T>(a, v, j * VE, marks, r, pl);
-            if (j < end) store_grad<T>(dx, a.vocab, j * VE, v);
+        for (int u = 0; u < UNROLL; ++u) {
+            const uint32_t j = base + u * blockDim.x + threadIdx.x;
+            raw[u] = u32x4_t{0u, 0u, 0u, 0u};
+            if (j < hi) raw[u] = load_raw<T>(x, a.vocab, j);
+        }
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+            const uint32_t j = base + u * blockDim.x + threadIdx.x;
+            if (j < hi) grad_store<T>(a, dx, j * kVec<T>, raw[u], r);
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
+    grad_named<T>(a, dx, lo, hi, shared, r, pl);
 }
 
 template <typename T>
@@ -479,18 +546,19 @@ __global__ __launch_bounds__(kLpBlock) void distill_backward_kernel(DsArgs a) {
     const uint32_t lo = min(sp * a.per_split, nvec), hi = min(lo + a.per_split, nvec);
     const float4 s = a.stats[row];
     const float g = a.g[row];
-    if (!load_places(a, row, pl)) {
+    if (!load_places<T>(a, row, x, pl)) {
         zero_part<T>(a, dx, lo, hi);
         return;
     }
     const RowStats rs = {s.x, s.y, s.z, s.w};
-    grad_part<T>(a, x, dx, lo, hi, grad_row(a, rs, teacher_row(a, pl, rs), g), pl, false);
+    const bool shared = places_share(pl, a.k);
+    grad_part<T, kLpUnroll>(a, x, dx, lo, hi, grad_row(a, rs, teacher_row(a, pl, rs), g), pl, shared);
 }
 
-// Sums and gradient of a row that fits the registers of one block, NV vectors a
-// thread: the row is read once.
-template <typename T, int BLOCK, int NV>
-__global__ __launch_bounds__(BLOCK) void distill_grad_kernel(DsArgs a) {
+// Sums (and gradient) of a row that fits the registers of one block, NV vectors a
+// thread: the row is read once, and before the places are.
+template <typename T, int BLOCK, int NV, bool GRAD>
+__global__ __launch_bounds__(BLOCK) void distill_row_kernel(DsArgs a) {
     constexpr int VE = kVec<T>, kGroup = 2;      // vectors unpacked at a time
     __shared__ Sums s_sums[BLOCK / kWave];
     const Places pl = places_lds(a.k);
@@ -501,24 +569,14 @@ __global__ __launch_bounds__(BLOCK) void distill_grad_kernel(DsArgs a) {
     const uint32_t wave0 = uint32_t(__builtin_amdgcn_readfirstlane(int(threadIdx.x & ~63u)));
     u32x4_t raw[NV];
 #pragma unroll
-    for (int n = 0; n < NV; ++n) {
-        const uint32_t e0 = (n * BLOCK + threadIdx.x) * VE;
-        if (e0 + VE <= a.vocab) {
-            raw[n] = reinterpret_cast<const RowVec<T>*>(x + e0)->v;
-        } else {
-            float v[VE];
-#pragma unroll
-            for (int i = 0; i < VE; ++i) v[i] = e0 + i < a.vocab ? widen(x[e0 + i]) : -INFINITY;
-            raw[n] = pack(v);
-        }
-    }
-    const float g = a.g[row];
-    if (!load_places(a, row, pl)) {
+    for (int n = 0; n < NV; ++n) raw[n] = load_raw<T>(x, a.vocab, n * BLOCK + threadIdx.x);
+    const float g = GRAD ? a.g[row] : 0.0f;
+    if (!load_places<T>(a, row, x, pl)) {
         write_empty(a, row);
-        zero_part<T>(a, dx, 0u, nvec);
+        if constexpr (GRAD) zero_part<T>(a, dx, 0u, nvec);
         return;
     }
-    mark_places<T>(pl, a.k, 0u, nvec);
+    const bool shared = mark_places<T>(pl, a.k, 0u, nvec);
     const float k2 = a.scale * kLog2e;
     Sums st = {sum_empty(), sum_empty()};
 #pragma unroll
@@ -535,48 +593,47 @@ __global__ __launch_bounds__(BLOCK) void distill_grad_kernel(DsArgs a) {
             for (int i = 0; i < VE; ++i) v[u * VE + i] = w[i];
             marks[u] = j < nvec ? marks_of(pl, j) : 0u;
         }
-        sums_add<T, kGroup>(st, v, marks, k2);
+        add_others<T, kGroup>(st.other, v, marks, k2);
         __builtin_amdgcn_sched_barrier(0);       // one group unpacked at a time
     }
+    add_named<T>(st.named, pl, a.k, 0u, nvec, shared, k2);
     st = sums_block<BLOCK>(st, k2, s_sums);
     const RowStats rs = row_stats(st, k2);
     const Teacher t = teacher_row(a, pl, rs);
-    write_row<T>(a, row, x, rs, t, pl);
-    __syncthreads();                 // the places' logits are read before dx (maybe x) is written
+    write_row(a, row, rs, t, pl);
+    if constexpr (!GRAD) return;
     const GradRow r = grad_row(a, rs, t, g);
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
         if (uint32_t(n * BLOCK) + wave0 >= nvec) break;
         const uint32_t j = n * BLOCK + threadIdx.x;
-        float v[VE];
-        unpack(raw[n], v);
-        grad_vector<T>(a, v, j * VE, j < nvec ? marks_of(pl, j) : 0u, r, pl);
-        if (j < nvec) store_grad<T>(dx, a.vocab, j * VE, v);
+        if (j < nvec) grad_store<T>(a, dx, j * VE, raw[n], r);
         __builtin_amdgcn_sched_barrier(0);
     }
+    grad_named<T>(a, dx, 0u, nvec, shared, r, pl);
 }
 
 // The same for longer rows: two passes over the row.
 template <typename T>
-__global__ __launch_bounds__(kLpWide) void distill_grad_long_kernel(DsArgs a) {
+__global__ __launch_bounds__(kLpWide, 8) void distill_grad_long_kernel(DsArgs a) {
     const Places pl = places_lds(a.k);
     const uint32_t row = blockIdx.x;
     const T* x = static_cast<const T*>(a.x) + int64_t(row) * a.stride;
     T* dx = static_cast<T*>(a.dx) + int64_t(row) * a.dx_stride;
     const uint32_t nvec = (a.vocab + kVec<T> - 1) / kVec<T>;
     const float g = a.g[row];
-    if (!load_places(a, row, pl)) {
+    if (!load_places<T>(a, row, x, pl)) {
         write_empty(a, row);
         zero_part<T>(a, dx, 0u, nvec);
         return;
     }
     const float k2 = a.scale * kLog2e;
-    const Sums st = row_sums<T, kLpWide>(a, x, 0u, nvec, k2, pl);
+    bool shared = false;
+    const Sums st = row_sums<T, kLpWide, kLpUnroll>(a, x, 0u, nvec, k2, pl, shared);
     const RowStats rs = row_stats(st, k2);
     const Teacher t = teacher_row(a, pl, rs);
-    write_row<T>(a, row, x, rs, t, pl);
-    __syncthreads();                 // the places' logits are read before dx (maybe x) is written
-    grad_part<T>(a, x, dx, 0u, nvec, grad_row(a, rs, t, g), pl, nvec <= kSegment);
+    write_row(a, row, rs, t, pl);
+    grad_part<T, kLpUnroll>(a, x, dx, 0u, nvec, grad_row(a, rs, t, g), pl, shared);
 }
 
 // ------------------------------------------------------------ host
@@ -638,6 +695,15 @@ template <typename T>
 static void ds_forward(DsArgs& a, void* ws, hipStream_t st) {
     a.splits = lp_splits(a.rows, a.vocab, sizeof(T), a.per_split);
     a.part = static_cast<float4*>(ws);
+    // short rows: as many in flight as there is room for
+    const uint32_t nvec = ds_vectors(a.vocab, sizeof(T)), block = nvec <= 64 * 4 ? 64u : nvec <= 128 * 4 ? 128u : 256u;
+    if (a.splits == 1 && nvec <= 256 * 4) {
+        const auto kernel = block == 64u    ? distill_row_kernel<T, 64, 4, false>
+                            : block == 128u ? distill_row_kernel<T, 128, 4, false>
+                                            : distill_row_kernel<T, 256, 4, false>;
+        launch(kernel, dim3(a.rows), dim3(block), places_bytes(a.k, nvec), st, a);
+        return;
+    }
     launch(distill_kernel<T>, dim3(a.rows * a.splits), dim3(kLpBlock), places_bytes(a.k, a.per_split), st, a);
     if (a.splits > 1) launch(distill_join_kernel<T>, dim3(a.rows), dim3(kLpBlock), places_bytes(a.k, 0), st, a);
 }
@@ -645,19 +711,19 @@ static void ds_forward(DsArgs& a, void* ws, hipStream_t st) {
 template <typename T>
 static void ds_backward(DsArgs& a, hipStream_t st) {
     a.splits = lp_splits(a.rows, a.vocab, sizeof(T), a.per_split);
-    launch(distill_backward_kernel<T>, dim3(a.rows * a.splits), dim3(kLpBlock), places_bytes(a.k, a.per_split), st, a);
+    launch(distill_backward_kernel<T>, dim3(a.rows * a.splits), dim3(kLpBlock), places_bytes(a.k, 0) + size_t(places_slots(a.k)) * 4, st, a);
 }
 
 // Whole rows: the smallest block whose registers hold one; longer rows are read twice.
 template <typename T, class Go>
 static void ds_grad_kernel(int64_t vocab, Go&& go) {
     const uint32_t nvec = ds_vectors(vocab, sizeof(T));
-    if (nvec <= 64 * 4) go(distill_grad_kernel<T, 64, 4>, 64u);
-    else if (nvec <= 128 * 4) go(distill_grad_kernel<T, 128, 4>, 128u);
-    else if (nvec <= 256 * 4) go(distill_grad_kernel<T, 256, 4>, 256u);
-    else if (nvec <= 256 * 8) go(distill_grad_kernel<T, 256, 8>, 256u);
-    else if (nvec <= 256 * 16) go(distill_grad_kernel<T, 256, 16>, 256u);
-    else if (sizeof(T) == 4 && nvec <= 512 * 16) go(distill_grad_kernel<T, 512, 16>, 512u);
+    if (nvec <= 64 * 4) go(distill_row_kernel<T, 64, 4, true>, 64u);
+    else if (nvec <= 128 * 4) go(distill_row_kernel<T, 128, 4, true>, 128u);
+    else if (nvec <= 256 * 4) go(distill_row_kernel<T, 256, 4, true>, 256u);
+    else if (nvec <= 256 * 8) go(distill_row_kernel<T, 256, 8, true>, 256u);
+    else if (nvec <= 256 * 16) go(distill_row_kernel<T, 256, 16, true>, 256u);
+    else if (sizeof(T) == 4 && nvec <= 512 * 16) go(distill_row_kernel<T, 512, 16, true>, 512u);
     else go(distill_grad_long_kernel<T>, unsigned(kLpWide));
 }
 

@@ -242,3 +242,31 @@ def test_the_same_for_any_stream_and_run():
         again, _ = calls(x, idx, lp, "rest", 1.0, w, stream=side)
         for n in first:
             assert torch.equal(first[n], again[n]), n
+
+
+@pytest.mark.parametrize("tail", ["renorm", "rest"])
+@pytest.mark.parametrize("rows,vocab,dtype", [(3, 600, torch.float32), (2, 30000, torch.bfloat16),
+                                              (1100, 5000, torch.bfloat16), (1100, 70000, torch.bfloat16)])
+def test_places_that_share_tokens(rows, vocab, dtype, tail):
+    """300 places for 40 tokens, the first and the last of the vocabulary among them."""
+    x, idx, lp, w = make(rows, vocab, dtype, 300 if vocab >= 1200 else 150, rows + vocab)
+    idx = idx % 40 * (vocab // 40)
+    idx[:, 7] = idx[:, 50] = vocab - 1
+    o, st = calls(x, idx, lp, tail, 1.0, w)
+    assert st == 0
+    check(o, x, idx, lp, tail, 1.0, w, rows=None if rows < 10 else [0, 500, rows - 1])
+
+
+@pytest.mark.parametrize("rows,vocab", [(5, 9000), (1100, 9000), (1030, 40000)])
+def test_gradient_over_the_logits(rows, vocab):
+    """The gradient may take the logits' place."""
+    x, idx, lp, w = make(rows, vocab, torch.bfloat16, 20, 12, pad=4)
+    o, _ = calls(x, idx, lp, "rest", 1.0, w)
+    ws = torch.zeros(e8q.e8q_distill_workspace_size(rows, vocab, 20), dtype=torch.uint8, device=x.device)
+    st = torch.zeros(1, dtype=torch.int32, device=x.device)
+    y = x.clone()
+    e8q.e8q_distill_grad(y, idx, lp, w, y, ws, st, tail=e8q.TAIL_REST)
+    assert torch.equal(y, o["grad1"])
+    y = x.clone()
+    e8q.e8q_distill_backward(y, idx, lp, o["stats"], w, y, st, tail=e8q.TAIL_REST)
+    assert torch.equal(y, o["grad"]) and int(st.item()) == 0
