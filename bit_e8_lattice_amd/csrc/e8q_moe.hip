@@ -552,25 +552,35 @@ __global__ __launch_bounds__(kMoeThreads) void moe_plan_kernel(MoeArgs a) {
 
 // ------------------------------------------------------------ the experts' products
 
-// 2z of an escaped slot: by halves among the sorted records of its expert; the first probe about where an even spread
-// would have it.
-__device__ __forceinline__ bool moe_record(const uint32_t* esc, uint64_t lo, uint64_t hi, uint32_t group, uint32_t groups,
-                                           uint32_t (&rec)[4]) {
-    uint64_t mid = 0ull;
-    if (lo < hi) {
-        const float at = float(group) * __builtin_amdgcn_rcpf(float(groups)) * float(hi - lo);
-        mid = min(lo + uint64_t(at), hi - 1u);
-    }
-    while (lo < hi) {
-        const uint32_t key = esc[mid * 5];
-        if (key == group) {
+// 2z of an escaped slot among the sorted records of its expert.  `next`: where the record behind the last one found
+// is, which is tried first (a lane's slots are consecutive groups); then probes where an even spread between
+// the keys known would have it, and halves if those do not end.
+constexpr uint32_t kNoRecord = 0xFFFFFFFFu;
+
+__device__ __forceinline__ bool moe_record(const uint32_t* esc, uint64_t begin, uint64_t end, uint32_t group,
+                                           uint32_t groups, uint32_t& next, uint32_t (&rec)[4]) {
+    const uint32_t* list = esc + begin * 5u;
+    uint32_t lo = 0u, hi = uint32_t(min(end - begin, uint64_t(groups))), from = 0u, to = groups;
+    for (uint32_t probes = 0u; lo < hi; ++probes) {
+        uint32_t mid = lo + ((hi - lo) >> 1);
+        if (probes == 0u && next < hi) mid = next;
+        else if (probes < 8u)
+            mid = lo + min(uint32_t(float(group - from) * __builtin_amdgcn_rcpf(float(to - from)) * float(hi - lo)), hi - lo - 1u);
+        const uint32_t* r = list + uint64_t(mid) * 5u;
+        const uint32_t key = r[0];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) rec[i] = esc[mid * 5 + 1 + i];
+        for (int i = 0; i < 4; ++i) rec[i] = r[1 + i];
+        if (key == group) {
+            next = mid + 1u;
             return true;
         }
-        if (key < group) lo = mid + 1;
-        else hi = mid;
-        mid = lo + ((hi - lo) >> 1);
+        if (key < group) {
+            lo = mid + 1u;
+            from = key + 1u;
+        } else {
+            hi = mid;
+            to = key;
+        }
     }
     return false;
 }
@@ -740,7 +750,7 @@ __device__ __forceinline__ void set_rows(Rows& r, int t, const MoeMatrix& m, uin
 // The operand of one slot that may be escaped: its point, or its record's low bytes (+ 8) or high bytes.
 template <int TAB>
 __device__ __forceinline__ uint2 resolve(const Points<TAB>& pts, const Rows& r, bool second, uint32_t id, uint32_t g, bool high,
-                                         bool& wide, uint32_t& flags) {
+                                         uint32_t (&next)[2], bool& wide, uint32_t& flags) {
     uint2 out = high ? make_uint2(0u, 0u) : make_uint2(kZeroBytes, kZeroBytes);
     if (id < pts.n) return high ? out : point_bytes(pts.word(id));
     if (g >= r.gpr || !(second ? r.ok[1] : r.ok[0])) return out;
@@ -748,22 +758,24 @@ __device__ __forceinline__ uint2 resolve(const Points<TAB>& pts, const Rows& r, 
         flags |= E8Q_STATUS_BAD_INDEX;
         return out;
     }
-    uint32_t rec[4];
+    uint32_t rec[4], at_next = second ? next[1] : next[0];
     const uint32_t group = (second ? r.first[1] : r.first[0]) + g, kept = second ? r.n_kept[1] : r.n_kept[0];
     bool found = false;
     if (kept != kManyRecords) {
         const uint32_t* list = second ? r.kept[1] : r.kept[0];
-        for (uint32_t i = 0; i < kept; ++i)
+        for (uint32_t i = at_next == kNoRecord ? 0u : at_next; i < kept; ++i)
             if (list[i * 5u] == group) {
                 found = true;
+                at_next = i + 1u;
 #pragma unroll
                 for (uint32_t k = 0; k < 4u; ++k) rec[k] = list[i * 5u + 1u + k];
                 break;
             }
     } else {
         const uint64_t* at = second ? r.offsets[1] : r.offsets[0];
-        found = moe_record(second ? r.esc[1] : r.esc[0], at[0], at[1], group, r.groups, rec);
+        found = moe_record(second ? r.esc[1] : r.esc[0], at[0], at[1], group, r.groups, at_next, rec);
     }
+    (second ? next[1] : next[0]) = at_next;
     if (!found) {
         flags |= E8Q_STATUS_ESC_MISSING;
         return out;
@@ -844,6 +856,7 @@ __device__ __forceinline__ void sweep_chunk(const Points<TAB>& pts, const Rows& 
         }
         return;
     }
+    uint32_t next[2] = {kNoRecord, kNoRecord};
     const uint32_t g0 = c * 32u + (here_only(0u) + (threadIdx.x & 63u)) / 16u * 8u;
     Rows rare = r;
     rare.gpr = here_only(r.gpr);
@@ -866,7 +879,7 @@ __device__ __forceinline__ void sweep_chunk(const Points<TAB>& pts, const Rows& 
             for (uint32_t k = 0; k < 4u; ++k) {            // tile k / 2, slot k % 2
                 const uint32_t v = k < 2u ? w[0] : w[1];
                 const uint2 out = resolve<TAB>(pts, rare, k >= 2u, (k & 1u) ? v >> 16 : v & 0xFFFFu, g0 + 2u * s + (k & 1u), HIGH,
-                                               wide, flags);
+                                               next, wide, flags);
 #pragma unroll
                 for (uint32_t i = 0; i < 4u; ++i)
                     if (k == i) p[i >> 1][i & 1u] = out;
