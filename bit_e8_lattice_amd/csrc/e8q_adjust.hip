@@ -21,8 +21,8 @@
 // biases each: 218 us with the wave for every element, 18).  Several of one element
 // are added in the order of their places.
 //
-// The bound is memory: the logits in and out, 54 us of the 68.8 at a large copy's
-// rate.  One row takes 4.8 us, the wait for its length, its ids and its logits in turn.
+// The bound is memory: logits in and out, history and mask are 60 us of the 68.8 at a
+// large copy's rate.  One row takes 4.8 us, the wait for its length, its ids and its logits in turn.
 #include "e8q_rows.hpp"
 
 namespace e8q {

@@ -11,10 +11,14 @@
 // sums on the int8 matrix cores:
 //   A (16 x 64): 16 rows x 8 groups of points, a byte for each 2z;
 //   B (64 x 16): the same groups' digits, column 3 j + d holding digit d of token j.
-// So one product serves five tokens, and a sweep over an expert's indices up to three
-// such products (15 tokens).  The rounding to fixed point, half a step of 2^-23 of the largest |x~|, is
-// of the size of float32's own; two digits (2^-15) would be more than a bfloat16 activation's
-// rounding in a vector with one strong channel.
+// So one product serves five tokens, and a sweep over an expert's indices up to two
+// such products (10 tokens; three left too few registers).  The step is 2^-23 of the largest |x~|,
+// so that the rounding is of the size of float32's own (5 tokens in float32: 3.2e-7 of
+// the result against float64, 5.1e-7 with float32 products of restored weights);
+// two digits (2^-15) would be more than a bfloat16 activation's rounding in a vector with one
+// strong channel.
+// A core point's bytes are 2z + 8, from a table of four bytes a point: the sums lose
+// 8 sum N at the end, and the LDS banks that a look-up takes are half of eight bytes'.
 // An escaped slot's 2z has up to 16 bits: its low byte goes into A, and where one has a
 // high byte the tile is swept once more for those.
 //
@@ -23,9 +27,18 @@
 //
 // Launches: the router's products (float64: a near-tie must not depend on the
 // order of a sum) beside the digits of x; the choice of experts (a few logits: inside the
-// next); gate and up of the chosen experts with the activation; down, whose blocks rotate h and
-// make its digits (past 2048 columns a launch before it); the weighted sum in the order of
-// the places (up to 16 places: inside down).
+// third); the plan of sweeps over the chosen experts; gate and up of them with the
+// activation; down, whose blocks rotate h and make its digits (past 2048 columns a launch before
+// it); the weighted sum in the order of the places (up to 16 places: inside down).
+//
+// What bounds it (128 experts of 2048 x 768, 8 a token, C(16) and 3.0 x row RMS, medians of
+// a kernel trace): for one token three dependent launches of 5.4 + 14.9 + 15.4 us, each a
+// chain of waits (the choice, the table, the indices, the sum over waves) for 9 MB in
+// all; for 64 tokens gate and up 50.6 us and down 45.4, where 151 MB of indices are
+// 31 us at a large copy's rate and the look-ups in LDS about as long, one after the other in a
+// wave.  Without escaped slots the two take 45.6 and 40.3: a chunk with one is swept step by
+// step, and its record is looked for among those that the block has gathered, or by probing the
+// sorted records.
 #include <float.h>
 
 #include "e8q_device.hpp"

@@ -478,8 +478,8 @@ size_t e8q_gemv_workspace_size(int64_t batch, int64_t m, int64_t rows, int64_t c
  *   y_out        [tokens, hidden] in y_dtype (bf16: nearest even); a token without a used
  *                place has y = 0
  *   workspace    e8q_moe_workspace_size(...) bytes, 256-byte aligned
- * Rounding: x~ = R x (float32) is taken in fixed point, off by at most 2^(e-23) with
- * 2^(e-1) <= max |x~| < 2^e (2^-22 of the largest), the row sums are exact, a product is rounded once to
+ * Rounding: x~ = R x (float32) is taken in fixed point, N = rint(x~ S) with S = 8355000 / max |x~|
+ * (off by at most 2^-23 of the largest), the row sums are exact, a product is rounded once to
  * float32; so is down's, of h = act(g) u.  The sum over the places is float32, in their order.
  * A token holding a NaN or infinity has NaN outputs, others are not affected
  * (E8Q_STATUS_NONFINITE); a NaN router logit counts as -inf.  Malformed exports and bad

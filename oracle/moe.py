@@ -6,7 +6,7 @@ y = sum_j w_j D ( act(G x) * (U x) ), each matrix R^T (s z): a product is s sum 
 kappa H (sign * x).  Matrices come as 2z [rows, cols] and scale [rows] of each expert.
 
 Bounds (u = 2^-24): x~ of a block of b columns is off by (log2 b + 2) u times the block's sum of |x| kappa, and by
-2^(e-23) <= 2^-22 max |x~| for the fixed point; a product adds u of itself; act * up 16 u of itself
+at most 2^-23 max |x~| for the fixed point (2^-22 is allowed); a product adds u of itself; act * up 16 u of itself
 (and of |g| |u|: 1 + tanh cancels for negative g); its error passes through down; weights and their sum 40 u, the sum over
 k places k u of its terms.
 """
