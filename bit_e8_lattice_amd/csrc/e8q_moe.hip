@@ -598,11 +598,11 @@ __device__ __forceinline__ bool moe_record(const uint32_t* esc, uint64_t begin, 
     return false;
 }
 
-constexpr uint32_t kMoeRecords = 32;         // records of a block's rows that it keeps in LDS
+constexpr uint32_t kMoeRecords = 64;         // records of a block's rows that it keeps in LDS
 constexpr uint32_t kManyRecords = 0xFFFFFFFFu;
 
 // The records of an expert whose groups are in [first, last) into LDS (five words each), by one wave; how many, or
-// kManyRecords if they are more than `cap` (64 at most).  Sorted keys: 64 probes at a time find the first one.
+// kManyRecords if they are more than `cap` (or 64 or more).  Sorted keys: 64 probes at a time find the first one.
 __device__ __forceinline__ uint32_t gather_records(const MoeMatrix& m, uint32_t expert, uint32_t first, uint32_t last,
                                                    uint32_t* to, uint32_t cap) {
     const uint32_t lane = threadIdx.x & 63u;
@@ -630,7 +630,7 @@ __device__ __forceinline__ uint32_t gather_records(const MoeMatrix& m, uint32_t 
         own = at < end ? m.esc[at * 5] : 0xFFFFFFFFu;
     }
     const uint32_t n = uint32_t(__popcll(__ballot(own < last)));
-    if (n > cap) return kManyRecords;
+    if (n > cap || n == kWave) return kManyRecords;
     if (lane < n) {
         to[lane * 5u] = own;
 #pragma unroll
@@ -645,7 +645,7 @@ __device__ __forceinline__ uint32_t point_word(const uint2& p) { return (p.x - 0
 
 __device__ __forceinline__ uint2 point_bytes(uint32_t w) { return make_uint2(w & 0x0F0F0F0Fu, (w >> 4) & 0x0F0F0F0Fu); }
 
-constexpr uint32_t kZeroPoint = 0x88888888u, kZeroBytes = 0x08080808u;
+constexpr uint32_t kZeroPoint = 0x88888888u;
 
 // The indices of eight groups from `at` on, in a matrix of `total` groups (eight at least): the words past its end are not
 // read.  A row's last ones can be the next row's: they meet digits of 0.
@@ -760,30 +760,29 @@ __device__ __forceinline__ void set_rows(Rows& r, int t, const MoeMatrix& m, uin
     r.ok[t] = row < row_end;
 }
 
-// The operand of one slot that may be escaped: its point, or its record's low bytes (+ 8) or high bytes.
-template <int TAB>
-__device__ __forceinline__ uint2 resolve(const Points<TAB>& pts, const Rows& r, bool second, uint32_t id, uint32_t g, bool high,
-                                         uint32_t (&next)[2], bool& wide, uint32_t& flags) {
-    uint2 out = high ? make_uint2(0u, 0u) : make_uint2(kZeroBytes, kZeroBytes);
-    if (id < pts.n) return high ? out : point_bytes(pts.word(id));
-    if (g >= r.gpr || !(second ? r.ok[1] : r.ok[0])) return out;
-    if (id != 0xFFFFu) {
-        flags |= E8Q_STATUS_BAD_INDEX;
-        return out;
-    }
+// The operand of an escaped slot: its record's low bytes, or high ones (2z = 256 high + low, low in [-128, 127]; |2z| <= 2^14 in
+// an encoder's records).
+__device__ __forceinline__ uint2 record_bytes(const Rows& r, bool second, uint32_t g, bool high, uint32_t (&next)[2], bool& wide,
+                                              uint32_t& flags) {
     uint32_t rec[4], at_next = second ? next[1] : next[0];
     const uint32_t group = (second ? r.first[1] : r.first[0]) + g, kept = second ? r.n_kept[1] : r.n_kept[0];
     bool found = false;
     if (kept != kManyRecords) {
         const uint32_t* list = second ? r.kept[1] : r.kept[0];
-        for (uint32_t i = at_next == kNoRecord ? 0u : at_next; i < kept; ++i)
-            if (list[i * 5u] == group) {
+        uint32_t lo = 0u, hi = kept, mid = at_next < kept ? at_next : kept / 2u;
+        while (lo < hi) {
+            const uint32_t key = list[mid * 5u];
+            if (key == group) {
                 found = true;
-                at_next = i + 1u;
+                at_next = mid + 1u;
 #pragma unroll
-                for (uint32_t k = 0; k < 4u; ++k) rec[k] = list[i * 5u + 1u + k];
+                for (uint32_t k = 0; k < 4u; ++k) rec[k] = list[mid * 5u + 1u + k];
                 break;
             }
+            if (key < group) lo = mid + 1u;
+            else hi = mid;
+            mid = (lo + hi) / 2u;
+        }
     } else {
         const uint64_t* at = second ? r.offsets[1] : r.offsets[0];
         found = moe_record(second ? r.esc[1] : r.esc[0], at[0], at[1], group, r.groups, at_next, rec);
@@ -791,25 +790,26 @@ __device__ __forceinline__ uint2 resolve(const Points<TAB>& pts, const Rows& r, 
     (second ? next[1] : next[0]) = at_next;
     if (!found) {
         flags |= E8Q_STATUS_ESC_MISSING;
-        return out;
+        return make_uint2(0u, 0u);
     }
-    // 2z = 256 hi + lo, lo + 8 in [-128, 127]; |2z| <= 2^14 in an encoder's records
-    uint32_t l[2] = {0u, 0u}, h[2] = {0u, 0u};
-    bool ok = true;
+    moe_u16x2 most = {0, 0};
+    uint32_t above[4];                                     // 2z + 128: its upper byte is the high one
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const int z = int(int16_t(uint16_t((k & 1) ? rec[k >> 1] >> 16 : rec[k >> 1] & 0xFFFFu)));
-        const int hi = (z + 136) >> 8;
-        ok = ok && z >= -16384 && z <= 16384;
-        l[k >> 2] |= (uint32_t(z + 8) & 0xFFu) << (8 * (k & 3));
-        h[k >> 2] |= (uint32_t(hi) & 0xFFu) << (8 * (k & 3));
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t word = rec[k];
+        const moe_u16x2 z = __builtin_bit_cast(moe_u16x2, word);
+        most = __builtin_elementwise_max(most, moe_u16x2(z + moe_u16x2{16384, 16384}));
+        above[k] = __builtin_bit_cast(uint32_t, moe_u16x2(z + moe_u16x2{128, 128}));
     }
-    if (!ok) {
+    if (most.x > 32768u || most.y > 32768u) {
         flags |= E8Q_STATUS_X_RANGE;
-        return out;
+        return make_uint2(0u, 0u);
     }
-    wide |= (h[0] | h[1]) != 0u;
-    return high ? make_uint2(h[0], h[1]) : make_uint2(l[0], l[1]);
+    const uint2 h = make_uint2(__builtin_amdgcn_perm(above[1], above[0], 0x07050301u),
+                               __builtin_amdgcn_perm(above[3], above[2], 0x07050301u));
+    wide |= (h.x | h.y) != 0u;
+    return high ? h : make_uint2(__builtin_amdgcn_perm(rec[1], rec[0], 0x06040200u),
+                                 __builtin_amdgcn_perm(rec[3], rec[2], 0x06040200u));
 }
 
 __device__ __forceinline__ uint32_t most_index(const uint4& w) {
@@ -854,25 +854,36 @@ __device__ __forceinline__ void plain_chunk(const Points<TAB>& pts, const uint4 
     }
 }
 
-// One chunk of both tiles against `groups` products' digits (N at most).  With an escaped (or malformed) slot in the
-// wave, or for the high bytes, step by step.
-template <int TAB, int N, bool HIGH>
-__device__ __forceinline__ void sweep_chunk(const Points<TAB>& pts, const Rows& r, const uint4 (&word)[2], uint32_t c,
-                                            const uint4* digits, uint32_t part, uint32_t groups, moe_i32x4 (&acc)[2][N],
-                                            bool& wide, uint32_t& flags) {
-    if (!HIGH && !__ballot(max(most_index(word[0]), most_index(word[1])) >= pts.n)) {
-        if constexpr (N == 1) {
-            plain_chunk<TAB, 1>(pts, word, digits, part, acc);
-        } else {
-            if (groups == 1u) plain_chunk<TAB, 1>(pts, word, digits, part, acc);
-            else plain_chunk<TAB, N>(pts, word, digits, part, acc);
-        }
-        return;
+// The escaped slots among a lane's sixteen of a chunk: bit 4 s + k for step s, tile k / 2, slot k % 2.  A malformed index is
+// flagged, and its slot is 0.
+__device__ __forceinline__ uint32_t escaped(const Rows& r, uint32_t n, const uint4 (&word)[2], uint32_t g0, uint32_t& flags) {
+    uint32_t mask = 0u;
+#pragma unroll
+    for (uint32_t i = 0; i < 16u; ++i) {
+        const uint32_t s = i >> 2, t = (i >> 1) & 1u;
+        const uint32_t v = s == 0u ? word[t].x : s == 1u ? word[t].y : s == 2u ? word[t].z : word[t].w;
+        const uint32_t id = (i & 1u) ? v >> 16 : v & 0xFFFFu;
+        if (id < n || g0 + 2u * s + (i & 1u) >= r.gpr || !r.ok[t]) continue;
+        if (id == 0xFFFFu) mask |= 1u << i;
+        else flags |= E8Q_STATUS_BAD_INDEX;
     }
+    return mask;
+}
+
+// Index n, the zero point, in place of every index past the core.
+__device__ __forceinline__ uint32_t within(uint32_t w, uint32_t n) {
+    const uint32_t most = n | (n << 16);
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_min(__builtin_bit_cast(moe_u16x2, w),
+                                                                  __builtin_bit_cast(moe_u16x2, most)));
+}
+
+// The products of the escaped slots of a chunk, by steps that have one.
+template <int N>
+__device__ __forceinline__ void escape_chunk(const Rows& r, uint32_t mask, uint32_t g0, bool high, const uint4* digits,
+                                             uint32_t part, uint32_t groups, moe_i32x4 (&acc)[2][N], bool& wide,
+                                             uint32_t& flags) {
     uint32_t next[2] = {kNoRecord, kNoRecord};
-    const uint32_t g0 = c * 32u + (here_only(0u) + (threadIdx.x & 63u)) / 16u * 8u;
     Rows rare = r;
-    rare.gpr = here_only(r.gpr);
     rare.groups = here_only(r.groups);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -881,30 +892,18 @@ __device__ __forceinline__ void sweep_chunk(const Points<TAB>& pts, const Rows& 
     }
 #pragma unroll 1
     for (uint32_t s = 0; s < 4u; ++s) {
-        uint32_t w[2];
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-            w[t] = (s & 2u) ? ((s & 1u) ? word[t].w : word[t].z) : ((s & 1u) ? word[t].y : word[t].x);
-        const uint32_t m = max(max(w[0] & 0xFFFFu, w[0] >> 16), max(w[1] & 0xFFFFu, w[1] >> 16));
+        const uint32_t slots = (mask >> (4u * s)) & 15u;
+        if (!__ballot(slots != 0u)) continue;
         uint2 p[2][2] = {};
-        if (__ballot(m >= pts.n)) {
 #pragma unroll 1
-            for (uint32_t k = 0; k < 4u; ++k) {            // tile k / 2, slot k % 2
-                const uint32_t v = k < 2u ? w[0] : w[1];
-                const uint2 out = resolve<TAB>(pts, rare, k >= 2u, (k & 1u) ? v >> 16 : v & 0xFFFFu, g0 + 2u * s + (k & 1u), HIGH,
-                                               next, wide, flags);
+        for (uint32_t k = 0; k < 4u; ++k) {
+            const bool mine = (slots >> k) & 1u;
+            if (!__ballot(mine)) continue;
+            uint2 out = make_uint2(0u, 0u);
+            if (mine) out = record_bytes(rare, k >= 2u, g0 + 2u * s + (k & 1u), high, next, wide, flags);
 #pragma unroll
-                for (uint32_t i = 0; i < 4u; ++i)
-                    if (k == i) p[i >> 1][i & 1u] = out;
-            }
-        } else if (!HIGH) {
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                uint32_t a, b;
-                pts.pair(w[t], a, b);
-                p[t][0] = point_bytes(a);
-                p[t][1] = point_bytes(b);
-            }
+            for (uint32_t i = 0; i < 4u; ++i)
+                if (k == i) p[i >> 1][i & 1u] = out;
         }
         // (the products of groups that have no digits are left out)
 #pragma unroll
@@ -916,6 +915,36 @@ __device__ __forceinline__ void sweep_chunk(const Points<TAB>& pts, const Rows& 
             acc[1][g] = one[1][0];
         }
     }
+}
+
+// One chunk of both tiles against `groups` products' digits (N at most): the core's points, and the low bytes of escaped
+// slots; or only the high bytes of those.
+template <int TAB, int N, bool HIGH>
+__device__ __forceinline__ void sweep_chunk(const Points<TAB>& pts, const Rows& r, uint4 (&word)[2], uint32_t c,
+                                            const uint4* digits, uint32_t part, uint32_t groups, moe_i32x4 (&acc)[2][N],
+                                            bool& wide, uint32_t& flags) {
+    uint32_t mask = 0u;
+    const bool rare = HIGH || __ballot(max(most_index(word[0]), most_index(word[1])) >= pts.n) != 0ull;
+    if (rare) {
+        const uint32_t g0 = c * 32u + (here_only(0u) + (threadIdx.x & 63u)) / 16u * 8u, n = here_only(pts.n);
+        mask = escaped(r, n, word, g0, flags);
+        if constexpr (!HIGH) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                word[t] = make_uint4(within(word[t].x, n), within(word[t].y, n), within(word[t].z, n), within(word[t].w, n));
+        }
+    }
+    if constexpr (!HIGH) {
+        if constexpr (N == 1) {
+            plain_chunk<TAB, 1>(pts, word, digits, part, acc);
+        } else {
+            if (groups == 1u) plain_chunk<TAB, 1>(pts, word, digits, part, acc);
+            else plain_chunk<TAB, N>(pts, word, digits, part, acc);
+        }
+    }
+    if (rare && __ballot(mask != 0u))
+        escape_chunk<N>(r, mask, c * 32u + (here_only(0u) + (threadIdx.x & 63u)) / 16u * 8u, HIGH, digits, part, groups, acc,
+                        wide, flags);
 }
 
 // Index words of both tiles, kAhead chunks ahead.
