@@ -109,9 +109,10 @@ struct MoeArgs {
     uint32_t split_direct;           // waves of a place
     int ready_down;                  // the digits of h are in the workspace
     MoeItem* items;                  // the sweeps
-    uint32_t* n_items;
+    uint4* plan;                     // sweeps, parts of a sweep's rows in gate and up and in down
     uint16_t* list;                  // [tokens k] routes by expert
     uint32_t most;                   // tokens of a sweep
+    uint32_t blocks;                 // of a product's launch
     int choose;                      // the product's blocks choose the experts, without items
     int direct;                      // down sums over the places
     uint32_t* status;
@@ -506,8 +507,40 @@ __global__ __launch_bounds__(256) void moe_choose_kernel(MoeArgs a) {
     if (lane < a.k) a.weight[uint64_t(t) * a.k + lane] = w;
 }
 
+// Time of a job of `units` units, in quarters of a chunk's (about 1 us): six chunks beside its sweep (its tokens' digits and
+// records, 5 to 6.5 us), a round of sixteen units a chunk's for each and 1.3 for the sums, half as much again for two products.  A
+// round of few units is split along the chunks.
+__device__ __forceinline__ uint32_t job_cost(uint32_t units, uint32_t chunks, bool two) {
+    const uint32_t full = units / kMoeWaves, left = units % kMoeWaves;
+    const uint32_t sweep = 4u * (full * chunks + (chunks * left + kMoeWaves - 1u) / kMoeWaves);
+    return 24u + 5u * (full + (left ? 1u : 0u)) + sweep + (two ? sweep / 2u : 0u);
+}
+
+// How long the blocks take for `items` sweeps cut into `parts`, the first `heavy` ones of two products: the longest of the
+// first block, the last, and the one with the last job.
+__device__ __forceinline__ uint32_t plan_span(uint32_t items, uint32_t heavy, uint32_t parts, uint32_t each, uint32_t chunks,
+                                              uint32_t blocks) {
+    const uint32_t units = (each + parts - 1u) / parts, jobs = items * parts, turns = (jobs + blocks - 1u) / blocks;
+    const uint32_t one = job_cost(units, chunks, false), two = job_cost(units, chunks, true);
+    const uint32_t pos = jobs - 1u - (turns - 1u) * blocks;
+    const uint32_t ends[3] = {0u, blocks - 1u, (turns - 1u) & 1u ? blocks - 1u - pos : pos};
+    uint32_t span = 0u;
+#pragma unroll
+    for (uint32_t i = 0; i < 3u; ++i) {
+        uint32_t sum = 0u;
+        for (uint32_t t = 0; t < turns; ++t) {
+            const uint32_t job = t * blocks + (t & 1u ? blocks - 1u - ends[i] : ends[i]);
+            if (job < jobs) sum += job < heavy * parts ? two : one;
+        }
+        span = max(span, sum);
+    }
+    return span;
+}
+
+constexpr uint32_t kTurns = 4;               // jobs of a block that the plan considers
+
 // The sweeps: the routes by expert (their order within one has no effect on any result), and an item for every `most` of
-// them; the items past an expert's first come first, so that an expert that many tokens chose does not hold up the end.
+// them; those of two products come first, so that a block whose second job is a longer one had the shortest first.
 __global__ __launch_bounds__(kMoeThreads) void moe_plan_kernel(MoeArgs a) {
     __shared__ uint32_t s_count[kMoeExperts], s_first[kMoeExperts], s_wave[3][kMoeWaves];
     const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6, routes = a.tokens * a.k;
@@ -525,9 +558,10 @@ __global__ __launch_bounds__(kMoeThreads) void moe_plan_kernel(MoeArgs a) {
 #pragma unroll
     for (uint32_t i = 0; i < kEach; ++i) place[i] = e[i] >= 0 ? atomicAdd(&s_count[e[i]], 1u) : 0u;
     __syncthreads();
-    // running sums over the experts: routes, first items, further items
-    const uint32_t n = s_count[tid], sweeps = (n + a.most - 1u) / a.most;
-    uint32_t run[3] = {n, n ? 1u : 0u, n ? sweeps - 1u : 0u};
+    // running sums over the experts: routes, items of one product, items of two
+    const uint32_t n = s_count[tid], sweeps = (n + a.most - 1u) / a.most, last = n - (sweeps ? sweeps - 1u : 0u) * a.most;
+    const uint32_t light = a.most > kMoeTokens ? (last > 0u && last <= kMoeTokens ? 1u : 0u) : sweeps;
+    uint32_t run[3] = {n, light, sweeps - light};
     const uint32_t own[3] = {run[0], run[1], run[2]};
 #pragma unroll
     for (uint32_t off = 1; off < 64u; off *= 2u)
@@ -551,16 +585,34 @@ __global__ __launch_bounds__(kMoeThreads) void moe_plan_kernel(MoeArgs a) {
         }
     const uint32_t first = run[0] - own[0];
     s_first[tid] = first;
-    if (n) {
-        a.items[total[2] + run[1] - 1u] = {tid, first, min(n, a.most), 0u};
-        for (uint32_t i = 1; i < sweeps; ++i)
-            a.items[run[2] - own[2] + i - 1u] = {tid, first + i * a.most, min(n - i * a.most, a.most), 0u};
+    for (uint32_t i = 0; i < sweeps; ++i) {
+        const bool one = i >= sweeps - light;
+        const uint32_t at = one ? total[2] + run[1] - own[1] + i - (sweeps - light) : run[2] - own[2] + i;
+        a.items[at] = {tid, first + i * a.most, min(n - i * a.most, a.most), 0u};
     }
-    if (tid == 0u) *a.n_items = total[1] + total[2];
     __syncthreads();
 #pragma unroll
     for (uint32_t i = 0; i < kEach; ++i)
         if (e[i] >= 0) a.list[s_first[e[i]] + place[i]] = uint16_t(i * kMoeThreads + tid);
+    // the parts of the items: as many as the blocks take in 1 ... kTurns turns (one part at least); a lane each, of gate and up and
+    // of down
+    if (wave != kMoeWaves - 1u) return;
+    const uint32_t items = total[1] + total[2], turns = lane % kTurns + 1u;
+    const bool down = lane / kTurns & 1u;
+    const uint32_t each = down ? (a.hidden + 31u) / 32u : (a.inter + 15u) / 16u;
+    const uint32_t parts = min(each, max(1u, turns * a.blocks / max(1u, items)));
+    uint32_t best = plan_span(max(1u, items), total[2], parts, each, moe_chunks(down ? a.inter : a.hidden), a.blocks);
+    uint32_t own_parts = parts;
+#pragma unroll
+    for (uint32_t off = 1; off < kTurns; off *= 2u) {
+        const uint32_t other = uint32_t(__shfl_xor(int(best), int(off), 64)), p = uint32_t(__shfl_xor(int(own_parts), int(off), 64));
+        if (other < best || (other == best && p < own_parts)) {
+            best = other;
+            own_parts = p;
+        }
+    }
+    const uint32_t parts_down = uint32_t(__shfl(int(own_parts), int(kTurns), 64));
+    if (lane == 0u) *a.plan = make_uint4(items, own_parts, parts_down, 0u);
 }
 
 // ------------------------------------------------------------ the experts' products
@@ -1296,7 +1348,7 @@ __global__ __launch_bounds__(kMoeThreads) void moe_product_kernel(MoeArgs a) {
     const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t cols = IN ? a.hidden : a.inter, rows = IN ? a.inter : a.hidden, gpr = cols / 8u;
     constexpr uint32_t kUnit = IN ? 16u : 32u;
-    uint32_t flags = 0u, n_items;
+    uint32_t flags = 0u, n_items, parts = 0u;
     uint32_t* table = TAB == 1 ? reinterpret_cast<uint32_t*>(s_table2) : reinterpret_cast<uint32_t*>(s_moe);
     const Points<TAB> pts = {table, reinterpret_cast<const uint2*>(a.pts), a.npts};
     uint4* digits = s_moe + (TAB == 2 ? a.npts / 4u + 1u : 0u);
@@ -1338,29 +1390,24 @@ __global__ __launch_bounds__(kMoeThreads) void moe_product_kernel(MoeArgs a) {
         firsts = __ballot(first);
         n_items = uint32_t(__popcll(firsts));
     } else {
-        n_items = *a.n_items;
+        const uint4 plan = *a.plan;
+        n_items = plan.x;
+        parts = IN ? plan.y : plan.z;
         pts.fill(table);
     }
     n_items = __builtin_amdgcn_readfirstlane(n_items);
 
-    // this block's units: a part of an item, where the items' parts fit the grid, or a share of all items' units
+    // jobs: equal parts of the items' units, the first ones longest; the blocks take them to and fro
     const uint32_t each = (rows + kUnit - 1u) / kUnit;
-    uint32_t share = (n_items * each + gridDim.x - 1u) / gridDim.x;
-    const uint32_t parts = share ? (each + share - 1u) / share : 1u;
-    uint32_t at, end;
-    if (n_items * parts <= gridDim.x) {
-        const uint32_t item = blockIdx.x / parts, part = blockIdx.x - item * parts;
-        share = (each + parts - 1u) / parts;
-        at = item < n_items ? item * each + min(part * share, each) : n_items * each;
-        end = min(at + share, min(item + 1u, n_items) * each);
-    } else {
-        at = min(blockIdx.x * share, n_items * each);
-        end = min(at + share, n_items * each);
-    }
+    parts = __builtin_amdgcn_readfirstlane(choose ? max(1u, min(each, gridDim.x / max(1u, n_items))) : parts);
+    const uint32_t units = (each + parts - 1u) / parts, jobs = n_items * parts;
 #pragma unroll 1
-    while (at < end) {
-        const uint32_t nth = __builtin_amdgcn_readfirstlane(at / each), unit0 = at - nth * each;
-        const uint32_t unit1 = min(each, unit0 + (end - at)), row0 = unit0 * kUnit, row_end = min(rows, unit1 * kUnit);
+    for (uint32_t turn = 0u, at = blockIdx.x; at < jobs;
+         ++turn, at = turn * gridDim.x + (turn & 1u ? gridDim.x - 1u - blockIdx.x : blockIdx.x)) {
+        const uint32_t nth = __builtin_amdgcn_readfirstlane(at / parts), unit0 = (at - nth * parts) * units;
+        if (unit0 >= each) continue;
+        const uint32_t unit1 = min(each, unit0 + units), row0 = unit0 * kUnit, row_end = min(rows, unit1 * kUnit);
+        if (turn) __syncthreads();
         uint32_t expert, n;
         if (choose) {
             // the nth first place's expert and its places
@@ -1388,8 +1435,6 @@ __global__ __launch_bounds__(kMoeThreads) void moe_product_kernel(MoeArgs a) {
         __syncthreads();
         const Job job = {digits, s_list, s_vec, s_red, &s_kept[0][0][0], s_n_kept, expert, row0, row_end, n};
         multiply<IN, TAB, G>(a, pts, job, unit1 - unit0, moe_chunks(cols), flags, s_max, s_sum);
-        at += unit1 - unit0;
-        if (at < end) __syncthreads();
     }
     flush_status(flags, a.status);
 }
@@ -1585,7 +1630,7 @@ template <bool IN, int TAB>
 static void moe_product(const MoeArgs& a, hipStream_t st) {
     const uint32_t groups = a.most / kMoeTokens;
     const size_t lds = moe_table_lds(a) + groups * moe_group_lds(IN ? a.hidden : a.inter);
-    const dim3 grid{unsigned(device_cu_count())};          // a block a CU: they share all sweeps' units
+    const dim3 grid{a.blocks};               // a block a CU: they share all sweeps' jobs
     if (groups == 1) launch(moe_product_kernel<IN, TAB, 1>, grid, dim3(kMoeThreads), lds, st, a);
     else launch(moe_product_kernel<IN, TAB, int(kMoeGroups)>, grid, dim3(kMoeThreads), lds, st, a);
 }
@@ -1700,7 +1745,8 @@ extern "C" e8q_status_t e8q_moe_core_escape(const e8q_experts_t* gate, const e8q
     a.hd = reinterpret_cast<uint8_t*>(ws + l.hd);
     a.hs = reinterpret_cast<Vector*>(ws + l.hs);
     a.part = reinterpret_cast<float*>(ws + l.part);
-    a.n_items = reinterpret_cast<uint32_t*>(ws + l.items);
+    a.plan = reinterpret_cast<uint4*>(ws + l.items);
+    a.blocks = uint32_t(device_cu_count());
     a.items = reinterpret_cast<MoeItem*>(ws + l.items) + 1;
     a.list = reinterpret_cast<uint16_t*>(ws + l.list);
     a.y = y_out;

@@ -179,3 +179,32 @@ def test_streams_workspaces_and_smaller_batches():
             y, idx, weight, st = layer.run(x[:t].contiguous(), 3, router, ws=ws, stream=stream)
             assert st == 0 and torch.equal(y, first[0][:t]) and torch.equal(idx, first[1][:t])
             assert torch.equal(weight, first[2][:t])
+
+
+@pytest.mark.parametrize("experts,tokens,k", [(1024, 900, 4), (300, 40, 7), (40, 64, 8)])
+def test_sweeps_of_several_turns(experts, tokens, k):
+    """More sweeps than the chip has blocks, and some in between; experts that no token chose, and one that all did."""
+    layer = Layer(experts, 64, 48, 16, 3.0, 32, 16, experts, device())
+    x, router = inputs(layer, tokens, torch.bfloat16, torch.float32, 7)
+    router[5] = x.float().mean(dim=0) * 3 + 0.2 * x[0].float()
+    router[6] = 0
+    y, idx, weight, st = layer.run(x, k, router)
+    want_idx, want_w = oracle.moe_route(x.float().cpu().numpy(), router.cpu().numpy(), k, True)
+    assert st == 0 and np.array_equal(idx.cpu().numpy(), want_idx)
+    close(y, *layer.expect(x, want_idx, want_w))
+
+
+@pytest.mark.parametrize("tokens", [1, 3])
+def test_given_places_of_few_tokens(tokens):
+    """At most 16 places, whose sum is formed with the products: unused ones, one expert twice, ids out of range."""
+    layer = Layer(6, 256, 128, 16, 3.0, 128, 128, 9, device())
+    x, _ = inputs(layer, tokens, torch.float32, torch.float32, 2)
+    idx = torch.tensor([[2, 2, -1, 4], [-7, -1, -2, -3], [5, 0, 0, 0]][:tokens], dtype=torch.int32, device=x.device)
+    weight = torch.randn((tokens, 4), device=x.device)
+    y, _, _, st = layer.run(x, 4, idx=idx, weight=weight)
+    assert st == 0
+    close(y, *layer.expect(x, idx.cpu().numpy(), weight.cpu().numpy()))
+    idx[0, 3] = 100
+    y, _, _, st = layer.run(x, 4, idx=idx, weight=weight)
+    assert st == e8q.STATUS_BITS["BAD_INDEX"]
+    close(y, *layer.expect(x, idx.cpu().numpy(), weight.cpu().numpy()))
