@@ -440,25 +440,32 @@ __device__ __forceinline__ uint64_t logit_key(double v) {
 }
 
 // Logits of a token that are greater than that of expert e, or equal and before it: by the keys' high halves, and by
-// the whole keys where another has the same.
+// the whole keys where another has the same.  kRankLanes neighbouring lanes share an expert.
+constexpr uint32_t kRankLanes = 4;
+
+__device__ __forceinline__ uint32_t add_rank_lanes(uint32_t v) {
+    v += lane_xor<1>(v);
+    return v + lane_xor<2>(v);
+}
+
 __device__ __forceinline__ uint32_t logit_rank(const uint32_t* high, const uint32_t* low, uint32_t experts, uint32_t e) {
-    const uint32_t own = high[e];
+    const uint32_t own = high[e], sub = threadIdx.x % kRankLanes;
     uint32_t rank = 0u, same = 0u;
-#pragma unroll 16
-    for (uint32_t j = 0; j < experts; ++j) {
+#pragma unroll 8
+    for (uint32_t j = sub; j < experts; j += kRankLanes) {
         const uint32_t h = high[j];
         rank += h > own ? 1u : 0u;
         same += h == own ? 1u : 0u;
     }
-    if (same > 1u) {
+    if (add_rank_lanes(same) > 1u) {
         const uint32_t mine = low[e];
-#pragma unroll 8
-        for (uint32_t j = 0; j < experts; ++j) {
+#pragma unroll 4
+        for (uint32_t j = sub; j < experts; j += kRankLanes) {
             const uint32_t l = low[j];
             rank += high[j] == own && (l > mine || (l == mine && j < e)) ? 1u : 0u;
         }
     }
-    return rank;
+    return add_rank_lanes(rank);
 }
 
 // The weights of a token's places from their logits (in LDS, by place), by one wave.
@@ -479,13 +486,15 @@ __device__ __forceinline__ float place_weight(const MoeArgs& a, const double* ch
 }
 
 // The choice of experts, a block a token.
-__global__ __launch_bounds__(256) void moe_choose_kernel(MoeArgs a) {
+constexpr uint32_t kChooseThreads = 512;
+
+__global__ __launch_bounds__(kChooseThreads) void moe_choose_kernel(MoeArgs a) {
     __shared__ uint32_t s_high[kMoeExperts], s_low[kMoeExperts];
     __shared__ double s_chosen[kMoeTopK];
     const uint32_t t = blockIdx.x, tid = threadIdx.x, lane = tid & 63u;
     const double* row = a.logits + uint64_t(t) * a.experts;
     uint32_t flags = 0u;
-    for (uint32_t e = tid; e < a.experts; e += 256u) {
+    for (uint32_t e = tid; e < a.experts; e += kChooseThreads) {
         const double v = row[e];
         if (!(v - v == 0.0)) flags |= E8Q_STATUS_NONFINITE;
         const uint64_t key = logit_key(v);
@@ -494,9 +503,9 @@ __global__ __launch_bounds__(256) void moe_choose_kernel(MoeArgs a) {
     }
     flush_status(flags, a.status);
     __syncthreads();
-    for (uint32_t e = tid; e < a.experts; e += 256u) {
+    for (uint32_t e = tid / kRankLanes; e < a.experts; e += kChooseThreads / kRankLanes) {
         const uint32_t rank = logit_rank(s_high, s_low, a.experts, e);
-        if (rank < a.k) {
+        if (rank < a.k && tid % kRankLanes == 0u) {
             a.route[uint64_t(t) * a.k + rank] = int32_t(e);
             s_chosen[rank] = row[e];
         }
@@ -1359,9 +1368,9 @@ __global__ __launch_bounds__(kMoeThreads) void moe_product_kernel(MoeArgs a) {
         // a few logits: every block ranks them; the first one writes the places
         const uint32_t cells = a.tokens * a.experts, routes = a.tokens * a.k;
         const bool writer = blockIdx.x == 0u;
-        double logit = 0.0;
+        static_assert(kMoeInline * kRankLanes <= kMoeThreads, "the block ranks every logit at once");
         if (tid < cells) {
-            logit = a.logits[tid];
+            const double logit = a.logits[tid];
             if (!(logit - logit == 0.0) && writer) flags |= E8Q_STATUS_NONFINITE;
             const uint64_t key = logit_key(logit);
             s_high[tid] = uint32_t(key >> 32);
@@ -1369,12 +1378,13 @@ __global__ __launch_bounds__(kMoeThreads) void moe_product_kernel(MoeArgs a) {
         }
         pts.fill(table);
         __syncthreads();
-        if (tid < cells) {
-            const uint32_t t = fdiv(tid, a.experts_div), e = tid - t * a.experts;
+        const uint32_t cell = tid / kRankLanes;
+        if (cell < cells) {
+            const uint32_t t = fdiv(cell, a.experts_div), e = cell - t * a.experts;
             const uint32_t rank = logit_rank(s_high + t * a.experts, s_low + t * a.experts, a.experts, e);
-            if (rank < a.k) {
+            if (rank < a.k && tid % kRankLanes == 0u) {
                 s_route[t * a.k + rank] = int32_t(e);
-                s_chosen[t * a.k + rank] = logit;
+                if (writer) s_chosen[t * a.k + rank] = a.logits[cell];
                 if (writer) a.route[t * a.k + rank] = int32_t(e);
             }
         }
@@ -1768,7 +1778,7 @@ extern "C" e8q_status_t e8q_moe_core_escape(const e8q_experts_t* gate, const e8q
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const uint32_t logits = (a.experts + kMoeWaves - 1u) / kMoeWaves * ((a.tokens + kRouteTokens - 1u) / kRouteTokens);
     launch(moe_prepare_kernel, dim3(3u + a.tokens + (router ? logits : 0u)), dim3(kMoeThreads), 0, s, a);
-    if (router && !a.choose) launch(moe_choose_kernel, dim3(a.tokens), dim3(256), 0, s, a);
+    if (router && !a.choose) launch(moe_choose_kernel, dim3(a.tokens), dim3(kChooseThreads), 0, s, a);
     if (!a.choose) launch(moe_plan_kernel, dim3(1), dim3(kMoeThreads), 0, s, a);
     moe_product<true>(a, s);
     if (a.direct) {
