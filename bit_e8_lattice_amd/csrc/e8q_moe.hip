@@ -32,13 +32,16 @@
 // it); the weighted sum in the order of the places (up to 16 places: inside down).
 //
 // What bounds it (128 experts of 2048 x 768, 8 a token, C(16) and 3.0 x row RMS, medians of
-// a kernel trace): for one token three dependent launches of 5.4 + 14.9 + 15.4 us, each a
-// chain of waits (the choice, the table, the indices, the sum over waves) for 9 MB in
-// all; for 64 tokens gate and up 50.6 us and down 45.4, where 151 MB of indices are
-// 31 us at a large copy's rate and the look-ups in LDS about as long, one after the other in a
-// wave.  Without escaped slots the two take 45.6 and 40.3: a chunk with one is swept step by
-// step, and its record is looked for among those that the block has gathered, or by probing the
-// sorted records.
+// a kernel trace): for one token three dependent launches of 5.9 + 13.7 + 14.0 us, each a
+// chain of waits (the choice, the table, the indices, the sum over waves) for 10 MB in
+// all; for 64 tokens gate and up 44.1 us and down 42.1, where 151 MB of indices are
+// 31 us at a large copy's rate: a turn of jobs on all CUs reads at 4.6 TB/s, but the second turn
+// has jobs for half of them.
+//
+// A chunk with escaped slots goes the plain way with zero points in them, then their records'
+// bytes alone: resolving slot by slot in one path took 107 us for 64 tokens where this
+// takes 100, and 127 instead of 86 where most chunks have one (89 experts of 896 x 544, 2.5 x
+// row RMS, 25 tokens).
 #include <float.h>
 
 #include "e8q_device.hpp"
