@@ -683,6 +683,8 @@ def e8q_adjust_logits(logits, out, status, history=None, history_len=None, promp
     if history is not None and history.dim() != 2:
         raise ValueError("history must be [rows, n]")
     hcols, hstride = _row_list(history, "history", rows, _IDX)
+    if history is not None and rows > 1 and hstride < hcols:
+        raise ValueError("history must have a row of its own for each row of logits")
     nb, bstride = _row_list(bias_idx, "bias_idx", rows, _IDX)
     nv, vstride = _row_list(bias, "bias", rows, (torch.float32,))
     if (nb, bstride) != (nv, vstride) or (bias_idx is None) != (bias is None):

@@ -207,3 +207,29 @@ def test_many_biases_of_a_token(vocab, n_bias, same):
     check(out, x, a)
     again, _ = run(x, a)
     assert torch.equal(out, again)
+
+
+def test_expanded_history_is_refused():
+    """Rows of one history in common (a stride of 0) cannot be passed on; biases and masks in common can."""
+    x, a = make(3, 500, torch.float32, 9, 4, True, 5)
+    for h in (a["history"][:1].expand(3, -1), torch.arange(40, device=x.device).as_strided((3, 9), (4, 1))):
+        with pytest.raises(ValueError):
+            run(x, {**a, "history": h})
+    wide = {**a, "bias_idx": a["bias_idx"][:1].expand(3, -1), "bias": a["bias"][:1].expand(3, -1),
+            "mask": a["mask"][:1].expand(3, -1)}
+    out, _ = run(x, wide)
+    same, _ = run(x, {n: v.contiguous() for n, v in wide.items()})
+    assert torch.equal(out, same)
+
+
+def test_offsets_past_32_bits():
+    """Rows of logits that start past 2^32 elements, in place and out of it."""
+    x, a = make(3, 1000, torch.bfloat16, 30, 5, True, 9)
+    stride = (1 << 31) + 24
+    far = torch.empty(2 * stride + 1000, dtype=torch.bfloat16, device=x.device).as_strided((3, 1000), (stride, 1))
+    far.copy_(x)
+    want, _ = run(x, a)
+    got, _ = run(far, a)
+    assert torch.equal(got, want)
+    run(far, a, out=far)
+    assert torch.equal(far.contiguous(), want)

@@ -270,3 +270,25 @@ def test_gradient_over_the_logits(rows, vocab):
     y = x.clone()
     e8q.e8q_distill_backward(y, idx, lp, o["stats"], w, y, st, tail=e8q.TAIL_REST)
     assert torch.equal(y, o["grad"]) and int(st.item()) == 0
+
+
+@pytest.mark.parametrize("vocab", [900, 300001])
+def test_offsets_past_32_bits(vocab):
+    """Rows of logits and gradients that start past 2^32 elements."""
+    x, idx, lp, w = make(3, vocab, torch.bfloat16, 9, 21)
+    stride = (1 << 31) + 24
+    far = torch.empty(2 * stride + vocab, dtype=torch.bfloat16, device=x.device).as_strided((3, vocab), (stride, 1))
+    far.copy_(x)
+    want, _ = calls(x, idx, lp, "rest", 1.0, w)
+    got = {}
+    st = torch.zeros(1, dtype=torch.int32, device=x.device)
+    ws = torch.zeros(e8q.e8q_distill_workspace_size(3, vocab, 9), dtype=torch.uint8, device=x.device)
+    got["loss"], got["stats"] = torch.zeros(3, device=x.device), torch.zeros((3, 4), device=x.device)
+    e8q.e8q_distill(far, idx, lp, ws, st, tail=TAIL["rest"], loss_out=got["loss"], stats_out=got["stats"])
+    e8q.e8q_distill_grad(far, idx, lp, w, far, ws, st, tail=TAIL["rest"])
+    torch.cuda.synchronize()
+    assert torch.equal(got["loss"], want["loss"]) and torch.equal(far.contiguous(), want["grad1"])
+    far.copy_(x)
+    e8q.e8q_distill_backward(far, idx, lp, got["stats"], w, far, st, tail=TAIL["rest"])
+    torch.cuda.synchronize()
+    assert torch.equal(far.contiguous(), want["grad"]) and int(st.item()) == 0
