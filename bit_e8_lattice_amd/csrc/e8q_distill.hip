@@ -14,7 +14,7 @@
 // the pass over the row, where a bit for every element (in LDS, a byte for each vector) says
 // whether the teacher names it; the named elements' from their own logits, gathered by
 // the places, one place for each element however often the teacher names it.
-// Outside K the gradient is exp2((x - m_r) k - log2 s_r) (P q_r - w_r), m_r and
+// Outside K the gradient is exp2((x - m_r) k) (P q_r - w_r) / s_r, m_r and
 // s_r the maximum and sum of the others, so its exponential is at most 1 and the
 // division by q_r is gone.  It is written for every element, and then, after a barrier, the
 // places write theirs over it: looking the named elements up in the stream took
@@ -332,15 +332,15 @@ __device__ __forceinline__ Sums row_sums(const DsArgs& a, const T* row, uint32_t
 
 // ------------------------------------------------------------ a row's end
 
-// What the gradient needs of a row: maxima and log2 of the sums, of all elements and of those
-// that no place names.
+// What the gradient needs of a row: maxima and sums, of all elements and of those that no place names.  The sums
+// themselves and not their logarithms, which would be rounded to 2^-20 of q for the whole row.
 struct RowStats {
-    float m, l2, m_other, l2_other;
+    float m, s, m_other, s_other;
 };
 
 __device__ __forceinline__ RowStats row_stats(const Sums& st, float k2) {
     const Sum all = sum_join(st.other, st.named, k2);
-    return {all.m, __log2f(all.s), st.other.m, __log2f(st.other.s)};
+    return {all.m, all.s, st.other.m, st.other.s};
 }
 
 // The teacher's side of a row: sum of the probabilities as given, the factor to the weights
@@ -359,7 +359,7 @@ __device__ __forceinline__ Teacher teacher_row(const DsArgs& a, const Places& pl
         t.factor = mass > 0.0f ? 1.0f / mass : mass;       // no mass: no weights (a NaN stays one)
         t.log_factor = -logf(mass);
         t.total = mass > 0.0f ? 1.0f : mass;
-    } else if (a.tail == E8Q_TAIL_REST && st.l2_other != -INFINITY) {
+    } else if (a.tail == E8Q_TAIL_REST && st.s_other != 0.0f) {
         t.rest = fmaxf(0.0f, 1.0f - mass);
         t.total = mass + t.rest;
     }
@@ -368,20 +368,20 @@ __device__ __forceinline__ Teacher teacher_row(const DsArgs& a, const Places& pl
 
 // log q_r.
 __device__ __forceinline__ float log_rest(const RowStats& st, float scale) {
-    return (st.m_other - st.m) * scale + (st.l2_other - st.l2) * kLn2;
+    return (st.m_other - st.m) * scale + logf(st.s_other / st.s);
 }
 
 // Loss and log probabilities of a row, by wave 0 of one block.
 __device__ __forceinline__ void write_row(const DsArgs& a, uint32_t row, const RowStats& st, const Teacher& t,
                                           const Places& pl) {
     if (threadIdx.x >= kWave) return;
-    const float ln_s = st.l2 * kLn2;
+    const float ln_s = logf(st.s);
     float loss = 0.0f;
     for (uint32_t j = threadIdx.x; j < a.k; j += kWave) {
         const int32_t id = pl.id[j];
         float lq = 0.0f;
         if (id >= 0) {
-            lq = st.l2 == -INFINITY ? -INFINITY : (pl.x[j] - st.m) * a.scale - ln_s;
+            lq = st.s == 0.0f ? -INFINITY : (pl.x[j] - st.m) * a.scale - ln_s;
             const float p = pl.p[j];
             if (!(p == 0.0f)) loss += p * t.factor * (pl.lp[j] + t.log_factor - lq);
         }
@@ -392,8 +392,8 @@ __device__ __forceinline__ void write_row(const DsArgs& a, uint32_t row, const R
     if (t.rest > 0.0f) loss += t.rest * (logf(t.rest) - log_rest(st, a.scale));
     if (threadIdx.x == 0u) {
         if (a.loss) a.loss[row] = loss;
-        if (a.stats) a.stats[row] = make_float4(st.m, st.l2, st.m_other, st.l2_other);
-        if (loss != loss || st.l2 != st.l2) atomicOr(a.status, uint32_t(E8Q_STATUS_NONFINITE));
+        if (a.stats) a.stats[row] = make_float4(st.m, st.s, st.m_other, st.s_other);
+        if (loss != loss || st.s != st.s) atomicOr(a.status, uint32_t(E8Q_STATUS_NONFINITE));
     }
 }
 
@@ -456,21 +456,21 @@ __global__ __launch_bounds__(kLpBlock) void distill_join_kernel(DsArgs a) {
 
 // ------------------------------------------------------------ gradient
 
-// The row's constants: c exp2((x - m) k2 - l2) outside K, and with q = exp2((x - m_all) k2 -
-// l2_all), scale g (P q - w) inside.
+// The row's constants: c exp2((x - m) k2) outside K; cq exp2((x - m_all) k2) - cw w inside.
 struct GradRow {
-    float c, m, l2, cq, m_all, l2_all, cw, k2;
+    float c, m, cq, m_all, cw, k2;
+    bool empty;                 // all logits are -inf
 };
 
 __device__ __forceinline__ GradRow grad_row(const DsArgs& a, const RowStats& st, const Teacher& t, float g) {
     const float up = a.scale * g;
-    GradRow r = {up * t.total, st.m, st.l2, up * t.total, st.m, st.l2, up * t.factor, a.scale * kLog2e};
-    if (st.l2_other == -INFINITY) {                    // all others are -inf: exp2 gives their 0
-        r.c = r.m = r.l2 = 0.0f;
+    GradRow r = {up * t.total / st.s, st.m, up * t.total / st.s, st.m, up * t.factor, a.scale * kLog2e, st.s == 0.0f};
+    if (st.s_other == 0.0f) {                          // all others are -inf: exp2 gives their 0
+        r.c = r.m = 0.0f;
     } else if (t.rest > 0.0f) {
-        r.c = up * (t.total * expf(log_rest(st, a.scale)) - t.rest);
+        const float rest = exp2_fast((st.m_other - st.m) * r.k2) * (st.s_other / st.s);
+        r.c = up * (t.total * rest - t.rest) / st.s_other;
         r.m = st.m_other;
-        r.l2 = st.l2_other;
     }
     return r;
 }
@@ -481,7 +481,7 @@ __device__ __forceinline__ void grad_store(const DsArgs& a, T* dx, uint32_t e0, 
     float v[kVec<T>];
     unpack(raw, v);
 #pragma unroll
-    for (int i = 0; i < kVec<T>; ++i) v[i] = r.c * exp2_fast((v[i] - r.m) * r.k2 - r.l2);
+    for (int i = 0; i < kVec<T>; ++i) v[i] = r.c * exp2_fast((v[i] - r.m) * r.k2);
     store_grad<T>(dx, a.vocab, e0, v);
 }
 
@@ -497,8 +497,8 @@ __device__ __forceinline__ void grad_named(const DsArgs& a, T* dx, uint32_t lo, 
             for (uint32_t i = 0u; i < a.k; ++i) sum += pl.id[i] == id ? pl.p[i] : 0.0f;
             w = float(sum);
         }
-        const float q = exp2_fast((pl.x[j] - r.m_all) * r.k2 - r.l2_all);
-        dx[id] = narrow<T>(r.l2_all == -INFINITY ? 0.0f : r.cq * q - r.cw * w);
+        const float q = exp2_fast((pl.x[j] - r.m_all) * r.k2);
+        dx[id] = narrow<T>(r.empty ? 0.0f : r.cq * q - r.cw * w);
     });
 }
 
