@@ -21,9 +21,9 @@
 // 1268 us where this takes 1015 (8192 rows of 131072 bf16 logits, 64 places).  Where
 // no other element is left (all named, or -inf), w_r counts as 0.
 //
-// Few rows are split over blocks (partial sums in the workspace) and joined by a second
-// kernel; whole rows are kept in registers between the sums and the gradient, or
-// read twice where they do not fit: the second time from the end, which the caches still
+// Rows that fit are kept in the registers of a block between the sums and the gradient.  Few
+// longer ones are split over blocks (partial sums in the workspace) and joined by a second
+// kernel; many are read twice: the second time from the end, which the caches still
 // hold (8192 rows of 131072: 1015 us from the start, 973 from the end; in the
 // registers of one block of 1024 threads, which has a CU to itself, 1176).  The bound
 // is memory: the bytes of the logits, and of the gradient.  Reached of them:
@@ -684,26 +684,45 @@ static uint32_t ds_vectors(int64_t vocab, size_t esz) { return uint32_t((uint64_
 
 static size_t ds_part_bytes(uint64_t blocks) { return size_t((blocks * sizeof(float4) + 255) / 256 * 256); }
 
+// Longest rows that every call keeps in registers, and that need no workspace.
+constexpr uint32_t kRowVectors = 256 * 16;
+
 // The parts' sums and the rows' statistics.
 static size_t ds_workspace(int64_t rows, int64_t vocab, size_t esz) {
     uint32_t per = 0;
     const uint64_t splits = lp_splits(rows, vocab, esz, per);
-    return splits == 1 ? 0 : ds_part_bytes(uint64_t(rows) * splits) + size_t(rows) * sizeof(float4);
+    return splits == 1 || ds_vectors(vocab, esz) <= kRowVectors ? 0 : ds_part_bytes(uint64_t(rows) * splits) + size_t(rows) * sizeof(float4);
+}
+
+// Rows that the registers of one block hold: the smallest such block; whether there is one.
+template <typename T, bool GRAD, class Go>
+static bool ds_row_kernel(int64_t vocab, Go&& go) {
+    const uint32_t nvec = ds_vectors(vocab, sizeof(T));
+    if (nvec <= 64 * 4) go(distill_row_kernel<T, 64, 4, GRAD>, 64u);
+    else if (nvec <= 128 * 4) go(distill_row_kernel<T, 128, 4, GRAD>, 128u);
+    else if (nvec <= 256 * 4) go(distill_row_kernel<T, 256, 4, GRAD>, 256u);
+    else if (nvec <= 256 * 8) go(distill_row_kernel<T, 256, 8, GRAD>, 256u);
+    else if (nvec <= kRowVectors) go(distill_row_kernel<T, 256, 16, GRAD>, 256u);
+    else if (sizeof(T) == 4 && GRAD && nvec <= 512 * 16) go(distill_row_kernel<T, 512, 16, GRAD>, 512u);
+    else return false;
+    return true;
+}
+
+template <typename T, bool GRAD>
+static bool ds_rows(DsArgs& a, hipStream_t st) {
+    return ds_row_kernel<T, GRAD>(a.vocab, [&](auto kernel, unsigned block) {
+        launch(kernel, dim3(a.rows), dim3(block), places_bytes(a.k, ds_vectors(a.vocab, sizeof(T))), st, a);
+    });
 }
 
 template <typename T>
 static void ds_forward(DsArgs& a, void* ws, hipStream_t st) {
     a.splits = lp_splits(a.rows, a.vocab, sizeof(T), a.per_split);
     a.part = static_cast<float4*>(ws);
-    // short rows: as many in flight as there is room for
-    const uint32_t nvec = ds_vectors(a.vocab, sizeof(T)), block = nvec <= 64 * 4 ? 64u : nvec <= 128 * 4 ? 128u : 256u;
-    if (a.splits == 1 && nvec <= 256 * 4) {
-        const auto kernel = block == 64u    ? distill_row_kernel<T, 64, 4, false>
-                            : block == 128u ? distill_row_kernel<T, 128, 4, false>
-                                            : distill_row_kernel<T, 256, 4, false>;
-        launch(kernel, dim3(a.rows), dim3(block), places_bytes(a.k, nvec), st, a);
-        return;
-    }
+    // one launch for the rows that registers hold: few rows (16 of 9000 bf16 logits 12.3 us in two, 9.5) or short ones;
+    // many longer ones are as fast in one pass without (4000 of 32000: 50.5 us, 53.5)
+    const bool few = a.splits > 1 || ds_vectors(a.vocab, sizeof(T)) <= 256 * 4;
+    if (few && ds_rows<T, false>(a, st)) return;
     launch(distill_kernel<T>, dim3(a.rows * a.splits), dim3(kLpBlock), places_bytes(a.k, a.per_split), st, a);
     if (a.splits > 1) launch(distill_join_kernel<T>, dim3(a.rows), dim3(kLpBlock), places_bytes(a.k, 0), st, a);
 }
@@ -711,40 +730,30 @@ static void ds_forward(DsArgs& a, void* ws, hipStream_t st) {
 template <typename T>
 static void ds_backward(DsArgs& a, hipStream_t st) {
     a.splits = lp_splits(a.rows, a.vocab, sizeof(T), a.per_split);
-    launch(distill_backward_kernel<T>, dim3(a.rows * a.splits), dim3(kLpBlock), places_bytes(a.k, 0) + size_t(places_slots(a.k)) * 4, st, a);
-}
-
-// Whole rows: the smallest block whose registers hold one; longer rows are read twice.
-template <typename T, class Go>
-static void ds_grad_kernel(int64_t vocab, Go&& go) {
-    const uint32_t nvec = ds_vectors(vocab, sizeof(T));
-    if (nvec <= 64 * 4) go(distill_row_kernel<T, 64, 4, true>, 64u);
-    else if (nvec <= 128 * 4) go(distill_row_kernel<T, 128, 4, true>, 128u);
-    else if (nvec <= 256 * 4) go(distill_row_kernel<T, 256, 4, true>, 256u);
-    else if (nvec <= 256 * 8) go(distill_row_kernel<T, 256, 8, true>, 256u);
-    else if (nvec <= 256 * 16) go(distill_row_kernel<T, 256, 16, true>, 256u);
-    else if (sizeof(T) == 4 && nvec <= 512 * 16) go(distill_row_kernel<T, 512, 16, true>, 512u);
-    else go(distill_grad_long_kernel<T>, unsigned(kLpWide));
+    launch(distill_backward_kernel<T>, dim3(a.rows * a.splits), dim3(kLpBlock),
+           places_bytes(a.k, 0) + size_t(places_slots(a.k)) * 4, st, a);
 }
 
 // A launch has fewer than 2^32 threads.
 template <typename T>
 static bool ds_grad_fits(int64_t rows, int64_t vocab) {
-    bool fits = false;
-    ds_grad_kernel<T>(vocab, [&](auto, unsigned block) { fits = uint64_t(rows) * block < uint64_t(1) << 32; });
-    return fits;
+    unsigned threads = kLpWide;
+    ds_row_kernel<T, true>(vocab, [&](auto, unsigned block) { threads = block; });
+    return uint64_t(rows) * threads < uint64_t(1) << 32;
 }
 
 template <typename T>
 static e8q_status_t ds_both(DsArgs& a, void* ws, size_t need, hipStream_t st) {
+    if (!ds_grad_fits<T>(a.rows, a.vocab)) return E8Q_ERR_UNSUPPORTED;
+    // one launch wherever registers hold a row (16 rows of 9000 bf16 logits 18.2 us in three, 10.5; 500 of 32000 float32
+    // ones 42.7, 25.4)
+    if (ds_rows<T, true>(a, st)) return launch_status();
     if (!need) {
-        if (!ds_grad_fits<T>(a.rows, a.vocab)) return E8Q_ERR_UNSUPPORTED;
-        ds_grad_kernel<T>(a.vocab, [&](auto kernel, unsigned block) {
-            launch(kernel, dim3(a.rows), dim3(block), places_bytes(a.k, ds_vectors(a.vocab, sizeof(T))), st, a);
-        });
+        launch(distill_grad_long_kernel<T>, dim3(a.rows), dim3(kLpWide), places_bytes(a.k, ds_vectors(a.vocab, sizeof(T))),
+               st, a);
         return launch_status();
     }
-    // few rows: the split passes, with the rows' statistics in the workspace
+    // few long rows: the split passes, with the rows' statistics in the workspace
     a.stats = reinterpret_cast<float4*>(static_cast<char*>(ws) + need - size_t(a.rows) * sizeof(float4));
     ds_forward<T>(a, ws, st);
     ds_backward<T>(a, st);

@@ -292,3 +292,52 @@ def test_offsets_past_32_bits(vocab):
     e8q.e8q_distill_backward(far, idx, lp, got["stats"], w, far, st, tail=TAIL["rest"])
     torch.cuda.synchronize()
     assert torch.equal(far.contiguous(), want["grad"]) and int(st.item()) == 0
+
+
+@pytest.mark.parametrize("tail", ["none", "renorm", "rest"])
+@pytest.mark.parametrize("rows,vocab,dtype,k", [(1, 131072, torch.bfloat16, 20), (3, 40001, torch.float32, 200),
+                                                (7, 70001, torch.bfloat16, 1), (300, 33001, torch.float32, 16),
+                                                (1, 600001, torch.float32, 64)])
+def test_few_long_rows(rows, vocab, dtype, k, tail):
+    """Rows that are split over blocks and joined, and the gradient from the stored statistics."""
+    x, idx, lp, w = make(rows, vocab, dtype, k, rows + vocab, pad=rows % 2)
+    idx[:, -1] = vocab - 1
+    if k > 4:
+        idx[0, 1] = idx[0, 0]
+    o, st = calls(x, idx, lp, tail, 1.0, w)
+    assert st == 0
+    check(o, x, idx, lp, tail, 1.0, w, rows=None if rows < 10 else [0, 7, rows - 1])
+
+
+def test_graph_of_split_rows():
+    """Few long rows in a graph, replayed with other inputs and eager calls between."""
+    x, idx, lp, w = make(4, 90001, torch.bfloat16, 12, 3)
+    x = x.contiguous()
+    ws = torch.zeros(e8q.e8q_distill_workspace_size(4, 90001, 12), dtype=torch.uint8, device=x.device)
+    st = torch.zeros(1, dtype=torch.int32, device=x.device)
+    outs = [torch.zeros(4, device=x.device), torch.zeros((4, 4), device=x.device), torch.zeros_like(x), torch.zeros_like(x)]
+
+    def work(loss, stats, grad, both):
+        e8q.e8q_distill(x, idx, lp, ws, st, tail=e8q.TAIL_REST, loss_out=loss, stats_out=stats)
+        e8q.e8q_distill_backward(x, idx, lp, stats, w, grad, st, tail=e8q.TAIL_REST)
+        e8q.e8q_distill_grad(x, idx, lp, w, both, ws, st, tail=e8q.TAIL_REST)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        work(*outs)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        work(*outs)
+    for seed in (1, 2, 3):
+        x.normal_(generator=torch.Generator(device=x.device).manual_seed(seed))
+        for t in outs:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = [torch.zeros_like(t) for t in outs]
+        work(*eager)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, eager)) and int(st.item()) == 0
