@@ -431,13 +431,14 @@ __global__ __launch_bounds__(kMoeThreads) void moe_prepare_kernel(MoeArgs a) {
     for (uint32_t t = 0; t < kRouteTokens; ++t) {
 #pragma unroll
         for (int off = 32; off >= 1; off >>= 1) acc[t] += __shfl_xor(acc[t], off, 64);
-        if (t < nt && lane == 0u) a.logits[uint64_t(t0 + t) * a.experts + e] = acc[t];
+        // (a NaN counts as -inf: no weight, and its place among equal ones)
+        if (t < nt && lane == 0u)
+            a.logits[uint64_t(t0 + t) * a.experts + e] = acc[t] != acc[t] ? -__builtin_inf() : acc[t];
     }
 }
 
-// A logit's place in the order of the values; NaN below everything.
+// A logit's place in the order of the values.
 __device__ __forceinline__ uint64_t logit_key(double v) {
-    if (v != v) return 0ull;
     const uint64_t b = uint64_t(__double_as_longlong(v + 0.0));
     return (b >> 63) ? ~b : b | 0x8000000000000000ull;
 }
@@ -471,17 +472,14 @@ __device__ __forceinline__ uint32_t logit_rank(const uint32_t* high, const uint3
     return add_rank_lanes(rank);
 }
 
-// The weights of a token's places from their logits (in LDS, by place), by one wave.
+// The weights of a token's places from their logits (in LDS, by place), by one wave; NaN where all logits are -inf.
 __device__ __forceinline__ float place_weight(const MoeArgs& a, const double* chosen, const double* logits, uint32_t lane) {
     const double most = chosen[0];
     const float own = lane < a.k ? expf(float(chosen[lane] - most)) : 0.0f;
     float sum = own;
     if (!a.normalize) {
         sum = 0.0f;
-        for (uint32_t e = lane; e < a.experts; e += kWave) {
-            const double v = logits[e];
-            sum += v != v ? 0.0f : expf(float(v - most));
-        }
+        for (uint32_t e = lane; e < a.experts; e += kWave) sum += expf(float(logits[e] - most));
     }
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);

@@ -482,8 +482,9 @@ size_t e8q_gemv_workspace_size(int64_t batch, int64_t m, int64_t rows, int64_t c
  * (off by at most 2^-23 of the largest), the row sums are exact, a product is rounded once to
  * float32; so is down's, of h = act(g) u.  The sum over the places is float32, in their order.
  * A token holding a NaN or infinity has NaN outputs, others are not affected
- * (E8Q_STATUS_NONFINITE); a NaN router logit counts as -inf.  Malformed exports and bad
- * scales are flagged as in e8q_decode_core_escape (the slot or row is 0); so is a
+ * (E8Q_STATUS_NONFINITE).  A NaN router logit counts as -inf (flagged so too): weight 0;
+ * where all logits of a token are -inf, or one is +inf, weights are NaN.  Malformed exports
+ * and bad scales are flagged as in e8q_decode_core_escape (the slot or row is 0); so is a
  * record with |2z| > 2^14, which no encoder writes (E8Q_STATUS_X_RANGE).
  * Limits: hidden, inter multiples of 8 and <= 32768; experts <= 1024; top_k <= 64;
  * tokens * top_k <= 4096.

@@ -68,8 +68,10 @@ def _product(two_z, scale, v, err):
 
 
 def moe_route(x, router, top_k, normalize):
-    """Places and weights [tokens, top_k]."""
-    logits = np.asarray(x, np.float64) @ np.asarray(router, np.float64).T
+    """Places and weights [tokens, top_k]; a NaN logit counts as -inf."""
+    with np.errstate(invalid="ignore"):
+        logits = np.asarray(x, np.float64) @ np.asarray(router, np.float64).T
+    logits = np.where(np.isnan(logits), -np.inf, logits)
     idx = np.argsort(-logits, axis=1, kind="stable")[:, :top_k]
     p = np.exp(logits - logits.max(axis=1, keepdims=True))
     w = np.take_along_axis(p, idx, axis=1)

@@ -208,3 +208,24 @@ def test_given_places_of_few_tokens(tokens):
     y, _, _, st = layer.run(x, 4, idx=idx, weight=weight)
     assert st == e8q.STATUS_BITS["BAD_INDEX"]
     close(y, *layer.expect(x, idx.cpu().numpy(), weight.cpu().numpy()))
+
+
+@pytest.mark.parametrize("normalize", [True, False])
+@pytest.mark.parametrize("tokens,k", [(1, 5), (3, 4), (5, 5), (6, 5), (40, 4)])
+def test_router_logits_that_are_no_numbers(tokens, k, normalize):
+    """A NaN logit counts as -inf: p = 0, and among equal ones the lowest index first.  Few tokens, whose experts the products'
+    blocks choose, and more."""
+    layer = Layer(5, 64, 40, 16, 3.0, 32, 8, 12, device())
+    x, router = inputs(layer, tokens, torch.float32, torch.float32, 5)
+    x[:, 0] = x[:, 0].abs() + 0.5
+    router[1, 7] = float("nan")
+    router[3, :] = 0
+    router[3, 0] = -float("inf")
+    router[4, 63] = float("nan")
+    y, idx, weight, st = layer.run(x, k, router, normalize)
+    assert st == e8q.STATUS_BITS["NONFINITE"]
+    want_idx, want_w = oracle.moe_route(x.cpu().numpy(), router.cpu().numpy(), k, normalize)
+    assert (want_idx[:, 2:] == [1, 3, 4][:k - 2]).all() and not want_w[:, 2:].any() and np.isfinite(want_w).all()
+    assert np.array_equal(idx.cpu().numpy(), want_idx)
+    assert np.abs(weight.cpu().numpy() - want_w).max() <= 40 * U
+    close(y, *layer.expect(x, want_idx, want_w))

@@ -87,6 +87,14 @@ def test_moe_against_dense_matrices():
         assert np.allclose(y[t], want) and (tol[t] > 0).all() and (tol[t] < 1e-3 * np.abs(y).max()).all()
 
 
+def test_moe_route_counts_nan_as_minus_infinity():
+    router = np.array([[np.nan, 1.0], [2.0, 0.0], [-np.inf, 0.0], [1.0, 0.0]])
+    for normalize in (True, False):
+        idx, w = oracle.moe_route(np.array([[1.0, 1.0]]), router, 4, normalize)
+        assert idx.tolist() == [[1, 3, 0, 2]]
+        assert np.allclose(w, [[1 / (1 + np.exp(-1)), 1 / (1 + np.exp(1)), 0, 0]])
+
+
 def test_lds_of_the_layers_kernels(tmp_path):
     """More LDS than a CU has, the kernel's own and what its launch asks for, ends the queue with an error that no
     call returns: the host side counts with kMoeOwn for the former, so the kernels may not have more."""
