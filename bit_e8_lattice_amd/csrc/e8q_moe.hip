@@ -380,7 +380,8 @@ __global__ __launch_bounds__(kMoeThreads) void moe_prepare_kernel(MoeArgs a) {
     if (blockIdx.x < 3u) {
         const MoeMatrix& m = blockIdx.x == 0u ? a.gate : blockIdx.x == 1u ? a.up : a.down;
         const int64_t c = tid < a.experts ? m.esc_count[tid] : 0;
-        const uint64_t own = c > 0 ? uint64_t(c) : 0ull;
+        // (a count past the records counts as all of them: the sums of 1024 stay in range, and the offsets in order)
+        const uint64_t own = c > 0 ? min(uint64_t(c), m.esc_capacity) : 0ull;
         uint64_t run = own;
         for (uint32_t off = 1u; off < 64u; off *= 2u) {
             const uint64_t o = __shfl_up(run, off, 64);

@@ -229,3 +229,23 @@ def test_router_logits_that_are_no_numbers(tokens, k, normalize):
     assert np.array_equal(idx.cpu().numpy(), want_idx)
     assert np.abs(weight.cpu().numpy() - want_w).max() <= 40 * U
     close(y, *layer.expect(x, want_idx, want_w))
+
+
+@pytest.mark.parametrize("tokens", [3, 20])
+def test_counts_whose_sum_passes_64_bits(tokens):
+    """Counts past the records, up to the type's largest: an expert before them is served, those behind have no records."""
+    layer = Layer(4, 256, 128, 16, 1.5, 32, 16, 13, device())
+    x, _ = inputs(layer, tokens, torch.float32, torch.float32, 6)
+    for i, m in enumerate((layer.gate, layer.up, layer.down)):
+        core, _, counts, _ = m.tensors
+        first = int(counts[0])
+        assert first > 2 and int(counts[1:].min()) > 0
+        counts[1:3] = 2 ** 63 - 1                          # the second sum is 2 below the first count, modulo 2^64
+        escaped = core.view(4, -1).cpu().numpy() == -1
+        two_z = layer.oracle[i][0].reshape(4, -1, 8)
+        two_z[2:][escaped[2:]] = 0
+    idx = torch.tensor([[0, 2], [3, 0], [2, 3]], dtype=torch.int32, device=x.device).repeat(tokens, 1)[:tokens]
+    weight = torch.rand((tokens, 2), device=x.device) + 0.5
+    y, _, _, st = layer.run(x, 2, idx=idx, weight=weight)
+    assert st == e8q.STATUS_BITS["ESC_MISSING"]
+    close(y, *layer.expect(x, idx.cpu().numpy(), weight.cpu().numpy()))
