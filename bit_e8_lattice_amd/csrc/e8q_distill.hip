@@ -2,7 +2,8 @@
 // distribution from a teacher's top logits.
 //
 // With y = scale x, q = softmax(y), the teacher's places i_j with probabilities
-// w_j (as given, or divided by their sum) and K the set of the named tokens,
+// w_j (as given, or divided by their sum: then of log probabilities less the row's largest, whose
+// exponentials keep float32's range whatever the scale of the given ones) and K the set of the named tokens,
 //   loss = sum_j w_j (log w_j - log q_{i_j})  [ + w_r (log w_r - log q_r) ],
 //   w_r = max(0, 1 - sum_j w_j),  q_r = sum of q outside K  (tail "rest" only),
 //   dloss/dy_i = P q_i - sum_{j: i_j = i} w_j              for i in K,
@@ -139,20 +140,21 @@ __device__ __forceinline__ Sums sums_block(Sums st, float k2, Sums* s) {
 
 // ------------------------------------------------------------ the teacher's places
 
-// A row's places in (dynamic) LDS: ids (-1: not used), probabilities and their logarithms as
-// given, the student's logits, and the marks of the vectors of a part of the row.
+// A row's places in (dynamic) LDS: ids (-1: not used), logarithms of the probabilities as given, the probabilities
+// (exp(lp - shift)), the student's logits, and the marks of the vectors of a part of the row.
 struct Places {
     int32_t* id;
     float* p;
     float* lp;
     float* x;
     uint32_t* marks;
+    float shift;                // the row's largest log probability if they are divided by their sum, else 0
 };
 
 __device__ __forceinline__ Places places_lds(uint32_t k) {
     extern __shared__ uint32_t s_places[];
     float* f = reinterpret_cast<float*>(s_places + k);
-    return {reinterpret_cast<int32_t*>(s_places), f, f + k, f + 2u * k, s_places + 4u * k};
+    return {reinterpret_cast<int32_t*>(s_places), f, f + k, f + 2u * k, s_places + 4u * k, 0.0f};
 }
 
 static size_t places_bytes(uint32_t k, uint32_t vectors) {
@@ -164,9 +166,19 @@ __device__ __forceinline__ int64_t place_id(const DsArgs& a, uint64_t i) {
     return a.i64 ? static_cast<const int64_t*>(a.idx)[i] : int64_t(static_cast<const int32_t*>(a.idx)[i]);
 }
 
-// Fills the places; whether one of them is used (a barrier for the whole block).
+__device__ __forceinline__ float max_wave(float v) {
+    v = fmaxf(v, lane_xor<32>(v));
+    v = fmaxf(v, lane_xor<16>(v));
+    v = fmaxf(v, lane_xor<8>(v));
+    v = fmaxf(v, lane_xor<4>(v));
+    v = fmaxf(v, lane_xor<2>(v));
+    return fmaxf(v, lane_xor<1>(v));
+}
+
+// Fills the places; whether one of them is used (a barrier for the whole block; the probabilities are there after the
+// next one).
 template <typename T>
-__device__ __forceinline__ bool load_places(const DsArgs& a, uint32_t row, const T* x, const Places& pl) {
+__device__ __forceinline__ bool load_places(const DsArgs& a, uint32_t row, const T* x, Places& pl) {
     uint32_t flags = 0u;
     int any = 0;
     for (uint32_t j = threadIdx.x; j < a.k; j += blockDim.x) {
@@ -181,7 +193,16 @@ __device__ __forceinline__ bool load_places(const DsArgs& a, uint32_t row, const
         any |= int(live);
     }
     flush_status(flags, a.status);
-    return __syncthreads_or(any) != 0;
+    any = __syncthreads_or(any);
+    if (a.tail == E8Q_TAIL_RENORM) {
+        // every wave finds the largest one (-FLT_MAX where all are -inf: they stay 0), every thread its places' probabilities
+        float most = -FLT_MAX;
+        for (uint32_t j = threadIdx.x & 63u; j < a.k; j += kWave) most = pl.id[j] >= 0 ? fmaxf(most, pl.lp[j]) : most;
+        pl.shift = max_wave(most);
+        for (uint32_t j = threadIdx.x; j < a.k; j += blockDim.x)
+            pl.p[j] = pl.id[j] >= 0 ? expf(pl.lp[j] - pl.shift) : 0.0f;
+    }
+    return any != 0;
 }
 
 // Marks the named elements of the vectors [lo, hi), at most kSegment of them; whether places share one.
@@ -343,7 +364,7 @@ __device__ __forceinline__ RowStats row_stats(const Sums& st, float k2) {
     return {all.m, all.s, st.other.m, st.other.s};
 }
 
-// The teacher's side of a row: sum of the probabilities as given, the factor to the weights
+// The teacher's side of a row: sum of the probabilities (less the shift), the factor to the weights
 // used, its logarithm, and the weight left to the rest.  The same in every wave.
 struct Teacher {
     float mass, factor, log_factor, rest, total;
@@ -383,7 +404,7 @@ __device__ __forceinline__ void write_row(const DsArgs& a, uint32_t row, const R
         if (id >= 0) {
             lq = st.s == 0.0f ? -INFINITY : (pl.x[j] - st.m) * a.scale - ln_s;
             const float p = pl.p[j];
-            if (!(p == 0.0f)) loss += p * t.factor * (pl.lp[j] + t.log_factor - lq);
+            if (!(p == 0.0f)) loss += p * t.factor * (pl.lp[j] - pl.shift + t.log_factor - lq);
         }
         if (a.logprob) a.logprob[uint64_t(row) * a.k + j] = lq;
     }
@@ -411,7 +432,7 @@ __device__ __forceinline__ void write_empty(const DsArgs& a, uint32_t row) {
 
 template <typename T>
 __global__ __launch_bounds__(kLpBlock) void distill_kernel(DsArgs a) {
-    const Places pl = places_lds(a.k);
+    Places pl = places_lds(a.k);
     const uint32_t row = a.splits == 1 ? blockIdx.x : blockIdx.x / a.splits;
     const uint32_t sp = blockIdx.x - row * a.splits;
     const T* x = static_cast<const T*>(a.x) + int64_t(row) * a.stride;
@@ -436,7 +457,7 @@ __global__ __launch_bounds__(kLpBlock) void distill_kernel(DsArgs a) {
 template <typename T>
 __global__ __launch_bounds__(kLpBlock) void distill_join_kernel(DsArgs a) {
     __shared__ Sums s_sums[kLpBlock / kWave];
-    const Places pl = places_lds(a.k);
+    Places pl = places_lds(a.k);
     const uint32_t row = blockIdx.x;
     const T* x = static_cast<const T*>(a.x) + int64_t(row) * a.stride;
     const float k2 = a.scale * kLog2e;
@@ -537,7 +558,7 @@ __device__ __forceinline__ void zero_part(const DsArgs& a, T* dx, uint32_t lo, u
 // From the stored statistics.
 template <typename T>
 __global__ __launch_bounds__(kLpBlock) void distill_backward_kernel(DsArgs a) {
-    const Places pl = places_lds(a.k);
+    Places pl = places_lds(a.k);
     const uint32_t row = a.splits == 1 ? blockIdx.x : blockIdx.x / a.splits;
     const uint32_t sp = blockIdx.x - row * a.splits;
     const T* x = static_cast<const T*>(a.x) + int64_t(row) * a.stride;
@@ -561,7 +582,7 @@ template <typename T, int BLOCK, int NV, bool GRAD>
 __global__ __launch_bounds__(BLOCK) void distill_row_kernel(DsArgs a) {
     constexpr int VE = kVec<T>, kGroup = 2;      // vectors unpacked at a time
     __shared__ Sums s_sums[BLOCK / kWave];
-    const Places pl = places_lds(a.k);
+    Places pl = places_lds(a.k);
     const uint32_t row = blockIdx.x;
     const T* x = static_cast<const T*>(a.x) + int64_t(row) * a.stride;
     T* dx = static_cast<T*>(a.dx) + int64_t(row) * a.dx_stride;
@@ -616,7 +637,7 @@ __global__ __launch_bounds__(BLOCK) void distill_row_kernel(DsArgs a) {
 // The same for longer rows: two passes over the row.
 template <typename T>
 __global__ __launch_bounds__(kLpWide, 8) void distill_grad_long_kernel(DsArgs a) {
-    const Places pl = places_lds(a.k);
+    Places pl = places_lds(a.k);
     const uint32_t row = blockIdx.x;
     const T* x = static_cast<const T*>(a.x) + int64_t(row) * a.stride;
     T* dx = static_cast<T*>(a.dx) + int64_t(row) * a.dx_stride;

@@ -735,7 +735,7 @@ e8q_status_t e8q_adjust_logits(const void* logits, e8q_dtype_t dtype,
  *   loss = sum_j w_j (log w_j - log q_{i_j})  [ + w_r (log w_r - log q_r) ]
  * with, by `tail`,
  *   E8Q_TAIL_NONE     w_j = p_j (the places' terms only),
- *   E8Q_TAIL_RENORM   w_j = p_j / sum p,
+ *   E8Q_TAIL_RENORM   w_j = p_j / sum p (whatever the size of the sum),
  *   E8Q_TAIL_REST     w_j = p_j, and all tokens that no place names as one event more:
  *                     w_r = max(0, 1 - sum p), q_r = their sum of q.  Where q is 0
  *                     there (all tokens named, or their logits -inf), w_r is 0.

@@ -341,3 +341,23 @@ def test_graph_of_split_rows():
         work(*eager)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, eager)) and int(st.item()) == 0
+
+
+@pytest.mark.parametrize("rows,vocab", [(8, 300), (8, 30000), (1100, 9000), (1030, 40000)])
+def test_renorm_of_far_log_probabilities(rows, vocab):
+    """A shift of a row's log probabilities leaves p / sum p as it is: sums below float32's least number and above its largest
+    are no limit.  Weights too small beside the row's largest are 0."""
+    x, idx, lp, w = make(rows, vocab, torch.float32, 12, 31)
+    for row, shift in enumerate((-90.0, -101.0, -120.0, -5000.0, 95.0, 300.0, -700.0)):
+        lp[row] += shift
+    lp[6, 3:] -= 200.0
+    lp[7, :4] = -float("inf")
+    lp[7, 4:] -= 95.0
+    idx[5, 4:] = -1
+    lp[5, 4:] = 1000.0                                       # (places that are not used)
+    o, st = calls(x, idx, lp, "renorm", 1.0, w)
+    assert st == 0
+    shifted = lp.clone()
+    shifted[3] += 5000.0                                     # (exact; the float64 oracle's exp(-5000) is 0)
+    ref = check(o, x, idx, shifted, "renorm", 1.0, w, rows=range(8))
+    assert (ref["loss"] > 0).all() and (np.abs(ref["w"].sum(axis=1) - 1) < 1e-12).all()
