@@ -410,6 +410,7 @@ __device__ __forceinline__ void write_row(const DsArgs& a, uint32_t row, const R
     }
     loss = add_wave(loss);
     if (t.mass != t.mass) loss = t.mass;
+    if (st.s != st.s) loss = st.s;                         // (a NaN or +inf among the logits, also where every p is 0)
     if (t.rest > 0.0f) loss += t.rest * (logf(t.rest) - log_rest(st, a.scale));
     if (threadIdx.x == 0u) {
         if (a.loss) a.loss[row] = loss;

@@ -35,7 +35,7 @@ def distill(x, scale, idx, lp, tail, grad_loss=None):
             p = np.exp(l)
             mass = p.sum()
             w, lw = (p, l) if tail != "renorm" else (p / mass if mass != 0 else p, l - np.log(mass))
-            terms = np.where(w == 0, 0.0, w * (lw - lq[i]))
+            terms = np.where((w == 0) & ~np.isnan(lse), 0.0, w * (lw - lq[i]))
             named = np.zeros(vocab, bool)
             named[i] = True
             w_r, lq_r, share = 0.0, -np.inf, np.zeros(vocab)

@@ -361,3 +361,22 @@ def test_renorm_of_far_log_probabilities(rows, vocab):
     shifted[3] += 5000.0                                     # (exact; the float64 oracle's exp(-5000) is 0)
     ref = check(o, x, idx, shifted, "renorm", 1.0, w, rows=range(8))
     assert (ref["loss"] > 0).all() and (np.abs(ref["w"].sum(axis=1) - 1) < 1e-12).all()
+
+
+@pytest.mark.parametrize("tail", ["none", "renorm", "rest"])
+@pytest.mark.parametrize("rows,vocab", [(4, 300), (4, 30000), (1100, 9000), (1030, 40000)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_non_finite_logits_where_no_place_weighs(rows, vocab, value, tail):
+    """NaN outputs where a logit is a NaN or infinite, though all places have p = 0; loss 0 where the logits are finite."""
+    x, idx, lp, w = make(rows, vocab, torch.float32, 8, 9)
+    x = x.contiguous()
+    lp[:3] = -float("inf")
+    x[0, idx[0, 2]] = value
+    x[1, (set(range(20)) - set(idx[1].tolist())).pop()] = value
+    o, st = calls(x, idx, lp, tail, 1.0, w)
+    assert st == e8q.STATUS_BITS["NONFINITE"]
+    for n in ("loss", "loss1", "logprob", "logprob1", "grad", "grad1"):
+        assert torch.isnan(o[n][:2]).all(), n
+    check(o, x, idx, lp, tail, 1.0, w, rows=[2, 3])
+    if tail != "rest":
+        assert float(o["loss"][2]) == 0.0 and not o["grad"][2].any()

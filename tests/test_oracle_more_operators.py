@@ -31,6 +31,20 @@ def test_distill_closed_forms():
 
 
 @pytest.mark.parametrize("tail", ["none", "renorm", "rest"])
+@pytest.mark.parametrize("value", [np.nan, np.inf])
+def test_distill_of_non_finite_logits(tail, value):
+    """NaN loss and gradient, whatever the places weigh; 0 where no place is used."""
+    lp = np.full((1, 2), -np.inf)
+    for at in (0, 1):
+        x = np.zeros((1, 4))
+        x[0, at] = value
+        r = oracle.distill(x, 1.0, np.array([[0, 2]]), lp, tail, np.ones(1))
+        assert np.isnan(r["loss"]).all() and np.isnan(r["grad"]).all() and np.isnan(r["logprob"]).all()
+        r = oracle.distill(x, 1.0, np.array([[-1, -1]]), lp, tail, np.ones(1))
+        assert not r["loss"].any() and not r["grad"].any()
+
+
+@pytest.mark.parametrize("tail", ["none", "renorm", "rest"])
 def test_distill_gradient_against_differences(tail):
     rng = np.random.default_rng(2)
     x = rng.normal(size=(3, 9)) * 2
