@@ -487,8 +487,9 @@ struct GradRow {
 __device__ __forceinline__ GradRow grad_row(const DsArgs& a, const RowStats& st, const Teacher& t, float g) {
     const float up = a.scale * g;
     GradRow r = {up * t.total / st.s, st.m, up * t.total / st.s, st.m, up * t.factor, a.scale * kLog2e, st.s == 0.0f};
-    if (st.s_other == 0.0f) {                          // all others are -inf: exp2 gives their 0
-        r.c = r.m = 0.0f;
+    if (st.s_other == 0.0f) {                          // all others are -inf: exp2 gives their 0, but for a NaN row's
+        r.c = r.c == r.c || r.empty ? 0.0f : r.c;
+        r.m = 0.0f;
     } else if (t.rest > 0.0f) {
         const float rest = exp2_fast((st.m_other - st.m) * r.k2) * (st.s_other / st.s);
         r.c = up * (t.total * rest - t.rest) / st.s_other;

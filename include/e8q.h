@@ -750,9 +750,10 @@ e8q_status_t e8q_adjust_logits(const void* logits, e8q_dtype_t dtype,
  *   workspace    e8q_distill_workspace_size(rows, vocab, k) bytes, 256-byte aligned
  *                (may be NULL if that is 0)
  * At least one output.  A row without a used place has loss 0 and gradient 0,
- * whatever its logits.  Otherwise a row holding a NaN or +inf (logit or used
- * log probability) has NaN outputs (E8Q_STATUS_NONFINITE), and a named token
- * of logit -inf with p > 0 loss +inf.  exp, sums and the running maximum are float32.
+ * whatever its logits.  Otherwise a row holding a NaN or +inf logit has NaN outputs, one
+ * with such a log probability at a used place a NaN loss and gradient (E8Q_STATUS_NONFINITE),
+ * and a named token of logit -inf with p > 0 loss +inf.  exp, sums and the running maximum
+ * are float32.
  * Limits: vocab < 2^31 - 16, rows < 2^24, k <= 1024.
  * ------------------------------------------------------------------------- */
 enum { E8Q_TAIL_NONE = 0, E8Q_TAIL_RENORM = 1, E8Q_TAIL_REST = 2 };

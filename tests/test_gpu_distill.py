@@ -380,3 +380,24 @@ def test_non_finite_logits_where_no_place_weighs(rows, vocab, value, tail):
     check(o, x, idx, lp, tail, 1.0, w, rows=[2, 3])
     if tail != "rest":
         assert float(o["loss"][2]) == 0.0 and not o["grad"][2].any()
+
+
+@pytest.mark.parametrize("tail", ["none", "renorm", "rest"])
+@pytest.mark.parametrize("rows,vocab", [(6, 300), (6, 30000), (1100, 9000), (1030, 40000)])
+def test_non_finite_rows_without_another_token(rows, vocab, tail):
+    """All tokens that no place names are -inf: a NaN or an infinity among the named ones, or a teacher's, reaches the
+    gradient of every token all the same."""
+    x, idx, lp, w = make(rows, vocab, torch.float32, 8, 10)
+    x = x.contiguous()
+    named = torch.gather(x, 1, idx)
+    x[:5] = -float("inf")
+    x[:5] = x[:5].scatter(1, idx[:5], named[:5])
+    x[0, idx[0, 1]] = float("nan")
+    x[1, idx[1, 1]] = float("inf")
+    lp[2, 3] = float("nan")
+    lp[3, 3] = float("inf")
+    o, st = calls(x, idx, lp, tail, 1.0, w)
+    assert st == e8q.STATUS_BITS["NONFINITE"]
+    for n in ("loss", "loss1", "grad", "grad1"):
+        assert torch.isnan(o[n][:4]).all(), n
+    check(o, x, idx, lp, tail, 1.0, w, rows=[4, 5])
