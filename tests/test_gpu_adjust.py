@@ -233,3 +233,24 @@ def test_offsets_past_32_bits():
     assert torch.equal(got, want)
     run(far, a, out=far)
     assert torch.equal(far.contiguous(), want)
+
+
+@pytest.mark.parametrize("penalties", [("frequency",), ("presence",), ("repetition",), ALL])
+@pytest.mark.parametrize("vocab", [40, 20000])
+def test_prompt_ids_past_the_vocabulary(vocab, penalties):
+    """An id past the vocabulary is flagged in the prompt too, also where no penalty is for the prompt."""
+    x, a = make(2, vocab, torch.float32, 700, 0, False, 13, penalties=penalties)
+    a["history_len"][:] = 690
+    a["prompt_len"][:] = 600
+    out, st = run(x, a)
+    assert st == 0
+    for at in (0, 599):
+        b = {**a, "history": a["history"].clone()}
+        b["history"][1, at] = vocab + at
+        out, st = run(x, b)
+        assert st == e8q.STATUS_BITS["BAD_INDEX"]
+        check(out, x, b)
+    b["history"][1, 599] = -1
+    b["history"][1, 690] = vocab                           # behind the history's end: not read as an id
+    out, st = run(x, b)
+    assert st == 0
