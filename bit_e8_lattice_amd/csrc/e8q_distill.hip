@@ -148,13 +148,12 @@ struct Places {
     float* lp;
     float* x;
     uint32_t* marks;
-    float shift;                // the row's largest log probability if they are divided by their sum, else 0
 };
 
 __device__ __forceinline__ Places places_lds(uint32_t k) {
     extern __shared__ uint32_t s_places[];
     float* f = reinterpret_cast<float*>(s_places + k);
-    return {reinterpret_cast<int32_t*>(s_places), f, f + k, f + 2u * k, s_places + 4u * k, 0.0f};
+    return {reinterpret_cast<int32_t*>(s_places), f, f + k, f + 2u * k, s_places + 4u * k};
 }
 
 static size_t places_bytes(uint32_t k, uint32_t vectors) {
@@ -175,10 +174,27 @@ __device__ __forceinline__ float max_wave(float v) {
     return fmaxf(v, lane_xor<1>(v));
 }
 
+// The thread's number, but nothing that is formed from it is kept for another use (no instruction): what the rare path
+// of a call forms early would cost the kernel a register until its end, and the step to the next occupancy.
+__device__ __forceinline__ uint32_t thread_here() {
+    uint32_t t = threadIdx.x;
+    asm volatile("" : "+v"(t));
+    return t;
+}
+
+// What the places' logarithms are less in their probabilities: the row's largest if these are divided by their sum
+// (-FLT_MAX where all are -inf, whose exponentials stay 0), else 0.  By a wave.
+__device__ __forceinline__ float places_shift(const DsArgs& a, const Places& pl) {
+    if (a.tail != E8Q_TAIL_RENORM) return 0.0f;
+    float most = -FLT_MAX;
+    for (uint32_t j = thread_here() & 63u; j < a.k; j += kWave) most = pl.id[j] >= 0 ? fmaxf(most, pl.lp[j]) : most;
+    return max_wave(most);
+}
+
 // Fills the places; whether one of them is used (a barrier for the whole block; the probabilities are there after the
 // next one).
 template <typename T>
-__device__ __forceinline__ bool load_places(const DsArgs& a, uint32_t row, const T* x, Places& pl) {
+__device__ __forceinline__ bool load_places(const DsArgs& a, uint32_t row, const T* x, const Places& pl) {
     uint32_t flags = 0u;
     int any = 0;
     for (uint32_t j = threadIdx.x; j < a.k; j += blockDim.x) {
@@ -195,12 +211,8 @@ __device__ __forceinline__ bool load_places(const DsArgs& a, uint32_t row, const
     flush_status(flags, a.status);
     any = __syncthreads_or(any);
     if (a.tail == E8Q_TAIL_RENORM) {
-        // every wave finds the largest one (-FLT_MAX where all are -inf: they stay 0), every thread its places' probabilities
-        float most = -FLT_MAX;
-        for (uint32_t j = threadIdx.x & 63u; j < a.k; j += kWave) most = pl.id[j] >= 0 ? fmaxf(most, pl.lp[j]) : most;
-        pl.shift = max_wave(most);
-        for (uint32_t j = threadIdx.x; j < a.k; j += blockDim.x)
-            pl.p[j] = pl.id[j] >= 0 ? expf(pl.lp[j] - pl.shift) : 0.0f;
+        const float shift = places_shift(a, pl);
+        for (uint32_t j = thread_here(); j < a.k; j += blockDim.x) pl.p[j] = pl.id[j] >= 0 ? expf(pl.lp[j] - shift) : 0.0f;
     }
     return any != 0;
 }
@@ -396,7 +408,7 @@ __device__ __forceinline__ float log_rest(const RowStats& st, float scale) {
 __device__ __forceinline__ void write_row(const DsArgs& a, uint32_t row, const RowStats& st, const Teacher& t,
                                           const Places& pl) {
     if (threadIdx.x >= kWave) return;
-    const float ln_s = logf(st.s);
+    const float ln_s = logf(st.s), shift = places_shift(a, pl);
     float loss = 0.0f;
     for (uint32_t j = threadIdx.x; j < a.k; j += kWave) {
         const int32_t id = pl.id[j];
@@ -404,7 +416,7 @@ __device__ __forceinline__ void write_row(const DsArgs& a, uint32_t row, const R
         if (id >= 0) {
             lq = st.s == 0.0f ? -INFINITY : (pl.x[j] - st.m) * a.scale - ln_s;
             const float p = pl.p[j];
-            if (!(p == 0.0f)) loss += p * t.factor * (pl.lp[j] - pl.shift + t.log_factor - lq);
+            if (!(p == 0.0f)) loss += p * t.factor * (pl.lp[j] - shift + t.log_factor - lq);
         }
         if (a.logprob) a.logprob[uint64_t(row) * a.k + j] = lq;
     }
@@ -433,7 +445,7 @@ __device__ __forceinline__ void write_empty(const DsArgs& a, uint32_t row) {
 
 template <typename T>
 __global__ __launch_bounds__(kLpBlock) void distill_kernel(DsArgs a) {
-    Places pl = places_lds(a.k);
+    const Places pl = places_lds(a.k);
     const uint32_t row = a.splits == 1 ? blockIdx.x : blockIdx.x / a.splits;
     const uint32_t sp = blockIdx.x - row * a.splits;
     const T* x = static_cast<const T*>(a.x) + int64_t(row) * a.stride;
@@ -458,7 +470,7 @@ __global__ __launch_bounds__(kLpBlock) void distill_kernel(DsArgs a) {
 template <typename T>
 __global__ __launch_bounds__(kLpBlock) void distill_join_kernel(DsArgs a) {
     __shared__ Sums s_sums[kLpBlock / kWave];
-    Places pl = places_lds(a.k);
+    const Places pl = places_lds(a.k);
     const uint32_t row = blockIdx.x;
     const T* x = static_cast<const T*>(a.x) + int64_t(row) * a.stride;
     const float k2 = a.scale * kLog2e;
@@ -560,7 +572,7 @@ __device__ __forceinline__ void zero_part(const DsArgs& a, T* dx, uint32_t lo, u
 // From the stored statistics.
 template <typename T>
 __global__ __launch_bounds__(kLpBlock) void distill_backward_kernel(DsArgs a) {
-    Places pl = places_lds(a.k);
+    const Places pl = places_lds(a.k);
     const uint32_t row = a.splits == 1 ? blockIdx.x : blockIdx.x / a.splits;
     const uint32_t sp = blockIdx.x - row * a.splits;
     const T* x = static_cast<const T*>(a.x) + int64_t(row) * a.stride;
@@ -584,7 +596,7 @@ template <typename T, int BLOCK, int NV, bool GRAD>
 __global__ __launch_bounds__(BLOCK) void distill_row_kernel(DsArgs a) {
     constexpr int VE = kVec<T>, kGroup = 2;      // vectors unpacked at a time
     __shared__ Sums s_sums[BLOCK / kWave];
-    Places pl = places_lds(a.k);
+    const Places pl = places_lds(a.k);
     const uint32_t row = blockIdx.x;
     const T* x = static_cast<const T*>(a.x) + int64_t(row) * a.stride;
     T* dx = static_cast<T*>(a.dx) + int64_t(row) * a.dx_stride;
@@ -639,7 +651,7 @@ __global__ __launch_bounds__(BLOCK) void distill_row_kernel(DsArgs a) {
 // The same for longer rows: two passes over the row.
 template <typename T>
 __global__ __launch_bounds__(kLpWide, 8) void distill_grad_long_kernel(DsArgs a) {
-    Places pl = places_lds(a.k);
+    const Places pl = places_lds(a.k);
     const uint32_t row = blockIdx.x;
     const T* x = static_cast<const T*>(a.x) + int64_t(row) * a.stride;
     T* dx = static_cast<T*>(a.dx) + int64_t(row) * a.dx_stride;
