@@ -243,9 +243,9 @@ __global__ __launch_bounds__(BLOCK) void adjust_kernel(AdjArgs a) {
 #pragma unroll
             for (int u = 0; u < kIds; ++u) {
                 const int64_t j = base + u * BLOCK + int64_t(tid);
-                if (j >= len) continue;
-                if (id[u] >= int64_t(a.vocab)) flags |= E8Q_STATUS_BAD_INDEX;
-                if (j < from) continue;
+                // (512 rows of 131072 with 2048 ids: 76 us so, 102 where the check stands between the two ends of the next)
+                if (j < len && id[u] >= int64_t(a.vocab)) flags |= E8Q_STATUS_BAD_INDEX;
+                if (j < from || j >= len) continue;
                 const int64_t e = id[u] - int64_t(lo);
                 if (id[u] < 0 || e < 0 || e >= int64_t(n)) continue;
                 if (j < prompt) atomicOr(&word[e], kSeen);
