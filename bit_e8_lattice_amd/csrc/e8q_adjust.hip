@@ -23,6 +23,8 @@
 //
 // The bound is memory: logits in and out, history and mask are 60 us of the 68.8 at a
 // large copy's rate.  One row takes 4.8 us, the wait for its length, its ids and its logits in turn.
+#include <float.h>
+
 #include "e8q_rows.hpp"
 
 namespace e8q {
@@ -59,10 +61,21 @@ __device__ __forceinline__ int64_t id_at(const void* p, int i64, int64_t i) {
     return i64 ? static_cast<const int64_t*>(p)[i] : int64_t(static_cast<const int32_t*>(p)[i]);
 }
 
-// x / r, correctly rounded but for subnormal results: inv = fl(1 / r).
-__device__ __forceinline__ float divide(float x, float r, float inv) {
-    const float q = x * inv;
-    return __builtin_isinf(q) ? q : fmaf(fmaf(-q, r, x), inv, q);
+// x / r for positive x and r from inv = fl(1 / r'), r' = r up: correctly rounded where x is above 2^-100 (the
+// remainder is exact).  up is a power of two that takes r' to where its reciprocal is a normal number, 0 for an infinite r.
+struct Divisor {
+    float r, inv, up;
+};
+
+__device__ __forceinline__ Divisor divisor(float r) {
+    const float up = r < 0x1p-64f ? 0x1p64f : r > 0x1p64f ? 0x1p-64f : 1.0f;
+    const float to = r * up > FLT_MAX ? FLT_MAX : r * up;      // (a NaN stays one)
+    return {to, 1.0f / to, __builtin_isinf(r) ? 0.0f : up};
+}
+
+__device__ __forceinline__ float divide(float x, const Divisor& d) {
+    const float q = x * d.inv;
+    return (__builtin_isinf(q) ? q : fmaf(fmaf(-q, d.r, x), d.inv, q)) * d.up;
 }
 
 // Biases of a part, each in the slot of its place in the row's list: chains of slots by the
@@ -206,7 +219,8 @@ __global__ __launch_bounds__(BLOCK) void adjust_kernel(AdjArgs a) {
         raw[u] = u32x4_t{0u, 0u, 0u, 0u};
         if (bits[u] != 0u && !in_place) load(u);
     }
-    float rep = 1.0f, inv = 1.0f, freq = 0.0f, pres = 0.0f;
+    float rep = 1.0f, freq = 0.0f, pres = 0.0f;
+    Divisor by = {1.0f, 1.0f, 1.0f};
     if constexpr (TABLE) {
         constexpr int kIds = 2;                 // places in flight per thread
         const int64_t hrow = int64_t(row) * a.hist_stride;
@@ -229,7 +243,7 @@ __global__ __launch_bounds__(BLOCK) void adjust_kernel(AdjArgs a) {
             if (a.rep) rep = a.rep[row];
             if (a.freq) freq = a.freq[row];
             if (a.pres) pres = a.pres[row];
-            inv = 1.0f / rep;
+            by = divisor(rep);
         }
         __syncthreads();
         // a prompt counts for the repetition penalty only
@@ -300,7 +314,7 @@ __global__ __launch_bounds__(BLOCK) void adjust_kernel(AdjArgs a) {
                 const uint32_t i0 = left ? uint32_t(__ffs(int(left)) - 1) : 0u, local = e0 + i0;
                 const uint32_t w = left ? word[local] : 0u, c = w & kCount;
                 float y = element<T>(raw[u], i0);
-                if (w & ~kBiased) y = y > 0.0f ? divide(y, rep, inv) : y * rep;
+                if (w & ~kBiased) y = y > 0.0f ? divide(y, by) : y * rep;
                 if (c) y -= freq * float(c) + pres;
                 if (__ballot((w & kBiased) != 0u)) {
                     float b = 0.0f;

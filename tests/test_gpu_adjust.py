@@ -254,3 +254,22 @@ def test_prompt_ids_past_the_vocabulary(vocab, penalties):
     b["history"][1, 690] = vocab                           # behind the history's end: not read as an id
     out, st = run(x, b)
     assert st == 0
+
+
+@pytest.mark.parametrize("value", [float("inf"), 3.4028234663852886e38, 2.0 ** 127, 2.0 ** 126, 2.0 ** -126, 1e-38, 1e-40,
+                                   2.0 ** -149, float("nan")])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_extreme_repetition(dtype, value):
+    """Penalties whose reciprocal is not a normal number: x / r all the same, as x r."""
+    x, a = make(2, 100, dtype, 100, 0, False, 14, penalties=("repetition",))
+    x = x.contiguous()
+    x[0, :12] = torch.tensor([1e-30, 1e-38, 1e-41, 1.0, 3e38, -1e-30, -1e-38, -3e38, 2.0 ** -126, 2.0 ** 127, 1.7e38, 0.0],
+                             device=x.device).to(dtype)
+    if value == float("inf"):
+        x[0, 11] = 1.0                                     # (0 * inf is a NaN)
+    a["history"][:] = torch.arange(100, device=x.device)
+    a["history_len"][:] = 100
+    a["repetition"][:] = value
+    out, st = run(x, a)
+    assert st == 0
+    check(out, x, a)
