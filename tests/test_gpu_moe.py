@@ -249,3 +249,101 @@ def test_counts_whose_sum_passes_64_bits(tokens):
     y, _, _, st = layer.run(x, 2, idx=idx, weight=weight)
     assert st == e8q.STATUS_BITS["ESC_MISSING"]
     close(y, *layer.expect(x, idx.cpu().numpy(), weight.cpu().numpy()))
+
+
+def wide_layer(experts, hidden, inter, bound, had_in, had_down):
+    layer = Layer(experts, hidden, inter, bound, 3.0, had_in, had_down, 21, device(), outliers=400)
+    assert all(np.abs(m[0]).max() > 200 for m in layer.oracle)      # (a wide rotation spreads them)
+    return layer
+
+
+@pytest.mark.parametrize("experts,hidden,inter,bound,had_in,had_down", [
+    (3, 256, 160, 16, 32, 32),
+    (3, 264, 1040, 24, 8, 16),                              # a table of changing place; down's columns in several chunks
+    (2, 2600, 2200, 16, 8, 8),                              # digits of every product in two parts, ready before down
+    (2, 600, 2048, 40, 8, 2048),                            # the table in memory
+])
+@pytest.mark.parametrize("tokens", [1, 7, 40])
+def test_wide_escapes_of_all_sweeps(experts, hidden, inter, bound, had_in, had_down, tokens):
+    """Escaped points of more than eight bits in gate, up and down: the direct sum, planned sweeps of one and two products, whole
+    rows and parts of them."""
+    layer = wide_layer(experts, hidden, inter, bound, had_in, had_down)
+    check(layer, tokens, 2, tokens)
+
+
+@pytest.mark.parametrize("hidden,inter", [(2600, 2200), (1104, 1600)])
+def test_wide_escapes_of_whole_rounds(hidden, inter):
+    """One expert's 1400 tokens in 140 sweeps and more: jobs of full rounds and a shared one behind them."""
+    layer = wide_layer(2, hidden, inter, 16, 8, 8)
+    x, _ = inputs(layer, 1400, torch.bfloat16, torch.float32, 8)
+    idx = torch.zeros((1400, 2), dtype=torch.int32, device=x.device)
+    idx[:, 1] = 1
+    weight = torch.rand((1400, 2), device=x.device)
+    y, _, _, st = layer.run(x, 2, idx=idx, weight=weight)
+    assert st == 0
+    close(y, *layer.expect(x, idx.cpu().numpy(), weight.cpu().numpy()))
+
+
+@pytest.mark.parametrize("which", [0, 1, 2])
+@pytest.mark.parametrize("tokens", [5, 23])
+def test_malformed_matrices(which, tokens):
+    """Bad scales and indices, missing and impossible records of gate, up and down in turn; the direct sum and planned sweeps."""
+    layer = Layer(4, 256, 64, 16, 1.5, 128, 64, 10, device())
+    m = (layer.gate, layer.up, layer.down)[which]
+    rows, cols = m.shape[1:]
+    x, router = inputs(layer, tokens, torch.float32, torch.float32, 3)
+    _, idx, weight, _ = layer.run(x, 2, router)
+    used = int(idx[0, 0])
+    core, esc, cnt, scale = m.tensors
+    two_z = layer.oracle[which][0]
+    slots, z = core.view(4, -1), two_z.reshape(4, -1, 8)
+
+    def expect(flag):
+        layer.oracle[which] = (two_z, scale.cpu().numpy().reshape(4, rows))
+        y, _, _, st = layer.run(x, 2, router)
+        assert st == e8q.STATUS_BITS[flag], flag
+        close(y, *layer.expect(x, idx.cpu().numpy(), weight.cpu().numpy()))
+
+    for value in (float("nan"), -1.0, float("inf"), 0.0):
+        keep = scale.clone()
+        scale[used * rows + 7] = value
+        expect("BAD_SCALE")
+        scale.copy_(keep)
+    plain = (slots[used] != -1).nonzero()[:, 0].tolist()
+    for at in (plain[0], plain[-1]):
+        for value, flag in ((oracle.core_size(16), "BAD_INDEX"), (-1, "ESC_MISSING")):
+            keep, was = core.clone(), z[used, at].copy()
+            slots[used, at] = value
+            z[used, at] = 0
+            expect(flag)
+            z[used, at] = was
+            core.copy_(keep)
+    first = int(cnt[:used].sum())
+    for at in (first, first + int(cnt[used]) - 1):
+        rec = esc.view(-1, 20)[at].view(torch.int16)
+        group = int(esc.view(-1, 20)[at].view(torch.int32)[0])
+        kept, was = rec.clone(), z[used, group].copy()
+        for value, flag in ((32767, "X_RANGE"), (-32768, "X_RANGE")):
+            rec[2 + 3] = value
+            z[used, group] = 0
+            expect(flag)
+        rec.copy_(kept)
+        z[used, group] = was
+    # no records from this expert on
+    cnt[used:] = 0
+    assert (slots[used] == -1).any()
+    z[used:][slots[used:].cpu().numpy() == -1] = 0
+    expect("ESC_MISSING")
+
+
+@pytest.mark.parametrize("tokens", [2, 30])
+def test_one_channel_far_above_the_others(tokens):
+    """Without a rotation, a channel of 10^5 times the others: the step of the fixed point is the largest one's, 2^-23 of it."""
+    layer = Layer(4, 256, 96, 16, 3.0, 0, 0, 22, device())
+    x, router = inputs(layer, tokens, torch.float32, torch.float32, 9)
+    x[:, 17] = 1e5
+    idx = (torch.arange(2 * tokens, device=x.device).view(tokens, 2) % 4).to(torch.int32)
+    weight = torch.full((tokens, 2), 0.5, device=x.device)
+    y, _, _, st = layer.run(x, 2, idx=idx, weight=weight)
+    assert st == 0
+    close(y, *layer.expect(x, idx.cpu().numpy(), weight.cpu().numpy()))
