@@ -401,3 +401,63 @@ def test_non_finite_rows_without_another_token(rows, vocab, tail):
     for n in ("loss", "loss1", "grad", "grad1"):
         assert torch.isnan(o[n][:4]).all(), n
     check(o, x, idx, lp, tail, 1.0, w, rows=[4, 5])
+
+
+def parts(rows, vocab, dtype):
+    """Elements of a block's part of a row, where few rows are split (as the host side splits them)."""
+    ve = 8 if dtype == torch.bfloat16 else 4
+    vectors = -(-vocab // ve)
+    n = max(1, min(-(-torch.cuda.get_device_properties(0).multi_processor_count * 4 // rows), -(-vectors // 1024), 256))
+    return -(-vectors // n) * ve
+
+
+@pytest.mark.parametrize("tail", ["none", "rest"])
+@pytest.mark.parametrize("rows,vocab,dtype", [
+    (1, 131071, torch.bfloat16), (3, 300001, torch.float32), (40, 50003, torch.float32),     # split
+    (1100, 70003, torch.bfloat16), (1100, 140005, torch.float32),                            # two passes, two segments of marks
+    (1030, 263007, torch.bfloat16),
+    (7, 2043, torch.bfloat16), (1100, 9001, torch.bfloat16), (5, 16381, torch.float32)])     # in registers
+def test_no_element_is_left_out(rows, vocab, dtype, tail):
+    """A logit far above all others, that no place names, at the row's ends and at the borders of vectors, parts and segments: without
+    it the loss would be 40 less."""
+    x, idx, lp, w = make(rows, vocab, dtype, 6, vocab)
+    x, ve = x.contiguous(), 8 if dtype == torch.bfloat16 else 4
+    part = parts(rows, vocab, dtype)
+    at = {0, 1, ve, vocab - 1, vocab - 2, vocab - vocab % ve, vocab - vocab % ve - 1, 32768 * ve - 1, 32768 * ve, 32768 * ve + 1}
+    for p in range(part, vocab, max(part, part * (vocab // part // 6))):
+        at |= {p - 1, p}
+    for block in (64, 128, 256, 1024):
+        at |= {block * ve - 1, block * ve, 4 * block * ve - 1, 4 * block * ve}
+    at = sorted(p for p in at if 0 <= p < vocab)
+    base = x.clone()
+    for i in range(0, len(at), rows):
+        x.copy_(base)
+        here = at[i:i + rows]
+        for r, p in enumerate(here):
+            idx[r][idx[r] == p] = -1
+            x[r, p] = float(base[r].float().max()) + 40.0
+        o, st = calls(x, idx, lp, tail, 1.0, w)
+        assert st == 0
+        ref = check(o, x, idx, lp, tail, 1.0, w, rows=range(len(here)))
+        live = (idx[:len(ref["loss"])] >= 0).cpu().numpy()
+        assert (ref["logprob"][live] < -38).all()
+
+
+@pytest.mark.parametrize("rows,vocab,dtype", [(1, 131072, torch.bfloat16), (2, 600001, torch.float32), (1100, 40001, torch.bfloat16),
+                                              (1100, 30001, torch.float32), (1030, 140001, torch.float32)])
+def test_log_probabilities_of_long_rows(rows, vocab, dtype):
+    """log q within what a thread really adds one after the other: pairs of vectors, of which a block of 256 threads or more has
+    V / (512 VE) a thread, each pair's elements in two chains; then the lanes, waves and parts (at most 256 of them).
+    b = u (16 + 4 log2 V + V / (512 VE) + VE): below a left-out vector's share of the sum, but for the longest row."""
+    x, idx, lp, w = make(rows, vocab, dtype, 16, 5)
+    o, st = calls(x, idx, lp, "none", 1.0, w)
+    assert st == 0
+    sel = sorted({0, rows // 2, rows - 1})
+    ref = oracle.distill(x[sel].float().cpu().numpy(), 1.0, idx[sel].cpu().numpy(), lp[sel].cpu().numpy(), "none")
+    ve = 8 if dtype == torch.bfloat16 else 4
+    b = U * (16 + 4 * np.log2(vocab) + vocab / (512 * ve) + ve)
+    assert b < ve / vocab or vocab > 200000
+    tol = b + 2 * U * np.abs(ref["logprob"]) + U * np.log(vocab)
+    for form in ("", "1"):
+        off = np.abs(o["logprob" + form][sel].cpu().numpy() - ref["logprob"])
+        assert (off <= tol).all(), (off.max(), tol.min())
