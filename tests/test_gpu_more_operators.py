@@ -128,3 +128,68 @@ def test_graph_replays_equal_eager_calls(tokens, k):
             for n in o:
                 assert same(o[n], eager[n]), (seed, n)
     assert int(status.item()) & ~e8q.STATUS_BITS["NONFINITE"] == 0
+
+
+@pytest.mark.parametrize("tokens,k", [(1, 2), (5, 3), (6, 4), (33, 4)])
+def test_graph_writes_every_output(tokens, k):
+    """A graph's outputs bit for bit as the eager calls', over marks of their own: what a call leaves unwritten differs, and so does
+    a NaN.  No status bit."""
+    d, places = device(), 9
+    layer = Layer(10, 256, 136, 16, 3.0, 128, 8, 15, d)
+    e, h, f = layer.shape
+    gen = torch.Generator(device=d).manual_seed(16)
+    router = torch.randn((e, h), generator=gen, device=d) / 16
+    x = torch.empty((tokens, h), dtype=torch.bfloat16, device=d)
+    logits, teacher = torch.empty((tokens, VOCAB), device=d), torch.empty((tokens, places), device=d)
+    ids = torch.empty((tokens, places), dtype=torch.int64, device=d)
+    _, a = test_gpu_adjust.make(tokens, VOCAB, torch.float32, 300, 20, False, 6)
+    status = torch.zeros(1, dtype=torch.int32, device=d)
+    one = torch.ones(tokens, device=d)
+    ws = [torch.full((max(1, size),), 0xFF, dtype=torch.uint8, device=d) for size in
+          (e8q.e8q_moe_workspace_size(e, h, f, tokens, k), e8q.e8q_distill_workspace_size(tokens, VOCAB, places))]
+    shapes = {"idx": ((tokens, k), torch.int32), "weight": ((tokens, k), torch.float32), "y": ((tokens, h), torch.bfloat16),
+              "adjusted": ((tokens, VOCAB), torch.float32), "loss": ((tokens,), torch.float32),
+              "logprob": ((tokens, places), torch.float32), "stats": ((tokens, 4), torch.float32),
+              "grad": ((tokens, VOCAB), torch.float32), "both": ((tokens, VOCAB), torch.float32), "loss1": ((tokens,), torch.float32)}
+    make = lambda mark: {n: torch.full(s, mark, dtype=t, device=d) for n, (s, t) in shapes.items()}  # noqa: E731
+
+    def work(o):
+        e8q.e8q_moe_core_escape(layer.gate, layer.up, layer.down, layer.bound, x, o["idx"], o["weight"], o["y"], ws[0], status,
+                                router=router, signs_in=layer.signs_in, had_block_in=layer.had_in,
+                                signs_down=layer.signs_down, had_block_down=layer.had_down, activation=ACT["silu"])
+        e8q.e8q_adjust_logits(logits, o["adjusted"], status, **a)
+        e8q.e8q_distill(o["adjusted"], ids, teacher, ws[1], status, tail=e8q.TAIL_REST, loss_out=o["loss"],
+                        logprob_out=o["logprob"], stats_out=o["stats"])
+        e8q.e8q_distill_backward(o["adjusted"], ids, teacher, o["stats"], one, o["grad"], status, tail=e8q.TAIL_REST)
+        e8q.e8q_distill_grad(logits, ids, teacher, one, o["both"], ws[1], status, tail=e8q.TAIL_RENORM, loss_out=o["loss1"])
+
+    def fill(seed):
+        g = torch.Generator(device=d).manual_seed(seed)
+        x.normal_(generator=g)
+        logits.normal_(0.0, 3.0, generator=g)
+        ids.copy_(torch.randint(-1, VOCAB, ids.shape, generator=g, device=d))
+        teacher.uniform_(-6.0, -2.5, generator=g)
+
+    fill(0)
+    out = make(-77)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        work(out)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        work(out)
+    for seed in (1, 2, 3):
+        fill(seed)
+        for t in out.values():
+            t.fill_(-77)
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = make(-99)
+        work(eager)
+        torch.cuda.synchronize()
+        for n in out:
+            assert torch.equal(out[n], eager[n]), (seed, n)
+    assert int(status.item()) == 0
