@@ -273,3 +273,22 @@ def test_extreme_repetition(dtype, value):
     out, st = run(x, a)
     assert st == 0
     check(out, x, a)
+
+
+def test_the_longest_row():
+    """2^31 - 17 logits: ids, biases and the mask's last words at both ends and in the middle, in place and out of it."""
+    vocab, d = (1 << 31) - 17, device()
+    x = torch.ones((1, vocab), dtype=torch.bfloat16, device=d)
+    at = torch.tensor([0, vocab // 2, vocab - 1], device=d)
+    mask = torch.full(((vocab + 31) // 32,), -1, dtype=torch.int32, device=d)
+    mask[(vocab - 2) // 32] &= ~(1 << (vocab - 2) % 32)
+    a = {"history": at[None].contiguous(), "frequency": torch.full((1,), 0.5, device=d), "bias_idx": at[1:] - 1,
+         "bias": torch.tensor([2.0, 4.0], device=d), "mask": mask}
+    for got in (None, x):
+        got, st = run(x, a, out=got)
+        assert st == 0
+        assert got[0, at].tolist() == [0.5, 0.5, 0.5] and float(got[0, vocab // 2 - 1]) == 3.0
+        assert float(got[0, vocab - 2]) == -float("inf")
+        got[0, at] = 1.0
+        got[0, at[1:] - 1] = 1.0
+        assert bool((got == 1.0).all())

@@ -461,3 +461,30 @@ def test_log_probabilities_of_long_rows(rows, vocab, dtype):
     for form in ("", "1"):
         off = np.abs(o["logprob" + form][sel].cpu().numpy() - ref["logprob"])
         assert (off <= tol).all(), (off.max(), tol.min())
+
+
+def test_the_longest_row():
+    """2^31 - 17 logits, all 0 but the last one: sums of ones, which float32 adds without loss up to 2^24 in a thread, then join by
+    rounding to 2^-24 each: eight lane and part levels, 16 u of the sum."""
+    vocab = (1 << 31) - 17
+    x = torch.zeros((1, vocab), dtype=torch.bfloat16, device=device())
+    x[0, -1] = 20.0
+    idx = torch.tensor([[0, vocab // 2, vocab - 2]], device=x.device)
+    lp = torch.log(torch.tensor([[0.25, 0.5, 0.125]], device=x.device))
+    w = torch.full((1,), 2.0 ** 20, device=x.device)
+    o, st = calls(x, idx, lp, "rest", 1.0, w)
+    assert st == 0
+    total, p = vocab - 1 + np.exp(20.0), np.exp(lp.cpu().numpy().astype(np.float64))[0]
+    lse, rest, w_rest = np.log(total), (total - 3) / total, 1 - p.sum()
+    loss = (p * (np.log(p) + lse)).sum() + w_rest * (np.log(w_rest) - np.log(rest))
+    plain, last = (1 - w_rest / rest) / total * 2.0 ** 20, (1 - w_rest / rest) * np.exp(20.0) / total * 2.0 ** 20
+    for form in ("", "1"):
+        assert abs(float(o["loss" + form][0]) - loss) < 64 * U * (lse + 1)
+        assert np.abs(o["logprob" + form][0].cpu().numpy() + lse).max() < 32 * U * lse
+        g = o["grad" + form][0]
+        named = (1 / total - p) * 2.0 ** 20
+        assert np.abs(g[idx[0]].float().cpu().numpy() - named).max() < 2.0 ** -8 * np.abs(named).max()
+        assert abs(float(g[-1]) - last) < 1.01 * 2.0 ** -8 * last
+        g[idx[0]] = g[1].clone()
+        g[-1] = g[1]
+        assert abs(float(g[1]) - plain) < 1.01 * 2.0 ** -8 * plain and bool((g == g[1]).all())

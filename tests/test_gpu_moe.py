@@ -347,3 +347,11 @@ def test_one_channel_far_above_the_others(tokens):
     y, _, _, st = layer.run(x, 2, idx=idx, weight=weight)
     assert st == 0
     close(y, *layer.expect(x, idx.cpu().numpy(), weight.cpu().numpy()))
+
+
+@pytest.mark.parametrize("hidden,inter,had_in,had_down", [(32768, 64, 0, 8), (64, 32768, 8, 0), (20480, 40, 4096, 8),
+                                                          (24, 20480, 8, 4096)])
+@pytest.mark.parametrize("tokens", [1, 12])
+def test_the_widest_matrices(hidden, inter, had_in, had_down, tokens):
+    layer = Layer(2, hidden, inter, 16, 3.0, had_in, had_down, 23, device())
+    check(layer, tokens, 2, tokens)
