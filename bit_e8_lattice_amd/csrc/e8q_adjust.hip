@@ -15,14 +15,16 @@
 // Few elements are touched (2048 ids in a vocabulary of 131072), so a lane takes its
 // touched elements one by one: all elements of every vector with a touched one, the wave
 // through, made the arithmetic the bound (512 rows of 131072 bf16 logits with 2048 ids,
-// biases and a mask: 81.5 us so, 68.8 one by one).  Biases of the part are
+// biases and a mask: 81.5 us so, 70 one by one).  Biases of the part are
 // chained in LDS by their elements; a lane walks the chain of its own, and the wave walks
 // all of them together for an element that has very many (483 rows of 930 tokens, 300
 // biases each: 218 us with the wave for every element, 18).  Several of one element
 // are added in the order of their places.
 //
-// The bound is memory: logits in and out, history and mask are 60 us of the 68.8 at a
-// large copy's rate.  One row takes 4.8 us, the wait for its length, its ids and its logits in turn.
+// The bound is memory: logits in and out, history and mask are 60 us of the 70 at a
+// large copy's rate.  One row takes 5 us, the wait for its length, its ids and its logits in turn.  In place, touched
+// vectors are loaded after the history is counted: as fast with a mask that touches most of them (70.5 us a call, 69 out
+// of place) as without one (71.6, 72.7).
 #include <float.h>
 
 #include "e8q_rows.hpp"

@@ -28,7 +28,7 @@
 // hold (8192 rows of 131072: 1015 us from the start, 973 from the end; in the
 // registers of one block of 1024 threads, which has a CU to itself, 1176).  The bound
 // is memory: the bytes of the logits, and of the gradient.  Reached of them:
-// 4.4 TB/s with 32768 and with 131072 bf16 logits a row (4096 rows 122 us), a copy 4.9.
+// 4.6 TB/s with 32768 bf16 logits a row (4096 rows 117 us), 4.4 with 131072 (8192 rows 976 us); a copy 4.9.
 #include <float.h>
 
 #include "e8q_rows.hpp"
@@ -722,14 +722,16 @@ static size_t ds_part_bytes(uint64_t blocks) { return size_t((blocks * sizeof(fl
 // Longest rows that every call keeps in registers, and that need no workspace.
 constexpr uint32_t kRowVectors = 256 * 16;
 
-// The parts' sums and the rows' statistics.
+// The parts' sums and the rows' statistics.  One size for the loss alone and for the one call with the gradient: the latter
+// does not use it for rows of 512 x 16 vectors.
 static size_t ds_workspace(int64_t rows, int64_t vocab, size_t esz) {
     uint32_t per = 0;
     const uint64_t splits = lp_splits(rows, vocab, esz, per);
     return splits == 1 || ds_vectors(vocab, esz) <= kRowVectors ? 0 : ds_part_bytes(uint64_t(rows) * splits) + size_t(rows) * sizeof(float4);
 }
 
-// Rows that the registers of one block hold: the smallest such block; whether there is one.
+// Rows that the registers of one block hold: the smallest such block; whether there is one.  512 x 16 vectors are for
+// float32 gradients only: the loss alone of such rows takes the split passes (301 rows of 32003: 11.7 + 4.5 us).
 template <typename T, bool GRAD, class Go>
 static bool ds_row_kernel(int64_t vocab, Go&& go) {
     const uint32_t nvec = ds_vectors(vocab, sizeof(T));

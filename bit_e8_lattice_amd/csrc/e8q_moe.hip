@@ -32,11 +32,11 @@
 // it); the weighted sum in the order of the places (up to 16 places: inside down).
 //
 // What bounds it (128 experts of 2048 x 768, 8 a token, C(16) and 3.0 x row RMS, medians of
-// a kernel trace): for one token three dependent launches of 5.9 + 13.7 + 14.0 us, each a
+// a kernel trace): for one token three dependent launches of 5.7 + 13.5 + 14.2 us, each a
 // chain of waits (the choice, the table, the indices, the sum over waves) for 10 MB in
-// all; for 64 tokens gate and up 44.1 us and down 42.1, where 151 MB of indices are
-// 31 us at a large copy's rate: a turn of jobs on all CUs reads at 4.6 TB/s, but the second turn
-// has jobs for half of them.
+// all, the last one on 64 blocks of 32 rows for 256 CUs; for 64 tokens gate and up 43.7 us and down 41.7, where 151 MB of
+// indices are 31 us at a large copy's rate: a turn of jobs on all CUs reads at 4.6 TB/s, but the second turn
+// has jobs for half of them, and every job of down makes the digits of its tokens' h again.
 //
 // A chunk with escaped slots goes the plain way with zero points in them, then their records'
 // bytes alone: resolving slot by slot in one path took 107 us for 64 tokens where this
@@ -520,7 +520,7 @@ __global__ __launch_bounds__(kChooseThreads) void moe_choose_kernel(MoeArgs a) {
 
 // Time of a job of `units` units, in quarters of a chunk's (about 1 us): six chunks beside its sweep (its tokens' digits and
 // records, 5 to 6.5 us), a round of sixteen units a chunk's for each and 1.3 for the sums, half as much again for two products.  A
-// round of few units is split along the chunks.
+// round of few units is split along the chunks.  Fitted to jobs of 2048 x 768 alone; elsewhere a guess that costs time, not results.
 __device__ __forceinline__ uint32_t job_cost(uint32_t units, uint32_t chunks, bool two) {
     const uint32_t full = units / kMoeWaves, left = units % kMoeWaves;
     const uint32_t sweep = 4u * (full * chunks + (chunks * left + kMoeWaves - 1u) / kMoeWaves);
