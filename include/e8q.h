@@ -486,8 +486,8 @@ size_t e8q_gemv_workspace_size(int64_t batch, int64_t m, int64_t rows, int64_t c
  * where all logits of a token are -inf, or one is +inf, weights are NaN.  Malformed exports
  * and bad scales are flagged as in e8q_decode_core_escape (the slot or row is 0); so is a
  * record with |2z| > 2^14, which no encoder writes (E8Q_STATUS_X_RANGE).
- * Limits: hidden, inter multiples of 8 and <= 32768; experts <= 1024; top_k <= 64;
- * tokens * top_k <= 4096.
+ * Limits: hidden, inter multiples of 8 and <= 32768; experts <= 1024; top_k <= 64 and
+ * <= experts, also with the caller's places; tokens * top_k <= 4096.
  * ------------------------------------------------------------------------- */
 enum { E8Q_ACT_SILU = 0, E8Q_ACT_GELU_TANH = 1 };
 
